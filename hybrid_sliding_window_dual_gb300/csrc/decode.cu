@@ -211,7 +211,7 @@ __device__ int32_t find_seq(const int4 *desc, int32_t n, int64_t u) {
         const int32_t idx = min(lo + lane * step, hi);
         const unsigned m = __ballot_sync(0xffffffffu, desc[idx].x <= u);
         const int32_t last = 31 - __clz(m);  // lane 0 probes lo, always true
-        lo += last * step;
+        lo = min(lo + last * step, hi);      // lanes past hi probed hi itself
         hi = min(lo + step - 1, hi);
     }
     const int32_t idx = lo + lane;
