@@ -29,6 +29,12 @@ HSWA_DTYPE_F32 = 0
 HSWA_DTYPE_BF16 = 1
 HSWA_DTYPE_FP8_E4M3 = 2
 HSWA_DECODE_MAX_TOKENS = 16
+HSWA_ROPE_MAX_AXES = 4
+HSWA_ROPE_HALVES = 0
+HSWA_ROPE_ADJACENT = 1
+HSWA_ROPE_SECTIONS = 0
+HSWA_ROPE_INTERLEAVED = 1
+HSWA_VERIFY_MAX_VOCAB = 1 << 20
 
 
 class HswaError(RuntimeError):
@@ -56,8 +62,15 @@ class Layer(ctypes.Structure):
                 ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
+class RopeConfig(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("pairing", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("order", ctypes.c_int32), ("section", ctypes.c_int32 * HSWA_ROPE_MAX_AXES),
+                ("theta", ctypes.c_double), ("inv_freq", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 _SIG = {
     "hswa_pool_create": (_I, [ctypes.POINTER(Config), _P, _P, ctypes.POINTER(_P)]),
     "hswa_pool_destroy": (_I, [_P]),
@@ -66,6 +79,8 @@ _SIG = {
     "hswa_seq_free": (_I, [_P, _I, _P]),
     "hswa_swa_drop": (_I, [_P, _I, _P, _P]),
     "hswa_swa_restore": (_I, [_P, _I, _P, _P]),
+    "hswa_seq_truncate": (_I, [_P, _I, _P, _P, _P]),
+    "hswa_evict": (_I, [_P, _I, _P, _P, _P, ctypes.c_int32, _P]),
     "hswa_get_tables": (_I, [_P, _P, _P, _P]),
     "hswa_get_free_list": (_I, [_P, _I, _P, ctypes.c_int32, _P]),
     "hswa_seq_share_prefix": (_I, [_P, ctypes.c_int32, ctypes.c_int32, _P, _P]),
@@ -79,6 +94,9 @@ _SIG = {
     "hswa_tree_nodes": (_I, [_P, _P, ctypes.c_int32, _P]),
     "hswa_sync_tables": (_I, [_P, _P, _P, _P, _P]),
     "hswa_append_kv": (_I, [_P, ctypes.POINTER(Layer), _P, _P, _P, _I, _P]),
+    "hswa_rope_create": (_I, [ctypes.POINTER(RopeConfig), ctypes.POINTER(_P)]),
+    "hswa_rope_destroy": (_I, [_P]),
+    "hswa_rope_append": (_I, [_P, ctypes.POINTER(Layer), _P, _P, _L, _P, _L, _P, _L, _P, _P, _P, _I, _P]),
     "hswa_decode_workspace_size": (ctypes.c_size_t, [_P, _I]),
     "hswa_decode": (_I, [_P, ctypes.POINTER(Layer), _P, _P, _P, _P, _I, ctypes.c_float, _P,
                          ctypes.c_size_t, _P]),
@@ -88,6 +106,11 @@ _SIG = {
     "hswa_decode_multi_workspace_size": (ctypes.c_size_t, [_P, _I, _I]),
     "hswa_decode_multi": (_I, [_P, ctypes.POINTER(Layer), _P, _P, _P, _P, _I, _I, ctypes.c_float, _P,
                                ctypes.c_size_t, _P]),
+    "hswa_decode_weights_workspace_size": (ctypes.c_size_t, [_P, _I]),
+    "hswa_decode_weights": (_I, [_P, ctypes.POINTER(Layer), _P, _P, _P, _P, _I, ctypes.c_float, _P, ctypes.c_float, _P,
+                                 _P, ctypes.c_size_t, _P]),
+    "hswa_evict_select": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P]),
+    "hswa_verify_draft": (_I, [_I, _P, _L, _P, _L, _P, _P, _P, _I, _I, _I, _P, _P, _P]),
     "hswa_prefill_chunk": (_I, [_P, ctypes.POINTER(Layer), _P, _P, _P, _P, _P, _I, _I, _I,
                                 ctypes.c_float, _P]),
     "hswa_prefill_workspace_size": (ctypes.c_size_t, [_P, ctypes.POINTER(Layer), _I, _I]),
@@ -205,6 +228,28 @@ def hswa_seq_free(pool, seq_ids):
     _check(lib.hswa_seq_free(pool, len(ids), _ptr(ids)), "hswa_seq_free")
 
 
+def hswa_seq_truncate(pool, seq_ids, new_len):
+    """Shorten sequences to new_len tokens; Full pages that became free."""
+    ids, n = _i32(seq_ids), _i32(new_len)
+    if ids.shape != n.shape:
+        raise ValueError("one new length per sequence")
+    out = ctypes.c_int32()
+    _check(lib.hswa_seq_truncate(pool, len(ids), _ptr(ids), _ptr(n), ctypes.addressof(out)), "hswa_seq_truncate")
+    return out.value
+
+
+def hswa_evict(pool, seq_ids, n_keep, keep):
+    """Keep pages keep[i, :n_keep[i]] of sequence seq_ids[i] (keep: [n, stride]
+    int32); Full pages that became free."""
+    ids, n, k = _i32(seq_ids), _i32(n_keep), _i32(keep)
+    if n.shape != ids.shape or k.ndim != 2 or k.shape[0] != len(ids):
+        raise ValueError("one list of pages per sequence")
+    out = ctypes.c_int32()
+    _check(lib.hswa_evict(pool, len(ids), _ptr(ids), _ptr(n), _ptr(k), k.shape[1], ctypes.addressof(out)),
+           "hswa_evict")
+    return out.value
+
+
 def hswa_get_tables(pool, config: Config):
     full = np.empty((config.max_seqs, config.max_pages_per_seq), np.int32)
     swa = np.empty_like(full)
@@ -296,6 +341,35 @@ def hswa_append_kv(pool, layer: Layer, k, v, d_slots, n_tokens, stream=None):
                               _stream(stream)), "hswa_append_kv")
 
 
+def hswa_rope_create(rotary_dim, sections, theta=10000.0, inv_freq=None, interleaved=False, adjacent=False):
+    """A rotary embedding: sections = pairs of each position axis."""
+    cfg = RopeConfig(rotary_dim=int(rotary_dim), pairing=HSWA_ROPE_ADJACENT if adjacent else HSWA_ROPE_HALVES,
+                     n_axes=len(sections), order=HSWA_ROPE_INTERLEAVED if interleaved else HSWA_ROPE_SECTIONS,
+                     theta=float(theta))
+    if len(sections) <= HSWA_ROPE_MAX_AXES:  # more is the library's to refuse
+        cfg.section[:len(sections)] = [int(x) for x in sections]
+    freq = None
+    if inv_freq is not None:
+        freq = np.ascontiguousarray(inv_freq, np.float64)
+        if freq.shape != (int(rotary_dim) // 2,):
+            raise ValueError("inv_freq must hold rotary_dim / 2 frequencies")
+        cfg.inv_freq = _ptr(freq)
+    out = ctypes.c_void_p()
+    _check(lib.hswa_rope_create(ctypes.byref(cfg), ctypes.byref(out)), "hswa_rope_create")
+    return out.value
+
+
+def hswa_rope_destroy(rope):
+    _check(lib.hswa_rope_destroy(rope), "hswa_rope_destroy")
+
+
+def hswa_rope_append(pool, layer: Layer, rope, q, q_stride, k, k_stride, v, v_stride, d_pos, d_slots, q_out, n_tokens,
+                     stream=None):
+    _check(lib.hswa_rope_append(pool, ctypes.byref(layer), rope, _ptr(q), int(q_stride), _ptr(k), int(k_stride),
+                                _ptr(v), int(v_stride), _ptr(d_pos), _ptr(d_slots), _ptr(q_out), int(n_tokens),
+                                _stream(stream)), "hswa_rope_append")
+
+
 def hswa_decode_workspace_size(pool, n_seqs):
     return int(lib.hswa_decode_workspace_size(pool, int(n_seqs)))
 
@@ -320,6 +394,31 @@ def hswa_decode_multi(pool, layer: Layer, q, o, d_bt, d_seq_len, n_seqs, n_tok, 
     _check(lib.hswa_decode_multi(pool, ctypes.byref(layer), _ptr(q), _ptr(o), _ptr(d_bt), _ptr(d_seq_len),
                                  int(n_seqs), int(n_tok), float(scale), _ptr(ws), int(ws_bytes), _stream(stream)),
            "hswa_decode_multi")
+
+
+def hswa_decode_weights_workspace_size(pool, n_seqs):
+    return int(lib.hswa_decode_weights_workspace_size(pool, int(n_seqs)))
+
+
+def hswa_decode_weights(pool, layer: Layer, q, o, d_bt, d_seq_len, n_seqs, scale, w_in, decay, w_out, ws, ws_bytes,
+                        stream=None):
+    _check(lib.hswa_decode_weights(pool, ctypes.byref(layer), _ptr(q), _ptr(o), _ptr(d_bt), _ptr(d_seq_len),
+                                   int(n_seqs), float(scale), _ptr(w_in), float(decay), _ptr(w_out), _ptr(ws),
+                                   int(ws_bytes), _stream(stream)), "hswa_decode_weights")
+
+
+def hswa_evict_select(pool, d_seq_len, w_in, d_budget, n_seqs, sink_pages, recent_tokens, keep, n_keep, w_out,
+                      stream=None):
+    _check(lib.hswa_evict_select(pool, _ptr(d_seq_len), _ptr(w_in), _ptr(d_budget), int(n_seqs), int(sink_pages),
+                                 int(recent_tokens), _ptr(keep), _ptr(n_keep), _ptr(w_out), _stream(stream)),
+           "hswa_evict_select")
+
+
+def hswa_verify_draft(dtype, p, p_stride, q, q_stride, d_draft, d_n_draft, u, n_seqs, n_tok, vocab, n_accept, tokens,
+                      stream=None):
+    _check(lib.hswa_verify_draft(int(dtype), _ptr(p), int(p_stride), _ptr(q), int(q_stride), _ptr(d_draft),
+                                 _ptr(d_n_draft), _ptr(u), int(n_seqs), int(n_tok), int(vocab), _ptr(n_accept),
+                                 _ptr(tokens), _stream(stream)), "hswa_verify_draft")
 
 
 def hswa_decode_noalloc(pool, layer: Layer, q, o, d_bt, d_seq_len, n_seqs, scale, stream=None):

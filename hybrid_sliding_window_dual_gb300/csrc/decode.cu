@@ -133,6 +133,10 @@ struct DecodeArgs {
     int32_t n_tok;  // query tokens per sequence (multi-token decode), 1 otherwise
     float scale_log2;
     int *err;
+    // decode with page weights (null otherwise): log2 of the sum of 2^score
+    // over a page, [n_seqs][Hkv][bt_stride][parts][8 heads], and over all of
+    // a sequence's keys, [n_seqs][Hq]
+    float *page_lse, *seq_lse;
 };
 
 // Row of q / o holding query token w of sequence s.
@@ -399,9 +403,28 @@ drain:
     }
 }
 
+// Write a page's log-sum of 8 heads (decode with page weights) from the
+// warp's sums of 2^(score - b) in the S fragment layout: thread (g, q) holds
+// its rows' sums of heads 2q (w0) and 2q + 1 (w1). Nothing seen: -inf.
+__device__ __forceinline__ void store_page_lse(const DecodeArgs &a, const StageDesc &d, int part, int parts, float b0,
+                                               float b1, float w0, float w1) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+        w0 += __shfl_xor_sync(0xffffffffu, w0, off);
+        w1 += __shfl_xor_sync(0xffffffffu, w1, off);
+    }
+    if (lane < 4) {
+        const int64_t at = (((int64_t)d.seq * a.hkv + d.kvh) * a.bt_stride + d.key0 / kP) * parts + part;
+        reinterpret_cast<float2 *>(a.page_lse)[at * 4 + lane] =
+            make_float2(w0 == 0.f ? -INFINITY : b0 + log2f(w0), w1 == 0.f ? -INFINITY : b1 + log2f(w1));
+    }
+}
+
 // One consumer warp: query token w (8 query heads) of the stage's (sequence,
 // kv head).
-template <int kTok>
+// kWeights: also write each page's log-sum per head (one token).
+template <int kTok, bool kWeights>
 __device__ void decode_consumer(DecodeSmemT<kTok> &sm, const DecodeArgs &a, int64_t u0, int64_t u1, int w) {
     constexpr int kStages = DecodeSmemT<kTok>::kStages;
     const int lane = threadIdx.x & 31;
@@ -492,10 +515,15 @@ __device__ void decode_consumer(DecodeSmemT<kTok> &sm, const DecodeArgs &a, int6
             m1 = n1;
             float ps0 = 0.f, ps1 = 0.f;
             uint32_t pb[4][2];
+            float w0 = 0.f, w1 = 0.f;
 #pragma unroll
             for (int kt = 0; kt < 4; ++kt) {
                 const float p0 = fast_exp2(sacc[kt][0] - b0), p1 = fast_exp2(sacc[kt][1] - b1);
                 const float p2 = fast_exp2(sacc[kt][2] - b0), p3 = fast_exp2(sacc[kt][3] - b1);
+                if constexpr (kWeights) {  // not rounded to bf16: the weights go out in fp32
+                    w0 += p0 + p2;
+                    w1 += p1 + p3;
+                }
                 const uint32_t x0 = pack_bf16(p0, p1), x1 = pack_bf16(p2, p3);
                 // sum what the MMA will see (the bf16-rounded weights)
                 const __nv_bfloat162 r0 = *reinterpret_cast<const __nv_bfloat162 *>(&x0);
@@ -507,6 +535,7 @@ __device__ void decode_consumer(DecodeSmemT<kTok> &sm, const DecodeArgs &a, int6
             }
             l0 = l0 * al0 + ps0;
             l1 = l1 * al1 + ps1;
+            if constexpr (kWeights) store_page_lse(a, d, 0, 1, b0, b1, w0, w1);
 #pragma unroll
             for (int dt = 0; dt < 8; ++dt) {
                 oacc[dt][0] *= al0;
@@ -526,6 +555,8 @@ __device__ void decode_consumer(DecodeSmemT<kTok> &sm, const DecodeArgs &a, int6
                     mma_bf16_16816(oacc[dt], a0, a1, a2, a3, pb[kt][0], pb[kt][1]);
                 }
             }
+        } else if constexpr (kWeights) {
+            store_page_lse(a, d, 0, 1, 0.f, 0.f, 0.f, 0.f);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.empty[stage]);
@@ -572,7 +603,7 @@ __device__ void decode_consumer(DecodeSmemT<kTok> &sm, const DecodeArgs &a, int6
 
 // Consumer warps 0 .. kTok - 1, one query token each (warps past n_tok stay
 // idle); warp kTok is the producer.
-template <int kTok>
+template <int kTok, bool kWeights>
 __global__ void __launch_bounds__(32 * (kTok + 1)) decode_mma_bf16_d128(const __grid_constant__ CUtensorMap tk,
                                                                       const __grid_constant__ CUtensorMap tv,
                                                                       DecodeArgs a) {
@@ -597,7 +628,7 @@ __global__ void __launch_bounds__(32 * (kTok + 1)) decode_mma_bf16_d128(const __
     if (warp == kTok)
         decode_producer<false>(sm, &tk, &tv, a, u0, u1);
     else if (warp < a.n_tok)
-        decode_consumer<kTok>(sm, a, u0, u1, warp);
+        decode_consumer<kTok, kWeights>(sm, a, u0, u1, warp);
 }
 
 // ---------------------------------------------------------- FP8 decode
@@ -666,7 +697,8 @@ __device__ __forceinline__ bool merge_sync(Smem &sm, uint32_t &phase, int *err) 
 // transpose. Every converted K and V fragment feeds the MMAs of all kTok
 // tokens. At the end of a piece warps 1-3 hand their (max, sum, o) to warp 0
 // through shared memory, which merges and writes.
-template <int kTok>
+// kWeights: also write the log-sum per head of the warp's 16 keys of a page.
+template <int kTok, bool kWeights>
 __device__ void decode_consumer_fp8(DecodeSmem8T<kTok> &sm, const DecodeArgs &a, int64_t u0, int64_t u1) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int gr = lane >> 2, qd = lane & 3;
@@ -772,6 +804,7 @@ __device__ void decode_consumer_fp8(DecodeSmem8T<kTok> &sm, const DecodeArgs &a,
                 const float p2 = fast_exp2(sacc[j][2] - b0), p3 = fast_exp2(sacc[j][3] - b1);
                 l0[j] = l0[j] * al0 + 256.f * (p0 + p2);
                 l1[j] = l1[j] * al1 + 256.f * (p1 + p3);
+                if constexpr (kWeights) store_page_lse(a, d, w, kConsumers8, b0, b1, p0 + p2, p1 + p3);
                 pb0[j] = movmatrix_t(pack_f16(p0 * w0, p1 * w0));
                 pb1[j] = movmatrix_t(pack_f16(p2 * w1, p3 * w1));
                 if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {  // a head's max moved
@@ -798,6 +831,8 @@ __device__ void decode_consumer_fp8(DecodeSmem8T<kTok> &sm, const DecodeArgs &a,
 #pragma unroll
                 for (int j = 0; j < kTok; ++j) mma_f16_16816(oacc[j][2 * dp + 1], a0, a1, a2, a3, pb0[j], pb1[j]);
             }
+        } else if constexpr (kWeights) {
+            store_page_lse(a, d, w, kConsumers8, 0.f, 0.f, 0.f, 0.f);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.empty[stage]);
@@ -905,7 +940,7 @@ __device__ void decode_consumer_fp8(DecodeSmem8T<kTok> &sm, const DecodeArgs &a,
     }
 }
 
-template <int kTok>
+template <int kTok, bool kWeights>
 __global__ void __launch_bounds__(32 * (kConsumers8 + 1)) decode_mma_fp8_d128(const __grid_constant__ CUtensorMap tk,
                                                                            const __grid_constant__ CUtensorMap tv,
                                                                            DecodeArgs a) {
@@ -930,7 +965,7 @@ __global__ void __launch_bounds__(32 * (kConsumers8 + 1)) decode_mma_fp8_d128(co
     if (threadIdx.x >= 32 * kConsumers8)
         decode_producer<true>(sm, &tk, &tv, a, u0, u1);
     else
-        decode_consumer_fp8<kTok>(sm, a, u0, u1);
+        decode_consumer_fp8<kTok, kWeights>(sm, a, u0, u1);
 }
 
 // ------------------------------------------------ tensor-core multi-token
@@ -1605,7 +1640,9 @@ __global__ void __launch_bounds__(Smem::kThreads, 1)
 }
 
 // Merge the partial records of segments split between CTAs; write zeros
-// for sequences without keys.
+// for sequences without keys. kParts > 0 (decode with page weights): also
+// the log-sum over a sequence's keys, from its pages' (kParts each).
+template <int kParts>
 __global__ void __launch_bounds__(256) decode_combine(DecodeArgs a, int32_t n_ctas) {
     const int32_t s = blockIdx.y / a.n_tok, w = blockIdx.y % a.n_tok, g = blockIdx.x;
     pdl_wait();
@@ -1617,9 +1654,25 @@ __global__ void __launch_bounds__(256) decode_combine(DecodeArgs a, int32_t n_ct
     __nv_bfloat16 *out = a.o + (q_row(a, s, w) * a.hq + (int64_t)g * kG + h) * kD + d0;
     if (units == 0) {
         for (int i = 0; i < 4; ++i) out[i] = __float2bfloat16_rn(0.f);
+        if (kParts > 0 && d0 == 0) a.seq_lse[(int64_t)s * a.hq + g * kG + h] = -INFINITY;
         return;
     }
     const int32_t npg = units / a.hkv;
+    if constexpr (kParts > 0) {
+        const float *lse = a.page_lse + ((int64_t)s * a.hkv + g) * a.bt_stride * kParts * kG + h;
+        float m = -INFINITY, l = 0.f;
+        for (int32_t i = threadIdx.x & 31; i < npg * kParts; i += 32) {
+            const float x = lse[(int64_t)i * kG];
+            const float n = fmaxf(m, x);
+            if (n > -INFINITY) l = l * exp2f(m - n) + exp2f(x - n);
+            m = n;
+        }
+        float M = m;
+        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        if (M > -INFINITY) l *= exp2f(m - M);
+        for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+        if (d0 == 0) a.seq_lse[(int64_t)s * a.hq + g * kG + h] = M > -INFINITY ? M + log2f(l) : -INFINITY;
+    }
     const int64_t lo = d.x + (int64_t)g * npg, hi = lo + npg;  // [lo, hi)
     const int64_t c_lo = cta_of(lo, U, N), c_hi = cta_of(hi - 1, U, N);
     if (c_lo == c_hi) return;
@@ -1655,6 +1708,125 @@ template <>
 __device__ __forceinline__ float from_f<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// ---------------------------------------------------- decode with page weights
+// Where the attention of a decode step went, page by page: the softmax
+// weights of all query heads summed over each page's keys. The decode
+// kernels leave the log-sum of every page and head (32 bytes a page and kv
+// head, a thousandth of the page) and the merge adds the log-sum of the
+// sequence; this pass turns them into weights and adds them to the caller's.
+// A row's entries past the sequence's last page become 0, so that pages
+// added later start from nothing.
+struct WeightArgs {
+    const float *page_lse;  // [n_seqs][Hkv][max_pages][parts][G], log2
+    const float *seq_lse;   // [n_seqs][Hkv][G], log2
+    const int32_t *seq_len;
+    const float *w_in;
+    float *w_out;
+    float decay;
+    int32_t hkv, group, parts, page, max_pages;
+};
+
+// 8 threads a page, each a part of the kv heads.
+__global__ void __launch_bounds__(256) page_weights(const WeightArgs a) {
+    const int sub = threadIdx.x & 7;
+    const int64_t s = blockIdx.y;
+    const int32_t p = blockIdx.x * 32 + (threadIdx.x >> 3);
+    pdl_wait();
+    pdl_launch_dependents();
+    const int32_t L = a.seq_len[s];
+    const bool there = p < a.max_pages && (int64_t)p * a.page < L;
+    float w = 0.f;
+    if (there) {
+        const int32_t n = a.parts * a.group;
+        for (int32_t g = sub; g < a.hkv; g += 8) {
+            const float *x = a.page_lse + ((s * a.hkv + g) * a.max_pages + p) * n;
+            const float *all = a.seq_lse + (s * a.hkv + g) * a.group;
+            for (int32_t i = 0; i < n; ++i) {
+                const float y = all[i % a.group];
+                if (y > -INFINITY) w += exp2f(x[i] - y);
+            }
+        }
+    }
+    for (int off = 4; off > 0; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
+    if (sub == 0 && p < a.max_pages) {
+        const int64_t at = s * a.max_pages + p;
+        a.w_out[at] = !there ? 0.f : a.w_in && a.decay != 0.f ? fmaf(a.decay, a.w_in[at], w) : w;
+    }
+}
+
+// Decode with page weights for any dtype / head_dim (<= 256) / head ratio /
+// page size: one CTA per (query head, sequence), its 8 warps taking the
+// pages in turn, each with a softmax of its own, merged at the end.
+template <typename T>
+__global__ void __launch_bounds__(256) decode_weights_any(const T *__restrict__ q, T *__restrict__ o,
+                                                          const T *__restrict__ kp, const T *__restrict__ vp,
+                                                          const int32_t *__restrict__ bt,
+                                                          const int32_t *__restrict__ seq_len, float *page_lse,
+                                                          float *seq_lse, int32_t bt_stride, int32_t hq, int32_t hkv,
+                                                          int32_t d, int32_t page, int32_t num_pages,
+                                                          float scale_log2, int *err) {
+    constexpr int kE = 8, kW = 8;
+    __shared__ float s_m[kW], s_l[kW], s_o[kW][32 * kE];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int32_t h = blockIdx.x, group = hq / hkv, g = h / group;
+    const int64_t s = blockIdx.y;
+    const int32_t L = max(seq_len[s], 0);
+    const int64_t row = (s * hq + h) * d;
+    float qv[kE], acc[kE];
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+        const int c = lane + 32 * e;
+        qv[e] = c < d ? to_f(q[row + c]) * scale_log2 : 0.f;
+        acc[e] = 0.f;
+    }
+    float m = -INFINITY, l = 0.f;
+    const int32_t npg = min((int32_t)(((int64_t)L + page - 1) / page), bt_stride);
+    for (int32_t p = warp; p < npg; p += kW) {
+        const int32_t pg = bt[s * bt_stride + p];
+        float pm = -INFINITY, pl = 0.f;  // this page's max and sum
+        if (pg < 0 || pg >= num_pages) {
+            if (lane == 0) set_error(err, HSWA_ERR_BOUNDS);
+        } else {
+            const int32_t n = min(page, L - p * page);
+            for (int32_t r = 0; r < n; ++r) {
+                const int64_t base = (((int64_t)pg * hkv + g) * page + r) * d;
+                float dot = 0.f;
+#pragma unroll
+                for (int e = 0; e < kE; ++e) {
+                    const int c = lane + 32 * e;
+                    if (c < d) dot += qv[e] * to_f(kp[base + c]);
+                }
+                for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+                const float nm = fmaxf(m, dot), np = fmaxf(pm, dot);
+                const float alpha = exp2f(m - nm), x = exp2f(dot - nm);
+                l = l * alpha + x;
+                pl = pl * exp2f(pm - np) + exp2f(dot - np);
+                m = nm;
+                pm = np;
+#pragma unroll
+                for (int e = 0; e < kE; ++e) {
+                    const int c = lane + 32 * e;
+                    acc[e] = acc[e] * alpha + (c < d ? x * to_f(vp[base + c]) : 0.f);
+                }
+            }
+        }
+        if (lane == 0) page_lse[((s * hkv + g) * bt_stride + p) * group + h % group] = pm + log2f(pl);
+    }
+    if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) s_o[warp][lane + 32 * e] = acc[e];
+    __syncthreads();
+    float M = -INFINITY, sum = 0.f, out = 0.f;
+    for (int w = 0; w < kW; ++w) M = fmaxf(M, s_m[w]);
+    for (int w = 0; w < kW; ++w) {
+        const float f = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - M);
+        sum += f * s_l[w];
+        out += f * s_o[w][threadIdx.x];
+    }
+    if (threadIdx.x < d) o[row + threadIdx.x] = from_f<T>(sum > 0.f ? out / sum : 0.f);
+    if (threadIdx.x == 0) seq_lse[s * hq + h] = sum > 0.f ? M + log2f(sum) : -INFINITY;
+}
 
 }  // namespace
 
@@ -1777,10 +1949,10 @@ bool decode_fp8_ok(const hswa_pool *pool, const hswa_layer *layer, const void *q
            ((uintptr_t)layer->k_scale & 15) == 0 && ((uintptr_t)layer->v_scale & 15) == 0;
 }
 
-template <int kTok>
+template <int kTok, bool kWeights = false>
 int decode_fp8_ctas_per_sm() {
     static int cache[kMaxDevices] = {};
-    return kernel_setup(decode_mma_fp8_d128<kTok>, decode_smem8_bytes<kTok>(), 32 * (kConsumers8 + 1), cache);
+    return kernel_setup(decode_mma_fp8_d128<kTok, kWeights>, decode_smem8_bytes<kTok>(), 32 * (kConsumers8 + 1), cache);
 }
 
 // Query tokens per sequence from which an FP8 decode runs on the tensor-core
@@ -1794,10 +1966,10 @@ bool decode_fast_ok(const hswa_pool *pool, const hswa_layer *layer, const void *
            ((uintptr_t)layer->k_pool & 15) == 0 && ((uintptr_t)layer->v_pool & 15) == 0;
 }
 
-template <int kTok>
+template <int kTok, bool kWeights = false>
 int decode_ctas_per_sm_t() {
     static int cache[kMaxDevices] = {};
-    return kernel_setup(decode_mma_bf16_d128<kTok>, decode_smem_bytes<kTok>(), 32 * (kTok + 1), cache);
+    return kernel_setup(decode_mma_bf16_d128<kTok, kWeights>, decode_smem_bytes<kTok>(), 32 * (kTok + 1), cache);
 }
 
 int decode_ctas_per_sm() { return decode_ctas_per_sm_t<1>(); }
@@ -1853,6 +2025,21 @@ int decode_ctas_per_sm_for(int n_tok) {
 
 constexpr int kMaxCtasPerSm = 4;
 
+// What hswa_decode_weights adds to a decode step.
+struct PageWeights {
+    float *page_lse, *seq_lse;  // workspace
+    const float *w_in;
+    float *w_out;
+    float decay;
+};
+
+cudaError_t launch_page_weights(const PageWeights &pw, const hswa_config &c, const int32_t *d_seq_len, int n_seqs,
+                                int parts, cudaStream_t st) {
+    const WeightArgs a = {pw.page_lse, pw.seq_lse, d_seq_len, pw.w_in, pw.w_out, pw.decay, c.n_kv_heads,
+                          c.n_q_heads / c.n_kv_heads, parts, c.page_size, c.max_pages_per_seq};
+    return launch_pdl(page_weights, dim3((c.max_pages_per_seq + 31) / 32, n_seqs), dim3(256), 0, st, a);
+}
+
 size_t desc_bytes(int n_seqs) { return ((size_t)(n_seqs + 1) * sizeof(int4) + 255) & ~(size_t)255; }
 
 }  // namespace
@@ -1902,6 +2089,7 @@ int fill_args(DecodeArgs &a, const hswa_pool *pool, const hswa_layer *layer, con
     a.n_tok = 1;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.err = error_word();
+    a.page_lse = a.seq_lse = nullptr;
     return num_pages;
 }
 
@@ -1910,13 +2098,15 @@ int fill_args(DecodeArgs &a, const hswa_pool *pool, const hswa_layer *layer, con
 // the tensor-core kernel with the pages turned into f16 in shared memory.
 int decode_fp8(const hswa_pool *pool, const hswa_layer *layer, const void *q, void *o, const int32_t *d_bt,
                const int32_t *d_seq_len, int n_seqs, int n_tok, float scale, void *ws, size_t ws_bytes,
-               const int32_t *slots, const void *k_new, const void *v_new, hswa_stream_t stream) {
+               const int32_t *slots, const void *k_new, const void *v_new, hswa_stream_t stream,
+               const PageWeights *pw) {
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (!decode_fp8_ok(pool, layer, q, o)) return HSWA_ERR_UNSUPPORTED;
     const int sms = sm_count();
     if (sms <= 0) return HSWA_ERR_CUDA;
     const bool tc = n_tok >= kTcMinTokensFp8;
-    const int per_sm = tc ? decode_tc_ctas_per_sm<DecodeTc8Smem>(n_tok)
+    const int per_sm = tc   ? decode_tc_ctas_per_sm<DecodeTc8Smem>(n_tok)
+                       : pw ? decode_fp8_ctas_per_sm<1, true>()
                           : n_tok == 1 ? decode_fp8_ctas_per_sm<1>() : decode_fp8_ctas_per_sm<2>();
     if (per_sm <= 0) return HSWA_ERR_CUDA;
     const int n_ctas = sms * std::min(per_sm, kMaxCtasPerSm);
@@ -1931,6 +2121,7 @@ int decode_fp8(const hswa_pool *pool, const hswa_layer *layer, const void *q, vo
     DecodeArgs a;
     const int32_t num_pages = fill_args(a, pool, layer, q, o, d_bt, d_seq_len, n_seqs, scale, ws);
     a.n_tok = n_tok;
+    if (pw) a.page_lse = pw->page_lse, a.seq_lse = pw->seq_lse;
     const uint64_t blocks = (uint64_t)num_pages * c.n_kv_heads;
     CUtensorMap tk, tv, tq;
     if (!make_tmap_2d(&tk, layer->k_pool, blocks * kP, kD, kP, kD, CU_TENSOR_MAP_DATA_TYPE_UINT8,
@@ -1939,36 +2130,68 @@ int decode_fp8(const hswa_pool *pool, const hswa_layer *layer, const void *q, vo
                       CU_TENSOR_MAP_SWIZZLE_64B) ||
         (tc && !make_q_tmap(&tq, q, c, n_seqs, n_tok)))
         return HSWA_ERR_CUDA;
-    set_last_kernel(tc ? "decode_tc_fp8_d128" : slots ? "append_kv_fp8+decode_mma_fp8_d128" : "decode_mma_fp8_d128");
+    set_last_kernel(tc ? "decode_tc_fp8_d128" : pw ? "decode_mma_fp8_d128+weights" : slots ? "append_kv_fp8+decode_mma_fp8_d128" : "decode_mma_fp8_d128");
     cudaError_t e = launch_pdl(decode_plan, dim3(1), dim3(1024), 0, st, d_seq_len, n_seqs, c.n_kv_heads, kP,
                                a.window, n_tok, static_cast<int4 *>(ws));
     if (e == cudaSuccess) {
         if (tc)
             e = launch_decode_tc<DecodeTc8Smem>(n_tok, n_ctas, st, tq, tk, tv, a);
+        else if (pw)
+            e = launch_pdl(decode_mma_fp8_d128<1, true>, dim3(n_ctas), dim3(32 * (kConsumers8 + 1)),
+                           decode_smem8_bytes<1>(), st, tk, tv, a);
         else if (n_tok == 1)
-            e = launch_pdl(decode_mma_fp8_d128<1>, dim3(n_ctas), dim3(32 * (kConsumers8 + 1)),
+            e = launch_pdl(decode_mma_fp8_d128<1, false>, dim3(n_ctas), dim3(32 * (kConsumers8 + 1)),
                            decode_smem8_bytes<1>(), st, tk, tv, a);
         else
-            e = launch_pdl(decode_mma_fp8_d128<2>, dim3(n_ctas), dim3(32 * (kConsumers8 + 1)),
+            e = launch_pdl(decode_mma_fp8_d128<2, false>, dim3(n_ctas), dim3(32 * (kConsumers8 + 1)),
                            decode_smem8_bytes<2>(), st, tk, tv, a);
     }
     if (e == cudaSuccess)
-        e = launch_pdl(decode_combine, dim3(c.n_kv_heads, n_seqs * n_tok), dim3(256), 0, st, a, n_ctas);
+        e = launch_pdl(pw ? decode_combine<kConsumers8> : decode_combine<0>, dim3(c.n_kv_heads, n_seqs * n_tok),
+                       dim3(256), 0, st, a, n_ctas);
+    if (e == cudaSuccess && pw) e = launch_page_weights(*pw, c, d_seq_len, n_seqs, kConsumers8, st);
     return e == cudaSuccess ? HSWA_OK : HSWA_ERR_CUDA;
 }
 
-template <int kTok>
+template <int kTok, bool kWeights = false>
 cudaError_t launch_decode_kernel(int n_ctas, cudaStream_t st, const CUtensorMap &tk, const CUtensorMap &tv,
                                  const DecodeArgs &a) {
-    return launch_pdl(decode_mma_bf16_d128<kTok>, dim3(n_ctas), dim3(32 * (kTok + 1)),
+    return launch_pdl(decode_mma_bf16_d128<kTok, kWeights>, dim3(n_ctas), dim3(32 * (kTok + 1)),
                       decode_smem_bytes<kTok>(), st, tk, tv, a);
+}
+
+int launch_decode_weights_any(const hswa_pool *pool, const hswa_layer *layer, const void *q, void *o,
+                              const int32_t *d_bt, const int32_t *d_seq_len, int n_seqs, float scale,
+                              const PageWeights &pw, cudaStream_t st) {
+    const hswa_config &c = pool->cfg;
+    if (c.head_dim > 256) return HSWA_ERR_UNSUPPORTED;
+    const dim3 grid(c.n_q_heads, n_seqs);
+    const float scale_log2 = scale * 1.4426950408889634f;
+    int *err = error_word();
+    if (c.dtype == HSWA_DTYPE_F32) {
+        set_last_kernel("decode_weights_any_f32");
+        decode_weights_any<float><<<grid, 256, 0, st>>>(
+            (const float *)q, (float *)o, (const float *)layer->k_pool, (const float *)layer->v_pool, d_bt, d_seq_len,
+            pw.page_lse, pw.seq_lse, c.max_pages_per_seq, c.n_q_heads, c.n_kv_heads, c.head_dim, c.page_size,
+            c.full_pages, scale_log2, err);
+    } else {
+        set_last_kernel("decode_weights_any_bf16");
+        decode_weights_any<__nv_bfloat16><<<grid, 256, 0, st>>>(
+            (const __nv_bfloat16 *)q, (__nv_bfloat16 *)o, (const __nv_bfloat16 *)layer->k_pool,
+            (const __nv_bfloat16 *)layer->v_pool, d_bt, d_seq_len, pw.page_lse, pw.seq_lse, c.max_pages_per_seq,
+            c.n_q_heads, c.n_kv_heads, c.head_dim, c.page_size, c.full_pages, scale_log2, err);
+    }
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch_page_weights(pw, c, d_seq_len, n_seqs, 1, st);
+    return e == cudaSuccess ? HSWA_OK : cuda_fail(e, "hswa_decode_weights");
 }
 
 // Decode of n_tok query tokens per sequence, with an optional fused append
 // of one new token (slots / k_new / v_new non-null, n_tok == 1 only).
 int decode_impl(const hswa_pool *pool, const hswa_layer *layer, const void *q, void *o, const int32_t *d_bt,
                 const int32_t *d_seq_len, int n_seqs, int n_tok, float scale, void *ws, size_t ws_bytes,
-                const int32_t *slots, const void *k_new, const void *v_new, hswa_stream_t stream) {
+                const int32_t *slots, const void *k_new, const void *v_new, hswa_stream_t stream,
+                const PageWeights *pw = nullptr) {
     if (!pool || !layer || n_seqs < 0 || n_seqs > pool->cfg.max_seqs || n_tok < 1 ||
         n_tok > HSWA_DECODE_MAX_TOKENS || (slots && n_tok != 1) ||
         (layer->kind != HSWA_KIND_FULL && layer->kind != HSWA_KIND_SWA) ||
@@ -1981,7 +2204,7 @@ int decode_impl(const hswa_pool *pool, const hswa_layer *layer, const void *q, v
     if (pool->cfg.dtype == HSWA_DTYPE_FP8_E4M3) {
         if ((int64_t)n_seqs * n_tok > 65535) return HSWA_ERR_UNSUPPORTED;  // rows of the combine grid
         return decode_fp8(pool, layer, q, o, d_bt, d_seq_len, n_seqs, n_tok, scale, ws, ws_bytes, slots, k_new,
-                          v_new, stream);
+                          v_new, stream, pw);
     }
     if (!decode_fast_ok(pool, layer, q, o) ||
         (fused && (((uintptr_t)k_new & 15) || ((uintptr_t)v_new & 15)))) {
@@ -1989,6 +2212,7 @@ int decode_impl(const hswa_pool *pool, const hswa_layer *layer, const void *q, v
             const int rc = hswa_append_kv(pool, layer, k_new, v_new, slots, n_seqs, stream);
             if (rc != HSWA_OK) return rc;
         }
+        if (pw) return launch_decode_weights_any(pool, layer, q, o, d_bt, d_seq_len, n_seqs, scale, *pw, st);
         return launch_attention_generic(pool, layer, q, o, d_bt, d_seq_len, nullptr, nullptr, n_seqs * n_tok,
                                         n_seqs, scale, 0, st, n_tok);
     }
@@ -1997,7 +2221,9 @@ int decode_impl(const hswa_pool *pool, const hswa_layer *layer, const void *q, v
     const int sms = sm_count();
     if (sms <= 0) return HSWA_ERR_CUDA;
     const bool tc = n_tok >= kTcMinTokens;
-    const int per_sm = tc ? decode_tc_ctas_per_sm<DecodeTcSmem>(n_tok) : decode_ctas_per_sm_for(n_tok);
+    const int per_sm = tc   ? decode_tc_ctas_per_sm<DecodeTcSmem>(n_tok)
+                       : pw ? decode_ctas_per_sm_t<1, true>()
+                            : decode_ctas_per_sm_for(n_tok);
     if (per_sm <= 0) return HSWA_ERR_CUDA;
     const int n_ctas = sms * std::min(per_sm, kMaxCtasPerSm);
     if (!ws || ((uintptr_t)ws & 255) ||
@@ -2009,6 +2235,7 @@ int decode_impl(const hswa_pool *pool, const hswa_layer *layer, const void *q, v
     a.k_new = static_cast<const __nv_bfloat16 *>(k_new);
     a.v_new = static_cast<const __nv_bfloat16 *>(v_new);
     a.n_tok = n_tok;
+    if (pw) a.page_lse = pw->page_lse, a.seq_lse = pw->seq_lse;
     CUtensorMap tk, tv, tq;
     const uint64_t rows = (uint64_t)num_pages * c.n_kv_heads * kP;
     if (!make_tmap_2d(&tk, layer->k_pool, rows, kD, 64, 64, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
@@ -2017,7 +2244,7 @@ int decode_impl(const hswa_pool *pool, const hswa_layer *layer, const void *q, v
                       CU_TENSOR_MAP_SWIZZLE_128B))
         return HSWA_ERR_CUDA;
     if (tc && !make_q_tmap(&tq, q, c, n_seqs, n_tok)) return HSWA_ERR_CUDA;
-    set_last_kernel(tc ? "decode_tc_bf16_d128" : fused ? "decode_mma_bf16_d128+append" : "decode_mma_bf16_d128");
+    set_last_kernel(tc ? "decode_tc_bf16_d128" : pw ? "decode_mma_bf16_d128+weights" : fused ? "decode_mma_bf16_d128+append" : "decode_mma_bf16_d128");
     // three launches chained with programmatic dependent launch: each one
     // is scheduled while its predecessor finishes and waits for it on entry
     if (launch_pdl(decode_plan, dim3(1), dim3(1024), 0, st, d_seq_len, n_seqs, c.n_kv_heads, kP, a.window, n_tok,
@@ -2026,14 +2253,17 @@ int decode_impl(const hswa_pool *pool, const hswa_layer *layer, const void *q, v
     cudaError_t e;
     if (tc) {
         e = launch_decode_tc<DecodeTcSmem>(n_tok, n_ctas, st, tq, tk, tv, a);
+    } else if (pw) {
+        e = launch_decode_kernel<1, true>(n_ctas, st, tk, tv, a);
     } else switch (n_tok) {
     case 1: e = launch_decode_kernel<1>(n_ctas, st, tk, tv, a); break;
     case 2: e = launch_decode_kernel<2>(n_ctas, st, tk, tv, a); break;
     default: e = launch_decode_kernel<3>(n_ctas, st, tk, tv, a); break;
     }
-    if (e != cudaSuccess ||
-        launch_pdl(decode_combine, dim3(c.n_kv_heads, n_seqs * n_tok), dim3(256), 0, st, a, n_ctas) != cudaSuccess)
+    if (e != cudaSuccess || launch_pdl(pw ? decode_combine<1> : decode_combine<0>,
+                                       dim3(c.n_kv_heads, n_seqs * n_tok), dim3(256), 0, st, a, n_ctas) != cudaSuccess)
         return HSWA_ERR_CUDA;
+    if (pw && launch_page_weights(*pw, c, d_seq_len, n_seqs, 1, st) != cudaSuccess) return HSWA_ERR_CUDA;
     return HSWA_OK;
 }
 
@@ -2064,6 +2294,36 @@ extern "C" int hswa_decode_multi(const hswa_pool *pool, const hswa_layer *layer,
     HSWA_NVTX("hswa_decode_multi");
     return decode_impl(pool, layer, q, o, d_bt, d_seq_len, n_seqs, n_tok, scale, ws, ws_bytes, nullptr, nullptr,
                        nullptr, stream);
+}
+
+extern "C" size_t hswa_decode_weights_workspace_size(const hswa_pool *pool, int n_seqs) {
+    if (!pool || n_seqs < 0) return 0;
+    const hswa_config &c = pool->cfg;
+    const size_t parts = c.dtype == HSWA_DTYPE_FP8_E4M3 ? kConsumers8 : 1;
+    const size_t base = (hswa_decode_workspace_size(pool, n_seqs) + 255) & ~(size_t)255;
+    return base + ((size_t)n_seqs * c.n_q_heads * c.max_pages_per_seq * parts + (size_t)n_seqs * c.n_q_heads) * 4;
+}
+
+extern "C" int hswa_decode_weights(const hswa_pool *pool, const hswa_layer *layer, const void *q, void *o,
+                                   const int32_t *d_bt, const int32_t *d_seq_len, int n_seqs, float scale,
+                                   const float *w_in, float decay, float *w_out, void *ws, size_t ws_bytes,
+                                   hswa_stream_t stream) {
+    HSWA_NVTX("hswa_decode_weights");
+    if (!pool || !layer || n_seqs < 0 || layer->kind != HSWA_KIND_FULL) return HSWA_ERR_INVALID_ARG;
+    if (n_seqs == 0) return HSWA_OK;
+    if (n_seqs > 65535) return HSWA_ERR_UNSUPPORTED;  // rows of the weight grid
+    if (!w_out || !ws || ((uintptr_t)ws & 255) || ws_bytes < hswa_decode_weights_workspace_size(pool, n_seqs))
+        return HSWA_ERR_INVALID_ARG;
+    const hswa_config &c = pool->cfg;
+    const size_t base = (hswa_decode_workspace_size(pool, n_seqs) + 255) & ~(size_t)255;
+    PageWeights pw;
+    pw.seq_lse = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + base);
+    pw.page_lse = pw.seq_lse + (size_t)n_seqs * c.n_q_heads;
+    pw.w_in = w_in;
+    pw.w_out = w_out;
+    pw.decay = decay;
+    return decode_impl(pool, layer, q, o, d_bt, d_seq_len, n_seqs, 1, scale, ws, base, nullptr, nullptr, nullptr,
+                       stream, &pw);
 }
 
 // ---------------------------------------------------- no-allocation decode

@@ -53,6 +53,9 @@ struct hswa_pool {
     // per sequence: no logical page below holds an SWA page (set_swa lowers
     // it, a release raises it), so a release scans only the pages it frees
     std::vector<int32_t> swa_low;          // [max_seqs]
+    // per sequence: whole pages that still follow from the text before them,
+    // INT32_MAX unless hswa_evict dropped one (then the first dropped page)
+    std::vector<int32_t> text_pages;       // [max_seqs]
     // holders of each page (sequence tables and prefix-tree nodes); a page
     // is on its free list exactly when its count is 0
     std::vector<int32_t> full_ref, swa_ref;

@@ -71,6 +71,7 @@ extern "C" int hswa_pool_create(const hswa_config *cfg, const int32_t *full_free
     p->swa_bt.assign(entries, -1);
     p->seq_len.assign(cfg->max_seqs, 0);
     p->swa_low.assign(cfg->max_seqs, 0);
+    p->text_pages.assign(cfg->max_seqs, INT32_MAX);
     p->full_ref.assign(cfg->full_pages, 0);
     p->swa_ref.assign(cfg->swa_pages, 0);
     p->dirty_flag.assign(2 * entries + cfg->max_seqs, 0);
@@ -172,8 +173,114 @@ extern "C" int hswa_seq_free(hswa_pool *pool, int n, const int32_t *seq_ids) {
             }
         }
         pool->set_len(s, 0);
+        pool->text_pages[s] = INT32_MAX;
     }
     return HSWA_OK;
+}
+
+extern "C" int hswa_seq_truncate(hswa_pool *pool, int n, const int32_t *seq_ids, const int32_t *new_len,
+                                 int32_t *n_freed_out) try {
+    HSWA_NVTX("hswa_seq_truncate");
+    std::vector<int32_t> ids;
+    if (!pool || (n > 0 && !new_len) || !sorted_ids(pool, n, seq_ids, ids)) return HSWA_ERR_INVALID_ARG;
+    const int64_t P = pool->cfg.page_size, W = pool->cfg.window, MP = pool->cfg.max_pages_per_seq;
+    std::vector<std::pair<int32_t, int32_t>> todo;  // (sequence, new length), ascending
+    for (int i = 0; i < n; ++i) todo.emplace_back(seq_ids[i], new_len[i]);
+    std::sort(todo.begin(), todo.end());
+    for (const auto &x : todo) {
+        const int64_t s = x.first, L = x.second;
+        if (L < 0 || L > pool->seq_len[s]) return HSWA_ERR_INVALID_ARG;
+        if (L == pool->seq_len[s] || L == 0) continue;
+        const int32_t *frow = &pool->full_bt[s * MP], *srow = &pool->swa_bt[s * MP];
+        for (int64_t p = std::max<int64_t>(0, L - W) / P; p <= (L - 1) / P; ++p)
+            if (srow[p] < 0) return HSWA_ERR_INVALID_ARG;  // the window there is gone
+        const int64_t p = L / P;
+        if (L % P && (pool->full_ref[frow[p]] > 1 || pool->swa_ref[srow[p]] > 1))
+            return HSWA_ERR_INVALID_ARG;  // the next token would be written into a shared page
+    }
+    int32_t freed = 0;
+    for (const auto &x : todo) {
+        const int64_t s = x.first, L = x.second, L0 = pool->seq_len[s];
+        if (L == L0) continue;
+        const int64_t first = (L + P - 1) / P, end = (L0 + P - 1) / P;
+        for (int64_t p = first; p < end; ++p) {
+            if (pool->full_bt[s * MP + p] < 0) continue;
+            freed += pool->unref_full(pool->full_bt[s * MP + p]);
+            pool->set_full((int32_t)s, (int32_t)p, -1);
+        }
+        for (int64_t p = first; p < end; ++p) {
+            if (pool->swa_bt[s * MP + p] < 0) continue;
+            pool->unref_swa(pool->swa_bt[s * MP + p]);
+            pool->set_swa((int32_t)s, (int32_t)p, -1);
+        }
+        pool->set_len((int32_t)s, (int32_t)L);
+        if (L <= (int64_t)pool->text_pages[s] * P) pool->text_pages[s] = INT32_MAX;  // nothing is left behind the gap
+    }
+    if (n_freed_out) *n_freed_out = freed;
+    return HSWA_OK;
+} catch (const std::bad_alloc &) {
+    return HSWA_ERR_INVALID_ARG;
+}
+
+extern "C" int hswa_evict(hswa_pool *pool, int n, const int32_t *seq_ids, const int32_t *n_keep, const int32_t *keep,
+                          int32_t keep_stride, int32_t *n_freed_out) try {
+    HSWA_NVTX("hswa_evict");
+    std::vector<int32_t> ids;
+    if (!pool || keep_stride < 0 || (n > 0 && (!n_keep || !keep)) || !sorted_ids(pool, n, seq_ids, ids))
+        return HSWA_ERR_INVALID_ARG;
+    const int64_t P = pool->cfg.page_size, W = pool->cfg.window, MP = pool->cfg.max_pages_per_seq;
+    std::vector<std::pair<int32_t, int>> todo;  // (sequence, place in the lists), ascending
+    for (int i = 0; i < n; ++i) todo.emplace_back(seq_ids[i], i);
+    std::sort(todo.begin(), todo.end());
+    for (const auto &x : todo) {
+        const int64_t L = pool->seq_len[x.first], pages = (L + P - 1) / P;
+        const int32_t *list = keep + (int64_t)x.second * keep_stride;
+        const int32_t m = n_keep[x.second];
+        if (m < 0 || m > keep_stride || m > pages) return HSWA_ERR_INVALID_ARG;
+        int64_t next = 0;  // first page not seen yet
+        for (int32_t i = 0; i <= m; ++i) {
+            const int64_t p = i < m ? list[i] : pages;
+            if (p < next || (i < m && p >= pages)) return HSWA_ERR_INVALID_ARG;
+            if (p > next && p * P > L - W) return HSWA_ERR_INVALID_ARG;  // page p - 1 is dropped
+            next = p + 1;
+        }
+    }
+    int32_t freed = 0;
+    for (const auto &x : todo) {
+        const int32_t s = x.first, m = n_keep[x.second];
+        const int32_t *list = keep + (int64_t)x.second * keep_stride;
+        const int32_t L = pool->seq_len[s], pages = (int32_t)((L + P - 1) / P);
+        if (m == pages) continue;
+        int32_t at = 0, low = 0, first = -1;  // pages that stay so far; below low none holds an SWA page
+        const int32_t old_low = pool->swa_low[s];
+        for (int32_t p = 0; p < pages; ++p) {
+            const int64_t i = (int64_t)s * MP + p;
+            const int32_t full = pool->full_bt[i], swa = pool->swa_bt[i];
+            if (at < m && list[at] == p) {
+                if (at != p) {
+                    pool->set_full(s, at, full);
+                    if (pool->swa_bt[(int64_t)s * MP + at] != swa) pool->set_swa(s, at, swa);
+                }
+                ++at;
+                if (p < old_low) low = at;
+                continue;
+            }
+            if (first < 0) first = p;
+            if (full >= 0) freed += pool->unref_full(full);
+            if (swa >= 0) pool->unref_swa(swa);
+        }
+        for (int32_t p = m; p < pages; ++p) {
+            pool->set_full(s, p, -1);
+            if (pool->swa_bt[(int64_t)s * MP + p] >= 0) pool->set_swa(s, p, -1);
+        }
+        pool->swa_low[s] = low;
+        pool->set_len(s, L - (int32_t)((pages - m) * P));
+        pool->text_pages[s] = std::min(pool->text_pages[s], first);
+    }
+    if (n_freed_out) *n_freed_out = freed;
+    return HSWA_OK;
+} catch (const std::bad_alloc &) {
+    return HSWA_ERR_INVALID_ARG;
 }
 
 extern "C" int hswa_swa_drop(hswa_pool *pool, int n, const int32_t *seq_ids, int32_t *n_freed_out) {

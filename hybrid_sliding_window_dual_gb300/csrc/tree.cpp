@@ -245,6 +245,7 @@ extern "C" int hswa_tree_insert(hswa_tree *t, int32_t seq_id, const int32_t *tok
     const int64_t n_pages = n_tokens / P;
     const int32_t *frow = &pool->full_bt[(int64_t)seq_id * MP];
     const int32_t *srow = &pool->swa_bt[(int64_t)seq_id * MP];
+    if (n_pages > pool->text_pages[seq_id]) return HSWA_ERR_INVALID_ARG;  // past an evicted page
     for (int64_t p = 0; p < n_pages; ++p)
         if (frow[p] < 0) return HSWA_ERR_INVALID_ARG;
     const uint64_t clock = ++t->clock;

@@ -66,6 +66,7 @@ class DualPoolSession:
                                        v_scale=vs.data_ptr() if vs is not None else None))
         self.ws = None
         self.prefill_ws = None
+        self.weights_ws = None
         self.tree = None
 
     def close(self):
@@ -97,6 +98,10 @@ class DualPoolSession:
 
     def swa_restore(self, seq_ids):
         return B.hswa_swa_restore(self.pool, seq_ids)
+
+    def truncate(self, seq_ids, new_len):
+        """Take back the last tokens (refused drafts); sync() before the next device call."""
+        return B.hswa_seq_truncate(self.pool, seq_ids, new_len)
 
     # ------------------------------------------------ prefix cache (host)
     def prefix_tree(self):
@@ -136,6 +141,50 @@ class DualPoolSession:
 
     def append(self, layer, k, v, d_slots):
         B.hswa_append_kv(self.pool, self.layers[layer], k, v, d_slots, k.shape[0], self.stream)
+
+    def rope_append(self, layer, rope, q, k, v, d_pos, d_slots, q_out):
+        """Rotate q (into q_out) and K, and append K and V. q, k, v: [T, heads *
+        d] or [T, heads, d], rows possibly slices of one projection."""
+        for x in (q, k, v):
+            heads = (x.stride(-1) == 1 and (x.dim() == 2 or x.stride(1) == x.shape[2])) or x.numel() == 0
+            if x.dim() not in (2, 3) or not heads:
+                raise ValueError("a token's heads must lie next to each other")
+        row = self.cfg.head_dim * self.cfg.n_q_heads, self.cfg.head_dim * self.cfg.n_kv_heads
+        one = q.shape[0] <= 1  # a single row's stride says nothing
+        B.hswa_rope_append(self.pool, self.layers[layer], rope, q, row[0] if one else q.stride(0),
+                           k, row[1] if one else k.stride(0), v, row[1] if one else v.stride(0), d_pos, d_slots,
+                           q_out, q.shape[0], self.stream)
+
+    def decode_weights(self, layer, q, o, n_seqs, scale, w_in, decay, w_out):
+        """decode() of a Full layer that adds the pages' attention weights:
+        w_out = decay * w_in + weights, [n_seqs, max_pages_per_seq] fp32."""
+        need = B.hswa_decode_weights_workspace_size(self.pool, n_seqs)
+        if self.weights_ws is None or self.weights_ws.numel() < need:
+            self.weights_ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        B.hswa_decode_weights(self.pool, self.layers[layer], q, o, self.bt(layer), self.d_seq_len, n_seqs, scale,
+                              w_in, decay, w_out, self.weights_ws, self.weights_ws.numel(), self.stream)
+
+    def evict_select(self, w_in, d_budget, n_seqs, sink_pages, recent_tokens, keep, n_keep, w_out):
+        B.hswa_evict_select(self.pool, self.d_seq_len, w_in, d_budget, n_seqs, sink_pages, recent_tokens, keep,
+                            n_keep, w_out, self.stream)
+
+    def evict_pages(self, seq_ids, n_keep, keep):
+        """Drop the pages of sequences that are not in keep[i, :n_keep[i]]
+        (host arrays, as evict_select chose); sync() before the next device call."""
+        return B.hswa_evict(self.pool, seq_ids, n_keep, keep)
+
+    def verify(self, p, q, d_draft, d_n_draft, u, n_accept, tokens):
+        """Verify drafts against probabilities p [n_seqs, n_tok, vocab] (q
+        [n_seqs, n_tok - 1, vocab], or None for greedy drafts), fp32 or bf16."""
+        n_seqs, n_tok, vocab = p.shape
+        dtype = {torch.float32: B.HSWA_DTYPE_F32, torch.bfloat16: B.HSWA_DTYPE_BF16}.get(p.dtype)
+        if dtype is None or (q is not None and q.dtype != p.dtype):
+            raise ValueError("p and q must both be float32 or bfloat16")
+        for x, t in ((p, n_tok), (q, n_tok - 1)):
+            if x is not None and x.numel() and (x.stride(2) != 1 or (x.shape[0] > 1 and x.stride(0) != t * x.stride(1))):
+                raise ValueError("rows must be evenly spaced")
+        B.hswa_verify_draft(dtype, p, p.stride(1), q, 0 if q is None else q.stride(1), d_draft, d_n_draft, u, n_seqs,
+                            n_tok, vocab, n_accept, tokens, self.stream)
 
     def decode(self, layer, q, o, n_seqs, scale):
         ws = self.workspace(n_seqs)

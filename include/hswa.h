@@ -179,6 +179,43 @@ int hswa_swa_drop(hswa_pool *pool, int n, const int32_t *seq_ids, int32_t *n_fre
  * (HSWA_ERR_NO_SPACE). Used before hswa_swa_scatter reloads a window. */
 int hswa_swa_restore(hswa_pool *pool, int n, const int32_t *seq_ids, int32_t *n_alloc_out);
 
+/* Take back the last tokens of sequences: the slots of drafted tokens that
+ * verification refused ("Following the Bottleneck: Optimizing MiniMax M3 on
+ * AMD Instinct MI355X", EAGLE3 adds a second decode loop: multi-token
+ * verification). new_len[i] in [0, length] becomes the length of seq_ids[i]
+ * (distinct, any order); pages that hold none of the tokens left are let go
+ * of, Full pages and SWA pages each in ascending (sequence, page) order, those no one else holds
+ * going to the tail of their free list. Two states cannot be taken back to
+ * and are refused (HSWA_ERR_INVALID_ARG, no change): a length that ends
+ * inside a page with another holder (a cached prefix: the next token would
+ * be written into the other holder's page), and one whose last W positions
+ * lie on a page whose SWA page was released (hswa_swa_release keeps the last
+ * W positions of the length it is called at, so call it before the drafts
+ * are reserved). *n_freed_out (may be NULL) counts the Full pages that went
+ * back to the free list. */
+int hswa_seq_truncate(hswa_pool *pool, int n, const int32_t *seq_ids, const int32_t *new_len, int32_t *n_freed_out);
+
+/* Shorten the Full cache of sequences to some of their pages: the host side
+ * of eviction by attention weight (hswa_decode_weights, hswa_evict_select).
+ * For the i-th listed sequence (distinct ids, any order) keep[i *
+ * keep_stride ..] names the n_keep[i] logical pages that stay, strictly
+ * ascending; the others are dropped from both tables and the pages that stay
+ * close up, so the sequence gets shorter by P tokens a page. A page may be
+ * dropped only if all its tokens are older than the last W ((p + 1) * P <=
+ * length - W, the release rule), so the window of the SWA layers stays what
+ * it was; a dropped page's SWA page, if it still has one, is let go of too.
+ * Pages are let go of in ascending (sequence, page) order, Full and SWA each. A list that is
+ * not ascending, names a page past the last one or drops a page inside the
+ * window is refused (HSWA_ERR_INVALID_ARG) with no change to any sequence.
+ * Afterwards positions in the cache are no longer positions in the text:
+ * the attention calls count cache positions, hswa_rope_append is given the
+ * text's. Pages from the first dropped one on no longer follow from the
+ * tokens before them, so hswa_tree_insert takes only tokens before it.
+ * *n_freed_out (may be NULL) counts the Full pages that went back to the
+ * free list. */
+int hswa_evict(hswa_pool *pool, int n, const int32_t *seq_ids, const int32_t *n_keep, const int32_t *keep,
+               int32_t keep_stride, int32_t *n_freed_out);
+
 /* Host mirrors, for inspection: copies the Full table, the SWA table
  * (int32 [max_seqs][max_pages_per_seq] each) and lengths (int32
  * [max_seqs]); any pointer may be NULL. */
@@ -241,7 +278,8 @@ int hswa_tree_match(hswa_tree *tree, const int32_t *tokens, int64_t n_tokens, in
                     int32_t *swa_pages_out, int32_t cap_pages, int32_t *n_pages_out, int32_t *raw_pages_out);
 
 /* Store the whole pages of the first n_tokens tokens of sequence seq_id
- * (n_tokens <= its length; each of those pages must have a Full page):
+ * (n_tokens <= its length; each of those pages must have a Full page, and
+ * none may lie at or behind a page that hswa_evict dropped):
  * pages new to the tree become nodes holding the sequence's Full and SWA
  * pages; where a node exists for the same tokens the tree keeps its own
  * pages (the sequence's copy is freed with the sequence) and takes the
@@ -293,6 +331,65 @@ int hswa_sync_tables(hswa_pool *pool, int32_t *d_full_bt, int32_t *d_swa_bt, int
 int hswa_append_kv(const hswa_pool *pool, const hswa_layer *layer, const void *k, const void *v,
                    const int32_t *d_slots, int n_tokens, hswa_stream_t stream);
 
+/* ------------------------------------ rotary positions with several axes
+ *
+ * A rotary embedding of a model's heads: which elements form pairs, how
+ * fast each pair turns, and on which position axis (time, height, width)
+ * it goes. Text tokens have the same position on every axis; an image's
+ * have one of their own on each. */
+#define HSWA_ROPE_MAX_AXES 4
+#define HSWA_ROPE_MAX_DIM 256  /* largest rotary_dim */
+#define HSWA_ROPE_MAX_HEAD 256 /* largest head_dim */
+
+#define HSWA_ROPE_HALVES 0   /* pair i is elements (i, i + rotary_dim / 2) */
+#define HSWA_ROPE_ADJACENT 1 /* pair i is elements (2 i, 2 i + 1)          */
+
+#define HSWA_ROPE_SECTIONS 0    /* axis 0 has the first section[0] pairs, axis 1 the next, ... */
+#define HSWA_ROPE_INTERLEAVED 1 /* pair i goes to axis i mod n_axes while that axis has had fewer
+                                   than section[axis] pairs, else to axis 0 */
+
+typedef struct hswa_rope_config {
+    int32_t rotary_dim;                  /* R: the first R elements of a head turn (even, 2..256)      */
+    int32_t pairing;                     /* HSWA_ROPE_HALVES or HSWA_ROPE_ADJACENT                     */
+    int32_t n_axes;                      /* position axes (1..HSWA_ROPE_MAX_AXES)                      */
+    int32_t order;                       /* HSWA_ROPE_SECTIONS or HSWA_ROPE_INTERLEAVED                */
+    int32_t section[HSWA_ROPE_MAX_AXES]; /* pairs of each axis; they add up to R / 2                   */
+    double theta;                        /* pair i turns by theta^(-2 i / R) a position (> 0)          */
+    const double *inv_freq;              /* or by inv_freq[i] (host, R / 2 values); NULL: from theta   */
+} hswa_rope_config;
+
+typedef struct hswa_rope hswa_rope; /* opaque, host memory only */
+
+/* Make a rotary embedding (host call; keeps no pointer of cfg). Interleaved
+ * sections must fit their turns: each axis ends up with section[axis]
+ * pairs, else HSWA_ERR_INVALID_ARG. */
+int hswa_rope_create(const hswa_rope_config *cfg, hswa_rope **out);
+int hswa_rope_destroy(hswa_rope *rope);
+
+/* Rotate q and K, and append K and V, in one pass over a step's or a chunk's
+ * projections (hswa_append_kv takes K rotated already). For token t <
+ * n_tokens: q_out[t][h] is q's head h turned, and if d_slots[t] >= 0 the
+ * slot of the layer kind's pool gets K's rows turned and V's rows as they
+ * are. Pair i of a head, (x, y), becomes (x cos - y sin, y cos + x sin) of
+ * the angle d_pos[axis(i)][t] * frequency(i); elements from R on pass
+ * through. Angles are exact to about 1e-7 radians at any int32 position,
+ * the arithmetic is fp32, and each result is rounded once, to the element
+ * type; for FP8 pools the turned K row is quantized as it is in fp32 (scale
+ * = amax / 448 as for hswa_append_kv, without a rounding to bf16 between).
+ * q, k, v: device, token t's heads at element t * stride, so that they may
+ * be slices of one projection's output (q_stride >= Hq * d, k_stride and
+ * v_stride >= Hkv * d); fp32 for fp32 pools, else bf16. q_out: device
+ * [n_tokens][Hq][d]; it may be q if q_stride is Hq * d, and must not meet
+ * q, k or v otherwise. d_pos: device int32 [n_axes][n_tokens]. d_slots:
+ * device int32 [n_tokens], distinct, as from hswa_reserve; a negative one
+ * appends nothing (q is rotated all the same), one past the pool sets
+ * HSWA_ERR_BOUNDS on the device and appends nothing. rotary_dim must be at
+ * most head_dim, and head_dim at most HSWA_ROPE_MAX_HEAD (128 for FP8
+ * pools), else HSWA_ERR_UNSUPPORTED. */
+int hswa_rope_append(const hswa_pool *pool, const hswa_layer *layer, const hswa_rope *rope, const void *q,
+                     int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                     const int32_t *d_pos, const int32_t *d_slots, void *q_out, int n_tokens, hswa_stream_t stream);
+
 /* Bytes of workspace hswa_decode needs for a batch of n_seqs sequences. */
 size_t hswa_decode_workspace_size(const hswa_pool *pool, int n_seqs);
 
@@ -323,6 +420,48 @@ int hswa_decode_append(const hswa_pool *pool, const hswa_layer *layer, const voi
                        const int32_t *d_seq_len, int n_seqs, float scale, void *ws, size_t ws_bytes,
                        hswa_stream_t stream);
 
+/* Bytes of workspace hswa_decode_weights needs: that of hswa_decode and one
+ * fp32 per query head and page of the batch's table rows (four for FP8
+ * pools). */
+size_t hswa_decode_weights_workspace_size(const hswa_pool *pool, int n_seqs);
+
+/* hswa_decode of a Full layer that also adds up where the attention went,
+ * for eviction by attention weight: for every page p of sequence i that
+ * holds one of its keys
+ *     w_out[i][p] = decay * w_in[i][p] + sum_h sum_{j on p} softmax_j(q[i][h])
+ * in fp32 (the sum over all query heads and the page's keys; a row gains
+ * Hq), and w_out[i][p] = 0 for every later p, so that pages added later
+ * start from nothing. w_in, w_out: device float [n_seqs][max_pages_per_seq];
+ * they may be the same; w_in NULL or decay 0 starts anew whatever w_in
+ * holds. Several layers add up by calls with the same w_in = w_out (decay
+ * on a step's first layer, 1 on the others). Sums have a fixed order: equal
+ * inputs give equal bits. The attention output is hswa_decode's. All pool
+ * dtypes and shapes that hswa_decode takes (head_dim at most 256, n_seqs at
+ * most 65535); an SWA layer is HSWA_ERR_INVALID_ARG. A page skipped for its
+ * table entry (HSWA_ERR_BOUNDS) weighs nothing. ws: device, 256-byte
+ * aligned, of at least hswa_decode_weights_workspace_size bytes, on every
+ * path. */
+int hswa_decode_weights(const hswa_pool *pool, const hswa_layer *layer, const void *q, void *o,
+                        const int32_t *d_bt, const int32_t *d_seq_len, int n_seqs, float scale, const float *w_in,
+                        float decay, float *w_out, void *ws, size_t ws_bytes, hswa_stream_t stream);
+
+/* Which pages of each sequence stay when its Full cache is cut to a budget,
+ * by accumulated attention weight. Of sequence i's n = ceil(L / P) pages (L
+ * = d_seq_len[i]) these always stay: the first sink_pages, and every page
+ * with a token among the last recent_tokens (at least the pool's window).
+ * Of the others the heaviest stay, so that max(d_budget[i], those) pages do
+ * in all (n at most); of equal weights the lower page stays, and NaN is
+ * lighter than any number. w_in: device float [n_seqs][max_pages_per_seq]
+ * (hswa_decode_weights). d_budget: device int32 [n_seqs], pages. keep:
+ * device int32 [n_seqs][max_pages_per_seq], the pages that stay in
+ * ascending order, then -1; n_keep: device int32 [n_seqs]; w_out: device
+ * float like w_in, the weights of the pages that stay, closed up to match
+ * the tables after hswa_evict, then 0. w_out may be w_in. hswa_evict, with
+ * host copies of keep and n_keep, does the rest. */
+int hswa_evict_select(const hswa_pool *pool, const int32_t *d_seq_len, const float *w_in, const int32_t *d_budget,
+                      int n_seqs, int sink_pages, int recent_tokens, int32_t *keep, int32_t *n_keep, float *w_out,
+                      hswa_stream_t stream);
+
 /* Most query tokens per sequence hswa_decode_multi takes. */
 #define HSWA_DECODE_MAX_TOKENS 16
 
@@ -352,6 +491,38 @@ size_t hswa_decode_multi_workspace_size(const hswa_pool *pool, int n_seqs, int n
 int hswa_decode_multi(const hswa_pool *pool, const hswa_layer *layer, const void *q, void *o,
                       const int32_t *d_bt, const int32_t *d_seq_len, int n_seqs, int n_tok, float scale,
                       void *ws, size_t ws_bytes, hswa_stream_t stream);
+
+/* Largest vocabulary hswa_verify_draft takes. */
+#define HSWA_VERIFY_MAX_VOCAB (1 << 20)
+
+/* Verification of drafted tokens against the target's probabilities, from
+ * given random numbers: the step after hswa_decode_multi and the model's
+ * output layer. A sequence brings n_tok query tokens: its last token and
+ * n_tok - 1 drafts, of which d_n_draft[i] (0 .. n_tok - 1; NULL: all) count.
+ * Row i * n_tok + w of p is the target's distribution after query token w,
+ * row i * (n_tok - 1) + w of q the draft's for draft w, d_draft[i][w] the
+ * token drawn from it, u[i][*] n_tok numbers in [0, 1). Draft w stays while
+ *     u[i][w] * q(x_w) < p(x_w);
+ * n_accept[i] = a counts those before the first that does not. The next
+ * token is drawn with u[i][n_tok - 1]: the first v whose cumulative weight
+ * is above u times the total, where v weighs max(p_a(v) - q_a(v), 0) after a
+ * refusal and p_a(v) when all drafts stayed (or where nothing is left of
+ * the former). tokens[i] (n_tok values) holds the a drafts that stayed, the
+ * drawn token, then -1; a row of p without a positive value draws -1. The
+ * cache keeps the a + 1 query tokens that stayed: hswa_seq_truncate to
+ * length - n_tok + 1 + a.
+ * q NULL: drafts taken greedily (their q is 1 at the draft and 0 elsewhere).
+ * dtype: of p and q, HSWA_DTYPE_F32 or HSWA_DTYPE_BF16; rows p_stride /
+ * q_stride (>= vocab) elements apart. For the draw, values are clamped to
+ * [0, 1] (NaN: 0) and counted in steps of 2^-50, and sums are exact: the
+ * token does not depend on the order of summation, only rows need not add
+ * up to exactly 1. u outside [0, 1) counts as the nearest inside. A draft
+ * outside [0, vocab) is refused and d_n_draft outside its range clamped,
+ * each setting HSWA_ERR_BOUNDS on the device. n_tok in [1,
+ * HSWA_DECODE_MAX_TOKENS]; d_draft and q may be NULL for n_tok = 1. */
+int hswa_verify_draft(int dtype, const void *p, int64_t p_stride, const void *q, int64_t q_stride,
+                      const int32_t *d_draft, const int32_t *d_n_draft, const float *u, int n_seqs, int n_tok,
+                      int vocab, int32_t *n_accept, int32_t *tokens, hswa_stream_t stream);
 
 /* One chunked-prefill chunk of attention (Sec. 1.1: chunked prefill is
  * close to compute-bound). Sequence i < n_seqs has d_prefix_len[i] cached

@@ -211,3 +211,60 @@ class DualPool:
 
     def live_full_pages(self, s):
         return int(np.count_nonzero(self.full_bt[s] >= 0))
+
+    # ------------------------------------------- taking back and evicting
+    def truncate(self, seq_ids, new_len):
+        """Shorten sequences to new_len tokens each (refused drafts); Full
+        pages that went back to the free list."""
+        todo = sorted((int(s), int(n)) for s, n in zip(seq_ids, new_len))
+        for s, n in todo:
+            if not 0 <= n <= self.seq_len[s]:
+                raise ValueError("new length out of range")
+            if n in (0, self.seq_len[s]):
+                continue
+            window = range(max(0, n - self.W) // self.P, (n - 1) // self.P + 1)
+            if any(self.swa_bt[s, p] < 0 for p in window):
+                raise ValueError("window released")
+            if n % self.P and (self.full_ref[self.full_bt[s, n // self.P]] > 1 or
+                               self.swa_ref[self.swa_bt[s, n // self.P]] > 1):
+                raise ValueError("ends inside a shared page")
+        freed = 0
+        for s, n in todo:
+            first = -(-n // self.P)
+            for p in range(first, self.full_bt.shape[1]):
+                if self.full_bt[s, p] >= 0:
+                    freed += self.unref_full(int(self.full_bt[s, p]))
+                    self.full_bt[s, p] = -1
+            for p in range(first, self.swa_bt.shape[1]):
+                if self.swa_bt[s, p] >= 0:
+                    self.unref_swa(int(self.swa_bt[s, p]))
+                    self.swa_bt[s, p] = -1
+            self.seq_len[s] = n
+        return freed
+
+    def evict(self, seq_ids, keep):
+        """Keep only the logical pages keep[i] (ascending) of sequence
+        seq_ids[i]; the columns of both tables close up."""
+        todo = sorted((int(s), [int(p) for p in k]) for s, k in zip(seq_ids, keep))
+        for s, k in todo:
+            L = int(self.seq_len[s])
+            pages = -(-L // self.P)
+            if k != sorted(set(k)) or any(not 0 <= p < pages for p in k):
+                raise ValueError("not an ascending list of pages")
+            if any((p + 1) * self.P > L - self.W for p in set(range(pages)) - set(k)):
+                raise ValueError("drops a page of the window")
+        freed = 0
+        for s, k in todo:
+            pages = -(-int(self.seq_len[s]) // self.P)
+            gone = sorted(set(range(pages)) - set(k))
+            for p in gone:
+                freed += self.unref_full(int(self.full_bt[s, p]))
+            for p in gone:
+                if self.swa_bt[s, p] >= 0:
+                    self.unref_swa(int(self.swa_bt[s, p]))
+            for table in (self.full_bt, self.swa_bt):
+                row = table[s, k].copy()
+                table[s] = -1
+                table[s, :len(k)] = row
+            self.seq_len[s] -= len(gone) * self.P
+        return freed

@@ -1,0 +1,281 @@
+"""Decode with page weights, and the choice of the pages that stay, on the GPU
+against the 64-bit oracle.
+
+Tolerances. A score is a sum of 128 products in fp32, off by at most 128 2^-24
+sum |q k| scale: below 1e-4 for N(0, 1) inputs (sum |q k| about 82, scale
+1/sqrt(128)); a weight is the exponential of the difference of two of them
+and of sums no less exact: 2.5e-4 of its value. fp32 pools of d = 64: the
+same with 64 products. On top, 1e-6 for what decay adds. The output is
+hswa_decode's: equal bits where the same kernel runs, else the usual 2e-2 for
+bf16 and 1e-5 for fp32. The choice of pages is exact."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import hswa_workloads as wl
+import oracle
+from oracle import serving
+from oracle.fp8 import e4m3_decode
+import hybrid_sliding_window_dual_gb300 as H
+from hybrid_sliding_window_dual_gb300.session import DualPoolSession
+from scenario import fill_normal_
+
+F32, BF16, FP8 = wl.DTYPE_F32, wl.DTYPE_BF16, H.HSWA_DTYPE_FP8_E4M3
+
+
+class Case:
+    def __init__(self, lens, hq, hkv, d, P, dtype, seed=0, spare=2):
+        S = len(lens)
+        self.lens, self.P, self.dtype, self.hq, self.hkv, self.d = np.array(lens), P, dtype, hq, hkv, d
+        pages = sum(-(-L // P) for L in lens) + 1
+        mp = max(-(-L // P) for L in lens) + spare
+        cfg = H.Config(window=128, page_size=P, n_q_heads=hq, n_kv_heads=hkv, head_dim=d, dtype=dtype, full_pages=pages,
+                       swa_pages=pages, max_seqs=S, max_pages_per_seq=mp)
+        self.sess = DualPoolSession(cfg, [wl.KIND_FULL], wl.permutation(pages, seed))
+        self.sess.reserve(range(S), lens)
+        self.sess.sync()
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        k, v = self.sess.k[0], self.sess.v[0]
+        if dtype == FP8:
+            for x in (k, v):
+                x.copy_((torch.randn(x.shape, generator=g, device="cuda") * 120).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8))
+            for x in (self.sess.ks[0], self.sess.vs[0]):
+                x.copy_(0.004 + 0.008 * torch.rand(x.shape, generator=g, device="cuda"))
+        else:
+            fill_normal_(k, seed + 1)
+            fill_normal_(v, seed + 2)
+        self.q = wl.normal((S, hq, d), seed + 3, F32 if dtype == F32 else BF16, "cuda")
+        self.w_in = torch.rand(S, mp, generator=g, device="cuda") * 3
+        self.scale = 1 / math.sqrt(d)
+        self.S, self.mp = S, mp
+
+    def values(self, which):
+        x = (self.sess.k if which == "k" else self.sess.v)[0]
+        if self.dtype != FP8:
+            return x.double().cpu().numpy()
+        s = (self.sess.ks if which == "k" else self.sess.vs)[0].double().cpu().numpy()  # [pages][Hkv][P][1]
+        x = e4m3_decode(x.cpu().numpy())
+        return (x if which == "k" else x.transpose(0, 1, 3, 2)) * s
+
+    def exact(self):
+        full = self.sess.d_full_bt.cpu().numpy()
+        return serving.decode_weights(self.q.double().cpu().numpy(), self.values("k"), self.values("v"), full, self.sess.d_seq_len.cpu().numpy(), self.scale)
+
+    def run(self, w_in, decay, w_out=None):
+        o = torch.full_like(self.q, 9)
+        w = torch.full((self.S, self.mp), 9.0, device="cuda") if w_out is None else w_out
+        self.sess.decode_weights(0, self.q, o, self.S, self.scale, w_in, decay, w)
+        return o, w
+
+    def check(self, decay=0.75, expect_kernel=None):
+        o, w = self.run(self.w_in, decay)
+        name = H.hswa_last_kernel()
+        assert self.sess.check() == 0
+        assert expect_kernel is None or name == expect_kernel, name
+        exact_o, exact_w = self.exact()
+        tol = 1e-5 if self.dtype == F32 else 2e-2
+        assert np.abs(o.double().cpu().numpy() - exact_o).max() <= tol
+        used = np.arange(self.mp)[None] * self.P < self.sess.d_seq_len.cpu().numpy()[:, None]
+        carried = np.where(used, decay * self.w_in.double().cpu().numpy(), 0)
+        got = w.double().cpu().numpy()
+        assert (np.abs(got - (exact_w + carried)) <= 2.5e-4 * exact_w + 1e-6).all()
+        assert (got[~used] == 0).all()
+        if "weights_any" not in name:
+            ref = torch.empty_like(o)
+            self.sess.decode(0, self.q, ref, self.S, self.scale)
+            assert torch.equal(o, ref)
+        again = self.run(self.w_in, decay)
+        assert torch.equal(again[0], o) and torch.equal(again[1], w)  # equal inputs, equal bits
+        return o, w
+
+
+LENS = [1, 63, 64, 65, 128, 700, 0, 3001, 64 * 33, 9000]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+@pytest.mark.parametrize("hkv", [1, 3, 8])
+def test_decode_weights_match_oracle(dtype, hkv):
+    c = Case(LENS, 8 * hkv, hkv, 128, 64, dtype, seed=hkv)
+    c.check(expect_kernel="decode_mma_%s_d128+weights" % ("bf16" if dtype == BF16 else "fp8"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,d,P,dtype", [(4, 1, 64, 16, F32), (6, 2, 64, 16, BF16), (8, 8, 96, 5, BF16), (3, 1, 256, 64, F32), (12, 2, 128, 64, F32),
+                                              (5, 5, 7, 1, F32), (16, 2, 128, 32, BF16)])
+def test_decode_weights_any_shape(hq, hkv, d, P, dtype):
+    c = Case([1, 15, 16, 17, 0, 300, 777], hq, hkv, d, P, dtype, seed=d)
+    c.check(expect_kernel="decode_weights_any_%s" % ("f32" if dtype == F32 else "bf16"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP8, F32])
+def test_decode_weights_one_long_sequence(dtype):
+    """One sequence split over every CTA; for fp32 a shorter one."""
+    c = Case([70001] if dtype != F32 else [4001], *((8, 1, 128, 64) if dtype != F32 else (4, 1, 64, 16)), dtype, seed=4)
+    c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+def test_decode_weights_many_short_sequences(dtype):
+    c = Case([(i * 37) % 200 for i in range(600)], 16, 2, 128, 64, dtype, seed=5)
+    c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP8, F32])
+def test_decode_weights_accumulate(dtype):
+    """In place, over layers and steps; starting anew whatever was there."""
+    c = Case([5, 200, 0, 1000], *((16, 2, 128, 64) if dtype != F32 else (4, 2, 64, 16)), dtype, seed=6)
+    _, once = c.run(None, 0.5)
+    nan = torch.full_like(once, float("nan"))
+    _, anew = c.run(nan, 0.0, nan)
+    assert anew is nan and torch.equal(anew, once)
+    total = once.clone()
+    c.run(total, 1.0, total)
+    c.run(total, 1.0, total)
+    assert torch.allclose(total, 3 * once, rtol=2.0 ** -22, atol=0)
+    rows = once.double().sum(1).cpu().numpy()
+    assert np.allclose(rows[c.lens > 0], c.hq, rtol=1e-4) and (rows[c.lens == 0] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP8, F32])
+def test_decode_weights_one_key_with_everything(dtype):
+    """Scores far apart: the page of the largest gets the whole weight, the
+    others underflow to 0, never to NaN."""
+    c = Case([64 * 9 + 3, 130], *((8, 1, 128, 64) if dtype != F32 else (4, 1, 64, 16)), dtype, seed=7)
+    c.scale = 60.0 if dtype != F32 else 200.0
+    _, w = c.run(None, 0)
+    assert c.sess.check() == 0
+    _, exact = c.exact()
+    assert torch.isfinite(w).all()
+    # an absolute error of a score of size |s| is at most 2^-17 |s| (as above), here |s| up to 60 * 45: 2e-2
+    assert np.abs(w.double().cpu().numpy() - exact).max() <= 0.05 * c.hq
+    c.scale = 0.0  # all keys alike
+    _, w = c.run(None, 0)
+    _, exact = c.exact()
+    assert np.allclose(w.double().cpu().numpy(), exact, rtol=1e-5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP8, F32])
+def test_decode_weights_skip_pages_with_a_bad_entry(dtype):
+    c = Case([300, 64, 1000], *((16, 2, 128, 64) if dtype != F32 else (4, 2, 64, 16)), dtype, seed=8)
+    good = c.run(None, 0)[1].clone()
+    c.sess.d_full_bt[0, 1] = -1
+    c.sess.d_full_bt[1, 0] = c.sess.cfg.full_pages  # P = 64: its only page
+    o, w = c.run(None, 0)
+    assert c.sess.check() == H.HSWA_ERR_BOUNDS
+    c.sess.d_full_bt[1, 0] = -1
+    exact_o, exact_w = c.exact()
+    assert np.abs(w.double().cpu().numpy() - exact_w).max() <= 2.5e-4 * c.hq
+    assert np.abs(o.double().cpu().numpy() - exact_o).max() <= (1e-5 if dtype == F32 else 2e-2)
+    assert w[0, 1] == 0 and torch.equal(w[2], good[2])
+
+
+@pytest.mark.gpu
+def test_decode_weights_on_a_stream_and_in_a_graph():
+    c = Case([100, 5000, 3], 64, 8, 128, 64, BF16, seed=9)
+    o, w = c.check()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    c.sess.stream = side
+    o2, w2 = c.run(c.w_in, 0.75)
+    assert c.sess.check() == 0 and torch.equal(o2, o) and torch.equal(w2, w)
+    c.sess.stream = None
+    ws = torch.empty(H.hswa_decode_weights_workspace_size(c.sess.pool, 3), dtype=torch.uint8, device="cuda")
+    o3, w3 = torch.zeros_like(o), torch.zeros_like(w)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        H.hswa_decode_weights(c.sess.pool, c.sess.layers[0], c.q, o3, c.sess.d_full_bt, c.sess.d_seq_len, 3, c.scale, c.w_in, 0.75, w3, ws, ws.numel(),
+                              torch.cuda.current_stream())
+    ws.fill_(255)  # nothing of the workspace is read before it is written
+    for _ in range(2):
+        o3.zero_(), w3.zero_()
+        g.replay()
+        assert H.hswa_check() == 0 and torch.equal(o3, o) and torch.equal(w3, w)
+
+
+# ---------------------------------------------------------------- selection
+def select(lens, w, budget, P, sink, recent, window=128, in_place=False):
+    S, mp = w.shape
+    pool = H.hswa_pool_create(H.Config(window=window, page_size=P, n_q_heads=8, n_kv_heads=1, head_dim=128, dtype=BF16, full_pages=1, swa_pages=1,
+                                       max_seqs=S, max_pages_per_seq=mp))
+    d_w = torch.as_tensor(w, device="cuda")
+    keep = torch.full((S, mp), -7, dtype=torch.int32, device="cuda")
+    n_keep = torch.full((S,), -7, dtype=torch.int32, device="cuda")
+    w_out = d_w.clone() if in_place else torch.full_like(d_w, 9)
+    H.hswa_evict_select(pool, torch.as_tensor(np.asarray(lens, np.int32), device="cuda"), w_out if in_place else d_w,
+                        torch.as_tensor(np.asarray(budget, np.int32), device="cuda"), S, sink, recent, keep, n_keep, w_out)
+    assert H.hswa_check() == 0
+    H.hswa_pool_destroy(pool)
+    keep, n_keep, got = keep.cpu().numpy(), n_keep.cpu().numpy(), w_out.cpu().numpy()
+    for i, stay in enumerate(serving.evict_select(lens, w, budget, P, sink, recent)):
+        assert n_keep[i] == len(stay)
+        assert keep[i].tolist() == stay + [-1] * (mp - len(stay))
+        assert np.array_equal(got[i].view(np.int32), np.concatenate([w[i, stay], np.zeros(mp - len(stay), np.float32)]).view(np.int32))
+
+
+def weights(rng, S, mp, kind):
+    w = np.exp(2.5 * rng.standard_normal((S, mp))).astype(np.float32)
+    if kind == "ties":
+        w = np.floor(w).clip(0, 3)
+    elif kind == "equal":
+        w[:] = 1.25
+    elif kind == "close":
+        w = np.float32(1) + np.arange(S * mp).reshape(S, mp)[:, ::-1] % 5 * np.float32(2 ** -23)
+    elif kind == "odd":
+        w *= rng.choice([-1, 1], w.shape).astype(np.float32)
+        at = rng.random(w.shape)
+        for i, x in enumerate((np.nan, np.inf, -np.inf, 0.0, -0.0, 1e-45, -1e-45)):
+            w[(at >= i * 0.08) & (at < (i + 1) * 0.08)] = x
+    return np.ascontiguousarray(w, np.float32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["plain", "ties", "equal", "close", "odd"])
+@pytest.mark.parametrize("mp", [1, 7, 33, 1024, 1025, 5000])
+def test_select_matches_oracle(kind, mp):
+    rng = np.random.default_rng(mp)
+    P, S = 16, 12
+    pages = rng.integers(0, mp + 1, S)
+    pages[0] = mp
+    lens = np.maximum(pages * P - rng.integers(0, P, S), 0)
+    lens[1] = 0
+    w = weights(rng, S, mp, kind)
+    budget = rng.integers(-2, mp + 3, S)
+    budget[2:4] = 0, mp
+    select(lens, w, budget, P, 2, 130)
+    select(lens, w, budget, P, 0, 128, in_place=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mp", [16384, 16385, 40000])
+def test_select_long_rows(mp):
+    rng = np.random.default_rng(mp)
+    for kind in ("plain", "ties", "odd"):
+        select([mp * 16, mp * 16 - 5, 16 * 9000], weights(rng, 3, mp, kind), [mp // 7, mp - 9, 400], 16, 3, 1000, in_place=kind == "ties")
+
+
+@pytest.mark.gpu
+def test_select_window_edges():
+    """Which pages may go at every length around a page's end, with windows
+    that do and do not end on a page."""
+    rng = np.random.default_rng(3)
+    for P, window, recent in ((16, 128, 128), (16, 100, 117), (5, 128, 131), (1, 128, 128), (64, 128, 2 ** 31 - 1)):
+        lens = np.arange(recent, recent + 40) if recent < 2 ** 30 else np.arange(500, 540)
+        mp = int(-(-lens.max() // P))
+        select(lens, weights(rng, 40, mp, "plain"), np.zeros(40, int), P, 1, recent, window)
+        select(lens, weights(rng, 40, mp, "plain"), np.zeros(40, int), P, mp + 5, recent, window)  # every page a sink
+
+
+@pytest.mark.gpu
+def test_select_many_sequences():
+    rng = np.random.default_rng(4)
+    lens = rng.integers(0, 64 * 90, 3000)
+    select(lens, weights(rng, 3000, 90, "ties"), rng.integers(0, 90, 3000), 64, 1, 128)
