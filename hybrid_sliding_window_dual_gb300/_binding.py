@@ -160,11 +160,9 @@ def _check(status, call):
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or x.__class__ is int:
         return x
-    if isinstance(x, np.ndarray):
+    if x.__class__ is np.ndarray:
         return x.ctypes.data
     return x.data_ptr()
 

@@ -135,6 +135,265 @@ __global__ void __launch_bounds__(256) rope_append_any(const __grid_constant__ R
     }
 }
 
+// The usual shapes: 16-byte chunks, two of a row per thread. A thread's two
+// chunks are the two halves of 8 (fp32: 4) pairs, or two neighbours where
+// pairs are adjacent or nothing turns. blockDim.x threads make a row,
+// blockDim.y rows go at a time, kItems of them in flight per thread.
+template <typename T>
+constexpr int kVec = 16 / (int)sizeof(T);
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4 &c, float (&x)[kVec<T>]) {
+    if constexpr (sizeof(T) == 4) {
+        x[0] = __uint_as_float(c.x), x[1] = __uint_as_float(c.y);
+        x[2] = __uint_as_float(c.z), x[3] = __uint_as_float(c.w);
+    } else {
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float (&x)[kVec<T>]) {
+    if constexpr (sizeof(T) == 4)
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    else
+        return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+
+// Turn pairs: V of them across chunks a and b (halves), or the V / 2 inside
+// chunk a (adjacent). cs, sn: from the first of them on.
+template <typename T>
+__device__ __forceinline__ void turn_across(float (&a)[kVec<T>], float (&b)[kVec<T>], const float *cs, const float *sn) {
+#pragma unroll
+    for (int i = 0; i < kVec<T>; i += 4) {
+        const float4 c = *reinterpret_cast<const float4 *>(cs + i), s = *reinterpret_cast<const float4 *>(sn + i);
+        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float x = a[i + k], y = b[i + k];
+            a[i + k] = x * cc[k] - y * ss[k];
+            b[i + k] = x * ss[k] + y * cc[k];
+        }
+    }
+}
+template <typename T>
+__device__ __forceinline__ void turn_inside(float (&a)[kVec<T>], const float *cs, const float *sn) {
+#pragma unroll
+    for (int i = 0; i < kVec<T> / 2; i += 2) {
+        const float2 c = *reinterpret_cast<const float2 *>(cs + i), s = *reinterpret_cast<const float2 *>(sn + i);
+        const float cc[2] = {c.x, c.y}, ss[2] = {s.x, s.y};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float x = a[2 * (i + k)], y = a[2 * (i + k) + 1];
+            a[2 * (i + k)] = x * cc[k] - y * ss[k];
+            a[2 * (i + k) + 1] = x * ss[k] + y * cc[k];
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+
+// 8 elements over a scale, as codes: the quotients are correctly rounded
+// before they become codes, as in hswa_append_kv. (A product with the
+// reciprocal, divided only next to a middle between codes, was slower: 75
+// against 70 us on 9999 tokens, for the registers it takes.)
+__device__ __forceinline__ uint2 e4m3x8(const float (&x)[8], float scale) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], scale);
+    return make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
+}
+
+// The scale of a row of 128 elements, 16 of them in each of 8 neighbouring lanes.
+__device__ __forceinline__ float row_scale(const float (&a)[8], const float (&b)[8]) {
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(a[i]), fabsf(b[i])));
+    const uint32_t mates = 0xffu << (threadIdx.y * 8 & 24);  // blockDim.x is 8
+    for (int off = 4; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mates, amax, off));
+    return amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+}
+
+constexpr int kMaxTile = 4;  // tokens per CTA
+constexpr int kVTile = 64;   // tokens per CTA of FP8 V rows
+
+// FP8 V: a page keeps V transposed ([d][rows]), so the codes of a tile of
+// tokens of one kv head turn around in shared memory and go out token by
+// lane: tokens of one sequence are neighbours there, and a warp's bytes for
+// one d fill whole sectors. (hswa_append_kv writes them one by one.)
+template <int kTokens>
+__device__ void rope_v_fp8(const RopeArgs &a, int32_t block) {
+    __shared__ uint8_t tile[128][kTokens + 1];  // an odd number of bytes: 8 rows of codes fall into 8 banks
+    __shared__ int64_t at[kTokens];  // element (0, row) of the token's page, or -1
+    const int tid = threadIdx.y * 8 + threadIdx.x;
+    const int64_t t0 = (int64_t)(block / a.hkv) * kTokens;
+    const int32_t h = block % a.hkv;
+    const int32_t n = (int32_t)min((int64_t)kTokens, a.n_tokens - t0);
+    for (int r = threadIdx.y; r < kTokens; r += 32) {
+        const bool there = r < n;
+        const int64_t t = t0 + (there ? r : 0);
+        const int32_t slot = a.slots[t];
+        const bool ok = there && slot >= 0 && slot < a.pool_slots;
+        const uint4 *x = reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.v + t * a.v_stride + h * 128);
+        float lo[8], hi[8];
+        unpack<__nv_bfloat16>(x[2 * threadIdx.x], lo);
+        unpack<__nv_bfloat16>(x[2 * threadIdx.x + 1], hi);
+        const float scale = row_scale(lo, hi);
+        const uint2 c0 = e4m3x8(lo, scale), c1 = e4m3x8(hi, scale);
+        const uint32_t w[4] = {c0.x, c0.y, c1.x, c1.y};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) tile[threadIdx.x * 16 + i][r] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+        if (threadIdx.x == 0) {
+            const int64_t blk = ok ? (int64_t)(slot / a.page) * a.hkv + h : 0;
+            at[r] = ok ? blk * 128 * a.page + slot % a.page : -1;
+            if (ok) a.vs[blk * a.page + slot % a.page] = scale;
+        }
+    }
+    __syncthreads();
+    uint8_t *vp = (uint8_t *)a.vp;
+    const int r = tid % kTokens;
+    if (r < n && at[r] >= 0)
+        for (int d = tid / kTokens; d < 128; d += 256 / kTokens) vp[at[r] + (int64_t)d * a.page] = tile[d][r];
+}
+
+// kTile tokens per CTA: their q and K rows and, but for FP8 pools, V rows;
+// for FP8 pools the CTAs from n_q_blocks on take the V rows.
+//
+// Bound by memory: a token reads and writes (Hq + 2 Hkv) d elements and does
+// three flops for each. What that takes is enough loads in flight, that is
+// CTAs per SM more than items per thread: capped at 48 registers (5 CTAs, 2
+// items of two 16-byte loads each) 32768 bf16 tokens of 64 / 8 heads take 201
+// us, 98 % of the copy bandwidth; at 74 registers with 4 items 268 us. FP8
+// codes need more registers (4 CTAs, 3 items): 9999 tokens in 70 us, 82 %;
+// 8 us of it is V's turning round, which the tiles at the end of the grid do
+// (put first or spread among the others they cost more: 72 and 77 us). A
+// decode step of 64 tokens takes 3.5 us on the device.
+template <typename T, bool kFP8, bool kAdjacent, int kTile, int kItems, int kMinCtas>
+__global__ void __launch_bounds__(256, kMinCtas) rope_append_vec(const __grid_constant__ RopeArgs a, int32_t n_q_blocks) {
+    constexpr int V = kVec<T>;
+    __shared__ __align__(16) float cs[kTile][HSWA_ROPE_MAX_DIM / 2], sn[kTile][HSWA_ROPE_MAX_DIM / 2];
+    __shared__ int32_t slot_of[kTile];
+    pdl_wait();
+    pdl_launch_dependents();
+    if constexpr (kFP8) {
+        if ((int32_t)blockIdx.x >= n_q_blocks) {
+            rope_v_fp8<kTile == 1 ? 8 : kVTile>(a, blockIdx.x - n_q_blocks);
+            return;
+        }
+    }
+    const int tid = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
+    const int64_t t0 = (int64_t)blockIdx.x * kTile;
+    const int nt = (int)min((int64_t)kTile, a.n_tokens - t0);
+    const int rows = a.hq + (kFP8 ? 1 : 2) * a.hkv;  // of a token: q, K, V
+    const int n = nt * rows, chunks = a.d / V;
+    // this thread's two chunks of a row: j-th of the first halves and its
+    // partner, or j and j + half the row; neighbours in a warp are neighbours
+    // in the row either way, so loads and stores cover whole sectors
+    const int j = threadIdx.x, rc = 2 * a.half / V, hc = kAdjacent ? 0 : rc / 2;
+    const bool across = j < hc;
+    const int rest = chunks - 2 * hc;  // chunks outside pairs of chunks
+    const int c0 = across ? j : hc + j, c1 = across ? j + hc : c0 + (rest + 1) / 2;
+    const bool two = c1 < chunks;
+    uint4 xa[kItems], xb[kItems];
+    const auto load = [&](int r0) {
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int r = r0 + i * blockDim.y;
+            xa[i] = xb[i] = make_uint4(0, 0, 0, 0);
+            if (r >= n) continue;
+            const int t = r / rows, h = r - t * rows;
+            const T *x = h < a.hq           ? (const T *)a.q + (t0 + t) * a.q_stride + (int64_t)h * a.d
+                         : h < a.hq + a.hkv ? (const T *)a.k + (t0 + t) * a.k_stride + (int64_t)(h - a.hq) * a.d
+                                            : (const T *)a.v + (t0 + t) * a.v_stride + (int64_t)(h - a.hq - a.hkv) * a.d;
+            xa[i] = reinterpret_cast<const uint4 *>(x)[c0];
+            if (two) xb[i] = reinterpret_cast<const uint4 *>(x)[c1];
+        }
+    };
+    load(threadIdx.y);  // on their way while the angles are made
+    for (int i = tid; i < nt * a.half; i += threads) {
+        const int t = i / a.half, p = i - t * a.half;
+        const float2 x = rope_turn(a, p, t0 + t);
+        cs[t][p] = x.x;
+        sn[t][p] = x.y;
+    }
+    if (tid < nt) {
+        const int32_t slot = a.slots[t0 + tid];
+        if (slot >= a.pool_slots) set_error(a.err, HSWA_ERR_BOUNDS);
+        slot_of[tid] = slot < a.pool_slots ? slot : -1;
+    }
+    __syncthreads();
+    for (int r0 = threadIdx.y; r0 < n; r0 += blockDim.y * kItems) {
+        if (r0 != (int)threadIdx.y) load(r0);
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int r = r0 + i * blockDim.y;
+            if (r >= n) continue;
+            const int t = r / rows, h = r - t * rows;
+            float lo[V], hi[V];
+            unpack<T>(xa[i], lo);
+            unpack<T>(xb[i], hi);
+            if (h < a.hq + a.hkv) {
+                if (!kAdjacent && across) turn_across<T>(lo, hi, &cs[t][c0 * V], &sn[t][c0 * V]);
+                if (kAdjacent && c0 < rc) turn_inside<T>(lo, &cs[t][c0 * (V / 2)], &sn[t][c0 * (V / 2)]);
+                if (kAdjacent && c1 < rc) turn_inside<T>(hi, &cs[t][c1 * (V / 2)], &sn[t][c1 * (V / 2)]);
+            }
+            if (h < a.hq) {
+                uint4 *o = reinterpret_cast<uint4 *>((T *)a.q_out + ((t0 + t) * a.hq + h) * a.d);
+                o[c0] = pack<T>(lo);
+                if (two) o[c1] = pack<T>(hi);
+                continue;
+            }
+            const int32_t slot = slot_of[t];
+            if (slot < 0) continue;
+            const bool is_k = h < a.hq + a.hkv;
+            const int64_t blk = (int64_t)(slot / a.page) * a.hkv + (h - a.hq - (is_k ? 0 : a.hkv));
+            const int64_t row = blk * a.page + slot % a.page;
+            if constexpr (kFP8) {
+                const float scale = row_scale(lo, hi);
+                uint2 *o = reinterpret_cast<uint2 *>((uint8_t *)a.kp + row * 128);
+                o[c0] = e4m3x8(lo, scale);
+                o[c1] = e4m3x8(hi, scale);
+                if (j == 0) a.ks[row] = scale;
+            } else {
+                uint4 *o = reinterpret_cast<uint4 *>((T *)(is_k ? a.kp : a.vp) + row * a.d);
+                o[c0] = pack<T>(lo);
+                if (two) o[c1] = pack<T>(hi);
+            }
+        }
+    }
+}
+
+// Tokens from which a CTA takes kMaxTile of them. One token per CTA ends
+// soonest while the grid is a few waves; with more, the angles and the start
+// of a CTA are paid for too often (64 / 8 heads, d = 128, one token against
+// four per CTA: bf16 2048 tokens 15.9 / 19.8 us, 4096 tokens 36.9 / 32.2 us;
+// FP8 1024 tokens 12.4 / 14.7, 1536 tokens 17.6 / 15.2; fp32 4096 tokens 52 /
+// 58, 16384 tokens equal).
+template <typename T, bool kFP8>
+constexpr int kTileFrom = kFP8 ? 1280 : sizeof(T) == 2 ? 2560 : 8192;
+
+template <typename T, bool kFP8, bool kAdjacent>
+cudaError_t launch_rope_vec(const RopeArgs &a, cudaStream_t st) {
+    const int units = (a.d / kVec<T> + 1) / 2;  // threads of a row
+    const bool tiled = a.n_tokens >= kTileFrom<T, kFP8>;
+    const int64_t nq = tiled ? ((int64_t)a.n_tokens + kMaxTile - 1) / kMaxTile : a.n_tokens;
+    const int64_t vt = tiled ? kVTile : 8;
+    const int64_t nv = kFP8 ? (a.n_tokens + vt - 1) / vt * a.hkv : 0;
+    const dim3 grid((unsigned)(nq + nv)), block(units, 256 / units);
+    constexpr int kItems = kFP8 || kAdjacent ? 3 : 2, kMinCtas = kFP8 || kAdjacent ? 4 : 5;
+    return tiled ? launch_pdl(rope_append_vec<T, kFP8, kAdjacent, kMaxTile, kItems, kMinCtas>, grid, block, 0, st, a, (int32_t)nq)
+                 : launch_pdl(rope_append_vec<T, kFP8, kAdjacent, 1, 3, 4>, grid, block, 0, st, a, (int32_t)nq);
+}
+
 }  // namespace
 }  // namespace hswa
 
@@ -237,13 +496,31 @@ extern "C" int hswa_rope_append(const hswa_pool *pool, const hswa_layer *layer, 
     std::copy(rope->turn, rope->turn + a.half, a.turn);
     std::copy(rope->axis, rope->axis + a.half, a.axis);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    set_last_kernel(fp8 ? "rope_append_any_fp8" : e == 4 ? "rope_append_any_f32" : "rope_append_any_bf16");
-    if (fp8)
-        rope_append_any<__nv_bfloat16, true><<<n_tokens, 256, 0, st>>>(a);
-    else if (e == 4)
-        rope_append_any<float, false><<<n_tokens, 256, 0, st>>>(a);
-    else
-        rope_append_any<__nv_bfloat16, false><<<n_tokens, 256, 0, st>>>(a);
-    const cudaError_t rc = cudaGetLastError();
+    // 16-byte chunks need every row on a 16-byte boundary and the turning part
+    // in whole pairs of chunks; the plain kernel takes the rest
+    const int64_t w = 16 / e;
+    const uintptr_t bases = (uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)q_out | (uintptr_t)a.kp | (uintptr_t)a.vp;
+    const bool vec = rope->rotary_dim % (a.adjacent ? w : 2 * w) == 0 && c.head_dim % w == 0 && (q_stride | k_stride | v_stride) % w == 0 &&
+                     (bases & 15) == 0 &&
+                     n_tokens + (fp8 ? (n_tokens + INT64_C(7)) / 8 * c.n_kv_heads : 0) <= INT32_MAX;
+    cudaError_t rc;
+    if (vec) {
+        set_last_kernel(fp8 ? "rope_append_fp8" : e == 4 ? "rope_append_f32" : "rope_append_bf16");
+        if (fp8)
+            rc = a.adjacent ? launch_rope_vec<__nv_bfloat16, true, true>(a, st) : launch_rope_vec<__nv_bfloat16, true, false>(a, st);
+        else if (e == 4)
+            rc = a.adjacent ? launch_rope_vec<float, false, true>(a, st) : launch_rope_vec<float, false, false>(a, st);
+        else
+            rc = a.adjacent ? launch_rope_vec<__nv_bfloat16, false, true>(a, st) : launch_rope_vec<__nv_bfloat16, false, false>(a, st);
+    } else {
+        set_last_kernel(fp8 ? "rope_append_any_fp8" : e == 4 ? "rope_append_any_f32" : "rope_append_any_bf16");
+        if (fp8)
+            rope_append_any<__nv_bfloat16, true><<<n_tokens, 256, 0, st>>>(a);
+        else if (e == 4)
+            rope_append_any<float, false><<<n_tokens, 256, 0, st>>>(a);
+        else
+            rope_append_any<__nv_bfloat16, false><<<n_tokens, 256, 0, st>>>(a);
+        rc = cudaGetLastError();
+    }
     return rc == cudaSuccess ? HSWA_OK : cuda_fail(rc, "hswa_rope_append");
 }
