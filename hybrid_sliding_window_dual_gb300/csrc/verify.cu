@@ -8,9 +8,9 @@
 //
 // Everything that decides is exact. The acceptance test compares a product
 // of two fp32 values with a third in 64-bit floating point, where the
-// product is exact. For the draw, probabilities are turned into integers
-// (2^50 steps to 1) and their differences summed in 64 and 96 bits, so the
-// sums, and with them the token, do not depend on how the row is split.
+// product is exact. For the draw, probabilities are counted in whole steps
+// and their differences summed as integers of up to 96 bits, so the sums, and
+// with them the token, do not depend on how the row is split.
 #include "common.cuh"
 #include "internal.h"
 
@@ -18,8 +18,7 @@ namespace hswa {
 namespace {
 
 constexpr int kWarps = 16;
-constexpr int kCluster = 8;                  // CTAs per sequence
-constexpr int kParts = kCluster * kWarps;    // a row is cut into that many slices, one per warp
+constexpr int kMaxCluster = 8;  // CTAs per sequence
 
 typedef unsigned __int128 u128;
 
@@ -28,7 +27,7 @@ struct VerifyArgs {
     int64_t p_stride, q_stride;
     const int32_t *draft, *n_draft;
     const float *u;
-    int32_t n_tok, vocab;
+    int32_t n_tok, vocab, cluster, part;  // part: positions of a warp's slice
     int32_t *n_accept, *tokens;
     int *err;
 };
@@ -42,10 +41,69 @@ __device__ __forceinline__ float prob<__nv_bfloat16>(const __nv_bfloat16 *row, i
     return __bfloat162float(row[i]);
 }
 
-// A probability in steps of 2^-50: [0, 1] clamped, NaN as 0.
-__device__ __forceinline__ uint64_t steps(float x) {
-    return __float2ull_rn(fminf(fmaxf(x, 0.f), 1.f) * 0x1p50f);
-}
+// A sum of probabilities in whole steps: 2^-50 for fp32, 2^-45 for bf16,
+// whose 8 significant bits that holds down to 2^-37. A value is cut into
+// digits of 16 or 22 bits by adding a power of two whose last place is the
+// digit's: the low bits of the sum are the digit, rounded to nearest, and
+// what is left over is exact. That is 7 to 10 plain instructions; a
+// conversion to a 64-bit integer took 20 times as long. 32-bit digits hold
+// 2^9 values, and are emptied into 64 bits before that.
+template <typename T>
+struct Steps;
+
+template <>
+struct Steps<float> {
+    uint32_t a = 0, b = 0, c = 0;  // units of 2^-16, 2^-33, 2^-50; signed, modulo 2^32
+
+    struct Digits {
+        uint32_t a, b, c;  // off by the constants' bits
+    };
+    static __device__ __forceinline__ Digits digits(float x) {
+        const float t = __fadd_rn(x, 128.f), r = __fsub_rn(x, __fsub_rn(t, 128.f));
+        const float u = __fadd_rn(r, 0x1.8p-10f), q = __fsub_rn(r, __fsub_rn(u, 0x1.8p-10f));
+        return {__float_as_uint(t), __float_as_uint(u), __float_as_uint(__fadd_rn(q, 0x1.8p-27f))};
+    }
+    // add_raw leaves the constants in; drop takes n of them out
+    __device__ __forceinline__ void add_raw(float x) {
+        const Digits d = digits(x);
+        a += d.a, b += d.b, c += d.c;
+    }
+    __device__ __forceinline__ void drop(int n) {
+        a -= n * 0x43000000, b -= n * 0x3ac00000, c -= n * 0x32400000;  // 128, 1.5 2^-10, 1.5 2^-27
+    }
+    __device__ __forceinline__ void add_difference(float x, float y) {
+        const Digits d = digits(x), z = digits(y);
+        a += d.a - z.a, b += d.b - z.b, c += d.c - z.c;
+    }
+    __device__ __forceinline__ uint64_t total() const {
+        return (uint64_t)(((int64_t)(int32_t)a << 34) + ((int64_t)(int32_t)b << 17) + (int32_t)c);
+    }
+};
+
+template <>
+struct Steps<__nv_bfloat16> {
+    uint32_t a = 0, b = 0;  // units of 2^-22, 2^-45; signed, modulo 2^32
+
+    struct Digits {
+        uint32_t a, b;
+    };
+    static __device__ __forceinline__ Digits digits(float x) {
+        const float t = __fadd_rn(x, 2.f), r = __fsub_rn(x, __fsub_rn(t, 2.f));
+        return {__float_as_uint(t), __float_as_uint(__fadd_rn(r, 0x1.8p-22f))};
+    }
+    __device__ __forceinline__ void add_raw(float x) {
+        const Digits d = digits(x);
+        a += d.a, b += d.b;
+    }
+    __device__ __forceinline__ void drop(int n) {
+        a -= n * 0x40000000, b -= n * 0x34c00000;  // 2, 1.5 2^-22
+    }
+    __device__ __forceinline__ void add_difference(float x, float y) {
+        const Digits d = digits(x), z = digits(y);
+        a += d.a - z.a, b += d.b - z.b;
+    }
+    __device__ __forceinline__ uint64_t total() const { return (uint64_t)(((int64_t)(int32_t)a << 23) + (int32_t)b); }
+};
 
 __device__ __forceinline__ uint64_t shfl_xor64(uint64_t x, int m) {
     return __shfl_xor_sync(0xffffffffu, (unsigned long long)x, m);
@@ -70,121 +128,289 @@ __device__ u128 times_fraction(u128 x, float u) {
     return shift < 128 ? (x * m) >> shift : 0;
 }
 
-// What the draw at row position i weighs: the target's probability less the
-// draft's (less everything at the drafted token when the draft is greedy).
+// Elements of a 16-byte load, and loads of a row in flight per thread (with
+// two rows 8 in all; fewer, or twice the threads with half of them, were 3 to
+// 30 % slower on 64 sequences, 8 in place of 4 of each row 12 %).
 template <typename T>
-__device__ __forceinline__ uint64_t weight(const T *p, const T *q, int64_t i, int64_t gone) {
-    const uint64_t x = steps(prob(p, i));
-    if (q) {
-        const uint64_t y = steps(prob(q, i));
-        return x > y ? x - y : 0;
-    }
-    return i == gone ? 0 : x;
-}
+constexpr int kVec = 16 / (int)sizeof(T);
+template <bool kBoth>
+constexpr int kUnroll = kBoth ? 4 : 8;
 
 template <typename T>
-__global__ void __launch_bounds__(32 * kWarps) verify_draft(const __grid_constant__ VerifyArgs a) {
-    __shared__ uint64_t sums[2][kParts];  // slice sums of both passes, in every CTA of the cluster
-    __shared__ int32_t s_accept;
-    __shared__ int32_t s_token;
+__device__ __forceinline__ void unpack(const uint4 &c, float (&x)[kVec<T>]) {
+    if constexpr (sizeof(T) == 4) {
+        x[0] = __uint_as_float(c.x), x[1] = __uint_as_float(c.y);
+        x[2] = __uint_as_float(c.z), x[3] = __uint_as_float(c.w);
+    } else {
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+}
+
+// What a sequence draws from: the target's row less the draft's (less
+// everything at `gone`, the drafted token, when the draft was greedy).
+template <typename T>
+struct Weights {
+    const T *p, *q;
+    int32_t gone;
+
+    // Add a position's weight, but for `gone`. __saturatef: [0, 1], NaN as 0.
+    // With one row the constants stay in (Steps::drop).
+    template <bool kBoth>
+    static __device__ __forceinline__ void add(Steps<T> &sum, float px, float qx) {
+        const float x = __saturatef(px);
+        if constexpr (kBoth)
+            sum.add_difference(x, fminf(x, __saturatef(qx)));
+        else
+            sum.add_raw(x);
+    }
+    __device__ __forceinline__ uint64_t at(int32_t i) const {
+        if (i == gone) return 0;
+        Steps<T> sum;
+        if (q) {
+            add<true>(sum, prob(p, i), prob(q, i));
+        } else {
+            add<false>(sum, prob(p, i), 0.f);
+            sum.drop(1);
+        }
+        return sum.total();
+    }
+
+    // Sum of this lane's share of positions [i0, i0 + kUnroll * 32 * kWide) of
+    // a row that ends at hi: kUnroll loads of each row in flight, of 16 bytes
+    // where both rows are aligned (positions count from a vector's first).
+    template <int kWide, bool kBoth>
+    __device__ __forceinline__ uint64_t chunk(int32_t i0, int32_t hi) const {
+        const int lane = threadIdx.x & 31;
+        constexpr int kUnroll = hswa::kUnroll<kBoth>;
+        Steps<T> sum;
+        if constexpr (kWide > 1) {
+            uint4 a[kUnroll], b[kUnroll];
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) {
+                const int32_t i = i0 + (k * 32 + lane) * kWide;
+                a[k] = b[k] = make_uint4(0, 0, 0, 0);
+                if (i + kWide <= hi) {
+                    a[k] = *reinterpret_cast<const uint4 *>(p + i);
+                    if constexpr (kBoth) b[k] = *reinterpret_cast<const uint4 *>(q + i);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) {
+                float x[kWide], y[kWide];
+                unpack<T>(a[k], x);
+                unpack<T>(b[k], y);
+#pragma unroll
+                for (int e = 0; e < kWide; ++e) add<kBoth>(sum, x[e], y[e]);
+            }
+            // the row's last elements, short of a vector
+            const int32_t i = hi / kWide * kWide + lane;
+            if (i < hi && i >= i0 && i < i0 + kUnroll * 32 * kWide) {
+                add<kBoth>(sum, prob(p, i), kBoth ? prob(q, i) : 0.f);
+                if (!kBoth) sum.drop(1);
+            }
+        } else {
+            float x[kUnroll], y[kUnroll];
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) {
+                const int32_t i = i0 + k * 32 + lane;
+                x[k] = i < hi ? prob(p, i) : 0.f;
+                y[k] = kBoth && i < hi ? prob(q, i) : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) add<kBoth>(sum, x[k], y[k]);
+        }
+        if (!kBoth) sum.drop(kUnroll * kWide);
+        uint64_t total = sum.total();
+        if (!kBoth && lane == 0 && gone >= i0 && gone < min(i0 + kUnroll * 32 * kWide, hi)) {
+            Steps<T> x;
+            add<false>(x, prob(p, gone), 0.f);
+            x.drop(1);
+            total -= x.total();  // the warp's sum stays at or above 0
+        }
+        return total;
+    }
+
+    // The warp's slice [lo, hi), a chunk at a time: lane k keeps the sums of
+    // chunks k and 32 + k. The slice's sum.
+    template <int kWide, bool kBoth>
+    __device__ __forceinline__ uint64_t slice(int32_t lo, int32_t hi, uint64_t (&chunks)[2]) const {
+        const int lane = threadIdx.x & 31;
+        uint64_t total = 0;
+        chunks[0] = chunks[1] = 0;
+        int c = 0;
+        for (int32_t i0 = lo; i0 < hi; i0 += kUnroll<kBoth> * 32 * kWide, ++c) {
+            uint64_t x = chunk<kWide, kBoth>(i0, hi);
+            for (int m = 16; m > 0; m >>= 1) x += shfl_xor64(x, m);
+            if (lane == (c & 31)) chunks[c >> 5] = x;
+            total += x;
+        }
+        return total;
+    }
+};
+
+// One cluster of a.cluster CTAs per sequence. Every CTA settles the
+// acceptance tests for itself (two rounds of loads); each warp sums its slice
+// of the row; the CTAs tell each other their sums through distributed shared
+// memory; the warp whose slice the draw falls into finds its chunk, by the
+// sums that its lanes kept; and its CTA finds the token there. (One warp
+// alone takes 5 us longer for that: its instructions wait on each other.)
+//
+// Bound by memory and, by half as much, by the 20 instructions a pair of
+// values takes; before and after the row comes a fixed 5 us of dependent
+// loads and barriers. 64 sequences, 150000 fp32 values: 18.7 us, of which
+// 11.3 are the rows' bytes at the copy rate; 256 of 131000 bf16 values,
+// greedy: 19.4 us and 9.9; one sequence of 100003: 6.1 us on the device.
+template <typename T>
+__global__ void __launch_bounds__(32 * kWarps, 2) verify_draft(const __grid_constant__ VerifyArgs a) {
+    __shared__ uint64_t s_cta[2][kMaxCluster][2];  // sums of the cluster's CTAs (low, high), both passes
     __shared__ uint64_t s_warp[kWarps];
+    __shared__ uint64_t s_left;
+    __shared__ int32_t s_accept, s_last, s_from, s_end;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int rank = blockIdx.x % kCluster;
-    const int64_t s = blockIdx.x / kCluster;
+    const int rank = blockIdx.x % a.cluster;
+    const int64_t s = blockIdx.x / a.cluster;
     const int n_rows = a.n_tok - 1;  // drafts a sequence can have
     cluster_arrive();  // awaited before the first store into another CTA's shared memory
+    pdl_wait();
+    pdl_launch_dependents();
+    const float u_draw = a.u[s * a.n_tok + n_rows];
     if (warp == 0) {
+        const bool row = lane < n_rows;
         int32_t n = a.n_draft ? a.n_draft[s] : n_rows;
+        const int32_t x = row ? a.draft[s * n_rows + lane] : 0;
+        const float u = row ? a.u[s * a.n_tok + lane] : 0.f;
+        const bool inside = x >= 0 && x < a.vocab;
+        double px = 0.0, qx = 1.0;
+        if (row && inside) {
+            px = prob((const T *)a.p + (s * a.n_tok + lane) * a.p_stride, x);
+            if (a.q) qx = prob((const T *)a.q + (s * n_rows + lane) * a.q_stride, x);
+        }
         bool bad = n < 0 || n > n_rows;
         n = max(0, min(n, n_rows));
-        bool stays = false;
-        if (lane < n) {
-            const int32_t x = a.draft[s * n_rows + lane];
-            if (x < 0 || x >= a.vocab) {
-                bad = true;
-            } else {
-                const double px = prob((const T *)a.p + (s * a.n_tok + lane) * a.p_stride, x);
-                const double qx = a.q ? (double)prob((const T *)a.q + (s * n_rows + lane) * a.q_stride, x) : 1.0;
-                stays = (double)a.u[s * a.n_tok + lane] * qx < px;
-            }
-        }
+        bad |= lane < n && !inside;
+        const bool stays = lane < n && inside && (double)u * qx < px;
         if (bad && rank == 0) set_error(a.err, HSWA_ERR_BOUNDS);
         const unsigned gone = __ballot_sync(0xffffffffu, !stays);  // lanes past the drafts are in it
+        const int32_t acc = __ffs(gone) - 1;
         if (lane == 0) {
-            s_accept = __ffs(gone) - 1;
-            s_token = n;
+            s_accept = acc;
+            s_last = n;
+        }
+        if (rank == 0) {
+            if (lane == 0) a.n_accept[s] = acc;
+            if (lane < a.n_tok && lane != acc) a.tokens[s * a.n_tok + lane] = lane < acc ? x : -1;
         }
     }
     __syncthreads();
     const int32_t acc = s_accept;
-    const bool refused = acc < s_token;
-    __syncthreads();
-    const T *p = (const T *)a.p + (s * a.n_tok + acc) * a.p_stride;
-    const T *q = refused && a.q ? (const T *)a.q + (s * n_rows + acc) * a.q_stride : nullptr;
-    int64_t gone = refused && !a.q ? a.draft[s * n_rows + acc] : -1;
-    const int32_t part = (a.vocab + kParts - 1) / kParts;
-
+    const bool refused = acc < s_last;
+    Weights<T> w;
+    w.p = (const T *)a.p + (s * a.n_tok + acc) * a.p_stride;
+    w.q = refused && a.q ? (const T *)a.q + (s * n_rows + acc) * a.q_stride : nullptr;
+    w.gone = refused && !a.q ? a.draft[s * n_rows + acc] : -1;
+    constexpr int V = kVec<T>;
+    const int32_t lo = (int32_t)min((int64_t)(rank * kWarps + warp) * a.part, (int64_t)a.vocab);
+    const int32_t hi = min(lo + a.part, a.vocab);
     u128 total = 0;
+    uint64_t chunks[2], sum;
+    bool wide;
     int pass = 0;
-    for (; pass < 2; ++pass) {
-        const int64_t lo = (int64_t)(rank * kWarps + warp) * part;
-        const int64_t hi = lo + part < a.vocab ? lo + part : a.vocab;
-        uint64_t sum = 0;
-        for (int64_t i = lo + lane; i < hi; i += 32) sum += weight(p, q, i, gone);
-        for (int m = 16; m > 0; m >>= 1) sum += shfl_xor64(sum, m);
+    while (true) {
+        wide = (((uintptr_t)w.p | (uintptr_t)w.q) & 15) == 0;
+        if (w.q)
+            sum = wide ? w.template slice<V, true>(lo, hi, chunks) : w.template slice<1, true>(lo, hi, chunks);
+        else
+            sum = wide ? w.template slice<V, false>(lo, hi, chunks) : w.template slice<1, false>(lo, hi, chunks);
+        if (lane == 0) s_warp[warp] = sum;
         if (pass == 0) cluster_wait();  // every CTA of the cluster has started
-        if (lane < kCluster) st_cluster_u64(&sums[pass][rank * kWarps + warp], lane, sum);
+        __syncthreads();
+        if (threadIdx.x < a.cluster) {
+            u128 x = 0;
+            for (int i = 0; i < kWarps; ++i) x += s_warp[i];
+            st_cluster_u64(&s_cta[pass][rank][0], threadIdx.x, (uint64_t)x);
+            st_cluster_u64(&s_cta[pass][rank][1], threadIdx.x, (uint64_t)(x >> 64));
+        }
         cluster_arrive();
         cluster_wait();
         total = 0;
-        for (int i = 0; i < kParts; ++i) total += sums[pass][i];
-        if (total != 0 || (!q && gone < 0)) break;
-        q = nullptr;  // nothing is left of the target where the draft was: draw from the target itself
-        gone = -1;
+        for (int i = 0; i < a.cluster; ++i) total += ((u128)s_cta[pass][i][1] << 64) + s_cta[pass][i][0];
+        if (total != 0 || pass == 1 || (!w.q && w.gone < 0)) break;
+        w.q = nullptr;  // nothing is left of the target where the draft was: draw from the target itself
+        w.gone = -1;
+        pass = 1;
     }
-    if (rank != 0) return;  // every store into this CTA's shared memory came before the barrier
-    pass = min(pass, 1);
-    // the first position whose cumulative weight passes u times the total
-    if (threadIdx.x == 0) s_token = -1;
-    __syncthreads();
-    if (total != 0) {
-        const float u = fminf(fmaxf(a.u[s * a.n_tok + a.n_tok - 1], 0.f), 0x1.fffffep-1f);
-        u128 left = times_fraction(total, u);
-        int slice = 0;
-        for (; slice < kParts - 1; ++slice) {
-            const uint64_t x = sums[pass][slice];
-            if (left < x) break;
-            left -= x;
-        }
+    if (total == 0) {  // a row without a positive value
+        if (rank == 0 && threadIdx.x == 0) a.tokens[s * a.n_tok + acc] = -1;
+        return;
+    }
+    // whose slice does u times the total fall into?
+    u128 left = times_fraction(total, fminf(fmaxf(u_draw, 0.f), 0x1.fffffep-1f));
+    for (int i = 0; i < rank; ++i) left -= ((u128)s_cta[pass][i][1] << 64) + s_cta[pass][i][0];
+    const u128 mine = ((u128)s_cta[pass][rank][1] << 64) + s_cta[pass][rank][0];
+    if (left >= mine) return;  // another CTA's; wrapped round if it came before
+    for (int i = 0; i < warp; ++i) left -= s_warp[i];
+    if (left < sum) {
         uint64_t t = (uint64_t)left;
-        const int64_t lo = (int64_t)slice * part;
-        const int64_t hi = lo + part < a.vocab ? lo + part : a.vocab;
-        for (int64_t base = lo; base < hi; base += blockDim.x) {
-            const int64_t i = base + threadIdx.x;
-            const uint64_t x = i < hi ? weight(p, q, i, gone) : 0;
-            uint64_t upto = x;  // inclusive sums over the warp, then over the warps before it
+        const int32_t step = (w.q ? kUnroll<true> : kUnroll<false>) * 32 * (wide ? V : 1);
+        int32_t c = 0;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {  // the chunk, among 32 at a time
+            uint64_t upto = chunks[half];
             for (int off = 1; off < 32; off <<= 1) {
                 const uint64_t y = __shfl_up_sync(0xffffffffu, (unsigned long long)upto, off);
                 if (lane >= off) upto += y;
             }
-            if (lane == 31) s_warp[warp] = upto;
-            __syncthreads();
-            uint64_t before = 0, all = 0;
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) before += s_warp[w];
-                all += s_warp[w];
+            const unsigned mask = __ballot_sync(0xffffffffu, upto > t);
+            const int at = mask ? __ffs(mask) - 1 : 31;
+            t -= __shfl_sync(0xffffffffu, (unsigned long long)(mask ? upto - chunks[half] : upto), at);
+            if (mask) {
+                c = half * 32 + at;
+                break;
             }
-            upto += before;
-            if (upto > t && upto - x <= t) s_token = (int32_t)i;  // one thread at most
-            __syncthreads();
-            if (all > t) break;
-            t -= all;
+        }
+        if (lane == 0) {
+            s_from = lo + c * step;
+            s_end = min(lo + (c + 1) * step, hi);
+            s_left = t;
         }
     }
-    if (threadIdx.x == 0) a.n_accept[s] = acc;
-    if (threadIdx.x < a.n_tok)
-        a.tokens[s * a.n_tok + threadIdx.x] =
-            threadIdx.x < acc ? a.draft[s * n_rows + threadIdx.x] : threadIdx.x == acc ? s_token : -1;
+    __syncthreads();
+    // the token in the chunk (128 to 2048 positions): neighbours in a thread
+    const int32_t each = (s_end - s_from + 32 * kWarps - 1) / (32 * kWarps);  // at most 4
+    const int32_t i0 = s_from + threadIdx.x * each, end = min(i0 + each, s_end);
+    uint64_t x[4], here = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        x[k] = i0 + k < end ? w.at(i0 + k) : 0;
+        here += x[k];
+    }
+    uint64_t upto = here;  // inclusive sums over the warp, then over the warps before it
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint64_t y = __shfl_up_sync(0xffffffffu, (unsigned long long)upto, off);
+        if (lane >= off) upto += y;
+    }
+    if (lane == 31) s_warp[warp] = upto;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i)
+        if (i < warp) upto += s_warp[i];
+    const uint64_t t = s_left;
+    if (upto > t && upto - here <= t) {  // one thread
+        uint64_t rest = t - (upto - here);
+        int32_t at = i0;
+        bool open = true;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            open = open && rest >= x[k];
+            if (open) rest -= x[k], ++at;
+        }
+        a.tokens[s * a.n_tok + acc] = at;
+    }
 }
 
 }  // namespace
@@ -198,7 +424,7 @@ extern "C" int hswa_verify_draft(int dtype, const void *p, int64_t p_stride, con
     HSWA_NVTX("hswa_verify_draft");
     if (n_seqs < 0 || n_tok < 1 || n_tok > HSWA_DECODE_MAX_TOKENS || vocab < 1) return HSWA_ERR_INVALID_ARG;
     if (dtype != HSWA_DTYPE_F32 && dtype != HSWA_DTYPE_BF16) return HSWA_ERR_UNSUPPORTED;
-    if (vocab > HSWA_VERIFY_MAX_VOCAB || n_seqs > INT32_MAX / kCluster) return HSWA_ERR_UNSUPPORTED;
+    if (vocab > HSWA_VERIFY_MAX_VOCAB || n_seqs > INT32_MAX / kMaxCluster) return HSWA_ERR_UNSUPPORTED;
     if (n_seqs == 0) return HSWA_OK;
     const int64_t e = dtype == HSWA_DTYPE_F32 ? 4 : 2;
     if (!p || !u || !n_accept || !tokens || (n_tok > 1 && !d_draft) || p_stride < vocab ||
@@ -212,16 +438,29 @@ extern "C" int hswa_verify_draft(int dtype, const void *p, int64_t p_stride, con
     a.n_tok = n_tok, a.vocab = vocab;
     a.n_accept = n_accept, a.tokens = tokens;
     a.err = error_word();
+    // As many CTAs per sequence as fit the GPU at once (2 per SM), so that a
+    // few sequences spread over it and many keep to one CTA each; enough of
+    // them that a slice's sum of ones, 2^50 steps each, stays below 2^64 and
+    // a slice has at most 64 chunks.
+    const int sms = sm_count();
+    if (sms <= 0) return HSWA_ERR_CUDA;
+    const auto part_of = [&](int c) { return ((vocab + c * kWarps - 1) / (c * kWarps) + 7) / 8 * 8; };
+    a.cluster = 1;
+    while (a.cluster < kMaxCluster && (n_seqs * (int64_t)a.cluster * 2 <= 2 * sms || part_of(a.cluster) > 64 * kUnroll<true> * 32))
+        a.cluster *= 2;
+    a.part = part_of(a.cluster);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)n_seqs * kCluster);
+    cfg.gridDim = dim3((unsigned)n_seqs * a.cluster);
     cfg.blockDim = dim3(32 * kWarps);
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kCluster;
+    attr[0].val.clusterDim.x = a.cluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     set_last_kernel(e == 4 ? "verify_draft_f32" : "verify_draft_bf16");
     const cudaError_t rc = e == 4 ? cudaLaunchKernelEx(&cfg, verify_draft<float>, a)
                                   : cudaLaunchKernelEx(&cfg, verify_draft<__nv_bfloat16>, a);

@@ -514,9 +514,9 @@ int hswa_decode_multi(const hswa_pool *pool, const hswa_layer *layer, const void
  * q NULL: drafts taken greedily (their q is 1 at the draft and 0 elsewhere).
  * dtype: of p and q, HSWA_DTYPE_F32 or HSWA_DTYPE_BF16; rows p_stride /
  * q_stride (>= vocab) elements apart. For the draw, values are clamped to
- * [0, 1] (NaN: 0) and counted in steps of 2^-50, and sums are exact: the
- * token does not depend on the order of summation, only rows need not add
- * up to exactly 1. u outside [0, 1) counts as the nearest inside. A draft
+ * [0, 1] (NaN: 0) and rounded to whole steps of 2^-50 (fp32) or 2^-45
+ * (bf16), whose sums are exact: the token does not depend on the order of
+ * summation. Rows need not add up to exactly 1. u outside [0, 1) counts as the nearest inside. A draft
  * outside [0, vocab) is refused and d_n_draft outside its range clamped,
  * each setting HSWA_ERR_BOUNDS on the device. n_tok in [1,
  * HSWA_DECODE_MAX_TOKENS]; d_draft and q may be NULL for n_tok = 1. */

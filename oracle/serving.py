@@ -74,15 +74,15 @@ def evict_select(seq_len, weight, budget, page_size, sink_pages, recent_tokens):
     return out
 
 
-def steps(row):
-    """Probabilities as whole steps of 2^-50: clamped to [0, 1], NaN as 0."""
+def steps(row, bits):
+    """Probabilities as whole steps of 2^-bits: clamped to [0, 1], NaN as 0."""
     x = np.asarray(row, np.float64)
-    return np.rint(np.clip(np.where(np.isnan(x), 0, x), 0, 1) * 2.0 ** 50).astype(np.int64)
+    return np.rint(np.clip(np.where(np.isnan(x), 0, x), 0, 1) * 2.0 ** bits).astype(np.int64)
 
 
-def verify(p, q, draft, n_draft, u):
+def verify(p, q, draft, n_draft, u, bits=50):
     """p [S][n][V], q [S][n - 1][V] or None, draft [S][n - 1], u [S][n]:
-    (accepted [S], tokens [S][n])."""
+    (accepted [S], tokens [S][n]). bits: 50 for fp32 values, 45 for bf16."""
     S, n, V = p.shape
     accepted, tokens = np.zeros(S, np.int32), np.full((S, n), -1, np.int32)
     for s in range(S):
@@ -96,7 +96,7 @@ def verify(p, q, draft, n_draft, u):
             if not all(np.isfinite((px, qx, ux))) or not Fraction(ux) * Fraction(qx) < Fraction(px):
                 break
             a += 1
-        target = steps(p[s, a])
+        target = steps(p[s, a], bits)
         weight = target
         if a < last:
             if q is None:
@@ -104,7 +104,7 @@ def verify(p, q, draft, n_draft, u):
                 if 0 <= draft[s, a] < V:
                     weight[int(draft[s, a])] = 0
             else:
-                weight = np.maximum(target - steps(q[s, a]), 0)
+                weight = np.maximum(target - steps(q[s, a], bits), 0)
             if not weight.any():
                 weight = target
         accepted[s] = a
