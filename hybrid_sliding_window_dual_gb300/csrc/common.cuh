@@ -152,6 +152,22 @@ __device__ __forceinline__ void fence_proxy_async_global() {
     asm volatile("fence.proxy.async.global;" ::: "memory");
 }
 
+// ------------------------------------------------------------- clusters
+// Barrier of all threads of a cluster; writes before it are seen after it,
+// in every CTA's shared memory.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// Address of a shared variable of this CTA in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(const void *mine, int rank) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(mine)), "r"(rank));
+    return at;
+}
+
+__device__ __forceinline__ void st_cluster_u64(const uint64_t *mine, int rank, uint64_t x) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_addr(mine, rank)), "l"(x) : "memory");
+}
+
 // ----------------------------------------------------------- bulk copies
 // 1-D bulk copy global -> shared, completing on an mbarrier (16-B aligned
 // addresses, size a multiple of 16).

@@ -30,6 +30,7 @@
 // (sequence, query head) with CUDA-core dot products.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -60,9 +61,22 @@ struct StageDesc {
 
 // kTok query tokens per sequence share every streamed page (one consumer
 // warp each): 1 for plain decode, 2 or 3 for multi-token decode.
-template <int kTok_>
+// What the consumer warps leave of a page for its log-sum (decode with page
+// weights): each thread's sums of 2^(score - max) for its two heads, and the
+// maxima by head. The producer warp, which has time to spare, reads them when
+// it comes back to the stage and adds them up once it has refilled it.
+template <int kWarps, int kStages>
+struct PageSums {
+    static constexpr int kFrom = kWarps;
+    float2 sum[kStages][kWarps][32];
+    float max[kStages][kWarps][kG];
+};
+struct NoPageSums {};
+
+template <int kTok_, bool kWeights_ = false>
 struct DecodeSmemT {
     static constexpr int kTok = kTok_;
+    static constexpr bool kWeights = kWeights_;
     static constexpr int kStages = kTok_ <= 2 ? ::hswa::kStages : 2;
     static constexpr bool kTcQ = false;  // q rows travel with the first page of a piece
     uint8_t k[kStages][kPageHeadBytes];
@@ -72,10 +86,11 @@ struct DecodeSmemT {
     uint64_t full[kStages];
     uint64_t empty[kStages];
     int32_t abort;
+    std::conditional_t<kWeights_, PageSums<1, kStages>, NoPageSums> sums;
 };
 
-template <int kTok>
-constexpr size_t decode_smem_bytes() { return sizeof(DecodeSmemT<kTok>) + 1024; }  // + alignment slack
+template <int kTok, bool kWeights = false>
+constexpr size_t decode_smem_bytes() { return sizeof(DecodeSmemT<kTok, kWeights>) + 1024; }  // + alignment slack
 
 // FP8 pools: a stage holds one page of one kv head as E4M3 codes, K as
 // [64 keys][128 B] (128-byte swizzle) and V transposed as [128 d][64 B]
@@ -86,10 +101,12 @@ constexpr uint32_t kScaleBytes = kP * 4;
 
 constexpr int kConsumers8 = 4;  // FP8 consumer warps, one 16-key group of a page each
 
-template <int kTok>
+template <int kTok, bool kWeights_ = false>
 struct DecodeSmem8T {
     static constexpr int kStages = 3;
     static constexpr bool kTcQ = false;
+    static constexpr bool kWeights = kWeights_;
+
     uint8_t k[kStages][kK8Bytes];
     uint8_t v[kStages][kV8Bytes];
     uint8_t q[kStages][kTok * kQBytes];
@@ -104,10 +121,11 @@ struct DecodeSmem8T {
     uint64_t empty[kStages];
     uint64_t merge;
     int32_t abort;
+    std::conditional_t<kWeights_, PageSums<kConsumers8, kStages>, NoPageSums> sums;
 };
 
-template <int kTok>
-constexpr size_t decode_smem8_bytes() { return sizeof(DecodeSmem8T<kTok>) + 1024; }
+template <int kTok, bool kWeights = false>
+constexpr size_t decode_smem8_bytes() { return sizeof(DecodeSmem8T<kTok, kWeights>) + 1024; }
 
 struct Partial {
     float m[kG];
@@ -134,9 +152,9 @@ struct DecodeArgs {
     float scale_log2;
     int *err;
     // decode with page weights (null otherwise): log2 of the sum of 2^score
-    // over a page, [n_seqs][Hkv][bt_stride][parts][8 heads], and over all of
-    // a sequence's keys, [n_seqs][Hq]
-    float *page_lse, *seq_lse;
+    // over a page, [n_seqs][Hkv][bt_stride][8 heads]; over a whole segment
+    // that one CTA covered, [n_seqs][Hq]; over a piece of one, [n_ctas][2][8]
+    float *page_lse, *seq_lse, *piece_lse;
 };
 
 // Row of q / o holding query token w of sequence s.
@@ -229,6 +247,40 @@ __device__ __forceinline__ uint32_t swz(int row, int d) {
     return (uint32_t)((d >> 6) * kBoxBytes + row * 128 + ((((d & 63) >> 3) ^ (row & 7)) << 4));
 }
 
+// Producer side. Lanes 8 p + h read p's share of the page in a stage: the sum
+// of head h over a quarter of the row groups (one consumer warp) or over one
+// warp's 16 keys (four), and the maximum that it is relative to. (The two
+// lanes of a pair of heads read half of the row groups each.)
+template <class Smem>
+__device__ __forceinline__ float2 read_page_sums(const Smem &sm, int stage) {
+    const int lane = threadIdx.x & 31, part = lane >> 3, pair = (lane >> 1) & 3, half = lane & 1;
+    constexpr bool kOne = decltype(sm.sums)::kFrom == 1;
+    static_assert(kOne || decltype(sm.sums)::kFrom == 4, "a warp per 8 lanes");
+    constexpr int kRows = kOne ? 1 : 4;
+    const float2 *x = &sm.sums.sum[stage][kOne ? 0 : part][((kOne ? 2 * part : 0) + half * kRows) * 4 + pair];
+    float2 s = x[0];
+#pragma unroll
+    for (int g = 1; g < kRows; ++g) s.x += x[4 * g].x, s.y += x[4 * g].y;
+    const float b = sm.sums.max[stage][kOne ? 0 : part][lane & 7];
+    const float other = __shfl_xor_sync(0xffffffffu, half ? s.x : s.y, 1);
+    return make_float2(b, (half ? s.y : s.x) + other);
+}
+
+// The log2 of the sum of 2^score over the page, of head (lane & 7); -inf if
+// nothing was seen.
+template <class Smem>
+__device__ __forceinline__ float page_log_sum(float2 x) {
+    float b = x.x, s = x.y;
+    if constexpr (decltype(Smem::sums)::kFrom > 1) {
+        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 8));
+        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 16));
+        s *= s == 0.f ? 0.f : fast_exp2(x.x - b);
+    }
+    s += __shfl_xor_sync(0xffffffffu, s, 8);
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+    return b + __log2f(s);  // __log2f(0) is -inf
+}
+
 // Streams the pages of units [u0, u1) into the stage ring. With
 // Smem::kTcQ the query tile of each piece goes by tensor map tq into the
 // q buffer of Smem::kQBufs slots (released by the MMA thread through q_empty) instead of
@@ -248,6 +300,10 @@ __device__ void decode_producer(Smem &sm, const CUtensorMap *tk, const CUtensorM
     uint32_t issued_parity[kStages];
     bool issued[kStages];
     for (int i = 0; i < kStages; ++i) issued[i] = false, issued_parity[i] = 0;
+    // kWeights: pages so far, where the log-sums (of this lane's head) of the
+    // last ones go, and of the next one
+    int32_t streamed = 0;
+    float *lse_at[kStages] = {}, *lse_next = nullptr;
     int32_t pc = 0;  // pieces started (kTcQ: q slot pc & 1)
     bool q_issued[2] = {false, false};
     uint32_t q_parity[2] = {0, 0};
@@ -281,6 +337,8 @@ __device__ void decode_producer(Smem &sm, const CUtensorMap *tk, const CUtensorM
         const bool direct = (u == seg_start) && (piece_end == seg_end);
         const int32_t slot = (u == u0) ? 0 : 1;
         const int32_t *btrow = a.bt + (int64_t)s * a.bt_stride;
+        if constexpr (Smem::kWeights)
+            lse_next = a.page_lse + (((int64_t)s * a.hkv + g) * a.bt_stride + pf + pi) * kG + (lane & 7);
         for (int32_t j = 0; j < n; ++j) {
             const int32_t p = pi + j;  // page index in the sequence's key range
             if (s != cached_s || (p >> 5) != cached_batch) {
@@ -310,6 +368,18 @@ __device__ void decode_producer(Smem &sm, const CUtensorMap *tk, const CUtensorM
                 __syncwarp();
             }
             bool ok = true;
+            float2 sums = make_float2(0.f, 0.f);
+            if constexpr (Smem::kWeights) {
+                // the page that was in this stage: its sums, before the stage
+                // is filled again (a new page's consumers write there)
+                if (streamed >= kStages) {
+                    if (lane == 0) ok = mbar_wait(&sm.empty[stage], phase ^ 1, a.err) && !*(volatile int32_t *)&sm.abort;
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    __syncwarp();  // the other lanes' reads stay behind lane 0's wait
+                    sums = read_page_sums(sm, stage);
+                    __syncwarp();  // read before lane 0 fills the stage again
+                }
+            }
             if (lane == 0) {
                 if constexpr (Smem::kTcQ) {
                     if (j == 0) {
@@ -388,9 +458,35 @@ __device__ void decode_producer(Smem &sm, const CUtensorMap *tk, const CUtensorM
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) goto drain;
+            if constexpr (Smem::kWeights) {
+                if (streamed >= kStages) {
+                    const float lse = page_log_sum<Smem>(sums);
+                    if (lane < 8) *lse_at[0] = lse;
+                }
+                ++streamed;
+#pragma unroll
+                for (int i = 0; i + 1 < kStages; ++i) lse_at[i] = lse_at[i + 1];
+                lse_at[kStages - 1] = lse_next;
+                lse_next += kG;
+            }
             if (++stage == kStages) stage = 0, phase ^= 1;
         }
         u = piece_end;
+    }
+    if constexpr (Smem::kWeights) {
+        // the last pages, oldest first
+#pragma unroll
+        for (int k = 0; k < kStages; ++k) {
+            const int32_t i = streamed - kStages + k;  // the k-th of the last pages
+            if (i < 0) continue;
+            bool ok = true;
+            if (lane == 0)
+                ok = mbar_wait(&sm.empty[i % kStages], i / kStages & 1, a.err) && !*(volatile int32_t *)&sm.abort;
+            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+            __syncwarp();  // the other lanes' reads stay behind lane 0's wait
+            const float lse = page_log_sum<Smem>(read_page_sums(sm, i % kStages));
+            if (lane < 8) *lse_at[k] = lse;
+        }
     }
 drain:
     // never leave the CTA with copies still landing in its shared memory
@@ -403,29 +499,32 @@ drain:
     }
 }
 
-// Write a page's log-sum of 8 heads (decode with page weights) from the
-// warp's sums of 2^(score - b) in the S fragment layout: thread (g, q) holds
-// its rows' sums of heads 2q (w0) and 2q + 1 (w1). Nothing seen: -inf.
-__device__ __forceinline__ void store_page_lse(const DecodeArgs &a, const StageDesc &d, int part, int parts, float b0,
-                                               float b1, float w0, float w1) {
+// Consumer side of a page's log-sum: this thread's sums w0, w1 of
+// 2^(score - b) in the S fragment layout (thread (g, q): heads 2q, 2q + 1).
+// Ordered before the producer's read by the arrival on the stage's empty
+// barrier.
+template <class Smem>
+__device__ __forceinline__ void leave_page_sums(Smem &sm, int stage, int warp, float b0, float b1, float w0, float w1) {
     const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int off = 4; off < 32; off <<= 1) {
-        w0 += __shfl_xor_sync(0xffffffffu, w0, off);
-        w1 += __shfl_xor_sync(0xffffffffu, w1, off);
-    }
-    if (lane < 4) {
-        const int64_t at = (((int64_t)d.seq * a.hkv + d.kvh) * a.bt_stride + d.key0 / kP) * parts + part;
-        reinterpret_cast<float2 *>(a.page_lse)[at * 4 + lane] =
-            make_float2(w0 == 0.f ? -INFINITY : b0 + log2f(w0), w1 == 0.f ? -INFINITY : b1 + log2f(w1));
-    }
+    sm.sums.sum[stage][warp][lane] = make_float2(w0, w1);
+    if (lane < 4) *reinterpret_cast<float2 *>(&sm.sums.max[stage][warp][2 * lane]) = make_float2(b0, b1);
+}
+
+// The log-sum of a piece at its end, from the thread of heads 2q, 2q + 1 whose
+// maxima are m0, m1 and sums l0, l1.
+__device__ __forceinline__ void store_piece_lse(const DecodeArgs &a, const StageDesc &d, float m0, float m1, float l0,
+                                                float l1) {
+    float *to = d.flags & kDirect ? a.seq_lse + (int64_t)d.seq * a.hq + d.kvh * kG
+                                  : a.piece_lse + ((int64_t)blockIdx.x * 2 + d.slot) * kG;
+    reinterpret_cast<float2 *>(to)[threadIdx.x & 3] =
+        make_float2(l0 == 0.f ? -INFINITY : m0 + log2f(l0), l1 == 0.f ? -INFINITY : m1 + log2f(l1));
 }
 
 // One consumer warp: query token w (8 query heads) of the stage's (sequence,
 // kv head).
-// kWeights: also write each page's log-sum per head (one token).
+// kWeights: also leave each page's sums for the producer (one token).
 template <int kTok, bool kWeights>
-__device__ void decode_consumer(DecodeSmemT<kTok> &sm, const DecodeArgs &a, int64_t u0, int64_t u1, int w) {
+__device__ void decode_consumer(DecodeSmemT<kTok, kWeights> &sm, const DecodeArgs &a, int64_t u0, int64_t u1, int w) {
     constexpr int kStages = DecodeSmemT<kTok>::kStages;
     const int lane = threadIdx.x & 31;
     const int gr = lane >> 2;  // fragment row group
@@ -433,6 +532,7 @@ __device__ void decode_consumer(DecodeSmemT<kTok> &sm, const DecodeArgs &a, int6
     uint32_t qf[8][2];
     float oacc[8][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float lw0 = 0.f, lw1 = 0.f;  // kWeights: the sums of the weights before they are rounded
     int stage = 0;
     uint32_t phase = 0;
     const uint32_t kbase = smem_u32(sm.k[0]), vbase = smem_u32(sm.v[0]);
@@ -456,6 +556,7 @@ __device__ void decode_consumer(DecodeSmemT<kTok> &sm, const DecodeArgs &a, int6
             for (int i = 0; i < 8; ++i) oacc[i][0] = oacc[i][1] = oacc[i][2] = oacc[i][3] = 0.f;
             m0 = m1 = -INFINITY;
             l0 = l1 = 0.f;
+            lw0 = lw1 = 0.f;
         }
         if (!(d.flags & kSkip)) {
             const uint32_t kb = kbase + stage * kPageHeadBytes, vb = vbase + stage * kPageHeadBytes;
@@ -535,7 +636,11 @@ __device__ void decode_consumer(DecodeSmemT<kTok> &sm, const DecodeArgs &a, int6
             }
             l0 = l0 * al0 + ps0;
             l1 = l1 * al1 + ps1;
-            if constexpr (kWeights) store_page_lse(a, d, 0, 1, b0, b1, w0, w1);
+            if constexpr (kWeights) {
+                lw0 = lw0 * al0 + w0;
+                lw1 = lw1 * al1 + w1;
+                leave_page_sums(sm, stage, 0, b0, b1, w0, w1);
+            }
 #pragma unroll
             for (int dt = 0; dt < 8; ++dt) {
                 oacc[dt][0] *= al0;
@@ -556,7 +661,7 @@ __device__ void decode_consumer(DecodeSmemT<kTok> &sm, const DecodeArgs &a, int6
                 }
             }
         } else if constexpr (kWeights) {
-            store_page_lse(a, d, 0, 1, 0.f, 0.f, 0.f, 0.f);
+            leave_page_sums(sm, stage, 0, 0.f, 0.f, 0.f, 0.f);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.empty[stage]);
@@ -569,6 +674,14 @@ __device__ void decode_consumer(DecodeSmemT<kTok> &sm, const DecodeArgs &a, int6
                 t1 += __shfl_xor_sync(0xffffffffu, t1, off);
             }
             const int h0 = 2 * qd, h1 = 2 * qd + 1;
+            if constexpr (kWeights) {
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) {
+                    lw0 += __shfl_xor_sync(0xffffffffu, lw0, off);
+                    lw1 += __shfl_xor_sync(0xffffffffu, lw1, off);
+                }
+                if (gr == 0) store_piece_lse(a, d, m0, m1, lw0, lw1);
+            }
             if (d.flags & kDirect) {
                 const float i0 = t0 > 0.f ? 1.f / t0 : 0.f, i1 = t1 > 0.f ? 1.f / t1 : 0.f;
                 __nv_bfloat16 *o0 = a.o + (q_row(a, d.seq, w) * a.hq + (int64_t)d.kvh * kG + h0) * kD;
@@ -607,7 +720,7 @@ template <int kTok, bool kWeights>
 __global__ void __launch_bounds__(32 * (kTok + 1)) decode_mma_bf16_d128(const __grid_constant__ CUtensorMap tk,
                                                                       const __grid_constant__ CUtensorMap tv,
                                                                       DecodeArgs a) {
-    using Smem = DecodeSmemT<kTok>;
+    using Smem = DecodeSmemT<kTok, kWeights>;
     extern __shared__ uint8_t raw[];
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     if (threadIdx.x == 0) {
@@ -697,9 +810,10 @@ __device__ __forceinline__ bool merge_sync(Smem &sm, uint32_t &phase, int *err) 
 // transpose. Every converted K and V fragment feeds the MMAs of all kTok
 // tokens. At the end of a piece warps 1-3 hand their (max, sum, o) to warp 0
 // through shared memory, which merges and writes.
-// kWeights: also write the log-sum per head of the warp's 16 keys of a page.
+// kWeights: also leave the sums of the warp's 16 keys of a page for the
+// producer.
 template <int kTok, bool kWeights>
-__device__ void decode_consumer_fp8(DecodeSmem8T<kTok> &sm, const DecodeArgs &a, int64_t u0, int64_t u1) {
+__device__ void decode_consumer_fp8(DecodeSmem8T<kTok, kWeights> &sm, const DecodeArgs &a, int64_t u0, int64_t u1) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int gr = lane >> 2, qd = lane & 3;
     constexpr int kStages = DecodeSmem8T<kTok>::kStages;
@@ -804,7 +918,7 @@ __device__ void decode_consumer_fp8(DecodeSmem8T<kTok> &sm, const DecodeArgs &a,
                 const float p2 = fast_exp2(sacc[j][2] - b0), p3 = fast_exp2(sacc[j][3] - b1);
                 l0[j] = l0[j] * al0 + 256.f * (p0 + p2);
                 l1[j] = l1[j] * al1 + 256.f * (p1 + p3);
-                if constexpr (kWeights) store_page_lse(a, d, w, kConsumers8, b0, b1, p0 + p2, p1 + p3);
+                if constexpr (kWeights) leave_page_sums(sm, stage, w, b0, b1, p0 + p2, p1 + p3);
                 pb0[j] = movmatrix_t(pack_f16(p0 * w0, p1 * w0));
                 pb1[j] = movmatrix_t(pack_f16(p2 * w1, p3 * w1));
                 if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {  // a head's max moved
@@ -832,7 +946,7 @@ __device__ void decode_consumer_fp8(DecodeSmem8T<kTok> &sm, const DecodeArgs &a,
                 for (int j = 0; j < kTok; ++j) mma_f16_16816(oacc[j][2 * dp + 1], a0, a1, a2, a3, pb0[j], pb1[j]);
             }
         } else if constexpr (kWeights) {
-            store_page_lse(a, d, w, kConsumers8, 0.f, 0.f, 0.f, 0.f);
+            leave_page_sums(sm, stage, w, 0.f, 0.f, 0.f, 0.f);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.empty[stage]);
@@ -901,6 +1015,8 @@ __device__ void decode_consumer_fp8(DecodeSmem8T<kTok> &sm, const DecodeArgs &a,
                             acc[dt][3] += f1 * sm.mo[i][j][h1][dt * 16 + gr + 8];
                         }
                     }
+                    if constexpr (kWeights)  // the sums carry 2^8
+                        if (gr == 0) store_piece_lse(a, d, M0 - 8.f, M1 - 8.f, L0, L1);
                     if (d.flags & kDirect) {
                         const float i0 = L0 > 0.f ? 1.f / L0 : 0.f, i1 = L1 > 0.f ? 1.f / L1 : 0.f;
                         __nv_bfloat16 *o0 = a.o + (q_row(a, d.seq, j) * a.hq + (int64_t)d.kvh * kG + h0) * kD;
@@ -944,7 +1060,7 @@ template <int kTok, bool kWeights>
 __global__ void __launch_bounds__(32 * (kConsumers8 + 1)) decode_mma_fp8_d128(const __grid_constant__ CUtensorMap tk,
                                                                            const __grid_constant__ CUtensorMap tv,
                                                                            DecodeArgs a) {
-    using Smem = DecodeSmem8T<kTok>;
+    using Smem = DecodeSmem8T<kTok, kWeights>;
     extern __shared__ uint8_t raw[];
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     if (threadIdx.x == 0) {
@@ -1014,6 +1130,7 @@ struct DecodeTcSmem {
     static constexpr int kSP = kStages;  // S / P buffers
     static constexpr int kQBufs = 2;
     static constexpr bool kTcQ = true;
+    static constexpr bool kWeights = false;
     static constexpr bool kQTmem = false;  // QK reads q from shared memory
     static constexpr int kThreads = 224;
     static constexpr uint32_t kQHalfBytes = 128 * 128;  // 128 rows x 64 columns of 16-bit values
@@ -1051,6 +1168,7 @@ struct DecodeTc8Smem {
     static constexpr int kSP = kConv;
     static constexpr int kQBufs = 1;
     static constexpr bool kTcQ = true;
+    static constexpr bool kWeights = false;
     static constexpr bool kQTmem = true;  // with copies (R > 1) QK reads q from TMEM column kTmemQ
     static constexpr int kConvThreads = 128;  // converter warps 7 ..
     static constexpr int kThreads = 224 + kConvThreads;
@@ -1639,60 +1757,73 @@ __global__ void __launch_bounds__(Smem::kThreads, 1)
     if (warp == 5) tmem_free<kTcCols>(sm.tmem_base);
 }
 
-// Merge the partial records of segments split between CTAs; write zeros
-// for sequences without keys. kParts > 0 (decode with page weights): also
-// the log-sum over a sequence's keys, from its pages' (kParts each).
-template <int kParts>
-__global__ void __launch_bounds__(256) decode_combine(DecodeArgs a, int32_t n_ctas) {
-    const int32_t s = blockIdx.y / a.n_tok, w = blockIdx.y % a.n_tok, g = blockIdx.x;
-    pdl_wait();
-    pdl_launch_dependents();
+// Merge the partial records of a segment split between CTAs (sequence s, query
+// token w, kv head g; 256 threads, a warp per head); write zeros for a
+// sequence without keys. A warp's lanes look at 32 records' maxima and sums
+// at once, then all take the records in order, 4 in flight. (Three short
+// sequences are cut into up to 20 pieces a head: a loop over the records that
+// found each with 64-bit divisions made their decode step 27 us, this 12.6.)
+__device__ void merge_segment(const DecodeArgs &a, int32_t n_ctas, int32_t s, int32_t w, int32_t g) {
     const int64_t U = a.sdesc[a.n_seqs].x, N = n_ctas;
     const int4 d = a.sdesc[s];
     const int32_t units = d.w;
-    const int h = threadIdx.x >> 5, d0 = (threadIdx.x & 31) * 4;
+    const int lane = threadIdx.x & 31, h = threadIdx.x >> 5, d0 = lane * 4;
     __nv_bfloat16 *out = a.o + (q_row(a, s, w) * a.hq + (int64_t)g * kG + h) * kD + d0;
     if (units == 0) {
         for (int i = 0; i < 4; ++i) out[i] = __float2bfloat16_rn(0.f);
-        if (kParts > 0 && d0 == 0) a.seq_lse[(int64_t)s * a.hq + g * kG + h] = -INFINITY;
         return;
     }
     const int32_t npg = units / a.hkv;
-    if constexpr (kParts > 0) {
-        const float *lse = a.page_lse + ((int64_t)s * a.hkv + g) * a.bt_stride * kParts * kG + h;
-        float m = -INFINITY, l = 0.f;
-        for (int32_t i = threadIdx.x & 31; i < npg * kParts; i += 32) {
-            const float x = lse[(int64_t)i * kG];
-            const float n = fmaxf(m, x);
-            if (n > -INFINITY) l = l * exp2f(m - n) + exp2f(x - n);
-            m = n;
-        }
-        float M = m;
-        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-        if (M > -INFINITY) l *= exp2f(m - M);
-        for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-        if (d0 == 0) a.seq_lse[(int64_t)s * a.hq + g * kG + h] = M > -INFINITY ? M + log2f(l) : -INFINITY;
-    }
     const int64_t lo = d.x + (int64_t)g * npg, hi = lo + npg;  // [lo, hi)
     const int64_t c_lo = cta_of(lo, U, N), c_hi = cta_of(hi - 1, U, N);
     if (c_lo == c_hi) return;
+    const int32_t n = (int32_t)(c_hi - c_lo + 1);
+    const int first_slot = cta_start(c_lo, U, N) < lo ? 1 : 0;
+    // the record of CTA c_lo + i, if that CTA had any units (it has when
+    // there are at least as many units as CTAs)
+    const auto record = [&](int32_t i) {
+        return a.part + ((c_lo + i) * 2 + (i == 0 ? first_slot : 0)) * a.n_tok + w;
+    };
+    const auto there = [&](int32_t i) {
+        return i < n && (U >= N || cta_start(c_lo + i, U, N) != cta_start(c_lo + i + 1, U, N));
+    };
     float M = -INFINITY;
-    for (int64_t c = c_lo; c <= c_hi; ++c) {
-        if (cta_start(c, U, N) == cta_start(c + 1, U, N)) continue;
-        const int slot = (c == c_lo && cta_start(c, U, N) < lo) ? 1 : 0;
-        M = fmaxf(M, a.part[(c * 2 + slot) * a.n_tok + w].m[h]);
-    }
+    for (int32_t i = lane; i < n; i += 32)
+        if (there(i)) M = fmaxf(M, record(i)->m[h]);
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int64_t c = c_lo; c <= c_hi; ++c) {
-        if (cta_start(c, U, N) == cta_start(c + 1, U, N)) continue;
-        const int slot = (c == c_lo && cta_start(c, U, N) < lo) ? 1 : 0;
-        const Partial &p = a.part[(c * 2 + slot) * a.n_tok + w];
-        const float wt = p.m[h] == -INFINITY ? 0.f : fast_exp2(p.m[h] - M);
-        L += wt * p.l[h];
-        for (int i = 0; i < 4; ++i) acc[i] += wt * p.o[h][d0 + i];
+    for (int32_t i0 = 0; i0 < n; i0 += 32) {
+        const bool mine = there(i0 + lane);
+        const float m = mine ? record(i0 + lane)->m[h] : -INFINITY, l = mine ? record(i0 + lane)->l[h] : 0.f;
+        const float wt = m == -INFINITY ? 0.f : fast_exp2(m - M);
+        const unsigned used = __ballot_sync(0xffffffffu, mine);
+        const int32_t k = min(32, n - i0);
+        for (int32_t j = 0; j < k; j += 4) {
+            float4 o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (used >> (j + e) & 1) o[e] = *reinterpret_cast<const float4 *>(&record(i0 + j + e)->o[h][d0]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float we = __shfl_sync(0xffffffffu, wt, (j + e) & 31), le = __shfl_sync(0xffffffffu, l, (j + e) & 31);
+                if (used >> (j + e) & 1) {
+                    L += we * le;
+                    acc[0] += we * o[e].x;
+                    acc[1] += we * o[e].y;
+                    acc[2] += we * o[e].z;
+                    acc[3] += we * o[e].w;
+                }
+            }
+        }
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
     for (int i = 0; i < 4; ++i) out[i] = __float2bfloat16_rn(acc[i] * inv);
+}
+
+__global__ void __launch_bounds__(256, 4) decode_combine(DecodeArgs a, int32_t n_ctas) {
+    pdl_wait();
+    pdl_launch_dependents();
+    merge_segment(a, n_ctas, blockIdx.y / a.n_tok, blockIdx.y % a.n_tok, blockIdx.x);
 }
 
 // ----------------------------------------------------------- generic path
@@ -1717,17 +1848,110 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return
 // sequence; this pass turns them into weights and adds them to the caller's.
 // A row's entries past the sequence's last page become 0, so that pages
 // added later start from nothing.
+//
+// Bound by memory, as the decode step is: 64 sequences of 1K to 32K, bf16 (64
+// / 8 heads): 652 us against 636 without the weights and 653 for the bytes at
+// the copy rate; 49 sequences, FP8: 282 against 266 and 257; three short ones
+// 13.0 against 12.6. What the weights cost the FP8 kernel, whose issue slots
+// are nearly full, is instructions: with the sums added up in the consumer
+// warps it was 358, and each page's 64-bit address and exact logarithm in the
+// producer made 295.
 struct WeightArgs {
-    const float *page_lse;  // [n_seqs][Hkv][max_pages][parts][G], log2
+    const float *page_lse;  // [n_seqs][Hkv][max_pages][G], log2
     const float *seq_lse;   // [n_seqs][Hkv][G], log2
     const int32_t *seq_len;
     const float *w_in;
     float *w_out;
     float decay;
-    int32_t hkv, group, parts, page, max_pages;
+    int32_t hkv, group, page, max_pages;
 };
 
-// 8 threads a page, each a part of the kv heads.
+// Weight of a head on a page; nothing if the sequence saw nothing.
+__device__ __forceinline__ float head_weight(float page, float all) { return all > -INFINITY ? exp2f(page - all) : 0.f; }
+
+__device__ __forceinline__ void store_weight(const WeightArgs &a, int64_t at, float w) {
+    a.w_out[at] = a.w_in && a.decay != 0.f ? fmaf(a.decay, a.w_in[at], w) : w;
+}
+
+// The end of a decode step with page weights on the 8-heads kernels, as one
+// launch: the first n_merge blocks merge split segments (merge_segment), the
+// others take kWeightPages pages of a sequence each. Such a block first joins
+// the log-sums of the pieces that each head's keys were split into, 4 lanes a
+// head (there are as many as CTAs shared the segment: 1 to 3 in a batch, 40
+// for one long sequence), then weighs its pages, 8 threads a page.
+//
+// (As a cluster of 8 blocks per sequence that added up the pages' log-sums
+// themselves and exchanged them, this took 15 us on 64 sequences of 1K to
+// 32K; as one launch after the merge, 8 and 5; now 10. More than 80 registers
+// or 64 pages a block leave it two waves.)
+constexpr int kWeightPages = 64;
+constexpr int kMaxWeightHeads = 2048;  // query heads whose log-sums fit shared memory
+
+__global__ void __launch_bounds__(256, 4) decode_finish_weights(DecodeArgs a, int32_t n_ctas, int32_t n_merge,
+                                                             int32_t chunks, const __grid_constant__ WeightArgs wa) {
+    extern __shared__ float4 smem_f4[];
+    float *all = reinterpret_cast<float *>(smem_f4);  // [Hq]
+    pdl_wait();
+    pdl_launch_dependents();
+    if ((int32_t)blockIdx.x < n_merge) {
+        merge_segment(a, n_ctas, blockIdx.x / a.hkv, 0, blockIdx.x % a.hkv);
+        return;
+    }
+    const int32_t s = (blockIdx.x - n_merge) / chunks, first = (blockIdx.x - n_merge) % chunks * kWeightPages;
+    const int32_t end = min(first + kWeightPages, wa.max_pages);
+    const int4 d = a.sdesc[s];
+    const int32_t npg = d.w / a.hkv;
+    const int64_t row = (int64_t)s * wa.max_pages;
+    const int sub = threadIdx.x & 7;
+    if (first < npg) {
+        const int64_t U = a.sdesc[a.n_seqs].x, N = n_ctas;
+        const int part = threadIdx.x & 3;
+        for (int32_t h0 = 0; h0 < a.hq; h0 += 64) {  // whole warps: 8 query heads to a kv head
+            const int32_t h = h0 + (threadIdx.x >> 2);
+            float top = -INFINITY, sum = 0.f;
+            if (h < a.hq) {
+                const int64_t lo = d.x + (int64_t)(h / kG) * npg, c_lo = cta_of(lo, U, N), c_hi = cta_of(lo + npg - 1, U, N);
+                if (c_lo == c_hi) {
+                    if (part == 0) top = a.seq_lse[(int64_t)s * a.hq + h], sum = 1.f;
+                } else {
+                    for (int64_t c = c_lo + part; c <= c_hi; c += 4) {
+                        if (U < N && cta_start(c, U, N) == cta_start(c + 1, U, N)) continue;  // no units
+                        const int slot = c == c_lo && cta_start(c, U, N) < lo ? 1 : 0;
+                        const float x = a.piece_lse[(c * 2 + slot) * kG + h % kG], n = fmaxf(top, x);
+                        if (n > -INFINITY) sum = sum * exp2f(top - n) + exp2f(x - n), top = n;
+                    }
+                }
+            }
+            float m = top;
+            for (int off = 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+            sum = top > -INFINITY ? sum * exp2f(top - m) : 0.f;
+            for (int off = 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            if (part == 0 && h < a.hq) all[h] = m > -INFINITY ? m + log2f(sum) : -INFINITY;
+        }
+        __syncthreads();
+        const float4 *lse = reinterpret_cast<const float4 *>(wa.page_lse) + (int64_t)s * a.hkv * wa.max_pages * 2;
+#pragma unroll
+        for (int k = 0; k < kWeightPages / 32; ++k) {
+            const int32_t p = first + k * 32 + (threadIdx.x >> 3);
+            float w = 0.f;
+            if (p < npg)
+                for (int32_t g = sub; g < a.hkv; g += 8) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float4 y = lse[((int64_t)g * wa.max_pages + p) * 2 + i];
+                        const float4 x = smem_f4[g * 2 + i];
+                        w += head_weight(y.x, x.x) + head_weight(y.y, x.y) + head_weight(y.z, x.z) + head_weight(y.w, x.w);
+                    }
+                }
+            for (int off = 4; off > 0; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
+            if (sub == 0 && p < npg) store_weight(wa, row + p, w);
+        }
+    }
+    for (int32_t p = max(first, npg) + threadIdx.x; p < end; p += blockDim.x) wa.w_out[row + p] = 0.f;
+}
+
+// Weights from both log-sums, any number of query heads to a kv head; 8
+// threads a page, each a part of the kv heads.
 __global__ void __launch_bounds__(256) page_weights(const WeightArgs a) {
     const int sub = threadIdx.x & 7;
     const int64_t s = blockIdx.y;
@@ -1738,20 +1962,19 @@ __global__ void __launch_bounds__(256) page_weights(const WeightArgs a) {
     const bool there = p < a.max_pages && (int64_t)p * a.page < L;
     float w = 0.f;
     if (there) {
-        const int32_t n = a.parts * a.group;
         for (int32_t g = sub; g < a.hkv; g += 8) {
-            const float *x = a.page_lse + ((s * a.hkv + g) * a.max_pages + p) * n;
+            const float *x = a.page_lse + ((s * a.hkv + g) * a.max_pages + p) * a.group;
             const float *all = a.seq_lse + (s * a.hkv + g) * a.group;
-            for (int32_t i = 0; i < n; ++i) {
-                const float y = all[i % a.group];
-                if (y > -INFINITY) w += exp2f(x[i] - y);
-            }
+            for (int32_t i = 0; i < a.group; ++i) w += head_weight(x[i], all[i]);
         }
     }
     for (int off = 4; off > 0; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
     if (sub == 0 && p < a.max_pages) {
         const int64_t at = s * a.max_pages + p;
-        a.w_out[at] = !there ? 0.f : a.w_in && a.decay != 0.f ? fmaf(a.decay, a.w_in[at], w) : w;
+        if (there)
+            store_weight(a, at, w);
+        else
+            a.w_out[at] = 0.f;
     }
 }
 
@@ -1952,7 +2175,7 @@ bool decode_fp8_ok(const hswa_pool *pool, const hswa_layer *layer, const void *q
 template <int kTok, bool kWeights = false>
 int decode_fp8_ctas_per_sm() {
     static int cache[kMaxDevices] = {};
-    return kernel_setup(decode_mma_fp8_d128<kTok, kWeights>, decode_smem8_bytes<kTok>(), 32 * (kConsumers8 + 1), cache);
+    return kernel_setup(decode_mma_fp8_d128<kTok, kWeights>, decode_smem8_bytes<kTok, kWeights>(), 32 * (kConsumers8 + 1), cache);
 }
 
 // Query tokens per sequence from which an FP8 decode runs on the tensor-core
@@ -1969,7 +2192,7 @@ bool decode_fast_ok(const hswa_pool *pool, const hswa_layer *layer, const void *
 template <int kTok, bool kWeights = false>
 int decode_ctas_per_sm_t() {
     static int cache[kMaxDevices] = {};
-    return kernel_setup(decode_mma_bf16_d128<kTok, kWeights>, decode_smem_bytes<kTok>(), 32 * (kTok + 1), cache);
+    return kernel_setup(decode_mma_bf16_d128<kTok, kWeights>, decode_smem_bytes<kTok, kWeights>(), 32 * (kTok + 1), cache);
 }
 
 int decode_ctas_per_sm() { return decode_ctas_per_sm_t<1>(); }
@@ -2027,17 +2250,22 @@ constexpr int kMaxCtasPerSm = 4;
 
 // What hswa_decode_weights adds to a decode step.
 struct PageWeights {
-    float *page_lse, *seq_lse;  // workspace
+    float *page_lse, *seq_lse, *piece_lse;  // workspace
     const float *w_in;
     float *w_out;
     float decay;
 };
 
-cudaError_t launch_page_weights(const PageWeights &pw, const hswa_config &c, const int32_t *d_seq_len, int n_seqs,
-                                int parts, cudaStream_t st) {
-    const WeightArgs a = {pw.page_lse, pw.seq_lse, d_seq_len, pw.w_in, pw.w_out, pw.decay, c.n_kv_heads,
-                          c.n_q_heads / c.n_kv_heads, parts, c.page_size, c.max_pages_per_seq};
-    return launch_pdl(page_weights, dim3((c.max_pages_per_seq + 31) / 32, n_seqs), dim3(256), 0, st, a);
+WeightArgs weight_args(const PageWeights &pw, const hswa_config &c, const int32_t *d_seq_len) {
+    return {pw.page_lse, pw.seq_lse, d_seq_len, pw.w_in, pw.w_out, pw.decay, c.n_kv_heads,
+            c.n_q_heads / c.n_kv_heads, c.page_size, c.max_pages_per_seq};
+}
+
+cudaError_t launch_finish_weights(const PageWeights &pw, const hswa_config &c, const DecodeArgs &a, int n_ctas,
+                                  cudaStream_t st) {
+    const int32_t n_merge = a.n_seqs * c.n_kv_heads, chunks = (c.max_pages_per_seq + kWeightPages - 1) / kWeightPages;
+    return launch_pdl(decode_finish_weights, dim3(n_merge + a.n_seqs * chunks), dim3(256),
+                      c.n_q_heads * sizeof(float), st, a, n_ctas, n_merge, chunks, weight_args(pw, c, a.seq_len));
 }
 
 size_t desc_bytes(int n_seqs) { return ((size_t)(n_seqs + 1) * sizeof(int4) + 255) & ~(size_t)255; }
@@ -2089,7 +2317,7 @@ int fill_args(DecodeArgs &a, const hswa_pool *pool, const hswa_layer *layer, con
     a.n_tok = 1;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.err = error_word();
-    a.page_lse = a.seq_lse = nullptr;
+    a.page_lse = a.seq_lse = a.piece_lse = nullptr;
     return num_pages;
 }
 
@@ -2121,7 +2349,7 @@ int decode_fp8(const hswa_pool *pool, const hswa_layer *layer, const void *q, vo
     DecodeArgs a;
     const int32_t num_pages = fill_args(a, pool, layer, q, o, d_bt, d_seq_len, n_seqs, scale, ws);
     a.n_tok = n_tok;
-    if (pw) a.page_lse = pw->page_lse, a.seq_lse = pw->seq_lse;
+    if (pw) a.page_lse = pw->page_lse, a.seq_lse = pw->seq_lse, a.piece_lse = pw->piece_lse;
     const uint64_t blocks = (uint64_t)num_pages * c.n_kv_heads;
     CUtensorMap tk, tv, tq;
     if (!make_tmap_2d(&tk, layer->k_pool, blocks * kP, kD, kP, kD, CU_TENSOR_MAP_DATA_TYPE_UINT8,
@@ -2138,7 +2366,7 @@ int decode_fp8(const hswa_pool *pool, const hswa_layer *layer, const void *q, vo
             e = launch_decode_tc<DecodeTc8Smem>(n_tok, n_ctas, st, tq, tk, tv, a);
         else if (pw)
             e = launch_pdl(decode_mma_fp8_d128<1, true>, dim3(n_ctas), dim3(32 * (kConsumers8 + 1)),
-                           decode_smem8_bytes<1>(), st, tk, tv, a);
+                           decode_smem8_bytes<1, true>(), st, tk, tv, a);
         else if (n_tok == 1)
             e = launch_pdl(decode_mma_fp8_d128<1, false>, dim3(n_ctas), dim3(32 * (kConsumers8 + 1)),
                            decode_smem8_bytes<1>(), st, tk, tv, a);
@@ -2147,9 +2375,8 @@ int decode_fp8(const hswa_pool *pool, const hswa_layer *layer, const void *q, vo
                            decode_smem8_bytes<2>(), st, tk, tv, a);
     }
     if (e == cudaSuccess)
-        e = launch_pdl(pw ? decode_combine<kConsumers8> : decode_combine<0>, dim3(c.n_kv_heads, n_seqs * n_tok),
-                       dim3(256), 0, st, a, n_ctas);
-    if (e == cudaSuccess && pw) e = launch_page_weights(*pw, c, d_seq_len, n_seqs, kConsumers8, st);
+        e = pw ? launch_finish_weights(*pw, c, a, n_ctas, st)
+               : launch_pdl(decode_combine, dim3(c.n_kv_heads, n_seqs * n_tok), dim3(256), 0, st, a, n_ctas);
     return e == cudaSuccess ? HSWA_OK : HSWA_ERR_CUDA;
 }
 
@@ -2157,7 +2384,7 @@ template <int kTok, bool kWeights = false>
 cudaError_t launch_decode_kernel(int n_ctas, cudaStream_t st, const CUtensorMap &tk, const CUtensorMap &tv,
                                  const DecodeArgs &a) {
     return launch_pdl(decode_mma_bf16_d128<kTok, kWeights>, dim3(n_ctas), dim3(32 * (kTok + 1)),
-                      decode_smem_bytes<kTok>(), st, tk, tv, a);
+                      decode_smem_bytes<kTok, kWeights>(), st, tk, tv, a);
 }
 
 int launch_decode_weights_any(const hswa_pool *pool, const hswa_layer *layer, const void *q, void *o,
@@ -2182,7 +2409,9 @@ int launch_decode_weights_any(const hswa_pool *pool, const hswa_layer *layer, co
             c.n_q_heads, c.n_kv_heads, c.head_dim, c.page_size, c.full_pages, scale_log2, err);
     }
     cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) e = launch_page_weights(pw, c, d_seq_len, n_seqs, 1, st);
+    if (e == cudaSuccess)
+        e = launch_pdl(page_weights, dim3((c.max_pages_per_seq + 31) / 32, n_seqs), dim3(256), 0, st,
+                       weight_args(pw, c, d_seq_len));
     return e == cudaSuccess ? HSWA_OK : cuda_fail(e, "hswa_decode_weights");
 }
 
@@ -2202,7 +2431,8 @@ int decode_impl(const hswa_pool *pool, const hswa_layer *layer, const void *q, v
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool fused = slots != nullptr;
     if (pool->cfg.dtype == HSWA_DTYPE_FP8_E4M3) {
-        if ((int64_t)n_seqs * n_tok > 65535) return HSWA_ERR_UNSUPPORTED;  // rows of the combine grid
+        if ((int64_t)n_seqs * n_tok > 65535 || (pw && pool->cfg.n_q_heads > kMaxWeightHeads))
+            return HSWA_ERR_UNSUPPORTED;  // rows of the combine grid
         return decode_fp8(pool, layer, q, o, d_bt, d_seq_len, n_seqs, n_tok, scale, ws, ws_bytes, slots, k_new,
                           v_new, stream, pw);
     }
@@ -2217,6 +2447,7 @@ int decode_impl(const hswa_pool *pool, const hswa_layer *layer, const void *q, v
                                         n_seqs, scale, 0, st, n_tok);
     }
     const hswa_config &c = pool->cfg;
+    if (pw && c.n_q_heads > kMaxWeightHeads) return HSWA_ERR_UNSUPPORTED;
     if ((int64_t)n_seqs * n_tok > 65535) return HSWA_ERR_UNSUPPORTED;  // rows of the combine grid
     const int sms = sm_count();
     if (sms <= 0) return HSWA_ERR_CUDA;
@@ -2235,7 +2466,7 @@ int decode_impl(const hswa_pool *pool, const hswa_layer *layer, const void *q, v
     a.k_new = static_cast<const __nv_bfloat16 *>(k_new);
     a.v_new = static_cast<const __nv_bfloat16 *>(v_new);
     a.n_tok = n_tok;
-    if (pw) a.page_lse = pw->page_lse, a.seq_lse = pw->seq_lse;
+    if (pw) a.page_lse = pw->page_lse, a.seq_lse = pw->seq_lse, a.piece_lse = pw->piece_lse;
     CUtensorMap tk, tv, tq;
     const uint64_t rows = (uint64_t)num_pages * c.n_kv_heads * kP;
     if (!make_tmap_2d(&tk, layer->k_pool, rows, kD, 64, 64, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
@@ -2260,10 +2491,10 @@ int decode_impl(const hswa_pool *pool, const hswa_layer *layer, const void *q, v
     case 2: e = launch_decode_kernel<2>(n_ctas, st, tk, tv, a); break;
     default: e = launch_decode_kernel<3>(n_ctas, st, tk, tv, a); break;
     }
-    if (e != cudaSuccess || launch_pdl(pw ? decode_combine<1> : decode_combine<0>,
-                                       dim3(c.n_kv_heads, n_seqs * n_tok), dim3(256), 0, st, a, n_ctas) != cudaSuccess)
-        return HSWA_ERR_CUDA;
-    if (pw && launch_page_weights(*pw, c, d_seq_len, n_seqs, 1, st) != cudaSuccess) return HSWA_ERR_CUDA;
+    if (e == cudaSuccess)
+        e = pw ? launch_finish_weights(*pw, c, a, n_ctas, st)
+               : launch_pdl(decode_combine, dim3(c.n_kv_heads, n_seqs * n_tok), dim3(256), 0, st, a, n_ctas);
+    if (e != cudaSuccess) return HSWA_ERR_CUDA;
     return HSWA_OK;
 }
 
@@ -2296,12 +2527,18 @@ extern "C" int hswa_decode_multi(const hswa_pool *pool, const hswa_layer *layer,
                        nullptr, stream);
 }
 
+// The workspace of hswa_decode_weights: that of hswa_decode, then the log-sums
+// of sequences, of pages and of pieces (as many as hswa_decode has records).
+static size_t weights_base(const hswa_pool *pool, int n_seqs) {
+    return (hswa_decode_workspace_size(pool, n_seqs) + 255) & ~(size_t)255;
+}
+
 extern "C" size_t hswa_decode_weights_workspace_size(const hswa_pool *pool, int n_seqs) {
     if (!pool || n_seqs < 0) return 0;
     const hswa_config &c = pool->cfg;
-    const size_t parts = c.dtype == HSWA_DTYPE_FP8_E4M3 ? kConsumers8 : 1;
-    const size_t base = (hswa_decode_workspace_size(pool, n_seqs) + 255) & ~(size_t)255;
-    return base + ((size_t)n_seqs * c.n_q_heads * c.max_pages_per_seq * parts + (size_t)n_seqs * c.n_q_heads) * 4;
+    const size_t pieces = (weights_base(pool, n_seqs) - desc_bytes(n_seqs)) / sizeof(Partial);
+    return weights_base(pool, n_seqs) +
+           ((size_t)n_seqs * c.n_q_heads * (c.max_pages_per_seq + (size_t)1) + pieces * kG) * sizeof(float);
 }
 
 extern "C" int hswa_decode_weights(const hswa_pool *pool, const hswa_layer *layer, const void *q, void *o,
@@ -2311,19 +2548,22 @@ extern "C" int hswa_decode_weights(const hswa_pool *pool, const hswa_layer *laye
     HSWA_NVTX("hswa_decode_weights");
     if (!pool || !layer || n_seqs < 0 || layer->kind != HSWA_KIND_FULL) return HSWA_ERR_INVALID_ARG;
     if (n_seqs == 0) return HSWA_OK;
-    if (n_seqs > 65535) return HSWA_ERR_UNSUPPORTED;  // rows of the weight grid
+    const hswa_config &c = pool->cfg;
+    // blocks of the last launch
+    if (n_seqs > 65535 ||
+        (int64_t)n_seqs * (c.n_kv_heads + c.max_pages_per_seq / kWeightPages + (int64_t)1) > INT32_MAX)
+        return HSWA_ERR_UNSUPPORTED;
     if (!w_out || !ws || ((uintptr_t)ws & 255) || ws_bytes < hswa_decode_weights_workspace_size(pool, n_seqs))
         return HSWA_ERR_INVALID_ARG;
-    const hswa_config &c = pool->cfg;
-    const size_t base = (hswa_decode_workspace_size(pool, n_seqs) + 255) & ~(size_t)255;
     PageWeights pw;
-    pw.seq_lse = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + base);
-    pw.page_lse = pw.seq_lse + (size_t)n_seqs * c.n_q_heads;
+    pw.seq_lse = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + weights_base(pool, n_seqs));
+    pw.page_lse = pw.seq_lse + (size_t)n_seqs * c.n_q_heads;  // 16-byte aligned where 8 heads share a kv head
+    pw.piece_lse = pw.page_lse + (size_t)n_seqs * c.n_q_heads * c.max_pages_per_seq;
     pw.w_in = w_in;
     pw.w_out = w_out;
     pw.decay = decay;
-    return decode_impl(pool, layer, q, o, d_bt, d_seq_len, n_seqs, 1, scale, ws, base, nullptr, nullptr, nullptr,
-                       stream, &pw);
+    return decode_impl(pool, layer, q, o, d_bt, d_seq_len, n_seqs, 1, scale, ws, weights_base(pool, n_seqs), nullptr,
+                       nullptr, nullptr, stream, &pw);
 }
 
 // ---------------------------------------------------- no-allocation decode

@@ -109,16 +109,6 @@ __device__ __forceinline__ uint64_t shfl_xor64(uint64_t x, int m) {
     return __shfl_xor_sync(0xffffffffu, (unsigned long long)x, m);
 }
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-
-// Store to the same shared variable of CTA `rank` of the cluster.
-__device__ __forceinline__ void st_cluster_u64(const uint64_t *mine, int rank, uint64_t x) {
-    uint32_t at;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(mine)), "r"(rank));
-    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(x) : "memory");
-}
-
 // floor(u x) for u in [0, 1)
 __device__ u128 times_fraction(u128 x, float u) {
     const uint32_t b = __float_as_uint(u);

@@ -420,9 +420,8 @@ int hswa_decode_append(const hswa_pool *pool, const hswa_layer *layer, const voi
                        const int32_t *d_seq_len, int n_seqs, float scale, void *ws, size_t ws_bytes,
                        hswa_stream_t stream);
 
-/* Bytes of workspace hswa_decode_weights needs: that of hswa_decode and one
- * fp32 per query head and page of the batch's table rows (four for FP8
- * pools). */
+/* Bytes of workspace hswa_decode_weights needs: that of hswa_decode and about
+ * one fp32 per query head and page of the batch's table rows. */
 size_t hswa_decode_weights_workspace_size(const hswa_pool *pool, int n_seqs);
 
 /* hswa_decode of a Full layer that also adds up where the attention went,
