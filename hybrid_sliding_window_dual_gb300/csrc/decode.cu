@@ -1979,17 +1979,70 @@ __global__ void __launch_bounds__(256) page_weights(const WeightArgs a) {
 }
 
 // Decode with page weights for any dtype / head_dim (<= 256) / head ratio /
-// page size: one CTA per (query head, sequence), its 8 warps taking the
-// pages in turn, each with a softmax of its own, merged at the end.
-template <typename T>
-__global__ void __launch_bounds__(256) decode_weights_any(const T *__restrict__ q, T *__restrict__ o,
+// page size: one CTA per (query head, sequence), its warps taking the pages in
+// turn, each with a softmax of its own, merged at the end. A warp takes kKeys
+// keys of a page at once, whose loads and sums across the lanes overlap: kE
+// elements a lane of each. Bound by latency (a table entry, a page's keys,
+// the sums across lanes, one after the other) and, with few CTAs, by
+// instructions: 16 sequences of 1000 to 2000 keys, fp32, d = 64, take 23 us;
+// with 8 warps and a key at a time it was 57, with every key's sum in every
+// lane 31.
+// Warps of a CTA: as many as their registers allow.
+template <int kE>
+constexpr int kAnyWarps = kE <= 2 ? 32 : 16;
+
+// Sums of kN values (4 or 8) over a warp's lanes, one value a lane: each step
+// a lane keeps half of its values and gets the other lane's share of them.
+// Lane l ends up with value (l >> 2) with its bits reversed (kN = 8; l >> 3
+// for 4), lane_of gives a lane that holds value k.
+template <int kN>
+__device__ __forceinline__ float sum_lanes(float (&x)[kN]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int n = kN / 2, off = 16; n > 0; n >>= 1, off >>= 1) {
+#pragma unroll
+        for (int k = 0; k < n; ++k) {
+            const bool upper = lane & off;
+            const float give = upper ? x[k] : x[n + k], hold = upper ? x[n + k] : x[k];
+            x[k] = hold + __shfl_xor_sync(0xffffffffu, give, off);
+        }
+    }
+#pragma unroll
+    for (int off = 16 / kN; off > 0; off >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], off);
+    return x[0];
+}
+template <int kN>
+__device__ __forceinline__ int value_of_lane() {
+    const int l = threadIdx.x & 31;
+    return kN == 8 ? (l >> 4 & 1) * 4 + (l >> 3 & 1) * 2 + (l >> 2 & 1) : (l >> 4 & 1) * 2 + (l >> 3 & 1);
+}
+template <int kN>
+__device__ __forceinline__ constexpr int lane_of(int k) {
+    return kN == 8 ? (k >> 2 & 1) * 16 + (k >> 1 & 1) * 8 + (k & 1) * 4 : (k >> 1 & 1) * 16 + (k & 1) * 8;
+}
+// Over the lanes that hold different values.
+template <int kN>
+__device__ __forceinline__ float sum_values(float x) {
+#pragma unroll
+    for (int off = 16; off >= 32 / kN; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+}
+template <int kN>
+__device__ __forceinline__ float max_values(float x) {
+#pragma unroll
+    for (int off = 16; off >= 32 / kN; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+    return x;
+}
+
+template <typename T, int kE>
+__global__ void __launch_bounds__(32 * kAnyWarps<kE>) decode_weights_any(const T *__restrict__ q, T *__restrict__ o,
                                                           const T *__restrict__ kp, const T *__restrict__ vp,
                                                           const int32_t *__restrict__ bt,
                                                           const int32_t *__restrict__ seq_len, float *page_lse,
                                                           float *seq_lse, int32_t bt_stride, int32_t hq, int32_t hkv,
                                                           int32_t d, int32_t page, int32_t num_pages,
                                                           float scale_log2, int *err) {
-    constexpr int kE = 8, kW = 8;
+    constexpr int kW = kAnyWarps<kE>, kKeys = kE <= 2 ? 8 : 4;
     __shared__ float s_m[kW], s_l[kW], s_o[kW][32 * kE];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int32_t h = blockIdx.x, group = hq / hkv, g = h / group;
@@ -2003,51 +2056,63 @@ __global__ void __launch_bounds__(256) decode_weights_any(const T *__restrict__ 
         qv[e] = c < d ? to_f(q[row + c]) * scale_log2 : 0.f;
         acc[e] = 0.f;
     }
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f;  // l: of this lane's keys
     const int32_t npg = min((int32_t)(((int64_t)L + page - 1) / page), bt_stride);
+    int32_t next = warp < npg ? bt[s * bt_stride + warp] : -1;
     for (int32_t p = warp; p < npg; p += kW) {
-        const int32_t pg = bt[s * bt_stride + p];
-        float pm = -INFINITY, pl = 0.f;  // this page's max and sum
+        const int32_t pg = next;
+        if (p + kW < npg) next = bt[s * bt_stride + p + kW];
+        float pl = 0.f;  // this page's sum, relative to the warp's maximum
         if (pg < 0 || pg >= num_pages) {
             if (lane == 0) set_error(err, HSWA_ERR_BOUNDS);
         } else {
             const int32_t n = min(page, L - p * page);
-            for (int32_t r = 0; r < n; ++r) {
-                const int64_t base = (((int64_t)pg * hkv + g) * page + r) * d;
-                float dot = 0.f;
+            const T *k0 = kp + ((int64_t)pg * hkv + g) * page * d + lane, *v0 = vp + (k0 - kp);
+            for (int32_t r0 = 0; r0 < n; r0 += kKeys) {
+                float dot[kKeys], v[kKeys][kE];
 #pragma unroll
-                for (int e = 0; e < kE; ++e) {
-                    const int c = lane + 32 * e;
-                    if (c < d) dot += qv[e] * to_f(kp[base + c]);
+                for (int k = 0; k < kKeys; ++k) {
+                    const int64_t at = (int64_t)min(r0 + k, n - 1) * d;  // past the last key: it again
+                    dot[k] = 0.f;
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) {
+                        const bool in = lane + 32 * e < d;
+                        if (in) dot[k] += qv[e] * to_f(k0[at + 32 * e]);
+                        v[k][e] = in ? to_f(v0[at + 32 * e]) : 0.f;
+                    }
                 }
-                for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-                const float nm = fmaxf(m, dot), np = fmaxf(pm, dot);
-                const float alpha = exp2f(m - nm), x = exp2f(dot - nm);
+                const float sum = sum_lanes<kKeys>(dot);
+                const float score = r0 + value_of_lane<kKeys>() < n ? sum : -INFINITY;
+                const float nm = fmaxf(m, max_values<kKeys>(score)), alpha = exp2f(m - nm), x = exp2f(score - nm);
                 l = l * alpha + x;
-                pl = pl * exp2f(pm - np) + exp2f(dot - np);
-                m = nm;
-                pm = np;
+                pl = pl * alpha + x;
 #pragma unroll
-                for (int e = 0; e < kE; ++e) {
-                    const int c = lane + 32 * e;
-                    acc[e] = acc[e] * alpha + (c < d ? x * to_f(vp[base + c]) : 0.f);
+                for (int e = 0; e < kE; ++e) acc[e] *= alpha;
+#pragma unroll
+                for (int k = 0; k < kKeys; ++k) {
+                    const float xk = __shfl_sync(0xffffffffu, x, lane_of<kKeys>(k));
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) acc[e] += xk * v[k][e];
                 }
+                m = nm;
             }
         }
-        if (lane == 0) page_lse[((s * hkv + g) * bt_stride + p) * group + h % group] = pm + log2f(pl);
+        pl = sum_values<kKeys>(pl);
+        if (lane == 0) page_lse[((s * hkv + g) * bt_stride + p) * group + h % group] = pl == 0.f ? -INFINITY : m + log2f(pl);
     }
+    l = sum_values<kKeys>(l);
     if (lane == 0) s_m[warp] = m, s_l[warp] = l;
 #pragma unroll
     for (int e = 0; e < kE; ++e) s_o[warp][lane + 32 * e] = acc[e];
     __syncthreads();
-    float M = -INFINITY, sum = 0.f, out = 0.f;
+    float M = -INFINITY, sum = 0.f;
     for (int w = 0; w < kW; ++w) M = fmaxf(M, s_m[w]);
-    for (int w = 0; w < kW; ++w) {
-        const float f = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - M);
-        sum += f * s_l[w];
-        out += f * s_o[w][threadIdx.x];
+    for (int w = 0; w < kW; ++w) sum += s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - M) * s_l[w];
+    if (threadIdx.x < d) {
+        float out = 0.f;
+        for (int w = 0; w < kW; ++w) out += s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - M) * s_o[w][threadIdx.x];
+        o[row + threadIdx.x] = from_f<T>(sum > 0.f ? out / sum : 0.f);
     }
-    if (threadIdx.x < d) o[row + threadIdx.x] = from_f<T>(sum > 0.f ? out / sum : 0.f);
     if (threadIdx.x == 0) seq_lse[s * hq + h] = sum > 0.f ? M + log2f(sum) : -INFINITY;
 }
 
@@ -2392,21 +2457,28 @@ int launch_decode_weights_any(const hswa_pool *pool, const hswa_layer *layer, co
                               const PageWeights &pw, cudaStream_t st) {
     const hswa_config &c = pool->cfg;
     if (c.head_dim > 256) return HSWA_ERR_UNSUPPORTED;
-    const dim3 grid(c.n_q_heads, n_seqs);
-    const float scale_log2 = scale * 1.4426950408889634f;
-    int *err = error_word();
+    const auto run = [&](auto kernel, int warps, auto type) {
+        using T = decltype(type);
+        kernel<<<dim3(c.n_q_heads, n_seqs), 32 * warps, 0, st>>>(
+            (const T *)q, (T *)o, (const T *)layer->k_pool, (const T *)layer->v_pool, d_bt, d_seq_len, pw.page_lse,
+            pw.seq_lse, c.max_pages_per_seq, c.n_q_heads, c.n_kv_heads, c.head_dim, c.page_size, c.full_pages,
+            scale * 1.4426950408889634f, error_word());
+    };
+    const auto run_type = [&](auto type) {
+        using T = decltype(type);
+        if (c.head_dim <= 64)
+            run(decode_weights_any<T, 2>, kAnyWarps<2>, type);
+        else if (c.head_dim <= 128)
+            run(decode_weights_any<T, 4>, kAnyWarps<4>, type);
+        else
+            run(decode_weights_any<T, 8>, kAnyWarps<8>, type);
+    };
     if (c.dtype == HSWA_DTYPE_F32) {
         set_last_kernel("decode_weights_any_f32");
-        decode_weights_any<float><<<grid, 256, 0, st>>>(
-            (const float *)q, (float *)o, (const float *)layer->k_pool, (const float *)layer->v_pool, d_bt, d_seq_len,
-            pw.page_lse, pw.seq_lse, c.max_pages_per_seq, c.n_q_heads, c.n_kv_heads, c.head_dim, c.page_size,
-            c.full_pages, scale_log2, err);
+        run_type(float());
     } else {
         set_last_kernel("decode_weights_any_bf16");
-        decode_weights_any<__nv_bfloat16><<<grid, 256, 0, st>>>(
-            (const __nv_bfloat16 *)q, (__nv_bfloat16 *)o, (const __nv_bfloat16 *)layer->k_pool,
-            (const __nv_bfloat16 *)layer->v_pool, d_bt, d_seq_len, pw.page_lse, pw.seq_lse, c.max_pages_per_seq,
-            c.n_q_heads, c.n_kv_heads, c.head_dim, c.page_size, c.full_pages, scale_log2, err);
+        run_type(__nv_bfloat16());
     }
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess)
