@@ -203,13 +203,27 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 }
 
 // 8 elements over a scale, as codes: the quotients are correctly rounded
-// before they become codes, as in hswa_append_kv. (A product with the
-// reciprocal, divided only next to a middle between codes, was slower: 75
-// against 70 us on 9999 tokens, for the registers it takes.)
+// before they become codes, as in hswa_append_kv. With y the correctly
+// rounded 1 / b and q within a step of x / b, q + (x - b q) y rounds to the
+// correctly rounded quotient (Markstein, "Computation of elementary functions
+// on the IBM RISC System/6000 processor", 1990): the second correction is
+// that one, the first makes q near enough. Scales so small or large that the
+// remainder is not exact are divided by. (67.6 against 69.7 us on 9999 tokens
+// with divisions alone.)
 __device__ __forceinline__ uint2 e4m3x8(const float (&x)[8], float scale) {
     float y[8];
+    if (scale > 0x1p-90f && scale < 0x1p90f) {
+        const float r = __frcp_rn(scale);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], scale);
+        for (int i = 0; i < 8; ++i) {
+            float q = x[i] * r;
+            q = fmaf(fmaf(-scale, q, x[i]), r, q);
+            y[i] = copysignf(fmaf(fmaf(-scale, q, x[i]), r, q), x[i]);  // -0 / b is -0
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], scale);
+    }
     return make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
 }
 
@@ -273,9 +287,10 @@ __device__ void rope_v_fp8(const RopeArgs &a, int32_t block) {
 // CTAs per SM more than items per thread: capped at 48 registers (5 CTAs, 2
 // items of two 16-byte loads each) 32768 bf16 tokens of 64 / 8 heads take 201
 // us, 98 % of the copy bandwidth; at 74 registers with 4 items 268 us. FP8
-// codes need more registers (4 CTAs, 3 items): 9999 tokens in 70 us, 82 %;
+// codes need more registers (4 CTAs, 3 items): 9999 tokens in 68 us, 85 %;
 // 8 us of it is V's turning round, which the tiles at the end of the grid do
-// (put first or spread among the others they cost more: 72 and 77 us). A
+// (put first or spread among the others they cost 2 and 7 us more; four
+// tokens' codes stored as a word where they make one, 9 more). A
 // decode step of 64 tokens takes 3.5 us on the device.
 template <typename T, bool kFP8, bool kAdjacent, int kTile, int kItems, int kMinCtas>
 __global__ void __launch_bounds__(256, kMinCtas) rope_append_vec(const __grid_constant__ RopeArgs a, int32_t n_q_blocks) {

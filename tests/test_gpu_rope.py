@@ -256,6 +256,35 @@ def test_rope_append_special_values():
 
 
 @pytest.mark.gpu
+def test_rope_append_codes_of_extreme_rows():
+    """V's codes are the oracle quantizer's for rows of every magnitude, with
+    zeros of both signs, subnormals, and quotients next to the middles between
+    codes."""
+    c = Case(256, 8, 2, 128, 64, FP8, 128, [64], seed=18, packed=False)
+    v = c.v.view(256, 2, 128)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(18)
+    size = torch.logspace(-39, 38, 256, device="cuda", dtype=torch.float64)
+    v.copy_((torch.randn(256, 2, 128, generator=g, device="cuda", dtype=torch.float64) * size[:, None, None]).clamp(-3e38, 3e38))
+    v[:, 0, 5], v[:, 0, 6], v[:, 1, 7] = 0.0, -0.0, 1e-40
+    # rows whose quotients are exact halves of steps, and just off them
+    steps = torch.arange(1, 129, device="cuda", dtype=torch.float64) * 3.5
+    v[100, 0], v[100, 1] = steps, steps * (1 + 2.0 ** -8)
+    v[101, 0], v[101, 1] = -steps / 7, steps * 2.0 ** -60
+    c.k.copy_(c.v)
+    # nothing turns: K has the same values, but for the sign of a zero: the
+    # turned -0 1 - y 0 is +0 for a negative y
+    c.pos_h[:] = 0
+    assert c.run() == 0
+    rows = v.float().cpu().numpy()
+    exp = [np.full(c.k_pool.shape, 7, np.uint8), np.full(c.ks.shape, 3, np.float32), np.full(c.v_pool.shape, 7, np.uint8), np.full(c.vs.shape, 3, np.float32)]
+    oracle.append_kv_fp8(*exp, rows, rows, c.slots_h)
+    for name, e in (("ks", exp[1]), ("vs", exp[3]), ("v_pool", exp[2])):
+        assert (getattr(c, name).cpu().numpy() == e).all(), name
+    assert (e4m3_decode(c.k_pool.cpu().numpy()) == e4m3_decode(exp[0])).all()
+
+
+@pytest.mark.gpu
 def test_rope_append_long_pool_offsets():
     """Slots whose elements lie past 2^31 bytes and 2^31 elements of the pool."""
     pages = 33000  # x 8 heads x 64 x 128 elements = 2.16e9
