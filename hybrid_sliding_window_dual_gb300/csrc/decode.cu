@@ -175,9 +175,11 @@ __device__ __forceinline__ void key_range(int32_t L, int32_t window, int32_t n_t
 
 // Per-sequence descriptors: the first unit of the sequence (prefix sum of
 // units(s) = Hkv * pages touched by the key range [lo, hi)), lo, hi, units.
-// desc[n].x is the total number of units.
+// desc[n].x is the total number of units. Keys from max_keys on, where a table
+// row ends, are left out and set HSWA_ERR_BOUNDS (page weights, which have an
+// entry for a table's pages only; INT64_MAX elsewhere).
 __global__ void decode_plan(const int32_t *__restrict__ seq_len, int32_t n, int32_t hkv, int32_t page,
-                            int32_t window, int32_t n_tok, int4 *__restrict__ desc) {
+                            int32_t window, int32_t n_tok, int4 *__restrict__ desc, int64_t max_keys, int *err) {
     __shared__ int32_t warp_tot[32];
     __shared__ int32_t carry;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -190,6 +192,10 @@ __global__ void decode_plan(const int32_t *__restrict__ seq_len, int32_t n, int3
         int32_t u = 0, lo = 0, hi = 0;
         if (i < n) {
             key_range(seq_len[i], window, n_tok, lo, hi);
+            if (hi > max_keys) {
+                hi = (int32_t)max_keys;
+                set_error(err, HSWA_ERR_BOUNDS);
+            }
             if (hi > lo) u = hkv * ((hi - 1) / page - lo / page + 1);
         }
         int32_t x = u;  // inclusive warp scan
@@ -2058,6 +2064,7 @@ __global__ void __launch_bounds__(32 * kAnyWarps<kE>) decode_weights_any(const T
     }
     float m = -INFINITY, l = 0.f;  // l: of this lane's keys
     const int32_t npg = min((int32_t)(((int64_t)L + page - 1) / page), bt_stride);
+    if (L > (int64_t)bt_stride * page && threadIdx.x == 0) set_error(err, HSWA_ERR_BOUNDS);  // past its table
     int32_t next = warp < npg ? bt[s * bt_stride + warp] : -1;
     for (int32_t p = warp; p < npg; p += kW) {
         const int32_t pg = next;
@@ -2321,6 +2328,10 @@ struct PageWeights {
     float decay;
 };
 
+int64_t max_keys(const hswa_config &c, const PageWeights *pw) {
+    return pw ? (int64_t)c.max_pages_per_seq * c.page_size : INT64_MAX;
+}
+
 WeightArgs weight_args(const PageWeights &pw, const hswa_config &c, const int32_t *d_seq_len) {
     return {pw.page_lse, pw.seq_lse, d_seq_len, pw.w_in, pw.w_out, pw.decay, c.n_kv_heads,
             c.n_q_heads / c.n_kv_heads, c.page_size, c.max_pages_per_seq};
@@ -2425,7 +2436,7 @@ int decode_fp8(const hswa_pool *pool, const hswa_layer *layer, const void *q, vo
         return HSWA_ERR_CUDA;
     set_last_kernel(tc ? "decode_tc_fp8_d128" : pw ? "decode_mma_fp8_d128+weights" : slots ? "append_kv_fp8+decode_mma_fp8_d128" : "decode_mma_fp8_d128");
     cudaError_t e = launch_pdl(decode_plan, dim3(1), dim3(1024), 0, st, d_seq_len, n_seqs, c.n_kv_heads, kP,
-                               a.window, n_tok, static_cast<int4 *>(ws));
+                               a.window, n_tok, static_cast<int4 *>(ws), max_keys(c, pw), a.err);
     if (e == cudaSuccess) {
         if (tc)
             e = launch_decode_tc<DecodeTc8Smem>(n_tok, n_ctas, st, tq, tk, tv, a);
@@ -2551,7 +2562,7 @@ int decode_impl(const hswa_pool *pool, const hswa_layer *layer, const void *q, v
     // three launches chained with programmatic dependent launch: each one
     // is scheduled while its predecessor finishes and waits for it on entry
     if (launch_pdl(decode_plan, dim3(1), dim3(1024), 0, st, d_seq_len, n_seqs, c.n_kv_heads, kP, a.window, n_tok,
-                   static_cast<int4 *>(ws)) != cudaSuccess)
+                   static_cast<int4 *>(ws), max_keys(c, pw), a.err) != cudaSuccess)
         return HSWA_ERR_CUDA;
     cudaError_t e;
     if (tc) {
@@ -2627,6 +2638,7 @@ extern "C" int hswa_decode_weights(const hswa_pool *pool, const hswa_layer *laye
         return HSWA_ERR_UNSUPPORTED;
     if (!w_out || !ws || ((uintptr_t)ws & 255) || ws_bytes < hswa_decode_weights_workspace_size(pool, n_seqs))
         return HSWA_ERR_INVALID_ARG;
+    if (overlap_but_differ(w_in, w_out, (size_t)n_seqs * c.max_pages_per_seq * sizeof(float))) return HSWA_ERR_INVALID_ARG;
     PageWeights pw;
     pw.seq_lse = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + weights_base(pool, n_seqs));
     pw.page_lse = pw.seq_lse + (size_t)n_seqs * c.n_q_heads;  // 16-byte aligned where 8 heads share a kv head

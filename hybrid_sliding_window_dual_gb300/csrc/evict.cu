@@ -214,6 +214,8 @@ extern "C" int hswa_evict_select(const hswa_pool *pool, const int32_t *d_seq_len
         return HSWA_ERR_INVALID_ARG;
     if (n_seqs == 0) return HSWA_OK;
     if (!d_seq_len || !w_in || !d_budget || !keep || !n_keep || !w_out) return HSWA_ERR_INVALID_ARG;
+    if (overlap_but_differ(w_in, w_out, (size_t)n_seqs * pool->cfg.max_pages_per_seq * sizeof(float)))
+        return HSWA_ERR_INVALID_ARG;
     const SelectArgs a = {d_seq_len, w_in, d_budget, sink_pages, recent_tokens, pool->cfg.page_size,
                           pool->cfg.max_pages_per_seq, keep, n_keep, w_out};
     set_last_kernel("evict_select");

@@ -19,6 +19,12 @@ struct NvtxRange {
 };
 #define HSWA_NVTX(name) NvtxRange hswa_nvtx_range_(name)
 
+// An output that may be its input itself, but not lie across it.
+inline bool overlap_but_differ(const void *in, const void *out, size_t bytes) {
+    const uintptr_t x = (uintptr_t)in, y = (uintptr_t)out;
+    return in && x != y && (x < y ? y - x : x - y) < bytes;
+}
+
 // FIFO free list of page indices (ring buffer; never holds more than the
 // pool's page count).
 struct PageQueue {

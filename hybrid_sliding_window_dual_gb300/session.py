@@ -145,11 +145,12 @@ class DualPoolSession:
     def rope_append(self, layer, rope, q, k, v, d_pos, d_slots, q_out):
         """Rotate q (into q_out) and K, and append K and V. q, k, v: [T, heads *
         d] or [T, heads, d], rows possibly slices of one projection."""
-        for x in (q, k, v):
-            heads = (x.stride(-1) == 1 and (x.dim() == 2 or x.stride(1) == x.shape[2])) or x.numel() == 0
-            if x.dim() not in (2, 3) or not heads:
-                raise ValueError("a token's heads must lie next to each other")
         row = self.cfg.head_dim * self.cfg.n_q_heads, self.cfg.head_dim * self.cfg.n_kv_heads
+        for x, n in ((q, row[0]), (k, row[1]), (v, row[1])):
+            if x.dim() not in (2, 3) or x.shape[0] != q.shape[0] or x[:1].numel() != n * min(x.shape[0], 1):
+                raise ValueError("q, k and v must hold a row of heads for the same tokens")
+            if x.numel() and not x[0].is_contiguous():
+                raise ValueError("a token's heads must lie next to each other")
         one = q.shape[0] <= 1  # a single row's stride says nothing
         B.hswa_rope_append(self.pool, self.layers[layer], rope, q, row[0] if one else q.stride(0),
                            k, row[1] if one else k.stride(0), v, row[1] if one else v.stride(0), d_pos, d_slots,
@@ -158,8 +159,8 @@ class DualPoolSession:
     def decode_weights(self, layer, q, o, n_seqs, scale, w_in, decay, w_out):
         """decode() of a Full layer that adds the pages' attention weights:
         w_out = decay * w_in + weights, [n_seqs, max_pages_per_seq] fp32."""
-        need = B.hswa_decode_weights_workspace_size(self.pool, n_seqs)
-        if self.weights_ws is None or self.weights_ws.numel() < need:
+        if self.weights_ws is None:  # for every sequence, so that captured calls keep theirs
+            need = B.hswa_decode_weights_workspace_size(self.pool, self.cfg.max_seqs)
             self.weights_ws = torch.empty(need, dtype=torch.uint8, device=self.device)
         B.hswa_decode_weights(self.pool, self.layers[layer], q, o, self.bt(layer), self.d_seq_len, n_seqs, scale,
                               w_in, decay, w_out, self.weights_ws, self.weights_ws.numel(), self.stream)
@@ -180,11 +181,20 @@ class DualPoolSession:
         dtype = {torch.float32: B.HSWA_DTYPE_F32, torch.bfloat16: B.HSWA_DTYPE_BF16}.get(p.dtype)
         if dtype is None or (q is not None and q.dtype != p.dtype):
             raise ValueError("p and q must both be float32 or bfloat16")
-        for x, t in ((p, n_tok), (q, n_tok - 1)):
-            if x is not None and x.numel() and (x.stride(2) != 1 or (x.shape[0] > 1 and x.stride(0) != t * x.stride(1))):
-                raise ValueError("rows must be evenly spaced")
-        B.hswa_verify_draft(dtype, p, p.stride(1), q, 0 if q is None else q.stride(1), d_draft, d_n_draft, u, n_seqs,
-                            n_tok, vocab, n_accept, tokens, self.stream)
+        if q is not None and q.shape != (n_seqs, n_tok - 1, vocab):
+            raise ValueError("q must hold a row per draft")
+        p_stride, q_stride = self._row_stride(p), 0 if q is None else self._row_stride(q)
+        B.hswa_verify_draft(dtype, p, p_stride, q, q_stride, d_draft, d_n_draft, u, n_seqs, n_tok, vocab, n_accept,
+                            tokens, self.stream)
+
+    @staticmethod
+    def _row_stride(x):
+        """Elements between neighbouring rows of x [n, t, vocab]; a dimension of one has any stride."""
+        n, t, vocab = x.shape
+        row = x.stride(1) if t > 1 else x.stride(0) if n > 1 else vocab
+        if x.numel() and ((vocab > 1 and x.stride(2) != 1) or (n > 1 and x.stride(0) != t * row)):
+            raise ValueError("rows must be evenly spaced")
+        return row
 
     def decode(self, layer, q, o, n_seqs, scale):
         ws = self.workspace(n_seqs)

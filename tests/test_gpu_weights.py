@@ -179,6 +179,53 @@ def test_decode_weights_skip_pages_with_a_bad_entry(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP8, F32])
+@pytest.mark.parametrize("excess", [1, 200])
+def test_decode_weights_of_lengths_past_the_table(dtype, excess):
+    # the keys past the last entry of a table row are left out and reported; no
+    # other row's weights are touched
+    P = 64 if dtype != F32 else 16
+    c = Case([3 * P, 10 * P, 5], *((16, 2, 128, P) if dtype != F32 else (4, 2, 64, P)), dtype, seed=11, spare=0)
+    good_o, good_w = c.run(c.w_in, 0.5)
+    c.sess.d_seq_len[1] += excess
+    w = torch.full((c.S + 2, c.mp), 9.0, device="cuda")
+    o, _ = c.run(c.w_in, 0.5, w[1:-1])
+    assert c.sess.check() == H.HSWA_ERR_BOUNDS
+    assert torch.equal(w[1:-1], good_w) and torch.equal(o, good_o)
+    assert (w[0] == 9).all() and (w[-1] == 9).all()
+
+
+@pytest.mark.gpu
+def test_decode_weights_two_calls_at_once():
+    # two streams, a workspace each; then two captured calls that share one, in turn
+    a, b = Case([3000, 70, 900], 64, 8, 128, 64, BF16, seed=12), Case([12000], 64, 8, 128, 64, BF16, seed=13)
+    want = [c.run(c.w_in, 0.5) for c in (a, b)]
+    for c in (a, b):
+        c.sess.stream = torch.cuda.Stream()
+        c.sess.stream.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        got = [c.run(c.w_in, 0.5) for c in (a, b)]
+        torch.cuda.synchronize()
+        for (o, w), (o1, w1) in zip(want, got):
+            assert torch.equal(o, o1) and torch.equal(w, w1)
+    ws = torch.empty(max(H.hswa_decode_weights_workspace_size(c.sess.pool, c.S) for c in (a, b)), dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for c in (a, b):
+        o, w, g = torch.zeros_like(c.q), torch.zeros_like(c.w_in), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            H.hswa_decode_weights(c.sess.pool, c.sess.layers[0], c.q, o, c.sess.d_full_bt, c.sess.d_seq_len, c.S, c.scale, c.w_in, 0.5, w, ws, ws.numel(),
+                                  torch.cuda.current_stream())
+        graphs.append(g)
+        outs.append((o, w))
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    assert H.hswa_check() == 0
+    for (o, w), (o1, w1) in zip(want, outs):
+        assert torch.equal(o, o1) and torch.equal(w, w1)
+
+
+@pytest.mark.gpu
 def test_decode_weights_on_a_stream_and_in_a_graph():
     c = Case([100, 5000, 3], 64, 8, 128, 64, BF16, seed=9)
     o, w = c.check()

@@ -5,10 +5,12 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 import oracle
 from oracle import serving
 import hybrid_sliding_window_dual_gb300 as H
+from hybrid_sliding_window_dual_gb300.session import DualPoolSession
 from test_abi import assert_same_state, make_pair
 
 INVALID, UNSUPPORTED = H.HSWA_ERR_INVALID_ARG, H.HSWA_ERR_UNSUPPORTED
@@ -346,3 +348,37 @@ def test_verify_refusals():
     bad(UNSUPPORTED, dtype=H.HSWA_DTYPE_FP8_E4M3)
     bad(UNSUPPORTED, vocab=(1 << 20) + 1, p_stride=1 << 21, q_stride=1 << 21)
     H.hswa_verify_draft(*{**ok, "n": 0, "p": None}.values())
+
+
+def test_outputs_across_their_inputs_are_refused():
+    p = pool()
+    need = H.hswa_decode_weights_workspace_size(p, 4)
+    row = 8 * 4  # bytes of a row of weights
+    for at in (X - 4 * row + 4, X - 4, X + 4, X + 4 * row - 4):
+        refused(INVALID, H.hswa_decode_weights, p, layer(), X, X, X, X, 4, 1.0, X, 0.5, at, X, need)
+        refused(INVALID, H.hswa_evict_select, p, X, X, X, 4, 1, 128, X, X, at)
+    H.hswa_pool_destroy(p)
+
+
+def test_session_refuses_shapes_that_do_not_fit():
+    cfg = H.Config(window=128, page_size=64, n_q_heads=4, n_kv_heads=2, head_dim=16, dtype=H.HSWA_DTYPE_F32, full_pages=4, swa_pages=4, max_seqs=2,
+                   max_pages_per_seq=4)
+    s = DualPoolSession(cfg, [H.HSWA_KIND_FULL], device="cpu")
+    rope = H.hswa_rope_create(16, [8])
+    f = torch.zeros  # shapes only
+    i32 = dict(dtype=torch.int32)
+    for q, k, v in ((f(3, 64), f(2, 32), f(3, 32)), (f(3, 64), f(3, 32), f(4, 32)), (f(3, 63), f(3, 32), f(3, 32)), (f(3, 4, 16), f(3, 1, 16), f(3, 32)),
+                    (f(64), f(32), f(32)), (f(3, 128)[:, ::2], f(3, 32), f(3, 32)), (f(3, 16, 4).transpose(1, 2), f(3, 32), f(3, 32))):
+        with pytest.raises(ValueError):
+            s.rope_append(0, rope, q, k, v, f(1, 3, **i32), f(3, **i32), f(3, 64))
+    out = f(2, **i32), f(2, 3, **i32)
+    draft, u = f(2, 2, **i32), f(2, 3)
+    p = f(2, 3, 50)
+    for p, q in ((p, f(2, 2, 49)), (p, f(2, 3, 50)), (p, f(1, 2, 50)), (p, f(2, 2, 50).bfloat16()), (p.double(), None), (f(3, 2, 50).transpose(0, 1), None),
+                 (f(2, 3, 100)[:, :, ::2], None), (f(2, 4, 50)[:, :3], None), (p, f(2, 5, 50)[:, :2])):
+        with pytest.raises(ValueError):
+            s.verify(p, q, draft, None, u, *out)
+    assert s._row_stride(f(5, 3, 50)[:, :1]) == 150 and s._row_stride(f(1, 3, 60)[:, :, :50]) == 60
+    assert s._row_stride(f(50)[None, None]) == 50 and s._row_stride(f(3, 2, 1)) == 1
+    H.hswa_rope_destroy(rope)
+    s.close()
