@@ -3,18 +3,19 @@
 // The heaviest pages stay (the attention weight that hswa_decode_weights
 // accumulated), beside the first pages and everything within the last
 // `recent` tokens. One CTA per sequence holds a row's weights in registers as
-// ordered integers, neighbours in a thread, and bisects between the smallest
-// and the largest: how many are at or above the middle? Once no more
-// candidates are left in between than threads, each takes one. It ends as
-// soon as the answer is the number that stays, or at a single weight, of
-// whose pages the lower ones stay. One scan in page order places the pages.
+// ordered integers. It counts the candidates in bins that cut the range from
+// the smallest to the largest into equal parts, takes the bin that the answer
+// lies in for the next range, and ends when that holds as many candidates as
+// still stay, or one weight, of whose pages the lower ones stay, or so few
+// candidates that each can count those above it. One scan in page order
+// places the pages.
 //
-// Bound by latency: a row is a few KB, and the loads, 10 to 20 rounds of a
-// barrier each and the scan follow one another. 64 rows of up to 512 pages
-// take 4.2 us on the device, 128 of 2048 6.1, 5 of 16384 20. A radix
-// selection, 8 bits a pass, took 7.2, 11 and 50 (the weights' first bits are
-// nearly all alike, so that its counters collide); one warp per row 5.9 on
-// the first; the row in shared memory instead of registers 8.0, 10 and 23.
+// Bound by latency: a row is a few KB, and the loads, the steps with a barrier
+// each and the scan follow one another. FIGURES
+//
+// (A bisection of the range, one barrier a bit, took 4.2, 6.1 and 20; a radix
+// selection, 8 bits a pass, 7.2, 11 and 50: the weights' first bits are
+// nearly all alike, so that its counters collide.)
 #include "common.cuh"
 #include "internal.h"
 
@@ -37,16 +38,19 @@ struct SelectArgs {
     float *w_out;
 };
 
-// kItems pages a thread in registers. kLong: rows longer than kThreads *
-// kItems; the bisection then reads the row again each time (it lies in L2),
-// and the pages are placed one stretch of that many after the other.
+// kItems pages a thread in registers, 32 neighbours in a warp's lanes. kLong:
+// rows longer than kThreads * kItems; the counts then read the row again each
+// time (it lies in L2), and the pages are placed one stretch of that many
+// after the other.
 template <int kItems, int kThreads, bool kLong>
 __global__ void __launch_bounds__(kThreads) evict_select(const SelectArgs a) {
-    constexpr int kWarps = kThreads / 32;
-    __shared__ int32_t s_count[2][kWarps], s_sure[kWarps], s_tied[kWarps];
-    __shared__ uint32_t s_min[kWarps], s_max[kWarps], s_few[kThreads];
-    __shared__ int32_t s_few_n;
+    constexpr int kWarps = kThreads / 32, kBinBits = kThreads <= 256 ? 9 : kThreads == 512 ? 10 : 11, kBins = 1 << kBinBits;
+    constexpr int kPer = kBins / kThreads;
+    constexpr int kFew = 128;  // candidates that count each other
+    __shared__ int32_t s_bin[kBins], s_sum[kWarps], s_tied[kWarps], s_found[3], s_few_n;
+    __shared__ uint32_t s_min[kWarps], s_max[kWarps], s_few[kFew];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const unsigned before_me = (1u << lane) - 1;
     pdl_wait();
     pdl_launch_dependents();
     const int64_t s = blockIdx.x;
@@ -56,19 +60,10 @@ __global__ void __launch_bounds__(kThreads) evict_select(const SelectArgs a) {
     // this thread's pages of a stretch, and their order
     float x[kItems];
     uint32_t key[kItems];
-    int32_t first = tid * kItems;
-    const bool wide = ((uintptr_t)w & 15) == 0;
+    int32_t first = warp * kItems * 32 + lane;  // the k-th is 32 k further
     const auto load = [&]() {
 #pragma unroll
-        for (int k = 0; k < kItems; k += 4) {
-            if (wide && first + k + 4 <= a.max_pages) {
-                const float4 y = *reinterpret_cast<const float4 *>(w + first + k);
-                x[k] = y.x, x[k + 1] = y.y, x[k + 2] = y.z, x[k + 3] = y.w;
-            } else {
-#pragma unroll
-                for (int i = k; i < k + 4; ++i) x[i] = first + i < a.max_pages ? w[first + i] : 0.f;
-            }
-        }
+        for (int k = 0; k < kItems; ++k) x[k] = first + 32 * k < a.max_pages ? w[first + 32 * k] : 0.f;
 #pragma unroll
         for (int k = 0; k < kItems; ++k) key[k] = order_of(x[k]);
     };
@@ -81,15 +76,16 @@ __global__ void __launch_bounds__(kThreads) evict_select(const SelectArgs a) {
     const int32_t fixed = pages - (c1 - c0);
     const int32_t n_keep = min(pages, max(a.budget[s], fixed));
     const int32_t left = n_keep - fixed;  // candidates that stay
+    for (int32_t p = n_keep + tid; p < a.max_pages; p += kThreads) keep[p] = -1;
+    if (tid == 0) a.n_keep[s] = n_keep;
     const auto may_go = [&](int32_t p) { return p >= c0 && p < c1; };
-    // f(order) of this thread's candidates
-    const auto each_candidate = [&](auto f) {
+    // f(is a candidate, its order), by whole warps
+    const auto each_page = [&](auto f) {
         if constexpr (kLong) {
-            for (int32_t p = c0 + tid; p < c1; p += kThreads) f(order_of(w[p]));
+            for (int32_t p = c0 + tid; p - lane < c1; p += kThreads) f(p < c1, p < c1 ? order_of(w[p]) : 0u);
         } else {
 #pragma unroll
-            for (int k = 0; k < kItems; ++k)
-                if (may_go(first + k)) f(key[k]);
+            for (int k = 0; k < kItems; ++k) f(may_go(first + 32 * k), key[k]);
         }
     };
     // Candidates above `bound` in order of weight stay, and `quota` at most of
@@ -101,99 +97,136 @@ __global__ void __launch_bounds__(kThreads) evict_select(const SelectArgs a) {
         quota = INT32_MAX;
     } else if (left > 0) {
         uint32_t lo = 0xffffffffu, hi = 0;
-        each_candidate([&](uint32_t o) { lo = min(lo, o), hi = max(hi, o); });
+        each_page([&](bool may, uint32_t o) {
+            if (may) lo = min(lo, o), hi = max(hi, o);
+        });
         lo = __reduce_min_sync(0xffffffffu, lo);
         hi = __reduce_max_sync(0xffffffffu, hi);
         if (lane == 0) s_min[warp] = lo, s_max[warp] = hi;
         if (tid == 0) s_few_n = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) s_bin[tid * kPer + k] = 0;
         __syncthreads();
         lo = __reduce_min_sync(0xffffffffu, lane < kWarps ? s_min[lane] : 0xffffffffu);
         hi = __reduce_max_sync(0xffffffffu, lane < kWarps ? s_max[lane] : 0u);
-        // `upto` >= left candidates are at or above lo, `above` < left above hi
-        int32_t above = 0, upto = c1 - c0;
-        bool exact = false, few = false;
-        uint32_t mine = 0;      // few: one of the candidates in [lo, hi] of then, or 0,
-        int32_t few_above = 0;  // and how many were above them
-        for (int round = 0; lo < hi && !exact; round ^= 1) {
-            if (kItems > 4 && !few && upto - above <= kThreads) {
-                // a thread each for those still in question
-                few = true;
-                few_above = above;
-                each_candidate([&](uint32_t o) {
-                    if (o >= lo && o <= hi) s_few[atomicAdd(&s_few_n, 1)] = o;
-                });
-                __syncthreads();
-                if (tid < upto - above) mine = s_few[tid];
-            }
-            const uint32_t mid = lo + (hi - lo) / 2 + 1;
-            int32_t n = 0;
-            if (few)
-                n = mine >= mid;
-            else
-                each_candidate([&](uint32_t o) { n += o >= mid; });
-            n = __reduce_add_sync(0xffffffffu, n);
-            if (lane == 0) s_count[round][warp] = n;
+        // `above` < left candidates are above hi, `here` in [lo, hi], and with
+        // those at least `left`
+        int32_t above = 0, here = c1 - c0;
+        bool all = false;  // all of [lo, hi] stay
+        // each time the range loses kBinBits of its at most 32 bits
+        for (int pass = 0; pass < (32 + kBinBits - 1) / kBinBits && lo < hi && !all && here > kFew; ++pass) {
+            const int shift = max(0, 32 - __clz(hi - lo) - kBinBits);
+            each_page([&](bool may, uint32_t o) {
+                const bool in = may && o >= lo && o <= hi;
+                const uint32_t b = (hi - o) >> shift;  // heavier bins first
+                const unsigned mask = __ballot_sync(0xffffffffu, in);
+                if (mask == 0) return;
+                // many weights may be alike: one count for those in the first one's bin
+                const int one = __ffs(mask) - 1;
+                const uint32_t of_one = __shfl_sync(0xffffffffu, b, one);  // by every lane
+                const bool same = in && b == of_one;
+                const unsigned with = __ballot_sync(0xffffffffu, same);
+                if (in && (!same || lane == one)) atomicAdd(&s_bin[b], same ? __popc(with) : 1);
+            });
             __syncthreads();
-            n = __reduce_add_sync(0xffffffffu, lane < kWarps ? s_count[round][lane] : 0) + few_above;
-            exact = n == left;
-            if (n >= left)
-                lo = mid, upto = n;
-            else
-                hi = mid - 1, above = n;
+            int32_t n[kPer], sum = 0;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                sum += n[k] = s_bin[tid * kPer + k];
+                s_bin[tid * kPer + k] = 0;
+            }
+            int32_t upto = sum;
+            for (int off = 1; off < 32; off <<= 1) {
+                const int32_t y = __shfl_up_sync(0xffffffffu, upto, off);
+                if (lane >= off) upto += y;
+            }
+            if (lane == 31) s_sum[warp] = upto;
+            __syncthreads();
+            int32_t at = above + upto - sum + __reduce_add_sync(0xffffffffu, lane < warp ? s_sum[lane] : 0);
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                if (at < left && at + n[k] >= left) s_found[0] = tid * kPer + k, s_found[1] = at, s_found[2] = n[k];
+                at += n[k];
+            }
+            __syncthreads();
+            const uint32_t width = (1u << shift) - 1;
+            hi -= (uint32_t)s_found[0] << shift;
+            if (hi - lo > width) lo = hi - width;
+            above = s_found[1];
+            here = s_found[2];
+            all = above + here == left;
+        }
+        if (lo < hi && !all) {
+            each_page([&](bool may, uint32_t o) {
+                if (may && o >= lo && o <= hi) s_few[atomicAdd(&s_few_n, 1)] = o;
+            });
+            __syncthreads();
+            if (tid < here) {
+                const uint32_t mine = s_few[tid];
+                int32_t over = above, upto = above;
+#pragma unroll 8
+                for (int i = 0; i < here; ++i) over += s_few[i] > mine, upto += s_few[i] >= mine;
+                if (over < left && upto >= left) s_found[0] = (int32_t)mine, s_found[1] = over;  // equal ones write the same
+            }
+            __syncthreads();
+            lo = (uint32_t)s_found[0];
+            above = s_found[1];
         }
         bound = lo;
-        quota = exact ? INT32_MAX : left - above;
+        quota = all ? INT32_MAX : left - above;
     }
-    // In page order: how many stay for sure before this thread's pages, and
-    // how many at the bound come before them. w_out may be w_in: a page goes
-    // to its own place or a lower one, after its stretch has been read.
-    int32_t sure_before = 0, tied_before = 0;  // in the stretches before
+    // In page order: how many stay before this warp's pages, and up to which
+    // page those at the bound do. w_out may be w_in: a page goes to its own
+    // place or a lower one, after its stretch has been read.
+    int32_t before = 0, tied_before = 0;  // sure and tied ones in the stretches before
     for (int32_t base = 0; base < pages; base += kThreads * kItems) {
         if (kLong) {
-            first = base + tid * kItems;
+            first = base + warp * kItems * 32 + lane;
             load();
         }
-        int32_t sure = 0, tied = 0;
+        uint32_t sure = 0, tied = 0;  // bit k: this thread's k-th page
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
-            const bool there = first + k < pages, may = may_go(first + k);
-            sure += there && (!may || key[k] > bound);
-            tied += there && may && key[k] == bound;
+            const int32_t p = first + 32 * k;
+            sure |= p < pages && (!may_go(p) || key[k] > bound) ? 1u << k : 0u;
+            tied |= may_go(p) && key[k] == bound ? 1u << k : 0u;
         }
-        int32_t sure_upto = sure, tied_upto = tied;
-        for (int off = 1; off < 32; off <<= 1) {
-            const int32_t y = __shfl_up_sync(0xffffffffu, sure_upto, off), z = __shfl_up_sync(0xffffffffu, tied_upto, off);
-            if (lane >= off) sure_upto += y, tied_upto += z;
-        }
-        if (lane == 31) s_sure[warp] = sure_upto, s_tied[warp] = tied_upto;
+        const int32_t n_sure = __reduce_add_sync(0xffffffffu, __popc(sure));
+        const int32_t n_tied = __reduce_add_sync(0xffffffffu, __popc(tied));
+        if (lane == 0) s_sum[warp] = n_sure, s_tied[warp] = n_tied;
         __syncthreads();
-        const int32_t y = lane < kWarps ? s_sure[lane] : 0, z = lane < kWarps ? s_tied[lane] : 0;
-        int32_t t = tied_before + __reduce_add_sync(0xffffffffu, lane < warp ? z : 0) + tied_upto - tied;
-        int32_t at = sure_before + __reduce_add_sync(0xffffffffu, lane < warp ? y : 0) + sure_upto - sure + min(t, quota);
+        const int32_t y = lane < kWarps ? s_sum[lane] : 0, z = lane < kWarps ? s_tied[lane] : 0;
+        const int32_t ties = tied_before + __reduce_add_sync(0xffffffffu, lane < warp ? z : 0);  // before this warp's
+        int32_t n = before + __reduce_add_sync(0xffffffffu, lane < warp ? y : 0) + min(ties, quota);
         if (kLong) {
-            sure_before += __reduce_add_sync(0xffffffffu, y);
+            before += __reduce_add_sync(0xffffffffu, y);
             tied_before += __reduce_add_sync(0xffffffffu, z);
         }
+        uint32_t stay = sure | tied;
+        if (ties + n_tied > quota) {  // by whole warps: some of its ties go
+            stay = sure;
+            int32_t t = ties;
+            for (int k = 0; k < kItems; ++k) {
+                const unsigned m = __ballot_sync(0xffffffffu, tied >> k & 1);
+                if ((tied >> k & 1) && t + __popc(m & before_me) < quota) stay |= 1u << k;
+                t += __popc(m);
+            }
+        }
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
-            if (first + k >= pages) continue;
-            const bool tie = may_go(first + k) && key[k] == bound;
-            if (!may_go(first + k) || key[k] > bound || (tie && t < quota)) {
-                keep[at] = first + k;
+            const unsigned m = __ballot_sync(0xffffffffu, stay >> k & 1);
+            if (stay >> k & 1) {
+                const int32_t at = n + __popc(m & before_me);
+                keep[at] = first + 32 * k;
                 w_out[at] = x[k];
-                ++at;
             }
-            t += tie;
+            n += __popc(m);
         }
         if (!kLong) break;
         __syncthreads();  // before the next stretch is read over the same sums
     }
     if (pages == 0) __syncthreads();  // every thread has read its pages
-    for (int32_t p = n_keep + tid; p < a.max_pages; p += kThreads) {
-        keep[p] = -1;
-        w_out[p] = 0.f;
-    }
-    if (tid == 0) a.n_keep[s] = n_keep;
+    for (int32_t p = n_keep + tid; p < a.max_pages; p += kThreads) w_out[p] = 0.f;
 }
 
 template <int kItems, int kThreads, bool kLong = false>

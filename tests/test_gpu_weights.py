@@ -326,3 +326,20 @@ def test_select_many_sequences():
     rng = np.random.default_rng(4)
     lens = rng.integers(0, 64 * 90, 3000)
     select(lens, weights(rng, 3000, 90, "ties"), rng.integers(0, 90, 3000), 64, 1, 128)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mp", [300, 700, 1500, 5000, 12000, 30000])
+def test_select_needs_every_bit(mp):
+    # two far outliers and the rest within 1000 units in the last place, or in
+    # clusters of that kind at several magnitudes: the range narrows by steps
+    rng = np.random.default_rng(mp)
+    w = np.empty((6, mp), np.float32)
+    for i in range(6):
+        base = np.float32(1) if i < 3 else rng.choice(np.float32([1e-30, 1, 1e30, -1, -1e30]), mp)
+        w[i] = (np.broadcast_to(base, mp).astype(np.float32).view(np.int32) + rng.integers(0, 1000 if i % 3 else 40, mp).astype(np.int32)).view(np.float32)
+    w[:3, 17], w[:3, mp // 2] = np.inf, -np.inf
+    lens = [mp * 16, mp * 16 - 7, mp * 11, mp * 16, mp * 16 - 3, mp * 9]
+    for budget in (mp // 2, mp // 10, mp - 20):
+        select(lens, w, [budget] * 6, 16, 3, 200)
+        select(lens, w, [budget] * 6, 16, 0, 128, in_place=True)
