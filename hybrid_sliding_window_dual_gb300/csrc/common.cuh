@@ -168,6 +168,12 @@ __device__ __forceinline__ void st_cluster_u64(const uint64_t *mine, int rank, u
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_addr(mine, rank)), "l"(x) : "memory");
 }
 
+__device__ __forceinline__ int32_t ld_cluster_i32(const int32_t *mine, int rank) {
+    int32_t x;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(cluster_addr(mine, rank)) : "memory");
+    return x;
+}
+
 // ----------------------------------------------------------- bulk copies
 // 1-D bulk copy global -> shared, completing on an mbarrier (16-B aligned
 // addresses, size a multiple of 16).

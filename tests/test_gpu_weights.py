@@ -343,3 +343,17 @@ def test_select_needs_every_bit(mp):
     for budget in (mp // 2, mp // 10, mp - 20):
         select(lens, w, [budget] * 6, 16, 3, 200)
         select(lens, w, [budget] * 6, 16, 0, 128, in_place=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("S,mp", [(1, 2049), (76, 4096), (77, 4096), (1, 8193), (19, 16384), (20, 16384), (40, 5000)])
+@pytest.mark.parametrize("kind", ["plain", "ties"])
+def test_select_split_rows(S, mp, kind):
+    # rows over several CTAs, and the same sizes with too many rows for that;
+    # lengths from nothing to the whole row, ends inside each CTA's part
+    rng = np.random.default_rng(mp + S)
+    w = weights(rng, S, mp, kind)
+    lens = np.linspace(0, mp * 16, S).astype(np.int64) if S > 1 else np.array([mp * 16])
+    budget = rng.integers(0, mp, S)
+    select(lens, w, budget, 16, 5, 200)
+    select(lens[::-1], w, budget // 4, 16, 0, 128, in_place=True)
