@@ -1856,8 +1856,8 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return
 // added later start from nothing.
 //
 // Bound by memory, as the decode step is: 64 sequences of 1K to 32K, bf16 (64
-// / 8 heads): 652 us against 636 without the weights and 653 for the bytes at
-// the copy rate; 49 sequences, FP8: 282 against 266 and 257; three short ones
+// / 8 heads): 649 us against 636 without the weights and 653 for the bytes at
+// the copy rate; 49 sequences, FP8: 284 against 266 and 257; three short ones
 // 13.0 against 12.6. What the weights cost the FP8 kernel, whose issue slots
 // are nearly full, is instructions: with the sums added up in the consumer
 // warps it was 358, and each page's 64-bit address and exact logarithm in the

@@ -9,9 +9,10 @@
 //
 // Angles. f_i / 2 pi is kept as a 64-bit fraction of a turn (made on the
 // host in 64-bit floating point), so pos * fraction mod 2^64 is the exact
-// phase of any int32 position: no range reduction, and far positions lose
-// nothing. The phase's upper 32 bits give the angle to 2^-25 of a half turn
-// (it is rounded to fp32 for sincospif): 1e-7 radians.
+// phase of that fraction at any int32 position: no range reduction. The
+// phase's upper 32 bits give the angle to 2^-25 of a half turn (it is rounded
+// to fp32 for sincospif), 1e-7 radians; the fraction's own rounding adds 4e-7
+// at position 2^31 (2^-53 of f / 2 pi a position, f = 1).
 #include <cmath>
 #include <new>
 
@@ -391,10 +392,10 @@ __global__ void __launch_bounds__(256, kMinCtas) rope_append_vec(const __grid_co
 // soonest while the grid is a few waves; with more, the angles and the start
 // of a CTA are paid for too often (64 / 8 heads, d = 128, one token against
 // four per CTA: bf16 2048 tokens 15.9 / 19.8 us, 4096 tokens 36.9 / 32.2 us;
-// FP8 1024 tokens 12.4 / 14.7, 1536 tokens 17.6 / 15.2; fp32 4096 tokens 52 /
+// FP8 1280 tokens 14.5 / 16.0, 1536 tokens 17.1 / 16.4; fp32 4096 tokens 52 /
 // 58, 16384 tokens equal).
 template <typename T, bool kFP8>
-constexpr int kTileFrom = kFP8 ? 1280 : sizeof(T) == 2 ? 2560 : 8192;
+constexpr int kTileFrom = kFP8 ? 1440 : sizeof(T) == 2 ? 2560 : 8192;
 
 template <typename T, bool kFP8, bool kAdjacent>
 cudaError_t launch_rope_vec(const RopeArgs &a, cudaStream_t st) {

@@ -281,11 +281,12 @@ struct Weights {
 // sums that its lanes kept; and its CTA finds the token there. (One warp
 // alone takes 5 us longer for that: its instructions wait on each other.)
 //
-// Bound by memory and, by half as much, by the 20 instructions a pair of
-// values takes; before and after the row comes a fixed 5 us of dependent
-// loads and barriers. 64 sequences, 150000 fp32 values: 18.7 us, of which
-// 11.3 are the rows' bytes at the copy rate; 256 of 131000 bf16 values,
-// greedy: 19.4 us and 9.9; one sequence of 100003: 6.1 us on the device.
+// Bound by memory while a row is read (64 sequences, 150000 fp32 values: 10
+// us of 17.9, for 11.3 of bytes at the copy rate less what L2 holds; 256 of
+// 131000 bf16 values, greedy: 10 to 11 of 18.3, for 9.9); before and after
+// comes a fixed 5 to 6 us of dependent loads and barriers: the launch 2, the
+// tests 1, the CTAs' sums 1.5, the token 2. One sequence of 100003 takes 6.1
+// us on the device.
 template <typename T>
 __global__ void __launch_bounds__(32 * kWarps, 2) verify_draft(const __grid_constant__ VerifyArgs a) {
     __shared__ uint64_t s_cta[2][kMaxCluster][2];  // sums of the cluster's CTAs (low, high), both passes

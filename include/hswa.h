@@ -94,10 +94,11 @@ extern "C" {
  * v_scale [pages][Hkv][P][d / 128] fp32. q, o and the new K/V handed to the
  * append stay bf16; the append quantizes: scale = amax / 448 (1 if amax is
  * 0), code = round-to-nearest-even(x / scale) saturating at 448. Supported
- * by hswa_append_kv, hswa_decode, hswa_decode_append, hswa_decode_multi
- * (d = 128, 8 query heads per kv head, P = 64), hswa_prefill_chunk_ws (d = 128, an even
+ * by hswa_append_kv, hswa_rope_append (d = 128), hswa_decode,
+ * hswa_decode_append, hswa_decode_multi, hswa_decode_weights (d = 128, 8
+ * query heads per kv head, P = 64), hswa_prefill_chunk_ws (d = 128, an even
  * number of query heads per kv head, P = 64) and hswa_swa_gather /
- * hswa_swa_scatter (d = 128, P = 64); other calls return
+ * hswa_swa_scatter (d = 128, P = 64); other calls on layers return
  * HSWA_ERR_UNSUPPORTED. */
 #define HSWA_DTYPE_FP8_E4M3 2
 
@@ -184,9 +185,9 @@ int hswa_swa_restore(hswa_pool *pool, int n, const int32_t *seq_ids, int32_t *n_
  * AMD Instinct MI355X", EAGLE3 adds a second decode loop: multi-token
  * verification). new_len[i] in [0, length] becomes the length of seq_ids[i]
  * (distinct, any order); pages that hold none of the tokens left are let go
- * of, Full pages and SWA pages each in ascending (sequence, page) order, those no one else holds
- * going to the tail of their free list. Two states cannot be taken back to
- * and are refused (HSWA_ERR_INVALID_ARG, no change): a length that ends
+ * of, Full pages and SWA pages each in ascending (sequence, page) order,
+ * those no one else holds going to the tail of their free list. Two states
+ * cannot be taken back to and are refused (HSWA_ERR_INVALID_ARG, no change): a length that ends
  * inside a page with another holder (a cached prefix: the next token would
  * be written into the other holder's page), and one whose last W positions
  * lie on a page whose SWA page was released (hswa_swa_release keeps the last
@@ -204,9 +205,9 @@ int hswa_seq_truncate(hswa_pool *pool, int n, const int32_t *seq_ids, const int3
  * dropped only if all its tokens are older than the last W ((p + 1) * P <=
  * length - W, the release rule), so the window of the SWA layers stays what
  * it was; a dropped page's SWA page, if it still has one, is let go of too.
- * Pages are let go of in ascending (sequence, page) order, Full and SWA each. A list that is
- * not ascending, names a page past the last one or drops a page inside the
- * window is refused (HSWA_ERR_INVALID_ARG) with no change to any sequence.
+ * Pages are let go of in ascending (sequence, page) order, Full and SWA each.
+ * A list that is not ascending, names a page past the last one or drops a
+ * page inside the window is refused (HSWA_ERR_INVALID_ARG) with no change to any sequence.
  * Afterwards positions in the cache are no longer positions in the text:
  * the attention calls count cache positions, hswa_rope_append is given the
  * text's. Pages from the first dropped one on no longer follow from the
@@ -372,8 +373,9 @@ int hswa_rope_destroy(hswa_rope *rope);
  * slot of the layer kind's pool gets K's rows turned and V's rows as they
  * are. Pair i of a head, (x, y), becomes (x cos - y sin, y cos + x sin) of
  * the angle d_pos[axis(i)][t] * frequency(i); elements from R on pass
- * through. Angles are exact to about 1e-7 radians at any int32 position,
- * the arithmetic is fp32, and each result is rounded once, to the element
+ * through. Angles are exact to about 1e-7 radians at positions up to 2^26
+ * and 5e-7 at any int32 position (frequencies of at most 1 radian a
+ * position; in proportion beyond), the arithmetic is fp32, and each result is rounded once, to the element
  * type; for FP8 pools the turned K row is quantized as it is in fp32 (scale
  * = amax / 448 as for hswa_append_kv, without a rounding to bf16 between).
  * q, k, v: device, token t's heads at element t * stride, so that they may
@@ -431,13 +433,15 @@ size_t hswa_decode_weights_workspace_size(const hswa_pool *pool, int n_seqs);
  * in fp32 (the sum over all query heads and the page's keys; a row gains
  * Hq), and w_out[i][p] = 0 for every later p, so that pages added later
  * start from nothing. w_in, w_out: device float [n_seqs][max_pages_per_seq];
- * they may be the same; w_in NULL or decay 0 starts anew whatever w_in
- * holds. Several layers add up by calls with the same w_in = w_out (decay
+ * they may be the same (an overlap otherwise is HSWA_ERR_INVALID_ARG); w_in
+ * NULL or decay 0 starts anew whatever w_in holds. Several layers add up by calls with the same w_in = w_out (decay
  * on a step's first layer, 1 on the others). Sums have a fixed order: equal
  * inputs give equal bits. The attention output is hswa_decode's. All pool
  * dtypes and shapes that hswa_decode takes (head_dim at most 256, n_seqs at
- * most 65535); an SWA layer is HSWA_ERR_INVALID_ARG. A page skipped for its
- * table entry (HSWA_ERR_BOUNDS) weighs nothing. ws: device, 256-byte
+ * most 65535; on bf16 and FP8 pools of d = 128, P = 64 and 8 query heads per
+ * kv head Hq at most 2048); an SWA layer is HSWA_ERR_INVALID_ARG. A page
+ * skipped for its table entry (HSWA_ERR_BOUNDS) weighs nothing; the keys of a
+ * length past the table's last page are left out (HSWA_ERR_BOUNDS). ws: device, 256-byte
  * aligned, of at least hswa_decode_weights_workspace_size bytes, on every
  * path. */
 int hswa_decode_weights(const hswa_pool *pool, const hswa_layer *layer, const void *q, void *o,
@@ -455,8 +459,9 @@ int hswa_decode_weights(const hswa_pool *pool, const hswa_layer *layer, const vo
  * device int32 [n_seqs][max_pages_per_seq], the pages that stay in
  * ascending order, then -1; n_keep: device int32 [n_seqs]; w_out: device
  * float like w_in, the weights of the pages that stay, closed up to match
- * the tables after hswa_evict, then 0. w_out may be w_in. hswa_evict, with
- * host copies of keep and n_keep, does the rest. */
+ * the tables after hswa_evict, then 0. w_out may be w_in (an overlap
+ * otherwise is HSWA_ERR_INVALID_ARG). hswa_evict, with host copies of keep
+ * and n_keep, does the rest. */
 int hswa_evict_select(const hswa_pool *pool, const int32_t *d_seq_len, const float *w_in, const int32_t *d_budget,
                       int n_seqs, int sink_pages, int recent_tokens, int32_t *keep, int32_t *n_keep, float *w_out,
                       hswa_stream_t stream);
@@ -515,10 +520,11 @@ int hswa_decode_multi(const hswa_pool *pool, const hswa_layer *layer, const void
  * q_stride (>= vocab) elements apart. For the draw, values are clamped to
  * [0, 1] (NaN: 0) and rounded to whole steps of 2^-50 (fp32) or 2^-45
  * (bf16), whose sums are exact: the token does not depend on the order of
- * summation. Rows need not add up to exactly 1. u outside [0, 1) counts as the nearest inside. A draft
- * outside [0, vocab) is refused and d_n_draft outside its range clamped,
- * each setting HSWA_ERR_BOUNDS on the device. n_tok in [1,
- * HSWA_DECODE_MAX_TOKENS]; d_draft and q may be NULL for n_tok = 1. */
+ * summation. Rows need not add up to exactly 1. u outside [0, 1) counts as
+ * the nearest inside for the draw. A draft outside [0, vocab) is refused and
+ * d_n_draft outside its range clamped, each setting HSWA_ERR_BOUNDS on the
+ * device. n_tok in [1, HSWA_DECODE_MAX_TOKENS]; d_draft and q may be NULL for
+ * n_tok = 1. */
 int hswa_verify_draft(int dtype, const void *p, int64_t p_stride, const void *q, int64_t q_stride,
                       const int32_t *d_draft, const int32_t *d_n_draft, const float *u, int n_seqs, int n_tok,
                       int vocab, int32_t *n_accept, int32_t *tokens, hswa_stream_t stream);
