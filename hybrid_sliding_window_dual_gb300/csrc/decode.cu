@@ -1766,9 +1766,10 @@ __global__ void __launch_bounds__(Smem::kThreads, 1)
 // Merge the partial records of a segment split between CTAs (sequence s, query
 // token w, kv head g; 256 threads, a warp per head); write zeros for a
 // sequence without keys. A warp's lanes look at 32 records' maxima and sums
-// at once, then all take the records in order, 4 in flight. (Three short
-// sequences are cut into up to 20 pieces a head: a loop over the records that
-// found each with 64-bit divisions made their decode step 27 us, this 12.6.)
+// at once, then all take the records in order, 4 in flight (8 spill at the
+// registers that keep 4 blocks on an SM: 0.6 us more). (Three short sequences
+// are cut into up to 20 pieces a head: a loop over the records that found each
+// with 64-bit divisions made their decode step 27 us, this 12.2.)
 __device__ void merge_segment(const DecodeArgs &a, int32_t n_ctas, int32_t s, int32_t w, int32_t g) {
     const int64_t U = a.sdesc[a.n_seqs].x, N = n_ctas;
     const int4 d = a.sdesc[s];
@@ -1790,27 +1791,32 @@ __device__ void merge_segment(const DecodeArgs &a, int32_t n_ctas, int32_t s, in
     const auto record = [&](int32_t i) {
         return a.part + ((c_lo + i) * 2 + (i == 0 ? first_slot : 0)) * a.n_tok + w;
     };
+    constexpr int kAhead = 4;
     const auto there = [&](int32_t i) {
         return i < n && (U >= N || cta_start(c_lo + i, U, N) != cta_start(c_lo + i + 1, U, N));
     };
-    float M = -INFINITY;
-    for (int32_t i = lane; i < n; i += 32)
+    // the lane's record of the first 32
+    const bool first_there = there(lane);
+    const float m0 = first_there ? record(lane)->m[h] : -INFINITY, l0 = first_there ? record(lane)->l[h] : 0.f;
+    float M = m0;
+    for (int32_t i = 32 + lane; i < n; i += 32)
         if (there(i)) M = fmaxf(M, record(i)->m[h]);
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
     for (int32_t i0 = 0; i0 < n; i0 += 32) {
-        const bool mine = there(i0 + lane);
-        const float m = mine ? record(i0 + lane)->m[h] : -INFINITY, l = mine ? record(i0 + lane)->l[h] : 0.f;
+        const bool mine = i0 == 0 ? first_there : there(i0 + lane);
+        const float m = i0 == 0 ? m0 : mine ? record(i0 + lane)->m[h] : -INFINITY;
+        const float l = i0 == 0 ? l0 : mine ? record(i0 + lane)->l[h] : 0.f;
         const float wt = m == -INFINITY ? 0.f : fast_exp2(m - M);
         const unsigned used = __ballot_sync(0xffffffffu, mine);
         const int32_t k = min(32, n - i0);
-        for (int32_t j = 0; j < k; j += 4) {
-            float4 o[4];
+        for (int32_t j = 0; j < k; j += kAhead) {
+            float4 o[kAhead];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < kAhead; ++e)
                 if (used >> (j + e) & 1) o[e] = *reinterpret_cast<const float4 *>(&record(i0 + j + e)->o[h][d0]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < kAhead; ++e) {
                 const float we = __shfl_sync(0xffffffffu, wt, (j + e) & 31), le = __shfl_sync(0xffffffffu, l, (j + e) & 31);
                 if (used >> (j + e) & 1) {
                     L += we * le;
@@ -1856,9 +1862,9 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return
 // added later start from nothing.
 //
 // Bound by memory, as the decode step is: 64 sequences of 1K to 32K, bf16 (64
-// / 8 heads): 649 us against 636 without the weights and 653 for the bytes at
-// the copy rate; 49 sequences, FP8: 284 against 266 and 257; three short ones
-// 13.0 against 12.6. What the weights cost the FP8 kernel, whose issue slots
+// / 8 heads): 648 us against 633 without the weights and 653 for the bytes at
+// the copy rate; 49 sequences, FP8: 281 against 265 and 257; three short ones
+// 12.6 against 12.2. What the weights cost the FP8 kernel, whose issue slots
 // are nearly full, is instructions: with the sums added up in the consumer
 // warps it was 358, and each page's 64-bit address and exact logarithm in the
 // producer made 295.
@@ -2328,6 +2334,10 @@ struct PageWeights {
     float decay;
 };
 
+// decode_plan's threads: no more warps at its barriers than the batch needs
+// (three sequences: the decode step 12.2 us, with 1024 threads 12.5).
+int plan_threads(int n_seqs) { return std::min(1024, (n_seqs + 31) / 32 * 32); }
+
 int64_t max_keys(const hswa_config &c, const PageWeights *pw) {
     return pw ? (int64_t)c.max_pages_per_seq * c.page_size : INT64_MAX;
 }
@@ -2435,7 +2445,7 @@ int decode_fp8(const hswa_pool *pool, const hswa_layer *layer, const void *q, vo
         (tc && !make_q_tmap(&tq, q, c, n_seqs, n_tok)))
         return HSWA_ERR_CUDA;
     set_last_kernel(tc ? "decode_tc_fp8_d128" : pw ? "decode_mma_fp8_d128+weights" : slots ? "append_kv_fp8+decode_mma_fp8_d128" : "decode_mma_fp8_d128");
-    cudaError_t e = launch_pdl(decode_plan, dim3(1), dim3(1024), 0, st, d_seq_len, n_seqs, c.n_kv_heads, kP,
+    cudaError_t e = launch_pdl(decode_plan, dim3(1), dim3(plan_threads(n_seqs)), 0, st, d_seq_len, n_seqs, c.n_kv_heads, kP,
                                a.window, n_tok, static_cast<int4 *>(ws), max_keys(c, pw), a.err);
     if (e == cudaSuccess) {
         if (tc)
@@ -2561,7 +2571,7 @@ int decode_impl(const hswa_pool *pool, const hswa_layer *layer, const void *q, v
     set_last_kernel(tc ? "decode_tc_bf16_d128" : pw ? "decode_mma_bf16_d128+weights" : fused ? "decode_mma_bf16_d128+append" : "decode_mma_bf16_d128");
     // three launches chained with programmatic dependent launch: each one
     // is scheduled while its predecessor finishes and waits for it on entry
-    if (launch_pdl(decode_plan, dim3(1), dim3(1024), 0, st, d_seq_len, n_seqs, c.n_kv_heads, kP, a.window, n_tok,
+    if (launch_pdl(decode_plan, dim3(1), dim3(plan_threads(n_seqs)), 0, st, d_seq_len, n_seqs, c.n_kv_heads, kP, a.window, n_tok,
                    static_cast<int4 *>(ws), max_keys(c, pw), a.err) != cudaSuccess)
         return HSWA_ERR_CUDA;
     cudaError_t e;
