@@ -282,7 +282,7 @@ struct Weights {
 // alone takes 5 us longer for that: its instructions wait on each other.)
 //
 // Bound by memory while a row is read (64 sequences, 150000 fp32 values: 10
-// us of 17.9, for 11.3 of bytes at the copy rate less what L2 holds; 256 of
+// us of 17.8, for 11.3 of bytes at the copy rate less what L2 holds; 256 of
 // 131000 bf16 values, greedy: 10 to 11 of 18.3, for 9.9); before and after
 // comes a fixed 5 to 6 us of dependent loads and barriers: the launch 2, the
 // tests 1, the CTAs' sums 1.5, the token 2. One sequence of 100003 takes 6.1
