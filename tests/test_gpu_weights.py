@@ -196,6 +196,22 @@ def test_decode_weights_of_lengths_past_the_table(dtype, excess):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP8, F32])
+def test_decode_weights_of_the_first_sequences(dtype):
+    # fewer sequences than the tables have rows: the others' rows are left alone
+    P = 64 if dtype != F32 else 16
+    c = Case([300, 70, 1000, 5], *((16, 2, 128, P) if dtype != F32 else (4, 2, 64, P)), dtype, seed=14)
+    exact_o, exact_w = c.exact()
+    for n in (0, 1, 3):
+        o, w = torch.full_like(c.q, 9), torch.full((c.S, c.mp), 9.0, device="cuda")
+        c.sess.decode_weights(0, c.q, o, n, c.scale, None, 0, w)
+        assert c.sess.check() == 0
+        assert (np.abs(w[:n].double().cpu().numpy() - exact_w[:n]) <= 2.5e-4 * exact_w[:n] + 1e-6).all()
+        assert n == 0 or np.abs(o[:n].double().cpu().numpy() - exact_o[:n]).max() <= (1e-5 if dtype == F32 else 2e-2)
+        assert (w[n:] == 9).all() and (o[n:] == 9).all()
+
+
+@pytest.mark.gpu
 def test_decode_weights_two_calls_at_once():
     # two streams, a workspace each; then two captured calls that share one, in turn
     a, b = Case([3000, 70, 900], 64, 8, 128, 64, BF16, seed=12), Case([12000], 64, 8, 128, 64, BF16, seed=13)
