@@ -1769,7 +1769,8 @@ __global__ void __launch_bounds__(Smem::kThreads, 1)
 // at once, then all take the records in order, 4 in flight (8 spill at the
 // registers that keep 4 blocks on an SM: 0.6 us more). (Three short sequences
 // are cut into up to 20 pieces a head: a loop over the records that found each
-// with 64-bit divisions made their decode step 27 us, this 12.2.)
+// with 64-bit divisions made their decode step 27 us, this 12.2, merge_heads
+// 11.3.)
 __device__ void merge_segment(const DecodeArgs &a, int32_t n_ctas, int32_t s, int32_t w, int32_t g) {
     const int64_t U = a.sdesc[a.n_seqs].x, N = n_ctas;
     const int4 d = a.sdesc[s];
@@ -1838,6 +1839,106 @@ __global__ void __launch_bounds__(256, 4) decode_combine(DecodeArgs a, int32_t n
     merge_segment(a, n_ctas, blockIdx.y / a.n_tok, blockIdx.y % a.n_tok, blockIdx.x);
 }
 
+// cta_start with 32-bit divisions: U < 2^31, N < 2^16.
+__device__ __forceinline__ int64_t share_start(uint32_t c, int64_t U, uint32_t N) {
+    const uint32_t q = (uint32_t)U / N, r = (uint32_t)U % N;
+    return (int64_t)c * q + c * r / N;
+}
+
+// The pieces of a segment [lo, hi) of units: CTAs c_lo .. c_hi, or, with fewer
+// units than CTAs, one CTA a unit (the CTAs between have none).
+struct Pieces {
+    int64_t lo, U, c_lo;
+    int32_t n_ctas, n;
+
+    __device__ Pieces(int64_t lo_, int64_t hi, int64_t U_, int32_t n_ctas_) : lo(lo_), U(U_), n_ctas(n_ctas_) {
+        c_lo = cta_of(lo, U, n_ctas);
+        n = (int32_t)(U < n_ctas ? hi - lo : cta_of(hi - 1, U, n_ctas) - c_lo + 1);
+    }
+    // record of piece i: its CTA's first or second
+    __device__ int32_t record(int32_t i) const {
+        if (U < n_ctas) return (int32_t)cta_of(lo + i, U, n_ctas) * 2;
+        const int64_t c = c_lo + i;
+        return (int32_t)(c * 2 + (i == 0 && share_start((uint32_t)c, U, n_ctas) < lo ? 1 : 0));
+    }
+};
+
+// The same merge for segments of many pieces, as few segments are: half a
+// block (128 threads, one d each) per head, the records' weights through
+// shared memory, 32 records in flight. The records are added up in the same
+// order: equal bits. Two sequences of 1566 and 14213 keys on one kv head, up to
+// 220 pieces: the decode step 15 us, by merge_segment 47; three up to 2515
+// keys 9.3 and 27. (With the pieces found among all CTAs between, and a test at
+// each record whether there is one, 34 and 23.)
+constexpr int kMergeHeads = 2;  // heads of a block
+constexpr int kMergeAhead = 32;
+
+// per head: (weight, sum) and place of each piece
+__host__ __device__ inline int merge_pieces(int n_ctas) { return (n_ctas + kMergeAhead - 1) / kMergeAhead * kMergeAhead; }
+size_t merge_heads_smem(int n_ctas) { return kMergeHeads * merge_pieces(n_ctas) * (sizeof(float2) + sizeof(int32_t)); }
+
+__device__ void merge_heads(const DecodeArgs &a, int32_t n_ctas, int32_t s, int32_t w, int32_t g, int32_t pair, float4 *smem) {
+    __shared__ float s_top[8];
+    const int64_t U = a.sdesc[a.n_seqs].x;
+    const int4 d = a.sdesc[s];
+    const int t = threadIdx.x & 127, half = threadIdx.x >> 7, h = pair * kMergeHeads + half;
+    const int32_t room = merge_pieces(n_ctas);
+    float2 *piece = reinterpret_cast<float2 *>(smem) + half * room;
+    int32_t *at = reinterpret_cast<int32_t *>(reinterpret_cast<float2 *>(smem) + kMergeHeads * room) + half * room;
+    __nv_bfloat16 *out = a.o + (q_row(a, s, w) * a.hq + (int64_t)g * kG + h) * kD + t;
+    if (d.w == 0) {
+        *out = __float2bfloat16_rn(0.f);
+        return;
+    }
+    const int32_t npg = d.w / a.hkv;
+    const int64_t lo = d.x + (int64_t)g * npg;
+    const Pieces pieces(lo, lo + npg, U, n_ctas);
+    const int32_t n = pieces.n;
+    if (n == 1) return;
+    float M = -INFINITY;
+    for (int32_t i = t; i < n; i += 128) {
+        const int32_t r = pieces.record(i) * a.n_tok + w;
+        const float m = a.part[r].m[h];
+        piece[i] = make_float2(m, a.part[r].l[h]);
+        at[i] = r;
+        M = fmaxf(M, m);
+    }
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    if ((t & 31) == 0) s_top[threadIdx.x >> 5] = M;
+    __syncthreads();
+    for (int i = 0; i < 4; ++i) M = fmaxf(M, s_top[half * 4 + i]);
+    for (int32_t i = t; i < n; i += 128) piece[i].x = piece[i].x == -INFINITY ? 0.f : fast_exp2(piece[i].x - M);
+    __syncthreads();
+    float L = 0.f, acc = 0.f;
+    const auto add = [&](int32_t i0, auto whole) {
+        float o[kMergeAhead];
+#pragma unroll
+        for (int e = 0; e < kMergeAhead; ++e)
+            o[e] = whole || i0 + e < n ? a.part[at[i0 + e]].o[h][t] : 0.f;
+#pragma unroll
+        for (int e = 0; e < kMergeAhead; ++e)
+            if (whole || i0 + e < n) {
+                const float2 x = piece[i0 + e];
+                L += x.x * x.y;
+                acc += x.x * o[e];
+            }
+    };
+    int32_t i0 = 0;
+    for (; i0 + kMergeAhead <= n; i0 += kMergeAhead) add(i0, std::true_type());
+    if (i0 < n) add(i0, std::false_type());
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    *out = __float2bfloat16_rn(acc * inv);
+}
+
+__global__ void __launch_bounds__(256) decode_combine_heads(DecodeArgs a, int32_t n_ctas) {
+    extern __shared__ float4 smem_f4[];
+    pdl_wait();
+    pdl_launch_dependents();
+    constexpr int kPairs = kG / kMergeHeads;
+    merge_heads(a, n_ctas, blockIdx.y / a.n_tok, blockIdx.y % a.n_tok, blockIdx.x / kPairs, blockIdx.x % kPairs,
+                smem_f4);
+}
+
 // ----------------------------------------------------------- generic path
 template <typename T>
 __device__ __forceinline__ float to_f(T x);
@@ -1862,9 +1963,9 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return
 // added later start from nothing.
 //
 // Bound by memory, as the decode step is: 64 sequences of 1K to 32K, bf16 (64
-// / 8 heads): 648 us against 633 without the weights and 653 for the bytes at
+// / 8 heads): 646 us against 634 without the weights and 653 for the bytes at
 // the copy rate; 49 sequences, FP8: 281 against 265 and 257; three short ones
-// 12.6 against 12.2. What the weights cost the FP8 kernel, whose issue slots
+// 12.5 against 11.3. What the weights cost the FP8 kernel, whose issue slots
 // are nearly full, is instructions: with the sums added up in the consumer
 // warps it was 358, and each page's 64-bit address and exact logarithm in the
 // producer made 295.
@@ -1886,7 +1987,7 @@ __device__ __forceinline__ void store_weight(const WeightArgs &a, int64_t at, fl
 }
 
 // The end of a decode step with page weights on the 8-heads kernels, as one
-// launch: the first n_merge blocks merge split segments (merge_segment), the
+// launch: the first n_merge blocks merge split segments (as decode_combine), the
 // others take kWeightPages pages of a sequence each. Such a block first joins
 // the log-sums of the pieces that each head's keys were split into, 4 lanes a
 // head (there are as many as CTAs shared the segment: 1 to 3 in a batch, 40
@@ -1899,14 +2000,21 @@ __device__ __forceinline__ void store_weight(const WeightArgs &a, int64_t at, fl
 constexpr int kWeightPages = 64;
 constexpr int kMaxWeightHeads = 2048;  // query heads whose log-sums fit shared memory
 
-__global__ void __launch_bounds__(256, 4) decode_finish_weights(DecodeArgs a, int32_t n_ctas, int32_t n_merge,
+template <bool kHeads>
+__global__ void __launch_bounds__(256, kHeads ? 2 : 4) decode_finish_weights(DecodeArgs a, int32_t n_ctas, int32_t n_merge,
                                                              int32_t chunks, const __grid_constant__ WeightArgs wa) {
     extern __shared__ float4 smem_f4[];
     float *all = reinterpret_cast<float *>(smem_f4);  // [Hq]
     pdl_wait();
     pdl_launch_dependents();
     if ((int32_t)blockIdx.x < n_merge) {
-        merge_segment(a, n_ctas, blockIdx.x / a.hkv, 0, blockIdx.x % a.hkv);
+        if constexpr (kHeads) {
+            constexpr int kPairs = kG / kMergeHeads;
+            const int32_t seg = blockIdx.x / kPairs;
+            merge_heads(a, n_ctas, seg / a.hkv, 0, seg % a.hkv, blockIdx.x % kPairs, smem_f4);
+        } else {
+            merge_segment(a, n_ctas, blockIdx.x / a.hkv, 0, blockIdx.x % a.hkv);
+        }
         return;
     }
     const int32_t s = (blockIdx.x - n_merge) / chunks, first = (blockIdx.x - n_merge) % chunks * kWeightPages;
@@ -1916,47 +2024,63 @@ __global__ void __launch_bounds__(256, 4) decode_finish_weights(DecodeArgs a, in
     const int64_t row = (int64_t)s * wa.max_pages;
     const int sub = threadIdx.x & 7;
     if (first < npg) {
-        const int64_t U = a.sdesc[a.n_seqs].x, N = n_ctas;
-        const int part = threadIdx.x & 3;
-        for (int32_t h0 = 0; h0 < a.hq; h0 += 64) {  // whole warps: 8 query heads to a kv head
-            const int32_t h = h0 + (threadIdx.x >> 2);
+        const int64_t U = a.sdesc[a.n_seqs].x;
+        // the pages' log-sums of this thread's first kv head and the weights
+        // so far, on their way while the sequence's log-sums are made
+        const float4 *lse = reinterpret_cast<const float4 *>(wa.page_lse) + (int64_t)s * a.hkv * wa.max_pages * 2;
+        constexpr int kRounds = kWeightPages / 32;
+        const bool carry = wa.w_in && wa.decay != 0.f;
+        float4 y[kRounds][2];
+        float so_far[kRounds];
+#pragma unroll
+        for (int k = 0; k < kRounds; ++k) {
+            const int32_t p = first + k * 32 + (threadIdx.x >> 3);
+            const bool there = p < npg && sub < a.hkv;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                y[k][i] = there ? lse[((int64_t)sub * wa.max_pages + p) * 2 + i] : make_float4(0.f, 0.f, 0.f, 0.f);
+            so_far[k] = p < npg && sub == 0 && carry ? wa.w_in[row + p] : 0.f;
+        }
+        // lanes of a head: all of the block for 8 heads
+        const int lanes = !kHeads || a.hq > 32 ? 4 : a.hq > 16 ? 8 : a.hq > 8 ? 16 : 32;
+        const int part = threadIdx.x & (lanes - 1);
+        for (int32_t h0 = 0; h0 < a.hq; h0 += 256 / lanes) {  // whole warps: 8 query heads to a kv head
+            const int32_t h = h0 + threadIdx.x / lanes;
             float top = -INFINITY, sum = 0.f;
             if (h < a.hq) {
-                const int64_t lo = d.x + (int64_t)(h / kG) * npg, c_lo = cta_of(lo, U, N), c_hi = cta_of(lo + npg - 1, U, N);
-                if (c_lo == c_hi) {
+                const int64_t lo = d.x + (int64_t)(h / kG) * npg;
+                const Pieces pieces(lo, lo + npg, U, n_ctas);
+                if (pieces.n == 1) {
                     if (part == 0) top = a.seq_lse[(int64_t)s * a.hq + h], sum = 1.f;
                 } else {
-                    for (int64_t c = c_lo + part; c <= c_hi; c += 4) {
-                        if (U < N && cta_start(c, U, N) == cta_start(c + 1, U, N)) continue;  // no units
-                        const int slot = c == c_lo && cta_start(c, U, N) < lo ? 1 : 0;
-                        const float x = a.piece_lse[(c * 2 + slot) * kG + h % kG], n = fmaxf(top, x);
+#pragma unroll 4
+                    for (int32_t i = part; i < pieces.n; i += lanes) {
+                        const float x = a.piece_lse[(int64_t)pieces.record(i) * kG + h % kG], n = fmaxf(top, x);
                         if (n > -INFINITY) sum = sum * exp2f(top - n) + exp2f(x - n), top = n;
                     }
                 }
             }
             float m = top;
-            for (int off = 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+            for (int off = lanes / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
             sum = top > -INFINITY ? sum * exp2f(top - m) : 0.f;
-            for (int off = 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            for (int off = lanes / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
             if (part == 0 && h < a.hq) all[h] = m > -INFINITY ? m + log2f(sum) : -INFINITY;
         }
         __syncthreads();
-        const float4 *lse = reinterpret_cast<const float4 *>(wa.page_lse) + (int64_t)s * a.hkv * wa.max_pages * 2;
+        const auto weigh = [&](float4 y, float4 x) {
+            return head_weight(y.x, x.x) + head_weight(y.y, x.y) + head_weight(y.z, x.z) + head_weight(y.w, x.w);
+        };
 #pragma unroll
-        for (int k = 0; k < kWeightPages / 32; ++k) {
+        for (int k = 0; k < kRounds; ++k) {
             const int32_t p = first + k * 32 + (threadIdx.x >> 3);
             float w = 0.f;
-            if (p < npg)
-                for (int32_t g = sub; g < a.hkv; g += 8) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float4 y = lse[((int64_t)g * wa.max_pages + p) * 2 + i];
-                        const float4 x = smem_f4[g * 2 + i];
-                        w += head_weight(y.x, x.x) + head_weight(y.y, x.y) + head_weight(y.z, x.z) + head_weight(y.w, x.w);
-                    }
-                }
+            if (p < npg && sub < a.hkv) {
+                w = weigh(y[k][0], smem_f4[sub * 2]) + weigh(y[k][1], smem_f4[sub * 2 + 1]);
+                for (int32_t g = sub + 8; g < a.hkv; g += 8)
+                    for (int i = 0; i < 2; ++i) w += weigh(lse[((int64_t)g * wa.max_pages + p) * 2 + i], smem_f4[g * 2 + i]);
+            }
             for (int off = 4; off > 0; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
-            if (sub == 0 && p < npg) store_weight(wa, row + p, w);
+            if (sub == 0 && p < npg) wa.w_out[row + p] = carry ? fmaf(wa.decay, so_far[k], w) : w;
         }
     }
     for (int32_t p = max(first, npg) + threadIdx.x; p < end; p += blockDim.x) wa.w_out[row + p] = 0.f;
@@ -2335,7 +2459,7 @@ struct PageWeights {
 };
 
 // decode_plan's threads: no more warps at its barriers than the batch needs
-// (three sequences: the decode step 12.2 us, with 1024 threads 12.5).
+// (three sequences: 0.3 us less than with 1024 threads).
 int plan_threads(int n_seqs) { return std::min(1024, (n_seqs + 31) / 32 * 32); }
 
 int64_t max_keys(const hswa_config &c, const PageWeights *pw) {
@@ -2347,11 +2471,30 @@ WeightArgs weight_args(const PageWeights &pw, const hswa_config &c, const int32_
             c.n_q_heads / c.n_kv_heads, c.page_size, c.max_pages_per_seq};
 }
 
+// Segments of 4 pieces or more (about: lengths differ) are merged head by
+// head. Decode steps of bf16, 304 CTAs, so and otherwise: 24 segments 11.3 / 12.1
+// us, 64 35.6 / 36.4, 128 60.2 / 59.3, 240 56.3 / 52.
+bool merge_by_heads(int64_t segments, int n_ctas) { return segments * 4 <= n_ctas; }
+
 cudaError_t launch_finish_weights(const PageWeights &pw, const hswa_config &c, const DecodeArgs &a, int n_ctas,
                                   cudaStream_t st) {
-    const int32_t n_merge = a.n_seqs * c.n_kv_heads, chunks = (c.max_pages_per_seq + kWeightPages - 1) / kWeightPages;
-    return launch_pdl(decode_finish_weights, dim3(n_merge + a.n_seqs * chunks), dim3(256),
-                      c.n_q_heads * sizeof(float), st, a, n_ctas, n_merge, chunks, weight_args(pw, c, a.seq_len));
+    const int32_t segments = a.n_seqs * c.n_kv_heads, chunks = (c.max_pages_per_seq + kWeightPages - 1) / kWeightPages;
+    const size_t smem = c.n_q_heads * sizeof(float);
+    if (merge_by_heads(segments, n_ctas)) {
+        const int32_t n_merge = segments * (kG / kMergeHeads);
+        return launch_pdl(decode_finish_weights<true>, dim3(n_merge + a.n_seqs * chunks), dim3(256),
+                          std::max(smem, merge_heads_smem(n_ctas)), st, a, n_ctas, n_merge, chunks,
+                          weight_args(pw, c, a.seq_len));
+    }
+    return launch_pdl(decode_finish_weights<false>, dim3(segments + a.n_seqs * chunks), dim3(256), smem, st, a, n_ctas,
+                      segments, chunks, weight_args(pw, c, a.seq_len));
+}
+
+cudaError_t launch_combine(const hswa_config &c, const DecodeArgs &a, int n_ctas, cudaStream_t st) {
+    if (merge_by_heads((int64_t)a.n_seqs * c.n_kv_heads * a.n_tok, n_ctas))
+        return launch_pdl(decode_combine_heads, dim3(c.n_kv_heads * (kG / kMergeHeads), a.n_seqs * a.n_tok), dim3(256),
+                          merge_heads_smem(n_ctas), st, a, n_ctas);
+    return launch_pdl(decode_combine, dim3(c.n_kv_heads, a.n_seqs * a.n_tok), dim3(256), 0, st, a, n_ctas);
 }
 
 size_t desc_bytes(int n_seqs) { return ((size_t)(n_seqs + 1) * sizeof(int4) + 255) & ~(size_t)255; }
@@ -2462,7 +2605,7 @@ int decode_fp8(const hswa_pool *pool, const hswa_layer *layer, const void *q, vo
     }
     if (e == cudaSuccess)
         e = pw ? launch_finish_weights(*pw, c, a, n_ctas, st)
-               : launch_pdl(decode_combine, dim3(c.n_kv_heads, n_seqs * n_tok), dim3(256), 0, st, a, n_ctas);
+               : launch_combine(c, a, n_ctas, st);
     return e == cudaSuccess ? HSWA_OK : HSWA_ERR_CUDA;
 }
 
@@ -2586,7 +2729,7 @@ int decode_impl(const hswa_pool *pool, const hswa_layer *layer, const void *q, v
     }
     if (e == cudaSuccess)
         e = pw ? launch_finish_weights(*pw, c, a, n_ctas, st)
-               : launch_pdl(decode_combine, dim3(c.n_kv_heads, n_seqs * n_tok), dim3(256), 0, st, a, n_ctas);
+               : launch_combine(c, a, n_ctas, st);
     if (e != cudaSuccess) return HSWA_ERR_CUDA;
     return HSWA_OK;
 }

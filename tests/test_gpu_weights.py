@@ -212,6 +212,14 @@ def test_decode_weights_of_the_first_sequences(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+@pytest.mark.parametrize("hkv", [1, 2, 4, 8])
+@pytest.mark.parametrize("lens", [[1566, 14213], [64, 65, 3000, 1, 0], [30000], [20000, 700]], ids=str)
+def test_decode_weights_of_few_segments(lens, hkv, dtype):
+    Case(lens, 8 * hkv, hkv, 128, 64, dtype, seed=20 + hkv).check()
+
+
+@pytest.mark.gpu
 def test_decode_weights_two_calls_at_once():
     # two streams, a workspace each; then two captured calls that share one, in turn
     a, b = Case([3000, 70, 900], 64, 8, 128, 64, BF16, seed=12), Case([12000], 64, 8, 128, 64, BF16, seed=13)
