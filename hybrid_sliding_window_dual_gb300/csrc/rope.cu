@@ -390,17 +390,27 @@ __global__ void __launch_bounds__(256, kMinCtas) rope_append_vec(const __grid_co
 
 // Tokens from which a CTA takes kMaxTile of them. One token per CTA ends
 // soonest while the grid is a few waves; with more, the angles and the start
-// of a CTA are paid for too often (64 / 8 heads, d = 128, one token against
-// four per CTA: bf16 2048 tokens 15.9 / 19.8 us, 4096 tokens 36.9 / 32.2 us;
-// FP8 1280 tokens 14.5 / 16.0, 1536 tokens 17.1 / 16.4; fp32 4096 tokens 52 /
-// 58, 16384 tokens equal).
+// of a CTA are paid for too often, the sooner the less there is to do for a
+// token: `threads` is its rows times the threads of a row. One token a CTA
+// against four, us: 80 threads (8 / 1 heads, d = 128, bf16) 256 tokens 2.8 / 3.3,
+// 1024 5.2 / 3.9, 4096 15.7 / 9.3; 160 (16 / 2) 256 2.9 / 4.0, 1024 5.5 / 4.8; 320 (32
+// / 4) 1024 6.7 / 6.6, 2048 12.2 / 11.5; 640 (64 / 8) 2048 15.9 / 19.8, 4096 36.9 /
+// 32.2; fp32 32 / 4 heads 2048 13.3 / 16.8, 4096 32.4 / 32.0, 64 / 8 4096 52 / 58,
+// 16384 equal; FP8 32 / 4 1024 9.2 / 9.4, 2048 16.0 / 11.2, 64 / 8 1280 14.5 / 16.0, 1536
+// 17.1 / 16.4. (Up to 16 tokens a CTA for few heads gained nothing.)
 template <typename T, bool kFP8>
-constexpr int kTileFrom = kFP8 ? 1440 : sizeof(T) == 2 ? 2560 : 8192;
+int tile_from(int threads) {
+    if (threads <= 160) return 640;
+    if (threads <= 320) return 1024;
+    if (kFP8) return 1440;
+    return threads > 640 ? 8192 : sizeof(T) == 2 ? 2560 : 4096;
+}
 
 template <typename T, bool kFP8, bool kAdjacent>
 cudaError_t launch_rope_vec(const RopeArgs &a, cudaStream_t st) {
     const int units = (a.d / kVec<T> + 1) / 2;  // threads of a row
-    const bool tiled = a.n_tokens >= kTileFrom<T, kFP8>;
+    const int rows = a.hq + (kFP8 ? 1 : 2) * a.hkv;
+    const bool tiled = a.n_tokens >= tile_from<T, kFP8>(rows * units);
     const int64_t nq = tiled ? ((int64_t)a.n_tokens + kMaxTile - 1) / kMaxTile : a.n_tokens;
     const int64_t vt = tiled ? kVTile : 8;
     const int64_t nv = kFP8 ? (a.n_tokens + vt - 1) / vt * a.hkv : 0;

@@ -324,3 +324,14 @@ def test_rope_append_on_a_stream_and_in_a_graph():
     assert H.hswa_check() == 0
     c.check()
     H.hswa_pool_destroy(pool)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32, FP8])
+@pytest.mark.parametrize("T,hq,hkv", [(639, 8, 1), (643, 8, 1), (1023, 32, 4), (1025, 32, 4)])
+@pytest.mark.parametrize("adjacent", [False, True])
+def test_rope_append_around_the_tiles(T, hq, hkv, dtype, adjacent):
+    # one token a CTA and four, the last CTA's tokens fewer
+    c = Case(T, hq, hkv, 128, 64, dtype, 128, [24, 20, 20], adjacent=adjacent, seed=T)
+    assert c.run() == 0
+    c.check()
