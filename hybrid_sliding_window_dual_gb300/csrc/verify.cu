@@ -19,6 +19,7 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kMaxCluster = 8;  // CTAs per sequence
+constexpr int kMaxPart = 8192;  // positions of a warp
 
 typedef unsigned __int128 u128;
 
@@ -153,8 +154,11 @@ __device__ u128 times_fraction(u128 x, float u) {
 // 30 % slower on 64 sequences, 8 in place of 4 of each row 12 %).
 template <typename T>
 constexpr int kVec = 16 / (int)sizeof(T);
-template <bool kBoth>
-constexpr int kUnroll = kBoth ? 4 : 8;
+// Rows off a 16-byte boundary take one element a load, and twice as many loads
+// (183 sequences of 100003 fp32 values 36.6 us, with as many 50, with four times
+// as many 39; one row alone: 256 of 32001 bf16 9.9, with as many 10.6).
+template <bool kBoth, int kWide>
+constexpr int kUnroll = (kBoth ? 4 : 8) * (kWide == 1 ? 2 : 1);
 
 template <typename T>
 __device__ __forceinline__ void unpack(const uint4 &c, float (&x)[kVec<T>]) {
@@ -206,7 +210,7 @@ struct Weights {
     template <int kWide, bool kBoth>
     __device__ __forceinline__ uint64_t chunk(int32_t i0, int32_t hi) const {
         const int lane = threadIdx.x & 31;
-        constexpr int kUnroll = hswa::kUnroll<kBoth>;
+        constexpr int kUnroll = hswa::kUnroll<kBoth, kWide>;
         Steps<T> sum;
         if constexpr (kWide > 1) {
             uint4 a[kUnroll], b[kUnroll];
@@ -263,7 +267,7 @@ struct Weights {
         uint64_t total = 0;
         chunks[0] = chunks[1] = 0;
         int c = 0;
-        for (int32_t i0 = lo; i0 < hi; i0 += kUnroll<kBoth> * 32 * kWide, ++c) {
+        for (int32_t i0 = lo; i0 < hi; i0 += kUnroll<kBoth, kWide> * 32 * kWide, ++c) {
             uint64_t x = chunk<kWide, kBoth>(i0, hi);
             for (int m = 16; m > 0; m >>= 1) x += shfl_xor64(x, m);
             if (lane == c) chunks[0] = x;
@@ -378,7 +382,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) verify_draft(const __grid_cons
     for (int i = 0; i < warp; ++i) left -= s_warp[i];
     if (left < sum) {
         uint64_t t = (uint64_t)left;
-        const int32_t step = (w.q ? kUnroll<true> : kUnroll<false>) * 32 * (wide ? V : 1);
+        const int32_t step = wide ? (w.q ? kUnroll<true, V> : kUnroll<false, V>) * 32 * V
+                                  : (w.q ? kUnroll<true, 1> : kUnroll<false, 1>) * 32;
         int32_t c = 0;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {  // the chunk, among 32 at a time
@@ -402,7 +407,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) verify_draft(const __grid_cons
         }
     }
     __syncthreads();
-    // the token in the chunk (128 to 2048 positions): neighbours in a thread
+    // the token in the chunk (256 to 2048 positions): neighbours in a thread
     const int32_t each = (s_end - s_from + 32 * kWarps - 1) / (32 * kWarps);  // at most 4
     const int32_t i0 = s_from + threadIdx.x * each, end = min(i0 + each, s_end);
     uint64_t x[4], here = 0;
@@ -468,7 +473,7 @@ extern "C" int hswa_verify_draft(int dtype, const void *p, int64_t p_stride, con
     if (sms <= 0) return HSWA_ERR_CUDA;
     const auto part_of = [&](int c) { return ((vocab + c * kWarps - 1) / (c * kWarps) + 7) / 8 * 8; };
     a.cluster = 1;
-    while (a.cluster < kMaxCluster && (n_seqs * (int64_t)a.cluster * 2 <= 2 * sms || part_of(a.cluster) > 64 * kUnroll<true> * 32))
+    while (a.cluster < kMaxCluster && (n_seqs * (int64_t)a.cluster * 2 <= 2 * sms || part_of(a.cluster) > kMaxPart))
         a.cluster *= 2;
     a.part = part_of(a.cluster);
     cudaLaunchConfig_t cfg = {};
