@@ -155,8 +155,9 @@ __device__ u128 times_fraction(u128 x, float u) {
 template <typename T>
 constexpr int kVec = 16 / (int)sizeof(T);
 // Rows off a 16-byte boundary take one element a load, and twice as many loads
-// (183 sequences of 100003 fp32 values 36.6 us, with as many 50, with four times
-// as many 39; one row alone: 256 of 32001 bf16 9.9, with as many 10.6).
+// (183 sequences of 100003 fp32 values 41 us, with as many 50; 64 of bf16 12.3,
+// with as many 14.3, with four times as many 15.2; one row alone: 256 of 32001
+// bf16 9.6, with as many 10.6).
 template <bool kBoth, int kWide>
 constexpr int kUnroll = (kBoth ? 4 : 8) * (kWide == 1 ? 2 : 1);
 
@@ -278,6 +279,22 @@ struct Weights {
     }
 };
 
+// Slices of rows off a 16-byte boundary: of fp32 rows out of line, since the
+// registers of their loads cost the 16-byte path more (64 sequences of 150000
+// values 17.8 us, in line 19.0) than the call costs them (of 100003 14.5, in line
+// 13.2); of bf16 rows in line (18.2 and 19.0 on the greedy rows).
+template <typename T, bool kBoth>
+__device__ __noinline__ uint64_t narrow_call(const Weights<T> &w, int32_t lo, int32_t hi, uint64_t (&chunks)[2]) {
+    return w.template slice<1, kBoth>(lo, hi, chunks);
+}
+template <typename T, bool kBoth>
+__device__ __forceinline__ uint64_t narrow_slice(const Weights<T> &w, int32_t lo, int32_t hi, uint64_t (&chunks)[2]) {
+    if constexpr (sizeof(T) == 4)
+        return narrow_call<T, kBoth>(w, lo, hi, chunks);
+    else
+        return w.template slice<1, kBoth>(lo, hi, chunks);
+}
+
 // One cluster of a.cluster CTAs per sequence. Every CTA settles the
 // acceptance tests for itself (two rounds of loads); each warp sums its slice
 // of the row; the CTAs tell each other their sums through distributed shared
@@ -349,9 +366,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2) verify_draft(const __grid_cons
     while (true) {
         wide = (((uintptr_t)w.p | (uintptr_t)w.q) & 15) == 0;
         if (w.q)
-            sum = wide ? w.template slice<V, true>(lo, hi, chunks) : w.template slice<1, true>(lo, hi, chunks);
+            sum = wide ? w.template slice<V, true>(lo, hi, chunks) : narrow_slice<T, true>(w, lo, hi, chunks);
         else
-            sum = wide ? w.template slice<V, false>(lo, hi, chunks) : w.template slice<1, false>(lo, hi, chunks);
+            sum = wide ? w.template slice<V, false>(lo, hi, chunks) : narrow_slice<T, false>(w, lo, hi, chunks);
         if (lane == 0) s_warp[warp] = sum;
         if (pass == 0) cluster_wait();  // every CTA of the cluster has started
         __syncthreads();
