@@ -506,9 +506,11 @@ drain:
 }
 
 // Consumer side of a page's log-sum: this thread's sums w0, w1 of
-// 2^(score - b) in the S fragment layout (thread (g, q): heads 2q, 2q + 1).
-// Ordered before the producer's read by the arrival on the stage's empty
-// barrier.
+// 2^(score - b) in the S fragment layout (thread (g, q): heads 2q, 2q + 1). A
+// warp that has seen no key leaves b = -inf, so that the producer's common
+// maximum is one of scores: any number in its place could lie so far above
+// them that the page's sum underflows. Ordered before the producer's read by
+// the arrival on the stage's empty barrier.
 template <class Smem>
 __device__ __forceinline__ void leave_page_sums(Smem &sm, int stage, int warp, float b0, float b1, float w0, float w1) {
     const int lane = threadIdx.x & 31;
@@ -667,7 +669,7 @@ __device__ void decode_consumer(DecodeSmemT<kTok, kWeights> &sm, const DecodeArg
                 }
             }
         } else if constexpr (kWeights) {
-            leave_page_sums(sm, stage, 0, 0.f, 0.f, 0.f, 0.f);
+            leave_page_sums(sm, stage, 0, -INFINITY, -INFINITY, 0.f, 0.f);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.empty[stage]);
@@ -924,7 +926,7 @@ __device__ void decode_consumer_fp8(DecodeSmem8T<kTok, kWeights> &sm, const Deco
                 const float p2 = fast_exp2(sacc[j][2] - b0), p3 = fast_exp2(sacc[j][3] - b1);
                 l0[j] = l0[j] * al0 + 256.f * (p0 + p2);
                 l1[j] = l1[j] * al1 + 256.f * (p1 + p3);
-                if constexpr (kWeights) leave_page_sums(sm, stage, w, b0, b1, p0 + p2, p1 + p3);
+                if constexpr (kWeights) leave_page_sums(sm, stage, w, n0, n1, p0 + p2, p1 + p3);
                 pb0[j] = movmatrix_t(pack_f16(p0 * w0, p1 * w0));
                 pb1[j] = movmatrix_t(pack_f16(p2 * w1, p3 * w1));
                 if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {  // a head's max moved
@@ -952,7 +954,7 @@ __device__ void decode_consumer_fp8(DecodeSmem8T<kTok, kWeights> &sm, const Deco
                 for (int j = 0; j < kTok; ++j) mma_f16_16816(oacc[j][2 * dp + 1], a0, a1, a2, a3, pb0[j], pb1[j]);
             }
         } else if constexpr (kWeights) {
-            leave_page_sums(sm, stage, w, 0.f, 0.f, 0.f, 0.f);
+            leave_page_sums(sm, stage, w, -INFINITY, -INFINITY, 0.f, 0.f);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.empty[stage]);

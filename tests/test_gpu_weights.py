@@ -381,3 +381,31 @@ def test_select_split_rows(S, mp, kind):
     budget = rng.integers(0, mp, S)
     select(lens, w, budget, 16, 5, 200)
     select(lens[::-1], w, budget // 4, 16, 0, 128, in_place=True)
+
+
+# ------------------------------------------------- scores far below zero
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP8, F32])
+def test_decode_weights_of_scores_far_below_zero(dtype):
+    """A softmax does not change when every score moves by the same amount:
+    with K near -c q all of them are about -150, whatever part of a page is
+    used. A score is off by at most d 2^-24 sum |q k| scale, here 128 2^-24 200
+    = 1.6e-3, a weight by the exponential of the difference of two: 3.2e-3;
+    their logarithms, about 216 in powers of two, by 2^-17 each: 4e-3."""
+    c = Case([1, 17, 48, 64 * 3 + 3, 0, 16, 33, 64, 1000], *((16, 2, 128, 64) if dtype != F32 else (4, 2, 64, 16)), dtype, seed=31)
+    base = wl.normal((1, c.hkv, 1, c.d), 32, F32, "cuda")  # the queries of a kv head are nearly alike
+    c.q.copy_((base + 0.1 * wl.normal((c.S, c.hkv, c.hq // c.hkv, c.d), 33, F32, "cuda")).view(c.S, c.hq, c.d))
+    far = 150 / (c.scale * (base * base).sum(-1, keepdim=True))
+    k = wl.normal(tuple(c.sess.k[0].shape), 34, F32, "cuda") - far * base
+    if dtype == FP8:
+        c.sess.ks[0].fill_(0.125)
+        c.sess.k[0].copy_((k * 8).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8))
+    else:
+        c.sess.k[0].copy_(k)
+    o, w = c.run(None, 0)
+    assert c.sess.check() == 0
+    exact_o, exact_w = c.exact()
+    got = w.double().cpu().numpy()
+    assert (np.abs(got - exact_w) <= 4e-3 * exact_w + 1e-6).all()
+    assert np.allclose(got.sum(1)[c.lens > 0], c.hq, rtol=4e-3)  # a row gains every head's weight
+    assert np.abs(o.double().cpu().numpy() - exact_o).max() <= (4e-3 * np.abs(c.values("v")).max() if dtype == F32 else 3e-2)
