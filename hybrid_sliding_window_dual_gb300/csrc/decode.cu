@@ -1981,8 +1981,9 @@ struct WeightArgs {
     int32_t hkv, group, page, max_pages;
 };
 
-// Weight of a head on a page; nothing if the sequence saw nothing.
-__device__ __forceinline__ float head_weight(float page, float all) { return all > -INFINITY ? exp2f(page - all) : 0.f; }
+// Weight of a head on a page; nothing if the sequence saw nothing, NaN if its
+// scores have no softmax.
+__device__ __forceinline__ float head_weight(float page, float all) { return all == -INFINITY ? 0.f : exp2f(page - all); }
 
 __device__ __forceinline__ void store_weight(const WeightArgs &a, int64_t at, float w) {
     a.w_out[at] = a.w_in && a.decay != 0.f ? fmaf(a.decay, a.w_in[at], w) : w;
@@ -2195,6 +2196,7 @@ __global__ void __launch_bounds__(32 * kAnyWarps<kE>) decode_weights_any(const T
         acc[e] = 0.f;
     }
     float m = -INFINITY, l = 0.f;  // l: of this lane's keys
+    bool seen = false;             // a key
     const int32_t npg = min((int32_t)(((int64_t)L + page - 1) / page), bt_stride);
     if (L > (int64_t)bt_stride * page && threadIdx.x == 0) set_error(err, HSWA_ERR_BOUNDS);  // past its table
     int32_t next = warp < npg ? bt[s * bt_stride + warp] : -1;
@@ -2205,6 +2207,7 @@ __global__ void __launch_bounds__(32 * kAnyWarps<kE>) decode_weights_any(const T
         if (pg < 0 || pg >= num_pages) {
             if (lane == 0) set_error(err, HSWA_ERR_BOUNDS);
         } else {
+            seen = true;
             const int32_t n = min(page, L - p * page);
             const T *k0 = kp + ((int64_t)pg * hkv + g) * page * d + lane, *v0 = vp + (k0 - kp);
             for (int32_t r0 = 0; r0 < n; r0 += kKeys) {
@@ -2222,7 +2225,10 @@ __global__ void __launch_bounds__(32 * kAnyWarps<kE>) decode_weights_any(const T
                 }
                 const float sum = sum_lanes<kKeys>(dot);
                 const float score = r0 + value_of_lane<kKeys>() < n ? sum : -INFINITY;
-                const float nm = fmaxf(m, max_values<kKeys>(score)), alpha = exp2f(m - nm), x = exp2f(score - nm);
+                // -inf until there is a greater score than that: such keys weigh
+                // nothing. fmaxf passes a NaN over, the sums take it in.
+                const float nm = fmaxf(m, max_values<kKeys>(score)), base = nm == -INFINITY ? 0.f : nm;
+                const float alpha = exp2f(m - base), x = exp2f(score - base);
                 l = l * alpha + x;
                 pl = pl * alpha + x;
 #pragma unroll
@@ -2243,16 +2249,18 @@ __global__ void __launch_bounds__(32 * kAnyWarps<kE>) decode_weights_any(const T
     if (lane == 0) s_m[warp] = m, s_l[warp] = l;
 #pragma unroll
     for (int e = 0; e < kE; ++e) s_o[warp][lane + 32 * e] = acc[e];
-    __syncthreads();
+    const bool any = __syncthreads_or(seen);
     float M = -INFINITY, sum = 0.f;
     for (int w = 0; w < kW; ++w) M = fmaxf(M, s_m[w]);
-    for (int w = 0; w < kW; ++w) sum += s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - M) * s_l[w];
+    // a warp whose maximum is -inf has sums of 0, or NaN
+    for (int w = 0; w < kW; ++w) sum += s_m[w] == -INFINITY ? s_l[w] : exp2f(s_m[w] - M) * s_l[w];
+    if (any && M == -INFINITY) sum = NAN;  // every score is -inf or NaN
     if (threadIdx.x < d) {
         float out = 0.f;
-        for (int w = 0; w < kW; ++w) out += s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - M) * s_o[w][threadIdx.x];
-        o[row + threadIdx.x] = from_f<T>(sum > 0.f ? out / sum : 0.f);
+        for (int w = 0; w < kW; ++w) out += s_m[w] == -INFINITY ? s_o[w][threadIdx.x] : exp2f(s_m[w] - M) * s_o[w][threadIdx.x];
+        o[row + threadIdx.x] = from_f<T>(sum == 0.f ? 0.f : out / sum);  // 0: no keys
     }
-    if (threadIdx.x == 0) seq_lse[s * hq + h] = sum > 0.f ? M + log2f(sum) : -INFINITY;
+    if (threadIdx.x == 0) seq_lse[s * hq + h] = sum == 0.f ? -INFINITY : M + log2f(sum);
 }
 
 }  // namespace

@@ -409,3 +409,62 @@ def test_decode_weights_of_scores_far_below_zero(dtype):
     assert (np.abs(got - exact_w) <= 4e-3 * exact_w + 1e-6).all()
     assert np.allclose(got.sum(1)[c.lens > 0], c.hq, rtol=4e-3)  # a row gains every head's weight
     assert np.abs(o.double().cpu().numpy() - exact_o).max() <= (4e-3 * np.abs(c.values("v")).max() if dtype == F32 else 3e-2)
+
+
+# ------------------------------------------------------ NaN and infinities
+def same_with_nan(got, exact, tol_rel, tol_abs):
+    got = got.double().cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(exact))
+    fine = ~np.isnan(exact)
+    assert (np.abs(got - exact)[fine] <= (tol_rel * np.abs(exact) + tol_abs)[fine]).all()
+
+
+def check_nan(c, places):
+    """Break q ("q", sequence, head), one key ("k", sequence, position, kv
+    head), or a page's ("page", sequence, page, kv head): outputs and weights are
+    the oracle's, NaN where it has NaN, and a sequence that is not broken keeps
+    its bits."""
+    whole_o, whole_w = c.run(None, 0)
+    table = c.sess.d_full_bt.cpu().numpy()
+    k, broken = c.sess.k[0], set()
+    for (what, s, at, *rest), value in places:
+        broken.add(s)
+        if what == "q":
+            c.q[s, at, 3] = value
+        elif what == "page":
+            k[table[s, at], rest[0], :, 3] = value
+        elif c.dtype == FP8:
+            assert math.isnan(value)
+            k[table[s, at // c.P], rest[0], at % c.P, 3] = 0x7F
+        else:
+            k[table[s, at // c.P], rest[0], at % c.P, 3] = value
+    o, w = c.run(None, 0)
+    assert c.sess.check() == 0
+    with np.errstate(invalid="ignore"):
+        exact_o, exact_w = c.exact()
+    same_with_nan(o, exact_o, 0, 1e-5 if c.dtype == F32 else 2e-2)
+    same_with_nan(w, exact_w, 2.5e-4, 1e-6)
+    sound = [s for s in range(c.S) if s not in broken]
+    assert torch.equal(o[sound], whole_o[sound]) and torch.equal(w[sound], whole_w[sound])
+    plain = torch.empty_like(o)
+    c.sess.decode(0, c.q, plain, c.S, c.scale)
+    return o, w, plain
+
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,d,P,dtype", [(4, 2, 64, 16, F32), (6, 2, 64, 16, BF16), (12, 2, 128, 64, F32), (3, 1, 256, 16, BF16)])
+def test_decode_weights_any_shape_keeps_nan(hq, hkv, d, P, dtype):
+    """A head with a NaN, or a score of +inf, has NaN for its output as
+    hswa_decode has, and for its weight on every page; a score of -inf weighs
+    nothing; all of them -inf leave NaN."""
+    lens = [300, 1, 700, 0, 40, 500, 333, 20]
+    c = Case(lens, hq, hkv, d, P, dtype, seed=41)
+    o, _, plain = check_nan(c, [(("q", 0, 1), NAN), (("q", 1, 0), NAN), (("k", 2, 650, 0), NAN), (("k", 4, 0, 0), NAN), (("k", 5, 499, 0), INF)])
+    assert torch.equal(torch.isnan(o), torch.isnan(plain)) and torch.isnan(o).any()
+    c = Case(lens, hq, hkv, d, P, dtype, seed=42)
+    c.q[..., 3] = c.q[..., 3].abs() + 0.5
+    check_nan(c, [(("k", 0, 17, 0), -INF), (("page", 2, 0, 0), -INF), (("page", 6, 1, 0), -INF)]
+              + [(("page", 7, p, 0), -INF) for p in range(-(-20 // P))])
