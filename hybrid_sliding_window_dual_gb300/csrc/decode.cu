@@ -1985,6 +1985,13 @@ struct WeightArgs {
 // scores have no softmax.
 __device__ __forceinline__ float head_weight(float page, float all) { return all == -INFINITY ? 0.f : exp2f(page - all); }
 
+// The greater of two log-sums; NaN if one of them is (fmaxf gives the other).
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float z;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+    return z;
+}
+
 __device__ __forceinline__ void store_weight(const WeightArgs &a, int64_t at, float w) {
     a.w_out[at] = a.w_in && a.decay != 0.f ? fmaf(a.decay, a.w_in[at], w) : w;
 }
@@ -2058,16 +2065,16 @@ __global__ void __launch_bounds__(256, kHeads ? 2 : 4) decode_finish_weights(Dec
                 } else {
 #pragma unroll 4
                     for (int32_t i = part; i < pieces.n; i += lanes) {
-                        const float x = a.piece_lse[(int64_t)pieces.record(i) * kG + h % kG], n = fmaxf(top, x);
-                        if (n > -INFINITY) sum = sum * exp2f(top - n) + exp2f(x - n), top = n;
+                        const float x = a.piece_lse[(int64_t)pieces.record(i) * kG + h % kG], n = max_nan(top, x);
+                        if (n != -INFINITY) sum = sum * exp2f(top - n) + exp2f(x - n), top = n;
                     }
                 }
             }
             float m = top;
-            for (int off = lanes / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-            sum = top > -INFINITY ? sum * exp2f(top - m) : 0.f;
+            for (int off = lanes / 2; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
+            sum = top != -INFINITY ? sum * exp2f(top - m) : 0.f;
             for (int off = lanes / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            if (part == 0 && h < a.hq) all[h] = m > -INFINITY ? m + log2f(sum) : -INFINITY;
+            if (part == 0 && h < a.hq) all[h] = m != -INFINITY ? m + log2f(sum) : -INFINITY;
         }
         __syncthreads();
         const auto weigh = [&](float4 y, float4 x) {

@@ -436,9 +436,10 @@ size_t hswa_decode_weights_workspace_size(const hswa_pool *pool, int n_seqs);
  * they may be the same (an overlap otherwise is HSWA_ERR_INVALID_ARG); w_in
  * NULL or decay 0 starts anew whatever w_in holds. Several layers add up by calls with the same w_in = w_out (decay
  * on a step's first layer, 1 on the others). Sums have a fixed order: equal
- * inputs give equal bits. The attention output is hswa_decode's. All pool
- * dtypes and shapes that hswa_decode takes (head_dim at most 256, n_seqs at
- * most 65535; on bf16 and FP8 pools of d = 128, P = 64 and 8 query heads per
+ * inputs give equal bits. The attention output is hswa_decode's. A head with
+ * a score of NaN or +inf has no softmax: its output is NaN, and so are the
+ * sequence's weights on all of its pages. All pool dtypes and shapes that
+ * hswa_decode takes (head_dim at most 256, n_seqs at most 65535; on bf16 and FP8 pools of d = 128, P = 64 and 8 query heads per
  * kv head Hq at most 2048); an SWA layer is HSWA_ERR_INVALID_ARG. A page
  * skipped for its table entry (HSWA_ERR_BOUNDS) weighs nothing; the keys of a
  * length past the table's last page are left out (HSWA_ERR_BOUNDS). ws: device, 256-byte

@@ -468,3 +468,23 @@ def test_decode_weights_any_shape_keeps_nan(hq, hkv, d, P, dtype):
     c.q[..., 3] = c.q[..., 3].abs() + 0.5
     check_nan(c, [(("k", 0, 17, 0), -INF), (("page", 2, 0, 0), -INF), (("page", 6, 1, 0), -INF)]
               + [(("page", 7, p, 0), -INF) for p in range(-(-20 // P))])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+@pytest.mark.parametrize("lens,hkv", [([300, 1, 9000, 0, 700, 40], 1), ([300, 1, 9000, 0, 700, 40], 8), ([30000, 5], 1), ([(i * 37) % 900 for i in range(300)], 2)],
+                         ids=["few", "some", "long", "many"])
+def test_decode_weights_keep_nan(lens, hkv, dtype):
+    """The weights of a head with a NaN are NaN on every page of the sequence,
+    whether one CTA or many went over it."""
+    c = Case(lens, 8 * hkv, hkv, 128, 64, dtype, seed=43)
+    places = [(("q", 0, 1), NAN)]
+    if len(lens) == 2:
+        places = [(("k", 0, 29999, 0), NAN)]
+    else:
+        places += [(("q", 1, 7), NAN), (("k", 2, lens[2] - 1, hkv - 1), NAN), (("k", 4, 0, 0), NAN)]
+        if dtype == BF16:
+            places.append((("k", 5, 39, 0), INF))
+    o, w, plain = check_nan(c, places)
+    assert torch.equal(torch.isnan(o), torch.isnan(plain)) and torch.equal(o.nan_to_num(7), plain.nan_to_num(7))
+    assert torch.isnan(w).any()
