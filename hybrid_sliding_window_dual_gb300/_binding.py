@@ -160,11 +160,20 @@ def _check(status, call):
 
 
 def _ptr(x):
+    # every call goes through here for each of its arrays: what they usually
+    # are comes first, subclasses of integers and arrays last
     if x is None or x.__class__ is int:
         return x
     if x.__class__ is np.ndarray:
         return x.ctypes.data
-    return x.data_ptr()
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        if isinstance(x, int):
+            return x
+        if isinstance(x, np.ndarray):
+            return x.ctypes.data
+        raise
 
 
 def _stream(stream):

@@ -382,3 +382,22 @@ def test_session_refuses_shapes_that_do_not_fit():
     assert s._row_stride(f(50)[None, None]) == 50 and s._row_stride(f(3, 2, 1)) == 1
     H.hswa_rope_destroy(rope)
     s.close()
+
+
+def test_binding_takes_subclasses_of_arrays_and_integers(tmp_path):
+    """What stands for an address or an array may be a subclass of one: a
+    mapped file for gathered windows, a masked array, an IntEnum, a bool."""
+    import enum
+    from hybrid_sliding_window_dual_gb300 import _binding as B
+
+    a = np.arange(6, dtype=np.int32)
+    mapped = np.memmap(tmp_path / "window", np.uint8, "w+", shape=(4096,))
+    masked = np.ma.masked_array(a, a > 3)
+    place = enum.IntEnum("place", {"X": X})
+    assert B._ptr(mapped) == mapped.ctypes.data and B._ptr(masked) == masked.ctypes.data and B._ptr(a.view(np.matrix)) == a.ctypes.data
+    assert B._ptr(place.X) == X and B._ptr(False) == 0 and B._ptr(None) is None and B._ptr(X) == X
+    t = torch.arange(3)
+    assert B._ptr(t) == t.data_ptr() and B._ptr(torch.nn.Parameter(torch.ones(2))) != 0
+    p = pool()
+    H.hswa_append_kv(p, layer(), mapped, mapped, place.X, 0)  # no tokens: nothing is followed
+    H.hswa_pool_destroy(p)
