@@ -93,7 +93,8 @@ def verify(p, q, draft, n_draft, u, bits=50):
             if not 0 <= x < V:
                 break
             px, qx, ux = float(p[s, a, x]), 1.0 if q is None else float(q[s, a, x]), float(u[s, a])
-            if not all(np.isfinite((px, qx, ux))) or not Fraction(ux) * Fraction(qx) < Fraction(px):
+            left = Fraction(ux) * Fraction(qx) if np.isfinite(ux) and np.isfinite(qx) else ux * qx
+            if not left < px:  # exact for finite values; NaN is below nothing
                 break
             a += 1
         target = steps(p[s, a], bits)

@@ -196,3 +196,34 @@ def test_verify_large_batch_streams_and_graph():
         g.replay()
         assert H.hswa_check() == 0
         assert np.array_equal(acc.cpu().numpy(), exp[0]) and np.array_equal(tok.cpu().numpy(), exp[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("sampled", [True, False])
+def test_verify_infinities(dtype, sampled):
+    """Infinities in p, q and u, at drafted values and others: the acceptance
+    test is the inequality as it stands (0 times infinity is no number and
+    refuses), the draw clamps them to [0, 1]."""
+    V, inf = 1003, float("inf")
+    p, q, draft, _, u = make(12, 4, V, dtype, not sampled, seed=8)
+    u[:, :3] *= 0.01
+    at = draft.long()
+    for i, x in enumerate((inf, -inf)):
+        p[i, 0, at[i, 0]] = x
+        p[2 + i, :, 40:44] = x
+        if sampled:
+            q[4 + i, 0, at[4 + i, 0]] = x
+            q[6 + i, :, 100:900:7] = x
+        u[8 + i, 0] = x
+    p[10, 1, at[10, 1]], u[10, 1] = inf, inf
+    p[11, 2, at[11, 2]], u[11, 2] = -inf, -inf
+    if sampled:
+        q[4, 1, at[4, 1]], u[4, :2] = inf, 0.0
+        q[11, 2, at[11, 2]] = inf
+    acc, _ = check(p, q if sampled else None, draft, None, u)
+    assert acc[0] > 0 and acc[1] == 0 and acc[8] == 0
+    u[:, :3] = 0.9
+    check(p, q if sampled else None, draft, None, u)
+    u[:, 3] = torch.tensor([inf, -inf] * 6, device="cuda")
+    check(p, q if sampled else None, draft, None, u)

@@ -401,3 +401,18 @@ def test_binding_takes_subclasses_of_arrays_and_integers(tmp_path):
     p = pool()
     H.hswa_append_kv(p, layer(), mapped, mapped, place.X, 0)  # no tokens: nothing is followed
     H.hswa_pool_destroy(p)
+
+
+def test_oracle_verify_infinities():
+    """u q < p as it stands: an infinite p keeps any draft that u q is below,
+    NaN (0 times infinity among them) refuses; the draw clamps to [0, 1]."""
+    inf, nan = float("inf"), float("nan")
+    for u, q, p, stays in ((0.5, 0.5, inf, True), (0.5, 0.5, -inf, False), (inf, 0.5, 1.0, False), (-inf, 0.5, 0.0, True), (-inf, 0.5, -inf, False),
+                           (inf, 0.5, inf, False), (0.0, inf, 1.0, False), (0.5, inf, 1.0, False), (-0.5, inf, -1.0, True), (inf, 0.0, 1.0, False),
+                           (nan, 0.5, inf, False), (0.5, nan, inf, False), (0.5, 0.5, nan, False)):
+        row = np.array([0.5, p, 0.25, 0.0])
+        a, t = serving.verify(np.stack([row, row])[None], np.array([[[0.0, q, 0.0, 0.0]]]), np.array([[1]]), None, np.array([[u, 0.0]]))
+        assert bool(a[0]) == stays, (u, q, p)
+        assert t[0, a[0]] == 0  # the first of what is left, 0.5 at token 0
+    row = np.array([-inf, 0.5, inf, 0.0])
+    assert [serving.verify(row[None, None], None, np.zeros((1, 0), int), None, np.array([[u]]))[1][0, 0] for u in (-inf, 0.0, 0.33, 0.34, inf)] == [1, 1, 1, 2, 2]
