@@ -41,6 +41,7 @@ struct SelectArgs {
     int32_t sink, recent, page, max_pages;
     int32_t *keep, *n_keep;
     float *w_out;
+    int *err;
     int32_t ctas;  // of a row
 };
 
@@ -83,8 +84,10 @@ __global__ void __launch_bounds__(kThreads) evict_select(const SelectArgs a) {
         for (int k = 0; k < kItems; ++k) key[k] = order_of(x[k]);
     };
     load();
-    const int64_t L = max(a.seq_len[s], 0);
-    const int32_t pages = (int32_t)min((L + a.page - 1) / a.page, (int64_t)a.max_pages);
+    // a length ends where its table row does, as in decode with page weights
+    const int64_t row_keys = (int64_t)a.max_pages * a.page, asked = a.seq_len[s], L = min(max(asked, (int64_t)0), row_keys);
+    if (asked > row_keys && rank == 0 && tid == 0) set_error(a.err, HSWA_ERR_BOUNDS);
+    const int32_t pages = (int32_t)((L + a.page - 1) / a.page);
     // pages [c0, c1) may go
     const int32_t c0 = min(a.sink, pages);
     const int32_t c1 = max(c0, L > a.recent ? (int32_t)min((L - a.recent) / a.page, (int64_t)pages) : 0);
@@ -329,7 +332,7 @@ extern "C" int hswa_evict_select(const hswa_pool *pool, const int32_t *d_seq_len
     if (overlap_but_differ(w_in, w_out, (size_t)n_seqs * pool->cfg.max_pages_per_seq * sizeof(float)))
         return HSWA_ERR_INVALID_ARG;
     const SelectArgs a = {d_seq_len, w_in, d_budget, sink_pages, recent_tokens, pool->cfg.page_size,
-                          pool->cfg.max_pages_per_seq, keep, n_keep, w_out, 1};
+                          pool->cfg.max_pages_per_seq, keep, n_keep, w_out, error_word(), 1};
     set_last_kernel("evict_select");
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int32_t n = a.max_pages;

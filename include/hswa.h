@@ -434,17 +434,17 @@ size_t hswa_decode_weights_workspace_size(const hswa_pool *pool, int n_seqs);
  * Hq), and w_out[i][p] = 0 for every later p, so that pages added later
  * start from nothing. w_in, w_out: device float [n_seqs][max_pages_per_seq];
  * they may be the same (an overlap otherwise is HSWA_ERR_INVALID_ARG); w_in
- * NULL or decay 0 starts anew whatever w_in holds. Several layers add up by calls with the same w_in = w_out (decay
- * on a step's first layer, 1 on the others). Sums have a fixed order: equal
- * inputs give equal bits. The attention output is hswa_decode's. A head with
- * a score of NaN or +inf has no softmax: its output is NaN, and so are the
- * sequence's weights on all of its pages. All pool dtypes and shapes that
- * hswa_decode takes (head_dim at most 256, n_seqs at most 65535; on bf16 and FP8 pools of d = 128, P = 64 and 8 query heads per
- * kv head Hq at most 2048); an SWA layer is HSWA_ERR_INVALID_ARG. A page
- * skipped for its table entry (HSWA_ERR_BOUNDS) weighs nothing; the keys of a
- * length past the table's last page are left out (HSWA_ERR_BOUNDS). ws: device, 256-byte
- * aligned, of at least hswa_decode_weights_workspace_size bytes, on every
- * path. */
+ * NULL or decay 0 starts anew whatever w_in holds. Several layers add up by
+ * calls with the same w_in = w_out (decay on a step's first layer, 1 on the
+ * others). Sums have a fixed order: equal inputs give equal bits. The
+ * attention output is hswa_decode's. A head with a score of NaN or +inf has no
+ * softmax: its output is NaN, and so are the sequence's weights on all of its
+ * pages. All pool dtypes and shapes that hswa_decode takes (head_dim at most 256, n_seqs at most 65535; on bf16 and
+ * FP8 pools of d = 128, P = 64 and 8 query heads per kv head Hq at most 2048);
+ * an SWA layer is HSWA_ERR_INVALID_ARG. A page skipped for its table entry
+ * (HSWA_ERR_BOUNDS) weighs nothing; the keys of a length past the table's last
+ * page are left out (HSWA_ERR_BOUNDS). ws: device, 256-byte aligned, of at
+ * least hswa_decode_weights_workspace_size bytes, on every path. */
 int hswa_decode_weights(const hswa_pool *pool, const hswa_layer *layer, const void *q, void *o,
                         const int32_t *d_bt, const int32_t *d_seq_len, int n_seqs, float scale, const float *w_in,
                         float decay, float *w_out, void *ws, size_t ws_bytes, hswa_stream_t stream);
@@ -452,7 +452,8 @@ int hswa_decode_weights(const hswa_pool *pool, const hswa_layer *layer, const vo
 /* Which pages of each sequence stay when its Full cache is cut to a budget,
  * by accumulated attention weight. Of sequence i's n = ceil(L / P) pages (L
  * = d_seq_len[i]) these always stay: the first sink_pages, and every page
- * with a token among the last recent_tokens (at least the pool's window).
+ * with a token among the last recent_tokens (at least the pool's window). A
+ * length past the table's last page counts as ending there (HSWA_ERR_BOUNDS).
  * Of the others the heaviest stay, so that max(d_budget[i], those) pages do
  * in all (n at most); of equal weights the lower page stays, and NaN is
  * lighter than any number. w_in: device float [n_seqs][max_pages_per_seq]

@@ -488,3 +488,25 @@ def test_decode_weights_keep_nan(lens, hkv, dtype):
     o, w, plain = check_nan(c, places)
     assert torch.equal(torch.isnan(o), torch.isnan(plain)) and torch.equal(o.nan_to_num(7), plain.nan_to_num(7))
     assert torch.isnan(w).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mp", [10, 600, 1500, 5000, 20000])
+@pytest.mark.parametrize("excess", [1, 16, 100000])
+def test_select_of_lengths_past_the_table(mp, excess):
+    """A length past a table row is reported and ends where the row does."""
+    rng = np.random.default_rng(mp)
+    P, S = 16, 5
+    w = torch.as_tensor(weights(rng, S, mp, "plain"), device="cuda")
+    lens = torch.tensor([mp * P, mp * P + excess, 77, mp * P, 0], dtype=torch.int32, device="cuda")
+    budget = torch.tensor([mp // 3] * S, dtype=torch.int32, device="cuda")
+    pool = H.hswa_pool_create(H.Config(window=128, page_size=P, n_q_heads=8, n_kv_heads=1, head_dim=128, dtype=BF16, full_pages=1, swa_pages=1,
+                                       max_seqs=S, max_pages_per_seq=mp))
+    keep = torch.full((S + 2, mp), -7, dtype=torch.int32, device="cuda")
+    n_keep, out = torch.full((S,), -7, dtype=torch.int32, device="cuda"), torch.full((S + 2, mp), 9.0, device="cuda")
+    H.hswa_evict_select(pool, lens, w, budget, S, 2, 130, keep[1:-1], n_keep, out[1:-1])
+    assert H.hswa_check() == H.HSWA_ERR_BOUNDS
+    H.hswa_pool_destroy(pool)
+    exp = serving.evict_select(lens.clamp(max=mp * P).tolist(), w.cpu().numpy(), budget.tolist(), P, 2, 130)
+    assert [k[:n].tolist() for k, n in zip(keep[1:-1].cpu().numpy(), n_keep.tolist())] == exp
+    assert (keep[[0, -1]] == -7).all() and (out[[0, -1]] == 9).all()
