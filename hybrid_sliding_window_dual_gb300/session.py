@@ -158,7 +158,9 @@ class DualPoolSession:
 
     def decode_weights(self, layer, q, o, n_seqs, scale, w_in, decay, w_out):
         """decode() of a Full layer that adds the pages' attention weights:
-        w_out = decay * w_in + weights, [n_seqs, max_pages_per_seq] fp32."""
+        w_out = decay * w_in + weights, [n_seqs, max_pages_per_seq] fp32. The
+        session's calls, captured ones among them, share one workspace: two of
+        them must not run at the same time."""
         if self.weights_ws is None:  # for every sequence, so that captured calls keep theirs
             need = B.hswa_decode_weights_workspace_size(self.pool, self.cfg.max_seqs)
             self.weights_ws = torch.empty(need, dtype=torch.uint8, device=self.device)

@@ -510,3 +510,30 @@ def test_select_of_lengths_past_the_table(mp, excess):
     exp = serving.evict_select(lens.clamp(max=mp * P).tolist(), w.cpu().numpy(), budget.tolist(), P, 2, 130)
     assert [k[:n].tolist() for k, n in zip(keep[1:-1].cpu().numpy(), n_keep.tolist())] == exp
     assert (keep[[0, -1]] == -7).all() and (out[[0, -1]] == 9).all()
+
+
+@pytest.mark.gpu
+def test_session_weights_first_called_inside_a_capture():
+    """The session's workspace is made by its first call; when that is being
+    captured, eager calls after the graph is gone still have it."""
+    c = Case([100, 5000, 3], 64, 8, 128, 64, BF16, seed=15)
+    ref = Case([100, 5000, 3], 64, 8, 128, 64, BF16, seed=15)
+    want_o, want_w = ref.run(ref.w_in, 0.75)  # sets the kernels up
+    o, w, g = torch.zeros_like(c.q), torch.zeros_like(c.w_in), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        c.sess.stream = torch.cuda.current_stream()
+        c.sess.decode_weights(0, c.q, o, c.S, c.scale, c.w_in, 0.75, w)
+    c.sess.stream = None
+    kept = c.sess.weights_ws
+    for _ in range(2):
+        o.zero_(), w.zero_()
+        g.replay()
+        assert H.hswa_check() == 0 and torch.equal(o, want_o) and torch.equal(w, want_w)
+    del g
+    torch.cuda.empty_cache()
+    other = [torch.full((kept.numel(),), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert all(x.data_ptr() != kept.data_ptr() for x in other)
+    got_o, got_w = c.run(c.w_in, 0.75)
+    assert c.sess.weights_ws is kept and all((x == 255).all() for x in other)
+    assert torch.equal(got_o, want_o) and torch.equal(got_w, want_w)
