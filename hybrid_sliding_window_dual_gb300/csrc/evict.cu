@@ -21,6 +21,8 @@
 // nearly all alike, so that its counters collide. A thread's pages next to
 // each other made placing them 1.6 times as long: its loads and stores are
 // 64 bytes apart over a warp.)
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -41,6 +43,7 @@ struct SelectArgs {
     int32_t sink, recent, page, max_pages;
     int32_t *keep, *n_keep;
     float *w_out;
+    int32_t row_keys;  // keys of a table row, INT32_MAX at most
     int *err;
     int32_t ctas;  // of a row
 };
@@ -85,17 +88,19 @@ __global__ void __launch_bounds__(kThreads) evict_select(const SelectArgs a) {
     };
     load();
     // a length ends where its table row does, as in decode with page weights
-    const int64_t row_keys = (int64_t)a.max_pages * a.page, asked = a.seq_len[s], L = min(max(asked, (int64_t)0), row_keys);
-    if (asked > row_keys && rank == 0 && tid == 0) set_error(a.err, HSWA_ERR_BOUNDS);
-    const int32_t pages = (int32_t)((L + a.page - 1) / a.page);
+    const int32_t asked = a.seq_len[s], L = min(max(asked, 0), a.row_keys);
+    const int32_t pages = (int32_t)(((uint32_t)L + (uint32_t)a.page - 1) / (uint32_t)a.page);
     // pages [c0, c1) may go
     const int32_t c0 = min(a.sink, pages);
-    const int32_t c1 = max(c0, L > a.recent ? (int32_t)min((L - a.recent) / a.page, (int64_t)pages) : 0);
+    const int32_t c1 = max(c0, L > a.recent ? (L - a.recent) / a.page : 0);
     const int32_t fixed = pages - (c1 - c0);
     const int32_t n_keep = min(pages, max(a.budget[s], fixed));
     const int32_t left = n_keep - fixed;  // candidates that stay
     for (int32_t p = n_keep + rank * kThreads + tid; p < a.max_pages; p += ctas * kThreads) keep[p] = -1;
-    if (rank == 0 && tid == 0) a.n_keep[s] = n_keep;
+    if (rank == 0 && tid == 0) {
+        a.n_keep[s] = n_keep;
+        if (asked > L) set_error(a.err, HSWA_ERR_BOUNDS);
+    }
     if constexpr (kSplit) cluster_wait();  // every CTA of the cluster has started
     const auto may_go = [&](int32_t p) { return p >= c0 && p < c1; };
     // f(is a candidate, its order), by whole warps
@@ -332,7 +337,9 @@ extern "C" int hswa_evict_select(const hswa_pool *pool, const int32_t *d_seq_len
     if (overlap_but_differ(w_in, w_out, (size_t)n_seqs * pool->cfg.max_pages_per_seq * sizeof(float)))
         return HSWA_ERR_INVALID_ARG;
     const SelectArgs a = {d_seq_len, w_in, d_budget, sink_pages, recent_tokens, pool->cfg.page_size,
-                          pool->cfg.max_pages_per_seq, keep, n_keep, w_out, error_word(), 1};
+                          pool->cfg.max_pages_per_seq, keep, n_keep, w_out,
+                          (int32_t)std::min((int64_t)pool->cfg.max_pages_per_seq * pool->cfg.page_size, (int64_t)INT32_MAX),
+                          error_word(), 1};
     set_last_kernel("evict_select");
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int32_t n = a.max_pages;
