@@ -385,9 +385,9 @@ int hswa_rope_destroy(hswa_rope *rope);
  * q, k or v otherwise. d_pos: device int32 [n_axes][n_tokens]. d_slots:
  * device int32 [n_tokens], distinct, as from hswa_reserve; a negative one
  * appends nothing (q is rotated all the same), one past the pool sets
- * HSWA_ERR_BOUNDS on the device and appends nothing. rotary_dim must be at
- * most head_dim, and head_dim at most HSWA_ROPE_MAX_HEAD (128 for FP8
- * pools), else HSWA_ERR_UNSUPPORTED. */
+ * HSWA_ERR_BOUNDS on the device and appends nothing. A rotary_dim above
+ * head_dim is HSWA_ERR_INVALID_ARG; a head_dim above HSWA_ROPE_MAX_HEAD, and
+ * on FP8 pools one other than 128, HSWA_ERR_UNSUPPORTED. */
 int hswa_rope_append(const hswa_pool *pool, const hswa_layer *layer, const hswa_rope *rope, const void *q,
                      int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                      const int32_t *d_pos, const int32_t *d_slots, void *q_out, int n_tokens, hswa_stream_t stream);
@@ -439,9 +439,10 @@ size_t hswa_decode_weights_workspace_size(const hswa_pool *pool, int n_seqs);
  * others). Sums have a fixed order: equal inputs give equal bits. The
  * attention output is hswa_decode's. A head with a score of NaN or +inf has no
  * softmax: its output is NaN, and so are the sequence's weights on all of its
- * pages. All pool dtypes and shapes that hswa_decode takes (head_dim at most 256, n_seqs at most 65535; on bf16 and
- * FP8 pools of d = 128, P = 64 and 8 query heads per kv head Hq at most 2048);
- * an SWA layer is HSWA_ERR_INVALID_ARG. A page skipped for its table entry
+ * pages. All pool dtypes and shapes that hswa_decode takes (head_dim at most
+ * 256, n_seqs at most 65535; on bf16 and FP8 pools of d = 128, P = 64 and 8
+ * query heads per kv head Hq at most 2048, else HSWA_ERR_UNSUPPORTED); an SWA
+ * layer is HSWA_ERR_INVALID_ARG. A page skipped for its table entry
  * (HSWA_ERR_BOUNDS) weighs nothing; the keys of a length past the table's last
  * page are left out (HSWA_ERR_BOUNDS). ws: device, 256-byte aligned, of at
  * least hswa_decode_weights_workspace_size bytes, on every path. */
