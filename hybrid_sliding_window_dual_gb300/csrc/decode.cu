@@ -1769,10 +1769,10 @@ __global__ void __launch_bounds__(Smem::kThreads, 1)
 // token w, kv head g; 256 threads, a warp per head); write zeros for a
 // sequence without keys. A warp's lanes look at 32 records' maxima and sums
 // at once, then all take the records in order, 4 in flight (8 spill at the
-// registers that keep 4 blocks on an SM: 0.6 us more). (Three short sequences
-// are cut into up to 20 pieces a head: a loop over the records that found each
-// with 64-bit divisions made their decode step 27 us, this 12.2, merge_heads
-// 11.3.)
+// registers that keep 4 blocks on an SM: 0.6 us more). (Three sequences of
+// 700 to 2500 keys on 8 kv heads are cut into up to 20 pieces a head: a loop
+// over the records that found each with 64-bit divisions made their decode step
+// 27 us, this 12.2, merge_heads 11.4.)
 __device__ void merge_segment(const DecodeArgs &a, int32_t n_ctas, int32_t s, int32_t w, int32_t g) {
     const int64_t U = a.sdesc[a.n_seqs].x, N = n_ctas;
     const int4 d = a.sdesc[s];
@@ -1869,8 +1869,8 @@ struct Pieces {
 // block (128 threads, one d each) per head, the records' weights through
 // shared memory, 32 records in flight. The records are added up in the same
 // order: equal bits. Two sequences of 1566 and 14213 keys on one kv head, up to
-// 220 pieces: the decode step 15 us, by merge_segment 47; three up to 2515
-// keys 9.3 and 27. (With the pieces found among all CTAs between, and a test at
+// 220 pieces: the decode step 14.5 us, by merge_segment 47; three of 318 to 2515
+// keys on one kv head 9.3 and 27. (With the pieces found among all CTAs between, and a test at
 // each record whether there is one, 34 and 23.)
 constexpr int kMergeHeads = 2;  // heads of a block
 constexpr int kMergeAhead = 32;
@@ -1965,9 +1965,9 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return
 // added later start from nothing.
 //
 // Bound by memory, as the decode step is: 64 sequences of 1K to 32K, bf16 (64
-// / 8 heads): 646 us against 634 without the weights and 653 for the bytes at
-// the copy rate; 49 sequences, FP8: 281 against 265 and 257; three short ones
-// 12.5 against 11.3. What the weights cost the FP8 kernel, whose issue slots
+// / 8 heads): 641 us against 623 without the weights and 653 for the bytes at
+// the copy rate; 49 sequences, FP8: 278 against 263 and 257; three of 700 to
+// 2500 keys 12.7 against 11.2. What the weights cost the FP8 kernel, whose issue slots
 // are nearly full, is instructions: with the sums added up in the consumer
 // warps it was 358, and each page's 64-bit address and exact logarithm in the
 // producer made 295.
@@ -2130,9 +2130,13 @@ __global__ void __launch_bounds__(256) page_weights(const WeightArgs a) {
 // keys of a page at once, whose loads and sums across the lanes overlap: kE
 // elements a lane of each. Bound by latency (a table entry, a page's keys,
 // the sums across lanes, one after the other) and, with few CTAs, by
-// instructions: 16 sequences of 1000 to 2000 keys, fp32, d = 64, take 23 us;
-// with 8 warps and a key at a time it was 57, with every key's sum in every
-// lane 31.
+// instructions: 16 sequences of 1000 to 2000 keys, fp32, d = 64, take 23 us
+// (1.8 for the bytes at the copy rate); with 8 warps and a key at a time it was
+// 57, with every key's sum in every lane 31. The keys are not split over CTAs
+// and every query head reads its kv head's keys for itself: one sequence of
+// 32768 fp32 keys takes 248 us (floor 2.5), of bf16 keys on 8 kv heads 256 (d =
+// 64, floor 10) to 860 (d = 128, 20); 64 sequences of 1K to 8K bf16 keys with 4
+// query heads a kv head, d = 128, 1097 (178), with 16 3700.
 // Warps of a CTA: as many as their registers allow.
 template <int kE>
 constexpr int kAnyWarps = kE <= 2 ? 32 : 16;

@@ -12,11 +12,12 @@
 //
 // Bound by latency: a row is a few KB, and the loads, the steps with a barrier
 // each and the scan follow one another, much of it by instructions that run
-// for the first time. On the device 64 rows of 512 pages take 3.4 us, 152 of
-// 2048 4.3, 8 of 16384, split, 7.7; rows beyond that 31 (32768 pages).
+// for the first time. On the device 64 rows of 512 pages take 3.3 us, 152 of
+// 2048 4.4, 8 of 16384, split, 8.1; rows beyond that 32 to 37 (32768 pages, one
+// CTA that reads the row from L2 for every count).
 //
 // (A bisection of the range, one barrier a bit, took 4.2 us on 64 rows of up
-// to 512 pages, 6.1 on 128 of 2048 and 20 on 5 of 16384, now 3.6, 5 and 7.3; a
+// to 512 pages, 6.1 on 128 of 2048 and 20 on 5 of 16384, now 3.3, 4.2 and 7.1; a
 // radix selection, 8 bits a pass, 7.2, 11 and 50: the weights' first bits are
 // nearly all alike, so that its counters collide. A thread's pages next to
 // each other made placing them 1.6 times as long: its loads and stores are
@@ -344,9 +345,9 @@ extern "C" int hswa_evict_select(const hswa_pool *pool, const int32_t *d_seq_len
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int32_t n = a.max_pages;
     // Threads for the row: fewer make cheaper barriers. Long rows are split as
-    // long as every CTA has an SM of its own (8 rows of 16384 pages 7.7 us, by
-    // one CTA each 12.4; 64 of 4096 6.6 and 7.3, but 64 of 8192 10.8 and 8.1,
-    // 64 of 16384 20 and 12.5).
+    // long as every CTA has an SM of its own (8 rows of 16384 pages 8.1 us, by
+    // one CTA each 13.7; 64 of 4096 6.7 and 9.1, but 64 of 8192 11.9 and 9.1,
+    // 64 of 16384 22 and 14).
     const int sms = sm_count();
     if (sms <= 0) return HSWA_ERR_CUDA;
     const bool split = n > 2048 && n <= 2048 * kMaxCtas && (int64_t)n_seqs * split_ctas(n) <= sms;

@@ -80,7 +80,9 @@ __device__ __forceinline__ float rotated(const T *x, int e, const RopeArgs &a, c
 
 // Any head_dim, rotary dim and alignment: one CTA per token, one warp per
 // row, a lane per element. A row is read before any of it is written, so q
-// may be rotated in place.
+// may be rotated in place. Bound by loads and instructions of one element each:
+// 4096 bf16 tokens of 64 / 8 heads, 100 of 128 elements turned, take 146 us, 25
+// for the bytes at the copy rate; 64 tokens 14.
 template <typename T, bool kFP8>
 __global__ void __launch_bounds__(256) rope_append_any(const __grid_constant__ RopeArgs a) {
     constexpr int kMaxE = HSWA_ROPE_MAX_HEAD / 32;
