@@ -724,10 +724,21 @@ __device__ void decode_consumer(DecodeSmemT<kTok, kWeights> &sm, const DecodeArg
 
 // Consumer warps 0 .. kTok - 1, one query token each (warps past n_tok stay
 // idle); warp kTok is the producer.
-template <int kTok, bool kWeights>
-__global__ void __launch_bounds__(32 * (kTok + 1)) decode_mma_bf16_d128(const __grid_constant__ CUtensorMap tk,
-                                                                      const __grid_constant__ CUtensorMap tv,
-                                                                      DecodeArgs a) {
+//
+// Registers of the one-token kernel: 162 where it is told the 2 CTAs per SM
+// that shared memory leaves it (0 leaves the others to the compiler's guess, 96
+// for this one). With more a warp has more fragments on their way, which tells
+// where K and V come from L2 or a CTA has few pages: 12 sequences of 2000 keys
+// (64 / 8 heads) 17.3 us, with 96 23.4; the windows of 64 sequences 12.9 and
+// 15.6; one sequence of 64 keys 8.0 and 8.5; 16 of 1000 to 9000, 0.3 GB, 57.5 and
+// 59.0. Where memory bounds it 96 are a little ahead: 64 of 1K to 8K, 1.2 GB,
+// 186 and 186; 32 of 1K to 32K, 2.2 GB, 326 and 323; 64 of them 638 and 634.
+// decode_large tells them apart.
+constexpr int min_ctas(int n_tok, bool weights, bool large) { return n_tok > 1 || weights ? 0 : large ? 10 : 2; }
+
+template <int kTok, bool kWeights, bool kLarge>
+__global__ void __launch_bounds__(32 * (kTok + 1), min_ctas(kTok, kWeights, kLarge))
+    decode_mma_bf16_d128(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, DecodeArgs a) {
     using Smem = DecodeSmemT<kTok, kWeights>;
     extern __shared__ uint8_t raw[];
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -2412,10 +2423,10 @@ bool decode_fast_ok(const hswa_pool *pool, const hswa_layer *layer, const void *
            ((uintptr_t)layer->k_pool & 15) == 0 && ((uintptr_t)layer->v_pool & 15) == 0;
 }
 
-template <int kTok, bool kWeights = false>
+template <int kTok, bool kWeights = false, bool kLarge = false>
 int decode_ctas_per_sm_t() {
     static int cache[kMaxDevices] = {};
-    return kernel_setup(decode_mma_bf16_d128<kTok, kWeights>, decode_smem_bytes<kTok, kWeights>(), 32 * (kTok + 1), cache);
+    return kernel_setup(decode_mma_bf16_d128<kTok, kWeights, kLarge>, decode_smem_bytes<kTok, kWeights>(), 32 * (kTok + 1), cache);
 }
 
 int decode_ctas_per_sm() { return decode_ctas_per_sm_t<1>(); }
@@ -2461,15 +2472,23 @@ bool make_q_tmap(CUtensorMap *tq, const void *q, const hswa_config &c, int n_seq
 // against 6.39).
 constexpr int kTcMinTokens = 4;
 
-int decode_ctas_per_sm_for(int n_tok) {
+int decode_ctas_per_sm_for(int n_tok, bool large = false) {
     switch (n_tok) {
-    case 1: return decode_ctas_per_sm_t<1>();
+    case 1: return large ? decode_ctas_per_sm_t<1, false, true>() : decode_ctas_per_sm_t<1>();
     case 2: return decode_ctas_per_sm_t<2>();
     default: return decode_ctas_per_sm_t<3>();
     }
 }
 
 constexpr int kMaxCtasPerSm = 4;
+
+// More than 1 GB of K and V, as far as the host can tell: the lengths are on
+// the device, so it counts the pages that the tables have room for, or the
+// window's, and no more than the pool has.
+bool decode_large(const hswa_config &c, const hswa_layer &layer, int n_seqs, int32_t num_pages) {
+    const int64_t per_seq = layer.kind == HSWA_KIND_SWA ? std::min(layer.window / kP + 2, c.max_pages_per_seq) : c.max_pages_per_seq;
+    return std::min<int64_t>(n_seqs * per_seq, num_pages) * c.n_kv_heads * 2 * kPageHeadBytes > INT64_C(1) << 30;
+}
 
 // What hswa_decode_weights adds to a decode step.
 struct PageWeights {
@@ -2630,10 +2649,10 @@ int decode_fp8(const hswa_pool *pool, const hswa_layer *layer, const void *q, vo
     return e == cudaSuccess ? HSWA_OK : HSWA_ERR_CUDA;
 }
 
-template <int kTok, bool kWeights = false>
+template <int kTok, bool kWeights = false, bool kLarge = false>
 cudaError_t launch_decode_kernel(int n_ctas, cudaStream_t st, const CUtensorMap &tk, const CUtensorMap &tv,
                                  const DecodeArgs &a) {
-    return launch_pdl(decode_mma_bf16_d128<kTok, kWeights>, dim3(n_ctas), dim3(32 * (kTok + 1)),
+    return launch_pdl(decode_mma_bf16_d128<kTok, kWeights, kLarge>, dim3(n_ctas), dim3(32 * (kTok + 1)),
                       decode_smem_bytes<kTok, kWeights>(), st, tk, tv, a);
 }
 
@@ -2709,9 +2728,10 @@ int decode_impl(const hswa_pool *pool, const hswa_layer *layer, const void *q, v
     const int sms = sm_count();
     if (sms <= 0) return HSWA_ERR_CUDA;
     const bool tc = n_tok >= kTcMinTokens;
+    const bool large = decode_large(c, *layer, n_seqs, layer->kind == HSWA_KIND_SWA ? c.swa_pages : c.full_pages);
     const int per_sm = tc   ? decode_tc_ctas_per_sm<DecodeTcSmem>(n_tok)
                        : pw ? decode_ctas_per_sm_t<1, true>()
-                            : decode_ctas_per_sm_for(n_tok);
+                            : decode_ctas_per_sm_for(n_tok, large);
     if (per_sm <= 0) return HSWA_ERR_CUDA;
     const int n_ctas = sms * std::min(per_sm, kMaxCtasPerSm);
     if (!ws || ((uintptr_t)ws & 255) ||
@@ -2744,7 +2764,9 @@ int decode_impl(const hswa_pool *pool, const hswa_layer *layer, const void *q, v
     } else if (pw) {
         e = launch_decode_kernel<1, true>(n_ctas, st, tk, tv, a);
     } else switch (n_tok) {
-    case 1: e = launch_decode_kernel<1>(n_ctas, st, tk, tv, a); break;
+    case 1:
+        e = large ? launch_decode_kernel<1, false, true>(n_ctas, st, tk, tv, a) : launch_decode_kernel<1>(n_ctas, st, tk, tv, a);
+        break;
     case 2: e = launch_decode_kernel<2>(n_ctas, st, tk, tv, a); break;
     default: e = launch_decode_kernel<3>(n_ctas, st, tk, tv, a); break;
     }
