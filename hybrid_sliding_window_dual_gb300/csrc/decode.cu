@@ -1783,7 +1783,7 @@ __global__ void __launch_bounds__(Smem::kThreads, 1)
 // registers that keep 4 blocks on an SM: 0.6 us more). (Three sequences of
 // 700 to 2500 keys on 8 kv heads are cut into up to 20 pieces a head: a loop
 // over the records that found each with 64-bit divisions made their decode step
-// 27 us, this 12.2, merge_heads 11.4.)
+// 27 us, this 11.1, merge_heads 10.2.)
 __device__ void merge_segment(const DecodeArgs &a, int32_t n_ctas, int32_t s, int32_t w, int32_t g) {
     const int64_t U = a.sdesc[a.n_seqs].x, N = n_ctas;
     const int4 d = a.sdesc[s];
@@ -1880,8 +1880,8 @@ struct Pieces {
 // block (128 threads, one d each) per head, the records' weights through
 // shared memory, 32 records in flight. The records are added up in the same
 // order: equal bits. Two sequences of 1566 and 14213 keys on one kv head, up to
-// 220 pieces: the decode step 14.5 us, by merge_segment 47; three of 318 to 2515
-// keys on one kv head 9.3 and 27. (With the pieces found among all CTAs between, and a test at
+// 220 pieces: the decode step 14 us, by merge_segment 47; three of 318 to 2515
+// keys on one kv head 8.7 and 27. (With the pieces found among all CTAs between, and a test at
 // each record whether there is one, 34 and 23.)
 constexpr int kMergeHeads = 2;  // heads of a block
 constexpr int kMergeAhead = 32;
@@ -1976,9 +1976,9 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return
 // added later start from nothing.
 //
 // Bound by memory, as the decode step is: 64 sequences of 1K to 32K, bf16 (64
-// / 8 heads): 641 us against 623 without the weights and 653 for the bytes at
-// the copy rate; 49 sequences, FP8: 278 against 263 and 257; three of 700 to
-// 2500 keys 12.7 against 11.2. What the weights cost the FP8 kernel, whose issue slots
+// / 8 heads): 646 us against 630 without the weights and 653 for the bytes at
+// the copy rate; 49 sequences, FP8: 279 against 265 and 257; three of 700 to
+// 2500 keys 12.5 against 10.3. What the weights cost the FP8 kernel, whose issue slots
 // are nearly full, is instructions: with the sums added up in the consumer
 // warps it was 358, and each page's 64-bit address and exact logarithm in the
 // producer made 295.
@@ -2512,8 +2512,9 @@ WeightArgs weight_args(const PageWeights &pw, const hswa_config &c, const int32_
 }
 
 // Segments of 4 pieces or more (about: lengths differ) are merged head by
-// head. Decode steps of bf16, 304 CTAs, so and otherwise: 24 segments 11.3 / 12.1
-// us, 64 35.6 / 36.4, 128 60.2 / 59.3, 240 56.3 / 52.
+// head. Decode steps of bf16, 304 CTAs, so and otherwise: 24 segments 10.2 / 11.1
+// us, 64 33.8 / 34.0, 128 57.6 / 57.4, 240 54 / 50; with page weights 64 35.9 /
+// 35.7, 128 61.8 / 59.2.
 bool merge_by_heads(int64_t segments, int n_ctas) { return segments * 4 <= n_ctas; }
 
 cudaError_t launch_finish_weights(const PageWeights &pw, const hswa_config &c, const DecodeArgs &a, int n_ctas,
