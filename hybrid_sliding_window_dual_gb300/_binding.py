@@ -28,6 +28,7 @@ HSWA_KIND_SWA = 1
 HSWA_DTYPE_F32 = 0
 HSWA_DTYPE_BF16 = 1
 HSWA_DTYPE_FP8_E4M3 = 2
+HSWA_DTYPE_FP4 = 3
 HSWA_DECODE_MAX_TOKENS = 16
 HSWA_ROPE_MAX_AXES = 4
 HSWA_ROPE_HALVES = 0
@@ -35,6 +36,7 @@ HSWA_ROPE_ADJACENT = 1
 HSWA_ROPE_SECTIONS = 0
 HSWA_ROPE_INTERLEAVED = 1
 HSWA_VERIFY_MAX_VOCAB = 1 << 20
+HSWA_LOGITS_MAX_BIAS = 1024
 
 
 class HswaError(RuntimeError):
@@ -94,6 +96,9 @@ _SIG = {
     "hswa_tree_nodes": (_I, [_P, _P, ctypes.c_int32, _P]),
     "hswa_sync_tables": (_I, [_P, _P, _P, _P, _P]),
     "hswa_append_kv": (_I, [_P, ctypes.POINTER(Layer), _P, _P, _P, _I, _P]),
+    "hswa_read_kv": (_I, [_P, ctypes.POINTER(Layer), _P, _I, _P, _P, _P]),
+    "hswa_count_tokens": (_I, [_P, _L, _P, _L, _P, _I, _I, _I, _I, _P]),
+    "hswa_logits_probs": (_I, [_I, _P, _L, _I, _P, _L, _P, _P, _L, _P, _P, _P, _I, _P, _L, _I, _I, _I, _P]),
     "hswa_rope_create": (_I, [ctypes.POINTER(RopeConfig), ctypes.POINTER(_P)]),
     "hswa_rope_destroy": (_I, [_P]),
     "hswa_rope_append": (_I, [_P, ctypes.POINTER(Layer), _P, _P, _L, _P, _L, _P, _L, _P, _P, _P, _I, _P]),
@@ -348,6 +353,11 @@ def hswa_append_kv(pool, layer: Layer, k, v, d_slots, n_tokens, stream=None):
                               _stream(stream)), "hswa_append_kv")
 
 
+def hswa_read_kv(pool, layer: Layer, d_slots, n_tokens, k, v, stream=None):
+    _check(lib.hswa_read_kv(pool, ctypes.byref(layer), _ptr(d_slots), int(n_tokens), _ptr(k), _ptr(v),
+                            _stream(stream)), "hswa_read_kv")
+
+
 def hswa_rope_create(rotary_dim, sections, theta=10000.0, inv_freq=None, interleaved=False, adjacent=False):
     """A rotary embedding: sections = pairs of each position axis."""
     cfg = RopeConfig(rotary_dim=int(rotary_dim), pairing=HSWA_ROPE_ADJACENT if adjacent else HSWA_ROPE_HALVES,
@@ -426,6 +436,21 @@ def hswa_verify_draft(dtype, p, p_stride, q, q_stride, d_draft, d_n_draft, u, n_
     _check(lib.hswa_verify_draft(int(dtype), _ptr(p), int(p_stride), _ptr(q), int(q_stride), _ptr(d_draft),
                                  _ptr(d_n_draft), _ptr(u), int(n_seqs), int(n_tok), int(vocab), _ptr(n_accept),
                                  _ptr(tokens), _stream(stream)), "hswa_verify_draft")
+
+
+def hswa_count_tokens(counts, count_stride, tokens, token_stride, d_n_prompt, n_seqs, n_tokens, vocab, clear,
+                      stream=None):
+    _check(lib.hswa_count_tokens(_ptr(counts), int(count_stride), _ptr(tokens), int(token_stride), _ptr(d_n_prompt),
+                                 int(n_seqs), int(n_tokens), int(vocab), int(clear), _stream(stream)),
+           "hswa_count_tokens")
+
+
+def hswa_logits_probs(logits_dtype, logits, logits_stride, p_dtype, p, p_stride, params, counts, count_stride, d_draft,
+                      bias_token, bias, n_bias, mask, mask_stride, n_seqs, n_tok, vocab, stream=None):
+    _check(lib.hswa_logits_probs(int(logits_dtype), _ptr(logits), int(logits_stride), int(p_dtype), _ptr(p),
+                                 int(p_stride), _ptr(params), _ptr(counts), int(count_stride), _ptr(d_draft),
+                                 _ptr(bias_token), _ptr(bias), int(n_bias), _ptr(mask), int(mask_stride),
+                                 int(n_seqs), int(n_tok), int(vocab), _stream(stream)), "hswa_logits_probs")
 
 
 def hswa_decode_noalloc(pool, layer: Layer, q, o, d_bt, d_seq_len, n_seqs, scale, stream=None):

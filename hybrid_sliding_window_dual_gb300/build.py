@@ -22,8 +22,8 @@ LIB = os.path.join(OUT_DIR, "libhswa.so")
 CUDA_HOME = os.environ.get("CUDA_HOME", "/usr/local/cuda")
 NVCC = os.path.join(CUDA_HOME, "bin", "nvcc")
 
-SOURCES = ["runtime.cu", "decode.cu", "prefill.cu", "copy.cu", "rope.cu", "verify.cu", "evict.cu", "pool.cpp", "tree.cpp"]
-HEADERS = ["common.cuh", "internal.h", "kernels.h", "tc.cuh"]
+SOURCES = ["runtime.cu", "decode.cu", "prefill.cu", "copy.cu", "rope.cu", "verify.cu", "evict.cu", "logits.cu", "pool.cpp", "tree.cpp"]
+HEADERS = ["common.cuh", "internal.h", "kernels.h", "tc.cuh", "fp4.cuh", "decode_fp4.cuh"]
 
 FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

@@ -15,6 +15,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "fp4.cuh"
 #include "internal.h"
 
 namespace hswa {
@@ -206,6 +207,144 @@ __global__ void append_kv_fp8_kernel(const __nv_bfloat16 *__restrict__ k, const 
     }
 }
 
+__device__ __forceinline__ void unpack_bf16x8(const uint4 &c, float *x) {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+// FP4 append: a thread per block of 16 elements, K's and V's; neighbouring
+// threads hold neighbouring blocks of a row, then rows of neighbouring heads,
+// so that a warp reads 1 KB runs and writes 256-byte runs of codes.
+__global__ void __launch_bounds__(256) append_kv_fp4_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v,
+                                                            uint2 *kp, uint2 *vp, uint8_t *ks, uint8_t *vs,
+                                                            const int32_t *__restrict__ slots, int64_t n_tokens,
+                                                            int32_t hkv, int32_t page, int32_t blocks,
+                                                            int64_t pool_slots, int *err) {
+    const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+    const int32_t per_tok = hkv * blocks;
+    if (i >= n_tokens * per_tok) return;
+    const int64_t t = i / per_tok;
+    const int32_t r = (int32_t)(i - t * per_tok), g = r / blocks, b = r - g * blocks;
+    const int32_t slot = slots[t];
+    if (slot < 0) return;
+    if (slot >= pool_slots) {
+        set_error(err, HSWA_ERR_BOUNDS);
+        return;
+    }
+    const uint4 in[4] = {k[2 * i], k[2 * i + 1], v[2 * i], v[2 * i + 1]};
+    const int64_t at = (((int64_t)(slot / page) * hkv + g) * page + slot % page) * blocks + b;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        float x[16];
+        unpack_bf16x8(in[2 * which], x);
+        unpack_bf16x8(in[2 * which + 1], x + 8);
+        const uint32_t scale = fp4_scale(amax16(x));
+        (which ? vp : kp)[at] = fp4_codes(x, scale);
+        (which ? vs : ks)[at] = (uint8_t)scale;
+    }
+}
+
+// hswa_read_kv: rows of the pool at given slots. 16-bit and 32-bit pools: 16
+// bytes a thread and pool.
+__global__ void __launch_bounds__(256) read_kv_kernel(chunk_t *__restrict__ k, chunk_t *__restrict__ v,
+                                                      const chunk_t *__restrict__ kp, const chunk_t *__restrict__ vp,
+                                                      const int32_t *__restrict__ slots, int64_t n_tokens, int32_t hkv,
+                                                      int32_t page, int32_t chunks, int64_t pool_slots, int *err) {
+    const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+    const int32_t per_tok = hkv * chunks;
+    if (i >= n_tokens * per_tok) return;
+    const int64_t t = i / per_tok;
+    const int32_t r = (int32_t)(i - t * per_tok), g = r / chunks, c = r - g * chunks;
+    const int32_t slot = slots[t];
+    chunk_t a = make_uint4(0, 0, 0, 0), b = a;
+    if (slot >= 0 && slot < pool_slots) {
+        const int64_t at = (((int64_t)(slot / page) * hkv + g) * page + slot % page) * chunks + c;
+        a = kp[at], b = vp[at];
+    } else if (slot >= 0) {
+        set_error(err, HSWA_ERR_BOUNDS);
+    }
+    k[i] = a;
+    v[i] = b;
+}
+
+// FP4 pools: a block of 16 elements a thread and pool. A value has at most 6
+// significant bits, so the bf16 is exact.
+__device__ __forceinline__ void fp4_block_bf16(uint2 codes, uint8_t scale, uint4 &lo, uint4 &hi) {
+    uint32_t p[8];
+    e2m1x8_f16(codes.x, p[0], p[1], p[2], p[3]);
+    e2m1x8_f16(codes.y, p[4], p[5], p[6], p[7]);
+    const float s = scale_value(scale);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&p[i]));
+        p[i] = pack_bf16(f.x * s, f.y * s);
+    }
+    lo = make_uint4(p[0], p[1], p[2], p[3]);
+    hi = make_uint4(p[4], p[5], p[6], p[7]);
+}
+
+__global__ void __launch_bounds__(256) read_kv_fp4_kernel(uint4 *__restrict__ k, uint4 *__restrict__ v,
+                                                          const uint2 *__restrict__ kp, const uint2 *__restrict__ vp,
+                                                          const uint8_t *__restrict__ ks, const uint8_t *__restrict__ vs,
+                                                          const int32_t *__restrict__ slots, int64_t n_tokens, int32_t hkv,
+                                                          int32_t page, int32_t blocks, int64_t pool_slots, int *err) {
+    const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+    const int32_t per_tok = hkv * blocks;
+    if (i >= n_tokens * per_tok) return;
+    const int64_t t = i / per_tok;
+    const int32_t r = (int32_t)(i - t * per_tok), g = r / blocks, b = r - g * blocks;
+    const int32_t slot = slots[t];
+    uint4 lo[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, hi[2] = {lo[0], lo[0]};
+    if (slot >= 0 && slot < pool_slots) {
+        const int64_t at = (((int64_t)(slot / page) * hkv + g) * page + slot % page) * blocks + b;
+        const uint2 ck = kp[at], cv = vp[at];
+        const uint8_t sk = ks[at], sv = vs[at];
+        fp4_block_bf16(ck, sk, lo[0], hi[0]);
+        fp4_block_bf16(cv, sv, lo[1], hi[1]);
+    } else if (slot >= 0) {
+        set_error(err, HSWA_ERR_BOUNDS);
+    }
+    k[2 * i] = lo[0], k[2 * i + 1] = hi[0];
+    v[2 * i] = lo[1], v[2 * i + 1] = hi[1];
+}
+
+// FP8 pools (d = 128): a warp per (token, kv head), 4 elements a lane; code *
+// scale is rounded once to bf16. V's codes lie in a column of its page.
+__global__ void __launch_bounds__(256) read_kv_fp8_kernel(uint2 *__restrict__ k, uint2 *__restrict__ v,
+                                                          const uint8_t *__restrict__ kp, const uint8_t *__restrict__ vp,
+                                                          const float *__restrict__ ks, const float *__restrict__ vs,
+                                                          const int32_t *__restrict__ slots, int64_t n_tokens, int32_t hkv,
+                                                          int32_t page, int64_t pool_slots, int *err) {
+    const int lane = threadIdx.x & 31;
+    const int64_t w = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
+    if (w >= n_tokens * hkv) return;
+    const int32_t slot = slots[w / hkv], g = (int32_t)(w % hkv);
+    uint2 out[2] = {make_uint2(0, 0), make_uint2(0, 0)};
+    if (slot >= 0 && slot < pool_slots) {
+        const int64_t blk = (int64_t)(slot / page) * hkv + g;
+        const int32_t row = slot % page;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            const float s = (which ? vs : ks)[blk * page + row];
+            float x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint8_t c = which ? vp[(blk * 128 + lane * 4 + i) * page + row] : kp[(blk * page + row) * 128 + lane * 4 + i];
+                x[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3))) * s;
+            }
+            out[which] = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+        }
+    } else if (slot >= 0 && lane == 0) {
+        set_error(err, HSWA_ERR_BOUNDS);
+    }
+    k[w * 32 + lane] = out[0];
+    v[w * 32 + lane] = out[1];
+}
+
 int esize(const hswa_config &c) { return c.dtype == HSWA_DTYPE_F32 ? 4 : 2; }
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
@@ -213,6 +352,16 @@ bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 int grid_for(int64_t work, int block) {
     const int64_t g = (work + block - 1) / block;
     return (int)std::max<int64_t>(1, std::min<int64_t>(g, (int64_t)sm_count() * 32));
+}
+
+int64_t pool_slots(const hswa_config &c, const hswa_layer *layer) {
+    return (int64_t)(layer->kind == HSWA_KIND_SWA ? c.swa_pages : c.full_pages) * c.page_size;
+}
+
+// FP4 rows are whole blocks, codes 8 bytes each; a launch has at most 2^31 - 1 CTAs.
+bool fp4_layout_ok(const hswa_config &c, const hswa_layer *layer, int n_tokens) {
+    return c.head_dim % kFp4Block == 0 && (((uintptr_t)layer->k_pool | (uintptr_t)layer->v_pool) & 7) == 0 &&
+           (int64_t)n_tokens * c.n_kv_heads * (c.head_dim / kFp4Block) / 256 < INT32_MAX;
 }
 
 }  // namespace
@@ -240,6 +389,20 @@ extern "C" int hswa_append_kv(const hswa_pool *pool, const hswa_layer *layer, co
             (int64_t)num_pages * c.page_size, error_word());
         return cudaGetLastError() == cudaSuccess ? HSWA_OK : HSWA_ERR_CUDA;
     }
+    if (c.dtype == HSWA_DTYPE_FP4) {
+        if (!layer->k_scale || !layer->v_scale) return HSWA_ERR_INVALID_ARG;
+        if (!fp4_layout_ok(c, layer, n_tokens) || !aligned16(k) || !aligned16(v)) return HSWA_ERR_UNSUPPORTED;
+        if (n_tokens == 0) return HSWA_OK;
+        const int32_t blocks = c.head_dim / kFp4Block;
+        const int64_t work = (int64_t)n_tokens * c.n_kv_heads * blocks;
+        set_last_kernel("append_kv_fp4");
+        append_kv_fp4_kernel<<<(unsigned)((work + 255) / 256), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+            (const uint4 *)k, (const uint4 *)v, (uint2 *)layer->k_pool, (uint2 *)layer->v_pool, (uint8_t *)layer->k_scale,
+            (uint8_t *)layer->v_scale, d_slots, n_tokens, c.n_kv_heads, c.page_size, blocks, pool_slots(c, layer),
+            error_word());
+        const cudaError_t e = cudaGetLastError();
+        return e == cudaSuccess ? HSWA_OK : cuda_fail(e, "append_kv_fp4");
+    }
     const int64_t row_bytes = (int64_t)c.head_dim * esize(c);
     if (row_bytes % 16 || !aligned16(k) || !aligned16(v) || !aligned16(layer->k_pool) || !aligned16(layer->v_pool))
         return HSWA_ERR_UNSUPPORTED;
@@ -254,6 +417,43 @@ extern "C" int hswa_append_kv(const hswa_pool *pool, const hswa_layer *layer, co
     return cudaGetLastError() == cudaSuccess ? HSWA_OK : HSWA_ERR_CUDA;
 }
 
+extern "C" int hswa_read_kv(const hswa_pool *pool, const hswa_layer *layer, const int32_t *d_slots, int n_tokens,
+                            void *k, void *v, hswa_stream_t stream) {
+    HSWA_NVTX("hswa_read_kv");
+    if (!pool || !layer || n_tokens < 0 || (n_tokens > 0 && (!k || !v || !d_slots)) || !layer->k_pool ||
+        !layer->v_pool || (layer->kind != HSWA_KIND_FULL && layer->kind != HSWA_KIND_SWA))
+        return HSWA_ERR_INVALID_ARG;
+    const hswa_config &c = pool->cfg;
+    const bool fp8 = c.dtype == HSWA_DTYPE_FP8_E4M3, fp4 = c.dtype == HSWA_DTYPE_FP4;
+    if ((fp8 || fp4) && (!layer->k_scale || !layer->v_scale)) return HSWA_ERR_INVALID_ARG;
+    const int64_t row_bytes = (int64_t)c.head_dim * esize(c);
+    if (!aligned16(k) || !aligned16(v) || (fp8 && c.head_dim != 128) || (fp4 && !fp4_layout_ok(c, layer, n_tokens)) ||
+        (!fp8 && !fp4 && (row_bytes % 16 || !aligned16(layer->k_pool) || !aligned16(layer->v_pool))))
+        return HSWA_ERR_UNSUPPORTED;
+    const int32_t units = fp8 ? 32 : fp4 ? c.head_dim / kFp4Block : (int32_t)(row_bytes / 16);
+    const int64_t ctas = ((int64_t)n_tokens * c.n_kv_heads * units + 255) / 256;
+    if (ctas > INT32_MAX) return HSWA_ERR_UNSUPPORTED;
+    if (n_tokens == 0) return HSWA_OK;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    set_last_kernel(fp8 ? "read_kv_fp8" : fp4 ? "read_kv_fp4" : "read_kv");
+    if (fp8)
+        read_kv_fp8_kernel<<<(unsigned)ctas, 256, 0, st>>>((uint2 *)k, (uint2 *)v, (const uint8_t *)layer->k_pool,
+                                                           (const uint8_t *)layer->v_pool, layer->k_scale, layer->v_scale,
+                                                           d_slots, n_tokens, c.n_kv_heads, c.page_size,
+                                                           pool_slots(c, layer), error_word());
+    else if (fp4)
+        read_kv_fp4_kernel<<<(unsigned)ctas, 256, 0, st>>>((uint4 *)k, (uint4 *)v, (const uint2 *)layer->k_pool,
+                                                           (const uint2 *)layer->v_pool, (const uint8_t *)layer->k_scale,
+                                                           (const uint8_t *)layer->v_scale, d_slots, n_tokens, c.n_kv_heads,
+                                                           c.page_size, units, pool_slots(c, layer), error_word());
+    else
+        read_kv_kernel<<<(unsigned)ctas, 256, 0, st>>>((chunk_t *)k, (chunk_t *)v, (const chunk_t *)layer->k_pool,
+                                                       (const chunk_t *)layer->v_pool, d_slots, n_tokens, c.n_kv_heads,
+                                                       c.page_size, units, pool_slots(c, layer), error_word());
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? HSWA_OK : cuda_fail(e, "hswa_read_kv");
+}
+
 static int swa_xfer(const hswa_pool *pool, const hswa_layer *layer, const int32_t *d_swa_bt,
                     const int32_t *d_seq_len, const int64_t *d_tok_offset, int n_seqs, void *buf, bool gather,
                     hswa_stream_t stream) {
@@ -262,6 +462,7 @@ static int swa_xfer(const hswa_pool *pool, const hswa_layer *layer, const int32_
         !layer->v_pool)
         return HSWA_ERR_INVALID_ARG;
     const hswa_config &c = pool->cfg;
+    if (c.dtype == HSWA_DTYPE_FP4) return HSWA_ERR_UNSUPPORTED;
     if (c.dtype == HSWA_DTYPE_FP8_E4M3) {
         if (c.head_dim != 128 || c.page_size != 64 || !layer->k_scale || !layer->v_scale || !aligned16(layer->k_pool) ||
             !aligned16(layer->v_pool) || ((uintptr_t)layer->k_scale & 3) || ((uintptr_t)layer->v_scale & 3) ||
@@ -313,6 +514,7 @@ extern "C" int hswa_swa_window_offsets(const hswa_pool *pool, const hswa_layer *
         layer->kind != HSWA_KIND_SWA || layer->window <= 0)
         return HSWA_ERR_INVALID_ARG;
     const hswa_config &c = pool->cfg;
+    if (c.dtype == HSWA_DTYPE_FP4) return HSWA_ERR_UNSUPPORTED;  // no packed window of that type
     const int32_t *lens = seq_len ? seq_len : pool->seq_len.data();
     int64_t off = 0;
     tok_offset_out[0] = 0;

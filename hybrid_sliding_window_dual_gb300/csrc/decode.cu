@@ -36,6 +36,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "fp4.cuh"
 #include "internal.h"
 #include "kernels.h"
 #include "tc.cuh"
@@ -79,6 +80,7 @@ struct DecodeSmemT {
     static constexpr bool kWeights = kWeights_;
     static constexpr int kStages = kTok_ <= 2 ? ::hswa::kStages : 2;
     static constexpr bool kTcQ = false;  // q rows travel with the first page of a piece
+    static constexpr bool kFP4 = false;
     uint8_t k[kStages][kPageHeadBytes];
     uint8_t v[kStages][kPageHeadBytes];
     uint8_t q[kStages][kTok * kQBytes];
@@ -99,12 +101,18 @@ constexpr uint32_t kK8Bytes = kP * kD;
 constexpr uint32_t kV8Bytes = kD * kP;
 constexpr uint32_t kScaleBytes = kP * 4;
 
+// FP4 pools: a page of one kv head is 64 rows of 64 bytes of codes and of 8
+// scales, for K and for V.
+constexpr uint32_t kK4Bytes = kP * kD / 2, kS4Bytes = kP * kD / kFp4Block;
+constexpr uint32_t kUnit4Bytes = 2 * (kK4Bytes + kS4Bytes);
+
 constexpr int kConsumers8 = 4;  // FP8 consumer warps, one 16-key group of a page each
 
 template <int kTok, bool kWeights_ = false>
 struct DecodeSmem8T {
     static constexpr int kStages = 3;
     static constexpr bool kTcQ = false;
+    static constexpr bool kFP4 = false;
     static constexpr bool kWeights = kWeights_;
 
     uint8_t k[kStages][kK8Bytes];
@@ -149,6 +157,7 @@ struct DecodeArgs {
     int64_t pool_slots;
     int32_t n_seqs, bt_stride, hkv, hq, window, num_pages;
     int32_t n_tok;  // query tokens per sequence (multi-token decode), 1 otherwise
+    int32_t tok0;   // FP4 pools: the first token of this launch
     float scale_log2;
     int *err;
     // decode with page weights (null otherwise): log2 of the sum of 2^score
@@ -426,14 +435,21 @@ __device__ void decode_producer(Smem &sm, const CUtensorMap *tk, const CUtensorM
                         flags |= kSkip;
                     }
                     d.flags = flags;
-                    const uint32_t page_bytes = kFP8 ? kK8Bytes + kV8Bytes + 2 * kScaleBytes : 4 * kBoxBytes;
+                    const uint32_t page_bytes = Smem::kFP4 ? kUnit4Bytes : kFP8 ? kK8Bytes + kV8Bytes + 2 * kScaleBytes : 4 * kBoxBytes;
                     const uint32_t q_bytes = (!Smem::kTcQ && j == 0) ? a.n_tok * kQBytes : 0;
                     const uint32_t bytes = (valid ? page_bytes : 0) + q_bytes;
                     if (bytes) {
                         mbar_arrive_expect_tx(&sm.full[stage], bytes);
                         if (valid) {
                             const int32_t blk = page * a.hkv + g;  // (page, kv head) block
-                            if constexpr (kFP8) {
+                            if constexpr (Smem::kFP4) {
+                                const uint8_t *kc = reinterpret_cast<const uint8_t *>(a.k_pool), *vc = reinterpret_cast<const uint8_t *>(a.v_pool);
+                                const uint8_t *ks = reinterpret_cast<const uint8_t *>(a.k_scale), *vs = reinterpret_cast<const uint8_t *>(a.v_scale);
+                                bulk_g2s(sm.k[stage], kc + (int64_t)blk * kK4Bytes, kK4Bytes, &sm.full[stage]);
+                                bulk_g2s(sm.v[stage], vc + (int64_t)blk * kK4Bytes, kK4Bytes, &sm.full[stage]);
+                                bulk_g2s(sm.ks[stage], ks + (int64_t)blk * kS4Bytes, kS4Bytes, &sm.full[stage]);
+                                bulk_g2s(sm.vs[stage], vs + (int64_t)blk * kS4Bytes, kS4Bytes, &sm.full[stage]);
+                            } else if constexpr (kFP8) {
                                 tma_load_2d(sm.k[stage], tk, 0, blk * kP, &sm.full[stage]);
                                 tma_load_2d(sm.v[stage], tv, 0, blk * kD, &sm.full[stage]);
                                 bulk_g2s(sm.ks[stage], a.k_scale + (int64_t)blk * kP, kScaleBytes, &sm.full[stage]);
@@ -1144,7 +1160,10 @@ constexpr float kTcRescaleLog2 = 8.0f;          // rescale O only when the max g
 // bf16 pools: page i is ready to score once its stage has landed, which
 // the producer only loads after PV(i - 4) emptied it.
 struct DecodeTcSmem {
-    static constexpr bool kFP8 = false;
+    static constexpr bool kFP8 = false, kFP4 = false;
+    static constexpr bool kConvert = false;  // pages arrive as MMA operands
+    static constexpr bool kScaled = false;   // K and V scales are left to the softmax
+    static constexpr bool kVT = false;       // V as loaded, [keys][d]: MN-major B
     static constexpr int kStages = 4;
     static constexpr int kSP = kStages;  // S / P buffers
     static constexpr int kQBufs = 2;
@@ -1181,7 +1200,9 @@ static_assert(offsetof(DecodeTcSmem, v) % 1024 == 0 && offsetof(DecodeTcSmem, q)
 // into f16 buffer i % 3 once PV(i - 3) has emptied it, so page i is ready
 // to score when its conversion is done.
 struct DecodeTc8Smem {
-    static constexpr bool kFP8 = true;
+    static constexpr bool kFP8 = true, kFP4 = false;
+    static constexpr bool kConvert = true, kScaled = true;
+    static constexpr bool kVT = true;  // V^T, [d][keys]: K-major B
     static constexpr int kStages = 4;
     static constexpr int kConv = 3;
     static constexpr int kSP = kConv;
@@ -1226,6 +1247,51 @@ static_assert(offsetof(DecodeTc8Smem, q) % 1024 == 0 && offsetof(DecodeTc8Smem, 
                   offsetof(DecodeTc8Smem, vc) % 1024 == 0,
               "128-byte swizzled tiles need 1024-byte alignment");
 
+// FP4 pools: as for FP8, but the converter multiplies each code by its block's
+// scale (exact in f16), so that the MMAs and the softmax are those of 16-bit
+// pages: V is written as [keys][d].
+struct DecodeTc4Smem {
+    static constexpr bool kFP8 = false, kFP4 = true;
+    static constexpr bool kConvert = true, kScaled = false;
+    static constexpr bool kVT = false;
+    static constexpr int kStages = 4;
+    static constexpr int kConv = 3;
+    static constexpr int kSP = kConv;
+    static constexpr int kQBufs = 1;
+    static constexpr bool kTcQ = true;
+    static constexpr bool kWeights = false;
+    static constexpr bool kQTmem = true;
+    static constexpr int kConvThreads = 128;
+    static constexpr int kThreads = 224 + kConvThreads;
+    static constexpr uint32_t kQHalfBytes = 128 * 128;
+    uint8_t q[kQBufs][2 * kQHalfBytes];
+    uint8_t kc[kConv][kPageHeadBytes];  // f16 K and V, [d half][64 keys][128 B], 128-byte swizzle
+    uint8_t vc[kConv][kPageHeadBytes];
+    uint8_t k[kStages][kK4Bytes], v[kStages][kK4Bytes];  // [64 keys][64 B]
+    uint8_t ks[kStages][kS4Bytes], vs[kStages][kS4Bytes];
+    float obuf[kD][32];
+    float ep_m[128], ep_l[128];
+    StageDesc desc[kStages];
+    StageDesc descc[kConv];
+    uint64_t full[kStages], empty[kStages];
+    uint64_t conv_full[kConv], conv_empty[kConv];
+    uint64_t q_full[2], q_empty[2], q_conv[2];
+    uint64_t s_full[kSP], p_full[kSP];
+    uint64_t mma_done[2], ep_bar;
+    uint32_t tmem_base;
+    int32_t abort;
+
+    __device__ uint64_t *ready(int64_t i) { return &conv_full[i % kConv]; }
+    __device__ uint64_t *pv_done(int64_t i) { return &conv_empty[i % kConv]; }
+    static __device__ uint32_t par(int64_t i) { return (uint32_t)(i / kConv) & 1; }
+    __device__ const StageDesc &page(int64_t i) const { return descc[i % kConv]; }
+    __device__ uint64_t *q_ready(int32_t pc) { return &q_conv[pc % kQBufs]; }
+    __device__ uint32_t k_addr(int64_t i) { return smem_u32(kc[i % kConv]); }
+    __device__ uint32_t v_addr(int64_t i) { return smem_u32(vc[i % kConv]); }
+};
+static_assert(offsetof(DecodeTc4Smem, kc) % 1024 == 0 && offsetof(DecodeTc4Smem, vc) % 1024 == 0,
+              "128-byte swizzled tiles need 1024-byte alignment");
+
 template <class Smem>
 constexpr size_t decode_tc_smem_bytes() { return sizeof(Smem) + 1024; }
 
@@ -1246,7 +1312,7 @@ constexpr size_t decode_tc_smem_bytes() { return sizeof(Smem) + 1024; }
 template <bool kQT, class Smem>
 __device__ bool decode_tc_qk(Smem &sm, const DecodeArgs &a, int64_t n) {
     constexpr int kSP = Smem::kSP, kQB = Smem::kQBufs;
-    constexpr uint32_t kIdQK = idesc_16(128, kP, false, Smem::kFP8);
+    constexpr uint32_t kIdQK = idesc_16(128, kP, false, Smem::kConvert);
     const uint32_t tb = sm.tmem_base, qb = smem_u32(sm.q[0]);
     int32_t pc = -1;  // piece of the last scored page
     for (int64_t i = 0; i < n; ++i) {
@@ -1283,9 +1349,9 @@ __device__ bool decode_tc_qk(Smem &sm, const DecodeArgs &a, int64_t n) {
 template <class Smem>
 __device__ bool decode_tc_pv(Smem &sm, const DecodeArgs &a, int64_t n) {
     constexpr int kSP = Smem::kSP;
-    // bf16: V as loaded, [keys][d] (d contiguous: MN-major B, d halves 8 KB
+    // bf16, FP4: V as [keys][d] (d contiguous: MN-major B, d halves 8 KB
     // apart); FP8: the converted V^T, [d][keys] (keys contiguous: K-major)
-    constexpr uint32_t kIdPV = idesc_16(128, kD, !Smem::kFP8, Smem::kFP8);
+    constexpr uint32_t kIdPV = idesc_16(128, kD, !Smem::kVT, Smem::kConvert);
     const uint32_t tb = sm.tmem_base;
     bool fresh = true;  // no PV yet in the current piece: the next one overwrites O
     for (int64_t i = 0; i < n; ++i) {
@@ -1297,10 +1363,10 @@ __device__ bool decode_tc_pv(Smem &sm, const DecodeArgs &a, int64_t n) {
         tc_fence_after();
         if (!(flags & kSkip)) {
             const uint32_t tp = tb + kTmemP + 32 * b, v = sm.v_addr(i);
-            const uint64_t vd = Smem::kFP8 ? sdesc(v, 16, 1024) : sdesc(v, kBoxBytes, 1024);
+            const uint64_t vd = Smem::kVT ? sdesc(v, 16, 1024) : sdesc(v, kBoxBytes, 1024);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)  // 16 keys a step: 32 bytes on (FP8 V^T rows) or 16 rows of 128 B
-                mma_ts(tb + kTmemO, tp + kk * 8, vd + (Smem::kFP8 ? kk * (32 >> 4) : kk * (2048 >> 4)), kIdPV,
+                mma_ts(tb + kTmemO, tp + kk * 8, vd + (Smem::kVT ? kk * (32 >> 4) : kk * (2048 >> 4)), kIdPV,
                        (fresh && kk == 0) ? 0u : 1u);
             fresh = false;
         }
@@ -1396,7 +1462,7 @@ __device__ void decode_tc_softmax(Smem &sm, const DecodeArgs &a, int64_t n) {
             tc_fence_after();
             uint32_t sr[kK];
             tmem_ld_s<kK>(sm.tmem_base + lane_off + 64 * b + c * kK, sr);
-            if constexpr (Smem::kFP8) {
+            if constexpr (Smem::kScaled) {
                 // the K codes entered the MMA as their exact values: a score
                 // in log2 units is S times the key's scale times scale log2 e,
                 // a product the converter stored per key
@@ -1432,7 +1498,7 @@ __device__ void decode_tc_softmax(Smem &sm, const DecodeArgs &a, int64_t n) {
                 m0 = max3(m0, __uint_as_float(sr[x]), __uint_as_float(sr[x + 1]));
                 m1 = max3(m1, __uint_as_float(sr[x + 2]), __uint_as_float(sr[x + 3]));
             }
-            const float mx = Smem::kFP8 ? fmaxf(m0, m1) : fmaxf(m0, m1) * a.scale_log2;
+            const float mx = Smem::kScaled ? fmaxf(m0, m1) : fmaxf(m0, m1) * a.scale_log2;
             const bool need = mx > m_used + kTcRescaleLog2;
             const bool resc = need && m_used != -INFINITY;
             const float alpha = resc ? fast_exp2(m_used - mx) : 1.f;
@@ -1444,13 +1510,15 @@ __device__ void decode_tc_softmax(Smem &sm, const DecodeArgs &a, int64_t n) {
 #pragma unroll
             for (int x = 0; x < kK / 2; ++x) {
                 const float2 sx = make_float2(__uint_as_float(sr[2 * x]), __uint_as_float(sr[2 * x + 1]));
-                const float2 y = Smem::kFP8 ? __fadd2_rn(sx, nm2) : __ffma2_rn(sx, sc2, nm2);
+                const float2 y = Smem::kScaled ? __fadd2_rn(sx, nm2) : __ffma2_rn(sx, sc2, nm2);
                 const float2 p = make_float2(fast_exp2(y.x), fast_exp2(y.y));
                 sum2 = __fadd2_rn(sum2, p);
-                if constexpr (Smem::kFP8) {  // P carries the V scale: V codes enter the MMA as they are
+                if constexpr (Smem::kScaled) {  // P carries the V scale: V codes enter the MMA as they are
                     const float4 v4 = reinterpret_cast<const float4 *>(sm.vsc[i % Smem::kConv] + c * kK)[x >> 1];
                     const float2 pv = __fmul2_rn(p, (x & 1) ? make_float2(v4.z, v4.w) : make_float2(v4.x, v4.y));
                     pk[x] = pack_f16(pv.x, pv.y);
+                } else if constexpr (Smem::kConvert) {
+                    pk[x] = pack_f16(p.x, p.y);
                 } else {
                     pk[x] = pack_bf16(p.x, p.y);
                 }
@@ -1608,6 +1676,21 @@ __device__ __forceinline__ void e4m3x16_to_f16(uint4 c, uint4 &lo, uint4 &hi) {
     e4m3x4_f16x2x2_cvt(c.w, hi.z, hi.w);
 }
 
+// 32 codes of a row of an FP4 page under two scales (the bytes of sc), as 4
+// chunks j0 .. j0 + 3 of a row of 128-byte swizzled f16; sw: the upper two first.
+__device__ __forceinline__ void fp4_to_f16_row(const uint4 &c, uint32_t sc, bool sw, uint8_t *row, int j0, int r7) {
+    const uint32_t s0 = scale_f16x2(sc & 0xff), s1 = scale_f16x2(sc >> 8);
+    const uint32_t w[4] = {sw ? c.z : c.x, sw ? c.w : c.y, sw ? c.x : c.z, sw ? c.y : c.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t s = (k < 2) != sw ? s0 : s1;
+        uint4 f;
+        e2m1x8_f16(w[k], f.x, f.y, f.z, f.w);
+        f = make_uint4(hmul2_bits(f.x, s), hmul2_bits(f.y, s), hmul2_bits(f.z, s), hmul2_bits(f.w, s));
+        *reinterpret_cast<uint4 *>(row + (((j0 + (sw ? k ^ 2 : k)) ^ r7) << 4)) = f;
+    }
+}
+
 // Warps 7-10 (FP8 pools): page i's E4M3 stage to f16 buffer i % kConv, once
 // PV(i - kConv) has emptied it (the f16 buffer's pv_done barrier, waited for
 // on every page, so it is never two phases ahead). K [64 keys][128 B]
@@ -1620,11 +1703,13 @@ __device__ __forceinline__ void e4m3x16_to_f16(uint4 c, uint4 &lo, uint4 &hi) {
 // loads that q tile only after the last QK of the previous piece, q_empty,
 // so the TMEM columns are free by the time it lands); else in place in
 // shared memory. Then the stage is released to the producer.
-template <bool kQT>
-__device__ void decode_tc_convert(DecodeTc8Smem &sm, const DecodeArgs &a, int64_t n) {
-    constexpr int kStages = DecodeTc8Smem::kStages, kConv = DecodeTc8Smem::kConv, kQB = DecodeTc8Smem::kQBufs;
-    constexpr int kCT = DecodeTc8Smem::kConvThreads, kPer = 512 / kCT;  // 16-byte chunks per thread and tile
-    constexpr uint32_t kQH = DecodeTc8Smem::kQHalfBytes;
+// FP4 pools the same with their own page: a 16-byte chunk holds 32 codes of a
+// row, which become 4 chunks of K or of V times the scales of their two blocks.
+template <bool kQT, class Smem>
+__device__ void decode_tc_convert(Smem &sm, const DecodeArgs &a, int64_t n) {
+    constexpr int kStages = Smem::kStages, kConv = Smem::kConv, kQB = Smem::kQBufs;
+    constexpr int kCT = Smem::kConvThreads, kPer = (Smem::kFP4 ? 256 : 512) / kCT;  // 16-byte chunks per thread and tile
+    constexpr uint32_t kQH = Smem::kQHalfBytes;
     const int t = threadIdx.x - 7 * 32;  // 0 .. kCT - 1
     const int quad = (threadIdx.x >> 5) & 3, row = 32 * quad + (threadIdx.x & 31);
     const uint32_t t_q = sm.tmem_base + ((uint32_t)(32 * quad) << 16) + kTmemQ;
@@ -1646,7 +1731,7 @@ __device__ void decode_tc_convert(DecodeTc8Smem &sm, const DecodeArgs &a, int64_
         if ((d.flags & kFirst) && !kQT) {  // f16 in place, for QK from shared memory
             uint4 *q = reinterpret_cast<uint4 *>(sm.q[pc % kQB]);
 #pragma unroll 4
-            for (int x = t; x < 2 * (int)DecodeTc8Smem::kQHalfBytes / 16; x += kCT) q[x] = bf16x8_to_f16x8(q[x]);
+            for (int x = t; x < 2 * (int)Smem::kQHalfBytes / 16; x += kCT) q[x] = bf16x8_to_f16x8(q[x]);
             fence_proxy_async_shared();
             mbar_arrive(&sm.q_conv[pc % kQB]);
         } else if (d.flags & kFirst) {  // f16 pairs into TMEM
@@ -1665,7 +1750,31 @@ __device__ void decode_tc_convert(DecodeTc8Smem &sm, const DecodeArgs &a, int64_
             tc_fence_before();
             mbar_arrive(&sm.q_conv[pc % kQB]);
         }
-        if (!(d.flags & kSkip)) {
+        if constexpr (Smem::kFP4) {
+            if (!(d.flags & kSkip)) {
+                // all loads first, as below
+                uint4 kin[kPer], vin[kPer];
+                uint32_t ksin[kPer], vsin[kPer];
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) {
+                    const int x = t + kCT * e;  // row x / 4 (key), chunk x % 4 (d 32 (x % 4) ..)
+                    kin[e] = reinterpret_cast<const uint4 *>(sm.k[st])[x];
+                    vin[e] = reinterpret_cast<const uint4 *>(sm.v[st])[x];
+                    ksin[e] = reinterpret_cast<const uint16_t *>(sm.ks[st])[x];
+                    vsin[e] = reinterpret_cast<const uint16_t *>(sm.vs[st])[x];
+                }
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) {
+                    const int x = t + kCT * e, r = x >> 2, c4 = x & 3;
+                    // the eight threads of a quarter warp share two rows; those of
+                    // the second d half (8 KB on: the same banks) begin with the
+                    // upper two of their chunks, so each store meets 8 distinct ones
+                    const bool sw = (c4 & 2) != 0;
+                    fp4_to_f16_row(kin[e], ksin[e], sw, sm.kc[b] + (c4 >> 1) * kBoxBytes + r * 128, 4 * (c4 & 1), r & 7);
+                    fp4_to_f16_row(vin[e], vsin[e], sw, sm.vc[b] + (c4 >> 1) * kBoxBytes + r * 128, 4 * (c4 & 1), r & 7);
+                }
+            }
+        } else if (!(d.flags & kSkip)) {
             const uint8_t *k8 = sm.k[st], *v8 = sm.v[st];
             uint8_t *kc = sm.kc[b], *vc = sm.vc[b];
             // all eight loads first: the stores below could alias them as far
@@ -1701,10 +1810,12 @@ __device__ void decode_tc_convert(DecodeTc8Smem &sm, const DecodeArgs &a, int64_
                 *reinterpret_cast<uint4 *>(vrow + (((2 * c4 + 1) ^ (dd & 7)) << 4)) = hi;
             }
         }
-        if (t < kP)
-            sm.ksc[b][t] = sm.ks[st][t] * a.scale_log2;
-        else if (t < 2 * kP)
-            sm.vsc[b][t - kP] = sm.vs[st][t - kP];
+        if constexpr (Smem::kScaled) {
+            if (t < kP)
+                sm.ksc[b][t] = sm.ks[st][t] * a.scale_log2;
+            else if (t < 2 * kP)
+                sm.vsc[b][t - kP] = sm.vs[st][t - kP];
+        }
         if (t == 0) sm.descc[b] = d;
         fence_proxy_async_shared();  // the f16 tiles are read by the tensor cores
         mbar_arrive(&sm.conv_full[b]);
@@ -1723,8 +1834,8 @@ __global__ void __launch_bounds__(Smem::kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < Smem::kStages; ++i) {
             mbar_init(&sm.full[i], 1);
-            // bf16: the PV thread's commit; FP8: the 128 converter threads
-            mbar_init(&sm.empty[i], Smem::kFP8 ? Smem::kThreads - 224 : 1);
+            // bf16: the PV thread's commit; FP8, FP4: the 128 converter threads
+            mbar_init(&sm.empty[i], Smem::kConvert ? Smem::kThreads - 224 : 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sm.q_full[b], 1);
@@ -1734,7 +1845,7 @@ __global__ void __launch_bounds__(Smem::kThreads, 1)
             mbar_init(&sm.s_full[b], 1);
             mbar_init(&sm.p_full[b], 128);
         }
-        if constexpr (Smem::kFP8) {
+        if constexpr (Smem::kConvert) {
             for (int b = 0; b < Smem::kConv; ++b) {
                 mbar_init(&sm.conv_full[b], Smem::kThreads - 224);
                 mbar_init(&sm.conv_empty[b], 1);
@@ -1767,7 +1878,7 @@ __global__ void __launch_bounds__(Smem::kThreads, 1)
                 decode_tc_issue<false, false>(sm, a, u1 - u0);
         }
         __syncwarp();
-    } else if constexpr (Smem::kFP8) {
+    } else if constexpr (Smem::kConvert) {
         decode_tc_convert<Smem::kQTmem && (kR > 1)>(sm, a, u1 - u0);
     }
     tc_fence_before();
@@ -1775,6 +1886,8 @@ __global__ void __launch_bounds__(Smem::kThreads, 1)
     tc_fence_after();
     if (warp == 5) tmem_free<kTcCols>(sm.tmem_base);
 }
+
+#include "decode_fp4.cuh"
 
 // Merge the partial records of a segment split between CTAs (sequence s, query
 // token w, kv head g; 256 threads, a warp per head); write zeros for a
@@ -2287,14 +2400,27 @@ __global__ void __launch_bounds__(32 * kAnyWarps<kE>) decode_weights_any(const T
 
 }  // namespace
 
+// Rows of a pool as values: row r is (page, kv head, slot), d elements long.
+template <typename T>
+struct PlainRows {
+    const T *p;
+    __device__ __forceinline__ float at(int64_t r, int32_t d, int32_t c) const { return to_f(p[r * d + c]); }
+};
+struct Fp4Rows {
+    const uint8_t *codes, *scales;
+    __device__ __forceinline__ float at(int64_t r, int32_t d, int32_t c) const {
+        return fp4_value(codes + r * (d / 2), scales + r * (d / kFp4Block), c);
+    }
+};
+
 // One warp per (query row, query head): query position t, keys [lo, t].
 // mode 0: decode, n_rows = sequences x n_tok (row i is token i mod n_tok of
 //         sequence i / n_tok, t = L - n_tok + i mod n_tok);
 // mode 1: prefill, n_rows = max rows per sequence; row r < n_s of sequence s
 //         is q row q_start[s] + r at t = prefix[s] + r.
-template <typename T, int MAXE>
-__global__ void attention_generic(const T *__restrict__ q, T *__restrict__ o, const T *__restrict__ kp,
-                                  const T *__restrict__ vp, const int32_t *__restrict__ bt,
+template <typename T, int MAXE, class Rows>
+__global__ void attention_generic(const T *__restrict__ q, T *__restrict__ o, const Rows kp, const Rows vp,
+                                  const int32_t *__restrict__ bt,
                                   const int32_t *__restrict__ seq_len, const int32_t *__restrict__ prefix,
                                   const int32_t *__restrict__ q_start, int32_t n_rows, int32_t n_seqs,
                                   int32_t bt_stride, int32_t hq, int32_t hkv, int32_t d, int32_t page,
@@ -2336,12 +2462,12 @@ __global__ void attention_generic(const T *__restrict__ q, T *__restrict__ o, co
             if (lane == 0) set_error(err, HSWA_ERR_BOUNDS);
             continue;
         }
-        const int64_t base = (((int64_t)pg * hkv + g) * page + j % page) * d;
+        const int64_t key = ((int64_t)pg * hkv + g) * page + j % page;
         float dot = 0.f;
 #pragma unroll
         for (int e = 0; e < MAXE; ++e) {
             const int c = lane + 32 * e;
-            if (e < ne && c < d) dot += qv[e] * to_f(kp[base + c]);
+            if (e < ne && c < d) dot += qv[e] * kp.at(key, d, c);
         }
         for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
         const float nm = fmaxf(m, dot);
@@ -2350,7 +2476,7 @@ __global__ void attention_generic(const T *__restrict__ q, T *__restrict__ o, co
 #pragma unroll
         for (int e = 0; e < MAXE; ++e) {
             const int c = lane + 32 * e;
-            const float vv = (e < ne && c < d) ? to_f(vp[base + c]) : 0.f;
+            const float vv = (e < ne && c < d) ? vp.at(key, d, c) : 0.f;
             acc[e] = acc[e] * alpha + p * vv;
         }
         m = nm;
@@ -2371,6 +2497,10 @@ int launch_attention_generic(const hswa_pool *pool, const hswa_layer *layer, con
                              cudaStream_t st, int32_t n_tok) {
     const hswa_config &c = pool->cfg;
     if (c.head_dim > 256 || c.dtype == HSWA_DTYPE_FP8_E4M3) return HSWA_ERR_UNSUPPORTED;
+    if (c.dtype == HSWA_DTYPE_FP4) {
+        if (c.head_dim % kFp4Block) return HSWA_ERR_UNSUPPORTED;
+        if (!layer->k_scale || !layer->v_scale) return HSWA_ERR_INVALID_ARG;
+    }
     if (n_rows == 0) return HSWA_OK;
     const int32_t window = layer->kind == HSWA_KIND_SWA ? layer->window : 0;
     const int32_t num_pages = layer->kind == HSWA_KIND_SWA ? c.swa_pages : c.full_pages;
@@ -2379,19 +2509,23 @@ int launch_attention_generic(const hswa_pool *pool, const hswa_layer *layer, con
     const int64_t grid = (threads + block - 1) / block;
     if (grid > INT32_MAX) return HSWA_ERR_UNSUPPORTED;
     int *err = error_word();
+    const auto run = [&](auto type, auto k, auto v) {
+        using T = decltype(type);
+        attention_generic<T, 8><<<(int)grid, block, 0, st>>>(
+            (const T *)q, (T *)o, k, v, bt, seq_len, prefix, q_start, n_rows, n_seqs, c.max_pages_per_seq,
+            c.n_q_heads, c.n_kv_heads, c.head_dim, c.page_size, window, num_pages, scale, mode, n_tok, err);
+    };
     if (c.dtype == HSWA_DTYPE_F32) {
         set_last_kernel(mode == 0 ? "decode_generic_f32" : "prefill_generic_f32");
-        attention_generic<float, 8><<<(int)grid, block, 0, st>>>(
-            (const float *)q, (float *)o, (const float *)layer->k_pool, (const float *)layer->v_pool, bt, seq_len,
-            prefix, q_start, n_rows, n_seqs, c.max_pages_per_seq, c.n_q_heads, c.n_kv_heads, c.head_dim,
-            c.page_size, window, num_pages, scale, mode, n_tok, err);
+        run(float(), PlainRows<float>{(const float *)layer->k_pool}, PlainRows<float>{(const float *)layer->v_pool});
+    } else if (c.dtype == HSWA_DTYPE_FP4) {
+        set_last_kernel(mode == 0 ? "decode_generic_fp4" : "prefill_generic_fp4");
+        run(__nv_bfloat16(), Fp4Rows{(const uint8_t *)layer->k_pool, (const uint8_t *)layer->k_scale},
+            Fp4Rows{(const uint8_t *)layer->v_pool, (const uint8_t *)layer->v_scale});
     } else {
         set_last_kernel(mode == 0 ? "decode_generic_bf16" : "prefill_generic_bf16");
-        attention_generic<__nv_bfloat16, 8><<<(int)grid, block, 0, st>>>(
-            (const __nv_bfloat16 *)q, (__nv_bfloat16 *)o, (const __nv_bfloat16 *)layer->k_pool,
-            (const __nv_bfloat16 *)layer->v_pool, bt, seq_len, prefix, q_start, n_rows, n_seqs,
-            c.max_pages_per_seq, c.n_q_heads, c.n_kv_heads, c.head_dim, c.page_size, window, num_pages, scale,
-            mode, n_tok, err);
+        run(__nv_bfloat16(), PlainRows<__nv_bfloat16>{(const __nv_bfloat16 *)layer->k_pool},
+            PlainRows<__nv_bfloat16>{(const __nv_bfloat16 *)layer->v_pool});
     }
     return cudaGetLastError() == cudaSuccess ? HSWA_OK : HSWA_ERR_CUDA;
 }
@@ -2532,11 +2666,34 @@ cudaError_t launch_finish_weights(const PageWeights &pw, const hswa_config &c, c
 }
 
 cudaError_t launch_combine(const hswa_config &c, const DecodeArgs &a, int n_ctas, cudaStream_t st) {
-    if (merge_by_heads((int64_t)a.n_seqs * c.n_kv_heads * a.n_tok, n_ctas))
+    // (the workers of an FP4 decode on a part with more SMs could need more shared memory than a kernel has by itself)
+    if (merge_by_heads((int64_t)a.n_seqs * c.n_kv_heads * a.n_tok, n_ctas) && merge_heads_smem(n_ctas) <= (47u << 10))
         return launch_pdl(decode_combine_heads, dim3(c.n_kv_heads * (kG / kMergeHeads), a.n_seqs * a.n_tok), dim3(256),
                           merge_heads_smem(n_ctas), st, a, n_ctas);
     return launch_pdl(decode_combine, dim3(c.n_kv_heads, a.n_seqs * a.n_tok), dim3(256), 0, st, a, n_ctas);
 }
+
+// FP4 pools: CTAs per SM of decode_mma_fp4_d128, and its workers.
+constexpr int kFp4CtasPerSm = 3;
+
+bool decode_fp4_ok(const hswa_pool *pool, const hswa_layer *layer, const void *q, const void *o) {
+    const hswa_config &c = pool->cfg;
+    return c.dtype == HSWA_DTYPE_FP4 && c.head_dim == kD && c.n_q_heads == kG * c.n_kv_heads && c.page_size == kP &&
+           layer->k_scale && layer->v_scale && ((uintptr_t)q & 15) == 0 && ((uintptr_t)o & 15) == 0 &&
+           ((uintptr_t)layer->k_pool & 15) == 0 && ((uintptr_t)layer->v_pool & 15) == 0 &&
+           ((uintptr_t)layer->k_scale & 15) == 0 && ((uintptr_t)layer->v_scale & 15) == 0;
+}
+
+template <int kTok>
+int decode_fp4_ctas_per_sm() {
+    static int cache[kMaxDevices] = {};
+    return kernel_setup(decode_mma_fp4_d128<kTok>, kDecodeSmem4Bytes, 32 * kFp4Warps, cache);
+}
+
+// Query tokens per sequence from which an FP4 decode runs on the tensor-core
+// kernel; below it decode_mma_fp4_d128 takes them two at a time, one launch
+// after the other.
+constexpr int kTcMinTokensFp4 = 5;
 
 size_t desc_bytes(int n_seqs) { return ((size_t)(n_seqs + 1) * sizeof(int4) + 255) & ~(size_t)255; }
 
@@ -2551,7 +2708,9 @@ extern "C" size_t hswa_decode_multi_workspace_size(const hswa_pool *pool, int n_
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         sms = 192;  // no device visible: size for the largest part
-    return desc_bytes(n_seqs) + (size_t)sms * kMaxCtasPerSm * 2 * n_tok * sizeof(Partial);
+    // FP4 pools: every warp leaves records of its own
+    const int per_sm = pool->cfg.dtype == HSWA_DTYPE_FP4 && n_tok < kTcMinTokensFp4 ? kFp4CtasPerSm * kFp4Warps : kMaxCtasPerSm;
+    return desc_bytes(n_seqs) + (size_t)sms * per_sm * 2 * n_tok * sizeof(Partial);
 }
 
 extern "C" size_t hswa_decode_workspace_size(const hswa_pool *pool, int n_seqs) {
@@ -2585,6 +2744,7 @@ int fill_args(DecodeArgs &a, const hswa_pool *pool, const hswa_layer *layer, con
     a.window = layer->kind == HSWA_KIND_SWA ? layer->window : 0;
     a.num_pages = num_pages;
     a.n_tok = 1;
+    a.tok0 = 0;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.err = error_word();
     a.page_lse = a.seq_lse = a.piece_lse = nullptr;
@@ -2650,6 +2810,60 @@ int decode_fp8(const hswa_pool *pool, const hswa_layer *layer, const void *q, vo
     return e == cudaSuccess ? HSWA_OK : HSWA_ERR_CUDA;
 }
 
+// Decode over an FP4 pool (a fused append quantizes first, as its own launch).
+int decode_fp4(const hswa_pool *pool, const hswa_layer *layer, const void *q, void *o, const int32_t *d_bt,
+               const int32_t *d_seq_len, int n_seqs, int n_tok, float scale, void *ws, size_t ws_bytes,
+               const int32_t *slots, const void *k_new, const void *v_new, hswa_stream_t stream) {
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const hswa_config &c = pool->cfg;
+    if (c.head_dim % kFp4Block) return HSWA_ERR_UNSUPPORTED;
+    if (!layer->k_scale || !layer->v_scale) return HSWA_ERR_INVALID_ARG;
+    const int32_t num_pages = layer->kind == HSWA_KIND_SWA ? c.swa_pages : c.full_pages;
+    const uint64_t rows = (uint64_t)num_pages * c.n_kv_heads * c.page_size;
+    // the tensor map's rows are 32-bit coordinates
+    const bool fast = decode_fp4_ok(pool, layer, q, o) && rows < (1ull << 31) && (int64_t)n_seqs * n_tok <= 65535;
+    const bool tc = n_tok >= kTcMinTokensFp4;
+    int n_ctas = 0, workers = 0;
+    if (fast) {
+        const int sms = sm_count();
+        if (sms <= 0) return HSWA_ERR_CUDA;
+        const int per_sm = tc ? decode_tc_ctas_per_sm<DecodeTc4Smem>(n_tok)
+                              : std::min(decode_fp4_ctas_per_sm<1>(), n_tok > 1 ? decode_fp4_ctas_per_sm<2>() : kFp4CtasPerSm);
+        if (per_sm <= 0) return HSWA_ERR_CUDA;
+        n_ctas = sms * std::min(per_sm, kFp4CtasPerSm);
+        workers = tc ? n_ctas : n_ctas * kFp4Warps;
+        if (!ws || ((uintptr_t)ws & 255) ||
+            ws_bytes < desc_bytes(n_seqs) + (size_t)workers * 2 * n_tok * sizeof(Partial))
+            return HSWA_ERR_INVALID_ARG;
+    }
+    if (slots) {
+        const int rc = hswa_append_kv(pool, layer, k_new, v_new, slots, n_seqs, stream);
+        if (rc != HSWA_OK) return rc;
+    }
+    if (!fast)
+        return launch_attention_generic(pool, layer, q, o, d_bt, d_seq_len, nullptr, nullptr, n_seqs * n_tok, n_seqs,
+                                        scale, 0, st, n_tok);
+    DecodeArgs a;
+    fill_args(a, pool, layer, q, o, d_bt, d_seq_len, n_seqs, scale, ws);
+    a.n_tok = n_tok;
+    CUtensorMap tv, tq;
+    if (tc ? !make_q_tmap(&tq, q, c, n_seqs, n_tok)
+           : !make_tmap_2d(&tv, layer->v_pool, rows, kD / 2, kP, kD / 2, CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                           CU_TENSOR_MAP_SWIZZLE_64B))
+        return HSWA_ERR_CUDA;
+    if (tc) tv = tq;  // pages go by plain bulk copies
+    set_last_kernel(tc ? "decode_tc_fp4_d128" : slots ? "append_kv_fp4+decode_mma_fp4_d128" : "decode_mma_fp4_d128");
+    cudaError_t e = launch_pdl(decode_plan, dim3(1), dim3(plan_threads(n_seqs)), 0, st, d_seq_len, n_seqs, c.n_kv_heads, kP,
+                               a.window, n_tok, static_cast<int4 *>(ws), INT64_MAX, a.err);
+    if (e == cudaSuccess && tc) e = launch_decode_tc<DecodeTc4Smem>(n_tok, n_ctas, st, tq, tv, tv, a);
+    if (!tc)
+        for (; e == cudaSuccess && a.tok0 < n_tok; a.tok0 += 2)
+            e = a.tok0 + 1 < n_tok ? launch_pdl(decode_mma_fp4_d128<2>, dim3(n_ctas), dim3(32 * kFp4Warps), kDecodeSmem4Bytes, st, tv, a)
+                                   : launch_pdl(decode_mma_fp4_d128<1>, dim3(n_ctas), dim3(32 * kFp4Warps), kDecodeSmem4Bytes, st, tv, a);
+    if (e == cudaSuccess) e = launch_combine(c, a, workers, st);
+    return e == cudaSuccess ? HSWA_OK : cuda_fail(e, "decode over an FP4 pool");
+}
+
 template <int kTok, bool kWeights = false, bool kLarge = false>
 cudaError_t launch_decode_kernel(int n_ctas, cudaStream_t st, const CUtensorMap &tk, const CUtensorMap &tv,
                                  const DecodeArgs &a) {
@@ -2712,6 +2926,11 @@ int decode_impl(const hswa_pool *pool, const hswa_layer *layer, const void *q, v
             return HSWA_ERR_UNSUPPORTED;  // rows of the combine grid
         return decode_fp8(pool, layer, q, o, d_bt, d_seq_len, n_seqs, n_tok, scale, ws, ws_bytes, slots, k_new,
                           v_new, stream, pw);
+    }
+    if (pool->cfg.dtype == HSWA_DTYPE_FP4) {
+        if (pw) return HSWA_ERR_UNSUPPORTED;
+        return decode_fp4(pool, layer, q, o, d_bt, d_seq_len, n_seqs, n_tok, scale, ws, ws_bytes, slots, k_new, v_new,
+                          stream);
     }
     if (!decode_fast_ok(pool, layer, q, o) ||
         (fused && (((uintptr_t)k_new & 15) || ((uintptr_t)v_new & 15)))) {
@@ -2878,6 +3097,7 @@ extern "C" int hswa_decode_noalloc(const hswa_pool *pool, const hswa_layer *laye
                                    hswa_stream_t stream) {
     HSWA_NVTX("hswa_decode_noalloc");
     if (!pool || n_seqs < 0 || n_seqs > HSWA_DECODE_NOALLOC_MAX_SEQS) return HSWA_ERR_INVALID_ARG;
+    if (pool->cfg.dtype == HSWA_DTYPE_FP4) return HSWA_ERR_UNSUPPORTED;  // its records need more than the fixed array
     if (n_seqs > 0 && layer && decode_fast_ok(pool, layer, q, o)) {
         // the exact scratch the fast path will use must fit the fixed array
         const int sms = sm_count();

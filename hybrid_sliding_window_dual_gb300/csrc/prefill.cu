@@ -41,6 +41,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "fp4.cuh"
 #include "internal.h"
 #include "kernels.h"
 #include "tc.cuh"
@@ -1173,7 +1174,7 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
 bool prefill_fast_ok(const hswa_pool *pool, const hswa_layer *layer, const void *q, const void *o) {
     const hswa_config &c = pool->cfg;
     const int g = c.n_q_heads / c.n_kv_heads;
-    return (c.dtype == HSWA_DTYPE_BF16 || c.dtype == HSWA_DTYPE_FP8_E4M3) && c.head_dim == kD && c.page_size == kP &&
+    return (c.dtype == HSWA_DTYPE_BF16 || c.dtype == HSWA_DTYPE_FP8_E4M3 || c.dtype == HSWA_DTYPE_FP4) && c.head_dim == kD && c.page_size == kP &&
            g % 2 == 0 && ((uintptr_t)q & 15) == 0 && ((uintptr_t)o & 15) == 0 &&
            ((uintptr_t)layer->k_pool & 15) == 0 && ((uintptr_t)layer->v_pool & 15) == 0;
 }
@@ -1196,6 +1197,13 @@ __host__ __device__ __forceinline__ void chunk_pages(int32_t pre, int32_t n, int
     const int32_t lo_key = (window > 0 && pre - window + 1 > 0) ? pre - window + 1 : 0;
     lo = lo_key / kP;
     hi = n > 0 ? (pre + n - 1) / kP : lo - 1;
+}
+
+// Whether chunks over such pools go through staged fp16 pages. (FP4 pools of
+// other shapes are read by the CUDA-core kernel.)
+bool staged(const hswa_config &c) {
+    return c.dtype == HSWA_DTYPE_FP8_E4M3 ||
+           (c.dtype == HSWA_DTYPE_FP4 && c.head_dim == kD && c.page_size == kP && c.n_q_heads / c.n_kv_heads % 2 == 0);
 }
 
 constexpr size_t align1k(size_t x) { return (x + 1023) & ~(size_t)1023; }
@@ -1277,14 +1285,14 @@ __device__ __forceinline__ __half2 dequant_f16x2(uint8_t c0, uint8_t c1, float s
     return __floats2half2_rn(fminf(fmaxf(f.x * s0, -65504.f), 65504.f), fminf(fmaxf(f.y * s1, -65504.f), 65504.f));
 }
 
-// One block per (logical page j, sequence s): writes the staging table entry
-// of (s, j) and, for a page the chunk reads, its fp16 copy (K rows stay
-// rows; each kv head's transposed V block [d][P] becomes [P][d]).
-__global__ void __launch_bounds__(256) prefill_stage_fp8(StageArgs a) {
+// Block (logical page j, sequence s): writes the staging table entry of (s, j)
+// and returns the copy that the page goes to, or -1 if the chunk does not read it.
+__device__ __forceinline__ int32_t stage_slot(const StageArgs &a, int32_t &page) {
     const int32_t j = blockIdx.x, s = blockIdx.y;
     int32_t lo_pg, hi_pg;
     chunk_pages(a.prefix[s], a.q_start[s + 1] - a.q_start[s], a.window, lo_pg, hi_pg);
-    int32_t page = -1, slot = -1;
+    int32_t slot = -1;
+    page = -1;
     if (j >= lo_pg && j <= hi_pg) {
         page = a.bt[(int64_t)s * a.bt_stride + j];
         const int32_t copy = a.stage_off[s] + (j - lo_pg);
@@ -1295,6 +1303,15 @@ __global__ void __launch_bounds__(256) prefill_stage_fp8(StageArgs a) {
         if (page >= 0 && page < a.num_pages) slot = copy;
     }
     if (threadIdx.x == 0) a.stage_bt[(int64_t)s * a.bt_stride + j] = slot;  // -1: the kernel reports it if read
+    return slot;
+}
+
+// One block per (logical page, sequence): the fp16 copy of a page that the
+// chunk reads (K rows stay rows; each kv head's transposed V block [d][P]
+// becomes [P][d]).
+__global__ void __launch_bounds__(256) prefill_stage_fp8(StageArgs a) {
+    int32_t page;
+    const int32_t slot = stage_slot(a, page);
     if (slot < 0) return;
     // K: 16 codes per thread and step
     const uint8_t *kc = a.k_codes + (int64_t)page * a.hkv * kP * kD;
@@ -1339,6 +1356,36 @@ __global__ void __launch_bounds__(256) prefill_stage_fp8(StageArgs a) {
             *reinterpret_cast<uint4 *>(vo + ((int64_t)h * kP + p) * kD + d0) = *reinterpret_cast<const uint4 *>(out);
         }
     }
+}
+
+// The same for an FP4 page: rows of K and of V stay rows, and every value is an
+// f16. 32 codes and two scales a thread and step.
+__device__ __forceinline__ void stage_fp4(const uint8_t *codes, const uint8_t *scales, __half *out, int32_t chunks) {
+    for (int32_t c = threadIdx.x; c < chunks; c += blockDim.x) {
+        const uint4 raw = reinterpret_cast<const uint4 *>(codes)[c];
+        const uint32_t sc = reinterpret_cast<const uint16_t *>(scales)[c];
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t s = scale_f16x2(i < 2 ? sc & 0xff : sc >> 8);
+            uint4 f;
+            e2m1x8_f16(w[i], f.x, f.y, f.z, f.w);
+            reinterpret_cast<uint4 *>(out)[4 * (int64_t)c + i] =
+                make_uint4(hmul2_bits(f.x, s), hmul2_bits(f.y, s), hmul2_bits(f.z, s), hmul2_bits(f.w, s));
+        }
+    }
+}
+
+__global__ void __launch_bounds__(256) prefill_stage_fp4(StageArgs a) {
+    int32_t page;
+    const int32_t slot = stage_slot(a, page);
+    if (slot < 0) return;
+    const int64_t rows = (int64_t)a.hkv * kP;
+    const int32_t chunks = a.hkv * kP * kD / 32;
+    stage_fp4(a.k_codes + page * rows * (kD / 2), reinterpret_cast<const uint8_t *>(a.k_scale) + page * rows * (kD / kFp4Block),
+              a.k_out + slot * rows * kD, chunks);
+    stage_fp4(a.v_codes + page * rows * (kD / 2), reinterpret_cast<const uint8_t *>(a.v_scale) + page * rows * (kD / kFp4Block),
+              a.v_out + slot * rows * kD, chunks);
 }
 
 // q (bf16) to fp16 for the fp16 MMAs: exact for magnitudes in
@@ -1431,7 +1478,7 @@ using namespace hswa;
 
 extern "C" size_t hswa_prefill_workspace_size(const hswa_pool *pool, const hswa_layer *layer, int n_seqs,
                                               int max_q_len) {
-    if (!pool || !layer || n_seqs < 0 || max_q_len < 0 || pool->cfg.dtype != HSWA_DTYPE_FP8_E4M3) return 0;
+    if (!pool || !layer || n_seqs < 0 || max_q_len < 0 || !staged(pool->cfg)) return 0;
     if (layer->kind == HSWA_KIND_SWA && layer->window <= 0) return 0;
     return stage_bytes(pool->cfg, n_seqs, (int64_t)n_seqs * max_q_len,
                        (int64_t)n_seqs * stage_pages_per_seq(pool->cfg, layer, max_q_len));
@@ -1439,8 +1486,7 @@ extern "C" size_t hswa_prefill_workspace_size(const hswa_pool *pool, const hswa_
 
 extern "C" size_t hswa_prefill_workspace_size_exact(const hswa_pool *pool, const hswa_layer *layer, int n_seqs,
                                                     const int32_t *prefix_len, const int32_t *q_start) {
-    if (!pool || !layer || n_seqs < 0 || (n_seqs > 0 && (!prefix_len || !q_start)) ||
-        pool->cfg.dtype != HSWA_DTYPE_FP8_E4M3)
+    if (!pool || !layer || n_seqs < 0 || (n_seqs > 0 && (!prefix_len || !q_start)) || !staged(pool->cfg))
         return 0;
     if (layer->kind == HSWA_KIND_SWA && layer->window <= 0) return 0;
     const int32_t window = layer->kind == HSWA_KIND_SWA ? layer->window : 0;
@@ -1471,9 +1517,12 @@ extern "C" int hswa_prefill_chunk_ws(const hswa_pool *pool, const hswa_layer *la
     const hswa_config &c = pool->cfg;
     const int32_t window = layer->kind == HSWA_KIND_SWA ? layer->window : 0;
     const int32_t num_pages = layer->kind == HSWA_KIND_SWA ? c.swa_pages : c.full_pages;
-    if (c.dtype == HSWA_DTYPE_FP8_E4M3) {
+    const bool fp4 = c.dtype == HSWA_DTYPE_FP4;
+    if (fp4 && (!layer->k_scale || !layer->v_scale)) return HSWA_ERR_INVALID_ARG;
+    if (staged(c)) {
         if (!prefill_fast_ok(pool, layer, q, o) || c.head_dim != 128 || !layer->k_scale || !layer->v_scale ||
-            ((uintptr_t)layer->k_pool & 15) || ((uintptr_t)layer->v_pool & 15))
+            ((uintptr_t)layer->k_pool & 15) || ((uintptr_t)layer->v_pool & 15) ||
+            (fp4 && (((uintptr_t)layer->k_scale | (uintptr_t)layer->v_scale) & 1)))
             return HSWA_ERR_UNSUPPORTED;
         const StageLayout l = stage_layout(c, n_seqs, total_q, ws_bytes);
         if (!ws || ((uintptr_t)ws & 255) || l.cap < 1) return HSWA_ERR_INVALID_ARG;
@@ -1502,17 +1551,24 @@ extern "C" int hswa_prefill_chunk_ws(const hswa_pool *pool, const hswa_layer *la
         sa.err = error_word();
         __half *q16 = reinterpret_cast<__half *>(base + l.q_off);
         const int64_t n8 = (int64_t)total_q * c.n_q_heads * kD / 8;
-        set_last_kernel(window > 0 && window <= kBN ? "prefill_stage_fp8+prefill_swa_tc_d128<f16>"
-                                                     : "prefill_stage_fp8+prefill_tc_bf16_d128<f16>");
+        if (fp4)
+            set_last_kernel(window > 0 && window <= kBN ? "prefill_stage_fp4+prefill_swa_tc_d128<f16>"
+                                                         : "prefill_stage_fp4+prefill_tc_bf16_d128<f16>");
+        else
+            set_last_kernel(window > 0 && window <= kBN ? "prefill_stage_fp8+prefill_swa_tc_d128<f16>"
+                                                         : "prefill_stage_fp8+prefill_tc_bf16_d128<f16>");
         prefill_stage_plan<<<1, 256, 0, st>>>(sa);
-        prefill_stage_fp8<<<dim3(c.max_pages_per_seq, n_seqs), 256, 0, st>>>(sa);
+        if (fp4)
+            prefill_stage_fp4<<<dim3(c.max_pages_per_seq, n_seqs), 256, 0, st>>>(sa);
+        else
+            prefill_stage_fp8<<<dim3(c.max_pages_per_seq, n_seqs), 256, 0, st>>>(sa);
         prefill_q_to_f16<<<(int)std::min<int64_t>((n8 + 255) / 256, 4096), 256, 0, st>>>(
             static_cast<const __nv_bfloat16 *>(q), q16, n8);
         if (cudaGetLastError() != cudaSuccess) return HSWA_ERR_CUDA;
         return launch_prefill_tc(c, window, sa.k_out, sa.v_out, true, (int32_t)staged_pages, sa.stage_bt, q16, o,
                                  d_prefix_len, d_q_start, n_seqs, total_q, max_q_len, scale, st);
     }
-    if (!prefill_fast_ok(pool, layer, q, o))
+    if (fp4 || !prefill_fast_ok(pool, layer, q, o))
         return launch_attention_generic(pool, layer, q, o, d_bt, nullptr, d_prefix_len, d_q_start, max_q_len,
                                         n_seqs, scale, 1, st);
     set_last_kernel(window > 0 && window <= kBN ? "prefill_swa_tc_d128" : "prefill_tc_bf16_d128");

@@ -19,6 +19,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "fp4.cuh"
 #include "internal.h"
 
 struct hswa_rope {
@@ -83,7 +84,8 @@ __device__ __forceinline__ float rotated(const T *x, int e, const RopeArgs &a, c
 // may be rotated in place. Bound by loads and instructions of one element each:
 // 4096 bf16 tokens of 64 / 8 heads, 100 of 128 elements turned, take 146 us, 25
 // for the bytes at the copy rate; 64 tokens 14.
-template <typename T, bool kFP8>
+// kQuant: 0 for pools of T, 8 and 4 for FP8 and FP4 pools.
+template <typename T, int kQuant>
 __global__ void __launch_bounds__(256) rope_append_any(const __grid_constant__ RopeArgs a) {
     constexpr int kMaxE = HSWA_ROPE_MAX_HEAD / 32;
     __shared__ float2 cs[HSWA_ROPE_MAX_DIM / 2];
@@ -119,7 +121,20 @@ __global__ void __launch_bounds__(256) rope_append_any(const __grid_constant__ R
         }
         const int64_t blk = (int64_t)(slot / a.page) * a.hkv + h;  // (page, kv head) block
         const int32_t row = slot % a.page;
-        if constexpr (kFP8) {
+        if constexpr (kQuant == 4) {  // a block is half a warp's elements, a byte two lanes'
+            uint8_t *p = (uint8_t *)(kind == 1 ? a.kp : a.vp) + (blk * a.page + row) * (a.d / 2);
+            uint8_t *sp = (uint8_t *)(kind == 1 ? a.ks : a.vs) + (blk * a.page + row) * (a.d / kFp4Block);
+#pragma unroll
+            for (int j = 0; j < kMaxE; ++j) {
+                const int e = lane + 32 * j;
+                float top = fabsf(y[j]);
+                for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                const uint32_t scale = fp4_scale(top), code = fp4_code(y[j], scale);
+                const uint32_t next = __shfl_xor_sync(0xffffffffu, code, 1);
+                if (e < a.d && !(lane & 1)) p[e / 2] = (uint8_t)(code | next << 4);
+                if (e < a.d && !(lane & 15)) sp[e / kFp4Block] = (uint8_t)scale;
+            }
+        } else if constexpr (kQuant == 8) {
             for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
             const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
             uint8_t *p = (uint8_t *)(kind == 1 ? a.kp : a.vp) + blk * a.page * a.d;
@@ -295,14 +310,14 @@ __device__ void rope_v_fp8(const RopeArgs &a, int32_t block) {
 // (put first or spread among the others they cost 2 and 7 us more; four
 // tokens' codes stored as a word where they make one, 9 more). A
 // decode step of 64 tokens takes 3.5 us on the device.
-template <typename T, bool kFP8, bool kAdjacent, int kTile, int kItems, int kMinCtas>
+template <typename T, int kQuant, bool kAdjacent, int kTile, int kItems, int kMinCtas>
 __global__ void __launch_bounds__(256, kMinCtas) rope_append_vec(const __grid_constant__ RopeArgs a, int32_t n_q_blocks) {
     constexpr int V = kVec<T>;
     __shared__ __align__(16) float cs[kTile][HSWA_ROPE_MAX_DIM / 2], sn[kTile][HSWA_ROPE_MAX_DIM / 2];
     __shared__ int32_t slot_of[kTile];
     pdl_wait();
     pdl_launch_dependents();
-    if constexpr (kFP8) {
+    if constexpr (kQuant == 8) {
         if ((int32_t)blockIdx.x >= n_q_blocks) {
             rope_v_fp8<kTile == 1 ? 8 : kVTile>(a, blockIdx.x - n_q_blocks);
             return;
@@ -311,7 +326,7 @@ __global__ void __launch_bounds__(256, kMinCtas) rope_append_vec(const __grid_co
     const int tid = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
     const int64_t t0 = (int64_t)blockIdx.x * kTile;
     const int nt = (int)min((int64_t)kTile, a.n_tokens - t0);
-    const int rows = a.hq + (kFP8 ? 1 : 2) * a.hkv;  // of a token: q, K, V
+    const int rows = a.hq + (kQuant == 8 ? 1 : 2) * a.hkv;  // of a token: q, K, V
     const int n = nt * rows, chunks = a.d / V;
     // this thread's two chunks of a row: j-th of the first halves and its
     // partner, or j and j + half the row; neighbours in a warp are neighbours
@@ -375,7 +390,24 @@ __global__ void __launch_bounds__(256, kMinCtas) rope_append_vec(const __grid_co
             const bool is_k = h < a.hq + a.hkv;
             const int64_t blk = (int64_t)(slot / a.page) * a.hkv + (h - a.hq - (is_k ? 0 : a.hkv));
             const int64_t row = blk * a.page + slot % a.page;
-            if constexpr (kFP8) {
+            if constexpr (kQuant == 4) {
+                // a block is this thread's chunk and its neighbour's (c0 and c1
+                // have j's parity: hswa_rope_append sees to it)
+                float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+                for (int e = 0; e < V; ++e) m0 = fmaxf(m0, fabsf(lo[e])), m1 = fmaxf(m1, fabsf(hi[e]));
+                const uint32_t mates = 3u << (tid & 30);
+                const uint32_t s0 = fp4_scale(fmaxf(m0, __shfl_xor_sync(mates, m0, 1)));
+                const uint32_t s1 = fp4_scale(fmaxf(m1, __shfl_xor_sync(mates, m1, 1)));
+                uint32_t *o = reinterpret_cast<uint32_t *>((uint8_t *)(is_k ? a.kp : a.vp) + row * (a.d / 2));
+                o[c0] = fp4_codes8(lo, s0);
+                o[c1] = fp4_codes8(hi, s1);
+                if (!(j & 1)) {
+                    uint8_t *sp = (uint8_t *)(is_k ? a.ks : a.vs) + row * (a.d / kFp4Block);
+                    sp[c0 / 2] = (uint8_t)s0;
+                    sp[c1 / 2] = (uint8_t)s1;
+                }
+            } else if constexpr (kQuant == 8) {
                 const float scale = row_scale(lo, hi);
                 uint2 *o = reinterpret_cast<uint2 *>((uint8_t *)a.kp + row * 128);
                 o[c0] = e4m3x8(lo, scale);
@@ -400,26 +432,26 @@ __global__ void __launch_bounds__(256, kMinCtas) rope_append_vec(const __grid_co
 // 32.2; fp32 32 / 4 heads 2048 13.3 / 16.8, 4096 32.4 / 32.0, 64 / 8 4096 52 / 58,
 // 16384 equal; FP8 32 / 4 1024 9.2 / 9.4, 2048 16.0 / 11.2, 64 / 8 1280 14.5 / 16.0, 1536
 // 17.1 / 16.4. (Up to 16 tokens a CTA for few heads gained nothing.)
-template <typename T, bool kFP8>
+template <typename T, int kQuant>
 int tile_from(int threads) {
     if (threads <= 160) return 640;
     if (threads <= 320) return 1024;
-    if (kFP8) return 1440;
+    if (kQuant == 8) return 1440;
     return threads > 640 ? 8192 : sizeof(T) == 2 ? 2560 : 4096;
 }
 
-template <typename T, bool kFP8, bool kAdjacent>
+template <typename T, int kQuant, bool kAdjacent>
 cudaError_t launch_rope_vec(const RopeArgs &a, cudaStream_t st) {
     const int units = (a.d / kVec<T> + 1) / 2;  // threads of a row
-    const int rows = a.hq + (kFP8 ? 1 : 2) * a.hkv;
-    const bool tiled = a.n_tokens >= tile_from<T, kFP8>(rows * units);
+    const int rows = a.hq + (kQuant == 8 ? 1 : 2) * a.hkv;
+    const bool tiled = a.n_tokens >= tile_from<T, kQuant>(rows * units);
     const int64_t nq = tiled ? ((int64_t)a.n_tokens + kMaxTile - 1) / kMaxTile : a.n_tokens;
     const int64_t vt = tiled ? kVTile : 8;
-    const int64_t nv = kFP8 ? (a.n_tokens + vt - 1) / vt * a.hkv : 0;
+    const int64_t nv = kQuant == 8 ? (a.n_tokens + vt - 1) / vt * a.hkv : 0;
     const dim3 grid((unsigned)(nq + nv)), block(units, 256 / units);
-    constexpr int kItems = kFP8 || kAdjacent ? 3 : 2, kMinCtas = kFP8 || kAdjacent ? 4 : 5;
-    return tiled ? launch_pdl(rope_append_vec<T, kFP8, kAdjacent, kMaxTile, kItems, kMinCtas>, grid, block, 0, st, a, (int32_t)nq)
-                 : launch_pdl(rope_append_vec<T, kFP8, kAdjacent, 1, 3, 4>, grid, block, 0, st, a, (int32_t)nq);
+    constexpr int kItems = kQuant || kAdjacent ? 3 : 2, kMinCtas = kQuant || kAdjacent ? 4 : 5;
+    return tiled ? launch_pdl(rope_append_vec<T, kQuant, kAdjacent, kMaxTile, kItems, kMinCtas>, grid, block, 0, st, a, (int32_t)nq)
+                 : launch_pdl(rope_append_vec<T, kQuant, kAdjacent, 1, 3, 4>, grid, block, 0, st, a, (int32_t)nq);
 }
 
 }  // namespace
@@ -490,10 +522,11 @@ extern "C" int hswa_rope_append(const hswa_pool *pool, const hswa_layer *layer, 
         (layer->kind != HSWA_KIND_FULL && layer->kind != HSWA_KIND_SWA))
         return HSWA_ERR_INVALID_ARG;
     const hswa_config &c = pool->cfg;
-    const bool fp8 = c.dtype == HSWA_DTYPE_FP8_E4M3;
+    const bool fp8 = c.dtype == HSWA_DTYPE_FP8_E4M3, fp4 = c.dtype == HSWA_DTYPE_FP4;
     if (rope->rotary_dim > c.head_dim) return HSWA_ERR_INVALID_ARG;
-    if (c.head_dim > HSWA_ROPE_MAX_HEAD || (fp8 && c.head_dim != 128)) return HSWA_ERR_UNSUPPORTED;
-    if (fp8 && (!layer->k_scale || !layer->v_scale)) return HSWA_ERR_INVALID_ARG;
+    if (c.head_dim > HSWA_ROPE_MAX_HEAD || (fp8 && c.head_dim != 128) || (fp4 && c.head_dim % kFp4Block))
+        return HSWA_ERR_UNSUPPORTED;
+    if ((fp8 || fp4) && (!layer->k_scale || !layer->v_scale)) return HSWA_ERR_INVALID_ARG;
     if (n_tokens == 0) return HSWA_OK;
     const int64_t q_row = (int64_t)c.n_q_heads * c.head_dim, kv_row = (int64_t)c.n_kv_heads * c.head_dim;
     if (!q || !k || !v || !d_pos || !d_slots || !q_out || q_stride < q_row || k_stride < kv_row || v_stride < kv_row)
@@ -530,24 +563,30 @@ extern "C" int hswa_rope_append(const hswa_pool *pool, const hswa_layer *layer, 
     const uintptr_t bases = (uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)q_out | (uintptr_t)a.kp | (uintptr_t)a.vp;
     const bool vec = rope->rotary_dim % (a.adjacent ? w : 2 * w) == 0 && c.head_dim % w == 0 && (q_stride | k_stride | v_stride) % w == 0 &&
                      (bases & 15) == 0 &&
+                     // FP4: the two chunks of a block belong to neighbouring threads
+                     (!fp4 || (c.head_dim % 32 == 0 && (a.adjacent || rope->rotary_dim % 32 == 0))) &&
                      n_tokens + (fp8 ? (n_tokens + INT64_C(7)) / 8 * c.n_kv_heads : 0) <= INT32_MAX;
     cudaError_t rc;
     if (vec) {
-        set_last_kernel(fp8 ? "rope_append_fp8" : e == 4 ? "rope_append_f32" : "rope_append_bf16");
+        set_last_kernel(fp8 ? "rope_append_fp8" : fp4 ? "rope_append_fp4" : e == 4 ? "rope_append_f32" : "rope_append_bf16");
         if (fp8)
-            rc = a.adjacent ? launch_rope_vec<__nv_bfloat16, true, true>(a, st) : launch_rope_vec<__nv_bfloat16, true, false>(a, st);
+            rc = a.adjacent ? launch_rope_vec<__nv_bfloat16, 8, true>(a, st) : launch_rope_vec<__nv_bfloat16, 8, false>(a, st);
+        else if (fp4)
+            rc = a.adjacent ? launch_rope_vec<__nv_bfloat16, 4, true>(a, st) : launch_rope_vec<__nv_bfloat16, 4, false>(a, st);
         else if (e == 4)
-            rc = a.adjacent ? launch_rope_vec<float, false, true>(a, st) : launch_rope_vec<float, false, false>(a, st);
+            rc = a.adjacent ? launch_rope_vec<float, 0, true>(a, st) : launch_rope_vec<float, 0, false>(a, st);
         else
-            rc = a.adjacent ? launch_rope_vec<__nv_bfloat16, false, true>(a, st) : launch_rope_vec<__nv_bfloat16, false, false>(a, st);
+            rc = a.adjacent ? launch_rope_vec<__nv_bfloat16, 0, true>(a, st) : launch_rope_vec<__nv_bfloat16, 0, false>(a, st);
     } else {
-        set_last_kernel(fp8 ? "rope_append_any_fp8" : e == 4 ? "rope_append_any_f32" : "rope_append_any_bf16");
+        set_last_kernel(fp8 ? "rope_append_any_fp8" : fp4 ? "rope_append_any_fp4" : e == 4 ? "rope_append_any_f32" : "rope_append_any_bf16");
         if (fp8)
-            rope_append_any<__nv_bfloat16, true><<<n_tokens, 256, 0, st>>>(a);
+            rope_append_any<__nv_bfloat16, 8><<<n_tokens, 256, 0, st>>>(a);
+        else if (fp4)
+            rope_append_any<__nv_bfloat16, 4><<<n_tokens, 256, 0, st>>>(a);
         else if (e == 4)
-            rope_append_any<float, false><<<n_tokens, 256, 0, st>>>(a);
+            rope_append_any<float, 0><<<n_tokens, 256, 0, st>>>(a);
         else
-            rope_append_any<__nv_bfloat16, false><<<n_tokens, 256, 0, st>>>(a);
+            rope_append_any<__nv_bfloat16, 0><<<n_tokens, 256, 0, st>>>(a);
         rc = cudaGetLastError();
     }
     return rc == cudaSuccess ? HSWA_OK : cuda_fail(rc, "hswa_rope_append");

@@ -11,7 +11,7 @@ import torch
 from . import _binding as B
 
 _TORCH_DTYPE = {B.HSWA_DTYPE_F32: torch.float32, B.HSWA_DTYPE_BF16: torch.bfloat16,
-                B.HSWA_DTYPE_FP8_E4M3: torch.uint8}
+                B.HSWA_DTYPE_FP8_E4M3: torch.uint8, B.HSWA_DTYPE_FP4: torch.uint8}
 
 
 class DualPoolSession:
@@ -38,11 +38,12 @@ class DualPoolSession:
         self.kinds = list(layer_kinds)
         self.k, self.v, self.ks, self.vs, self.layers = [], [], [], [], []
         self.fp8 = config.dtype == B.HSWA_DTYPE_FP8_E4M3
+        self.fp4 = config.dtype == B.HSWA_DTYPE_FP4
         shared = None
         for kind in self.kinds:
             pages = config.full_pages if kind == B.HSWA_KIND_FULL else config.swa_pages
             P, d, hkv = config.page_size, config.head_dim, config.n_kv_heads
-            shape = (pages, hkv, P, d)
+            shape = (pages, hkv, P, d // 2 if self.fp4 else d)
             if kind == B.HSWA_KIND_FULL and share_full_pool and shared is not None:
                 k, v, ks, vs = shared
             else:
@@ -55,6 +56,9 @@ class DualPoolSession:
                 if self.fp8:
                     ks = torch.ones((pages, hkv, P, d // 128), dtype=torch.float32, device=self.device)
                     vs = torch.ones_like(ks)
+                if self.fp4:  # a scale byte per 16 elements
+                    ks = torch.zeros((pages, hkv, P, d // 16), dtype=torch.uint8, device=self.device)
+                    vs = torch.zeros_like(ks)
                 if kind == B.HSWA_KIND_FULL and share_full_pool:
                     shared = (k, v, ks, vs)
             self.k.append(k)
@@ -142,6 +146,10 @@ class DualPoolSession:
     def append(self, layer, k, v, d_slots):
         B.hswa_append_kv(self.pool, self.layers[layer], k, v, d_slots, k.shape[0], self.stream)
 
+    def read(self, layer, d_slots, k, v):
+        """K and V rows at slots as values: k, v [T, n_kv_heads, head_dim]."""
+        B.hswa_read_kv(self.pool, self.layers[layer], d_slots, d_slots.shape[0], k, v, self.stream)
+
     def rope_append(self, layer, rope, q, k, v, d_pos, d_slots, q_out):
         """Rotate q (into q_out) and K, and append K and V. q, k, v: [T, heads *
         d] or [T, heads, d], rows possibly slices of one projection."""
@@ -188,6 +196,43 @@ class DualPoolSession:
         p_stride, q_stride = self._row_stride(p), 0 if q is None else self._row_stride(q)
         B.hswa_verify_draft(dtype, p, p_stride, q, q_stride, d_draft, d_n_draft, u, n_seqs, n_tok, vocab, n_accept,
                             tokens, self.stream)
+
+    def count_tokens(self, counts, tokens, n_prompt=None, clear=False):
+        """Count tokens [n_seqs, n] (negative ones are skipped) in counts
+        [n_seqs, vocab] int16 (bit 15: in the prompt); the first n_prompt[i]
+        of a row are its prompt. clear: counts start from nothing."""
+        n_seqs, n = tokens.shape
+        if counts.dtype.itemsize != 2 or counts.shape[0] != n_seqs or (counts.numel() and counts.stride(1) != 1):
+            raise ValueError("counts must hold a row of 16-bit values per sequence")
+        if tokens.dtype != torch.int32 or (n > 1 and tokens.stride(1) != 1):
+            raise ValueError("tokens must be rows of int32")
+        vocab = counts.shape[1]
+        B.hswa_count_tokens(counts, counts.stride(0) if n_seqs > 1 else vocab, tokens, tokens.stride(0) if n_seqs > 1 else n,
+                            n_prompt, n_seqs, n, vocab, clear, self.stream)
+
+    def probs(self, logits, p, params=None, counts=None, d_draft=None, bias_token=None, bias=None, mask=None):
+        """logits [n_seqs, n_tok, vocab] to probabilities p (may be logits):
+        params [n_seqs, 4] fp32 (temperature, repetition, frequency, presence),
+        counts [n_seqs, vocab] int16, d_draft [n_seqs, n_tok - 1], bias_token
+        and bias [n_seqs, n_bias], mask [n_seqs * n_tok, words] int32 bits."""
+        dtype = {torch.float32: B.HSWA_DTYPE_F32, torch.bfloat16: B.HSWA_DTYPE_BF16}
+        n_seqs, n_tok, vocab = logits.shape
+        if logits.dtype not in dtype or p.dtype not in dtype or p.shape != logits.shape:
+            raise ValueError("logits and p must be float32 or bfloat16 of one shape")
+        if counts is not None and (counts.dtype.itemsize != 2 or counts.shape != (n_seqs, vocab) or (vocab > 1 and counts.stride(1) != 1)):
+            raise ValueError("counts must hold a row of 16-bit values per sequence")
+        if (bias_token is None) != (bias is None) or (bias is not None and bias.shape != bias_token.shape):
+            raise ValueError("a bias for each token of the list")
+        for x, shape in ((params, (n_seqs, 4)), (d_draft, (n_seqs, n_tok - 1)), (bias_token, (n_seqs, 0 if bias is None else bias.shape[1]))):
+            if x is not None and (x.shape != shape or not x.is_contiguous()):
+                raise ValueError("params, drafts and biases must be contiguous rows, one per sequence")
+        if mask is not None and (mask.dtype.itemsize != 4 or mask.shape != (n_seqs * n_tok, -(-vocab // 32)) or (mask.shape[1] > 1 and mask.stride(1) != 1)):
+            raise ValueError("mask must hold a row of 32-bit words per query token")
+        B.hswa_logits_probs(dtype[logits.dtype], logits, self._row_stride(logits), dtype[p.dtype], p, self._row_stride(p),
+                            params, counts, 0 if counts is None else counts.stride(0) if n_seqs > 1 else vocab, d_draft,
+                            bias_token, bias, 0 if bias is None else bias.shape[1], mask,
+                            0 if mask is None else mask.stride(0) if mask.shape[0] > 1 else mask.shape[1], n_seqs, n_tok,
+                            vocab, self.stream)
 
     @staticmethod
     def _row_stride(x):

@@ -94,13 +94,33 @@ extern "C" {
  * v_scale [pages][Hkv][P][d / 128] fp32. q, o and the new K/V handed to the
  * append stay bf16; the append quantizes: scale = amax / 448 (1 if amax is
  * 0), code = round-to-nearest-even(x / scale) saturating at 448. Supported
- * by hswa_append_kv, hswa_rope_append (d = 128), hswa_decode,
+ * by hswa_append_kv, hswa_read_kv, hswa_rope_append (d = 128), hswa_decode,
  * hswa_decode_append, hswa_decode_multi, hswa_decode_weights (d = 128, 8
  * query heads per kv head, P = 64), hswa_prefill_chunk_ws (d = 128, an even
  * number of query heads per kv head, P = 64) and hswa_swa_gather /
  * hswa_swa_scatter (d = 128, P = 64); other calls on layers return
  * HSWA_ERR_UNSUPPORTED. */
 #define HSWA_DTYPE_FP8_E4M3 2
+/* FP4 KV cache: K and V are E2M1 codes (sign, 2 exponent bits, 1 mantissa bit:
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6) in blocks of 16 elements of a row (a token's
+ * K or V of one kv head), each block under a scale byte E5M3 (an IEEE half
+ * without its sign and its last 7 bits: half bits = byte << 7); value = code *
+ * scale. Layout per layer: k_pool and v_pool [pages][Hkv][P][d / 2] bytes,
+ * element 2 i of a row in the lower half of byte i; k_scale and v_scale (passed
+ * as float *) [pages][Hkv][P][d / 16] bytes: 72 bytes a row of 128 elements.
+ * q, o and the new K/V handed to the append stay bf16; the append quantizes
+ * each block: scale = the nearest E5M3 value (ties to the even byte) to the
+ * fp32 quotient amax / 6, at most 10240; code = the nearest E2M1 value (ties to
+ * the even code) to x / scale, saturating at 6, all 0 where the scale is 0
+ * (amax / 6 of at most 2^-18). So magnitudes above 61440 are stored as that
+ * (infinities too; what a NaN becomes is not defined, but finite), and every
+ * stored value is exact in fp16 and in bf16. d must be a multiple of 16.
+ * Supported by hswa_append_kv, hswa_rope_append, hswa_read_kv, hswa_decode,
+ * hswa_decode_append, hswa_decode_multi, hswa_prefill_chunk and
+ * hswa_prefill_chunk_ws, any head ratio and page size, head_dim at most 256
+ * (fastest with d = 128, 8 query heads per kv head, P = 64); other calls
+ * on layers return HSWA_ERR_UNSUPPORTED. */
+#define HSWA_DTYPE_FP4 3
 
 /* A CUDA stream (the same handle as cudaStream_t); NULL = default stream. */
 typedef struct CUstream_st *hswa_stream_t;
@@ -125,8 +145,9 @@ typedef struct hswa_layer {
     int32_t window; /* keys per query for an SWA layer (> 0); ignored for Full  */
     void *k_pool;   /* device [num_pages][Hkv][P][d], caller-owned             */
     void *v_pool;   /* device, same shape ([num_pages][Hkv][d][P] for FP8)     */
-    float *k_scale; /* FP8 only: device [num_pages][Hkv][P][d/128], else NULL  */
-    float *v_scale; /* FP8 only: same shape                                    */
+    float *k_scale; /* FP8: device [num_pages][Hkv][P][d/128]; FP4: bytes
+                       [num_pages][Hkv][P][d/16]; else NULL                    */
+    float *v_scale; /* FP8 and FP4: same shape                                 */
 } hswa_layer;
 
 /* ------------------------------------------------ pool bookkeeping (host) */
@@ -332,6 +353,15 @@ int hswa_sync_tables(hswa_pool *pool, int32_t *d_full_bt, int32_t *d_swa_bt, int
 int hswa_append_kv(const hswa_pool *pool, const hswa_layer *layer, const void *k, const void *v,
                    const int32_t *d_slots, int n_tokens, hswa_stream_t stream);
 
+/* The inverse of hswa_append_kv: the K and V rows of the pool at given slots as
+ * values, for a cache that moves to a pool of another type or out of it.
+ * k, v: device [n_tokens][Hkv][d], 16-byte aligned; fp32 for fp32 pools, else
+ * bf16 (exact for bf16 and FP4 pools; code * scale rounded once for FP8
+ * pools, d = 128). A negative slot gives a row of zeros; one past the pool too,
+ * and sets HSWA_ERR_BOUNDS on the device. Slots may repeat. */
+int hswa_read_kv(const hswa_pool *pool, const hswa_layer *layer, const int32_t *d_slots, int n_tokens, void *k,
+                 void *v, hswa_stream_t stream);
+
 /* ------------------------------------ rotary positions with several axes
  *
  * A rotary embedding of a model's heads: which elements form pairs, how
@@ -377,7 +407,8 @@ int hswa_rope_destroy(hswa_rope *rope);
  * and 5e-7 at any int32 position (frequencies of at most 1 radian a
  * position; in proportion beyond), the arithmetic is fp32, and each result is rounded once, to the element
  * type; for FP8 pools the turned K row is quantized as it is in fp32 (scale
- * = amax / 448 as for hswa_append_kv, without a rounding to bf16 between).
+ * = amax / 448 as for hswa_append_kv, without a rounding to bf16 between),
+ * and so are the blocks of FP4 pools.
  * q, k, v: device, token t's heads at element t * stride, so that they may
  * be slices of one projection's output (q_stride >= Hq * d, k_stride and
  * v_stride >= Hkv * d); fp32 for fp32 pools, else bf16. q_out: device
@@ -531,6 +562,60 @@ int hswa_decode_multi(const hswa_pool *pool, const hswa_layer *layer, const void
 int hswa_verify_draft(int dtype, const void *p, int64_t p_stride, const void *q, int64_t q_stride,
                       const int32_t *d_draft, const int32_t *d_n_draft, const float *u, int n_seqs, int n_tok,
                       int vocab, int32_t *n_accept, int32_t *tokens, hswa_stream_t stream);
+
+/* Times each token occurred in each sequence, for the penalties of
+ * hswa_logits_probs. counts: device uint16 [n_seqs][vocab], rows count_stride
+ * (>= vocab) elements apart; bit 15 of an entry says that the token is in the
+ * prompt, the others how often it has been generated (staying at 32767). Row i
+ * takes tokens[i][0 .. n_tokens), rows token_stride apart; the first
+ * d_n_prompt[i] of them (device int32 [n_seqs]; NULL: none) are the prompt's.
+ * A negative token is skipped (the tokens of hswa_verify_draft can be passed
+ * as they are), one past the vocabulary too, setting HSWA_ERR_BOUNDS on the
+ * device. clear != 0: the rows start from nothing (a request is admitted), whatever
+ * counts holds; else what they hold stays. tokens may be NULL if n_tokens is 0. */
+int hswa_count_tokens(uint16_t *counts, int64_t count_stride, const int32_t *tokens, int64_t token_stride,
+                      const int32_t *d_n_prompt, int n_seqs, int n_tokens, int vocab, int clear,
+                      hswa_stream_t stream);
+
+/* Most biases of a sequence hswa_logits_probs takes. */
+#define HSWA_LOGITS_MAX_BIAS 1024
+
+/* From logits to the probabilities that hswa_verify_draft takes, in one pass:
+ * penalties for tokens that occurred, biases, grammar masks, temperature and
+ * softmax. Row i * n_tok + w belongs to query token w of sequence i. For token
+ * v let c be the times it has been generated: its count in counts[i] (see
+ * hswa_count_tokens) plus its occurrences among d_draft[i][0 .. w). Then, each
+ * step rounded to fp32,
+ *     z = logit(v)
+ *     v occurred (c > 0 or in the prompt): z = z > 0 ? z / repetition : z * repetition
+ *     c > 0: z = z - frequency * c, then z = z - presence
+ *     v in the bias list: z = z + bias
+ *     v not allowed by the mask, or z NaN: z = -inf
+ *     p(v) = exp(z / temperature) / sum of all exp(z / temperature)
+ * and for a temperature that is not above 0, p is 1 at the first token with
+ * the largest z and 0 elsewhere. Values of +inf share the probability evenly;
+ * a row with nothing but -inf becomes zeros. Sums have a fixed order: equal
+ * inputs give equal bits. p is within about 1e-6 of that in relative terms
+ * (times 1 + |z| / temperature for z's own roundings), rounded once to its type.
+ * logits, p: device rows of vocab values, HSWA_DTYPE_F32 or HSWA_DTYPE_BF16
+ * each by itself, logits_stride / p_stride (>= vocab) elements apart; p may be the
+ * logits if type and stride are the same (an overlap otherwise is
+ * HSWA_ERR_INVALID_ARG). params: device float [n_seqs][4], temperature,
+ * repetition (above 0, else it counts as 1), frequency, presence; NULL: 1, 1, 0,
+ * 0. counts: as above, NULL: no penalties. d_draft: device int32
+ * [n_seqs][n_tok - 1]; NULL: none. bias_token, bias: device [n_seqs][n_bias],
+ * negative tokens unused; of equal tokens the last entry counts; one past the
+ * vocabulary is skipped, setting HSWA_ERR_BOUNDS on the device. mask: device
+ * uint32 [n_seqs * n_tok], rows mask_stride (>= ceil(vocab / 32)) words apart, bit v % 32
+ * of word v / 32 set where v is allowed; NULL: all are. vocab at most
+ * HSWA_VERIFY_MAX_VOCAB, n_bias at most HSWA_LOGITS_MAX_BIAS, n_tok in [1,
+ * HSWA_DECODE_MAX_TOKENS]. Fastest with rows on 16-byte boundaries and a
+ * vocabulary of at most 163840. */
+int hswa_logits_probs(int logits_dtype, const void *logits, int64_t logits_stride, int p_dtype, void *p,
+                      int64_t p_stride, const float *params, const uint16_t *counts, int64_t count_stride,
+                      const int32_t *d_draft, const int32_t *bias_token, const float *bias, int n_bias,
+                      const uint32_t *mask, int64_t mask_stride, int n_seqs, int n_tok, int vocab,
+                      hswa_stream_t stream);
 
 /* One chunked-prefill chunk of attention (Sec. 1.1: chunked prefill is
  * close to compute-bound). Sequence i < n_seqs has d_prefix_len[i] cached

@@ -118,3 +118,61 @@ def verify(p, q, draft, n_draft, u, bits=50):
             at = int(Fraction(ux) * int(cum[-1]))  # floor
             tokens[s, a] = int(np.searchsorted(cum, at, side="right"))
     return accepted, tokens
+
+
+def count_tokens(tokens, n_prompt, vocab, counts=None):
+    """Counts [S][vocab] (bit 15: in the prompt, the others: times generated,
+    at most 32767) of token lists, on top of earlier ones."""
+    out = np.zeros((len(tokens), vocab), np.int64) if counts is None else np.asarray(counts).astype(np.int64)
+    for i, row in enumerate(tokens):
+        for j, v in enumerate(row):
+            if not 0 <= v < vocab:
+                continue
+            if n_prompt is not None and j < n_prompt[i]:
+                out[i, v] |= 1 << 15
+            elif out[i, v] & 0x7fff < 0x7fff:
+                out[i, v] += 1
+    return out.astype(np.uint16)
+
+
+def logits_probs(logits, params=None, counts=None, draft=None, bias_token=None, bias=None, allowed=None):
+    """logits [S][n][V] to (probabilities, z) in 64 bits. params [S][4]:
+    temperature, repetition, frequency, presence; counts [S][V] as above;
+    draft [S][n - 1]; bias_token, bias [S][m]; allowed [S * n][V] bool."""
+    S, n, V = logits.shape
+    p, zs = np.zeros((S, n, V)), np.full((S, n, V), -np.inf)
+    for i in range(S):
+        T, rep, freq, pres = (1.0, 1.0, 0.0, 0.0) if params is None else [float(x) for x in params[i]]
+        rep = rep if rep > 0 else 1.0
+        for w in range(n):
+            z = np.asarray(logits[i, w], np.float64).copy()
+            if counts is not None:
+                c = (counts[i].astype(np.int64) & 0x7fff).astype(np.float64)
+                if draft is not None:
+                    for v in draft[i, :w]:
+                        if 0 <= v < V:
+                            c[v] += 1
+                seen = (c > 0) | (counts[i] >> 15 > 0)
+                z[seen] = np.where(z[seen] > 0, z[seen] / rep, z[seen] * rep)
+                z[c > 0] -= freq * c[c > 0] + pres
+            if bias is not None:
+                last = {int(v): float(b) for v, b in zip(bias_token[i], bias[i])}
+                for v, b in last.items():
+                    if 0 <= v < V:
+                        z[v] += b
+            if allowed is not None:
+                z[~allowed[i * n + w]] = -np.inf
+            z[np.isnan(z)] = -np.inf
+            zs[i, w] = z
+            top = z.max()
+            if top == -np.inf:
+                continue
+            if not T > 0:
+                p[i, w, int(np.argmax(z))] = 1
+            elif top == np.inf:
+                p[i, w] = (z == np.inf) / (z == np.inf).sum()
+            else:
+                with np.errstate(invalid="ignore"):
+                    e = np.where(z == -np.inf, 0, np.exp((z - top) / T))
+                p[i, w] = e / e.sum()
+    return p, zs
