@@ -157,7 +157,6 @@ struct DecodeArgs {
     int64_t pool_slots;
     int32_t n_seqs, bt_stride, hkv, hq, window, num_pages;
     int32_t n_tok;  // query tokens per sequence (multi-token decode), 1 otherwise
-    int32_t tok0;   // FP4 pools: the first token of this launch
     float scale_log2;
     int *err;
     // decode with page weights (null otherwise): log2 of the sum of 2^score
@@ -2666,15 +2665,16 @@ cudaError_t launch_finish_weights(const PageWeights &pw, const hswa_config &c, c
 }
 
 cudaError_t launch_combine(const hswa_config &c, const DecodeArgs &a, int n_ctas, cudaStream_t st) {
-    // (the workers of an FP4 decode on a part with more SMs could need more shared memory than a kernel has by itself)
-    if (merge_by_heads((int64_t)a.n_seqs * c.n_kv_heads * a.n_tok, n_ctas) && merge_heads_smem(n_ctas) <= (47u << 10))
+    const size_t smem = merge_heads_smem(n_ctas);
+    if (smem > (47u << 10)) {  // the workers of an FP4 decode: more than a kernel has by itself
+        static int cache[kMaxDevices] = {};
+        if (kernel_setup(decode_combine_heads, 100u << 10, 256, cache) < 0 || smem > (100u << 10)) return cudaErrorInvalidConfiguration;
+    }
+    if (merge_by_heads((int64_t)a.n_seqs * c.n_kv_heads * a.n_tok, n_ctas))
         return launch_pdl(decode_combine_heads, dim3(c.n_kv_heads * (kG / kMergeHeads), a.n_seqs * a.n_tok), dim3(256),
                           merge_heads_smem(n_ctas), st, a, n_ctas);
     return launch_pdl(decode_combine, dim3(c.n_kv_heads, a.n_seqs * a.n_tok), dim3(256), 0, st, a, n_ctas);
 }
-
-// FP4 pools: CTAs per SM of decode_mma_fp4_d128, and its workers.
-constexpr int kFp4CtasPerSm = 3;
 
 bool decode_fp4_ok(const hswa_pool *pool, const hswa_layer *layer, const void *q, const void *o) {
     const hswa_config &c = pool->cfg;
@@ -2684,15 +2684,23 @@ bool decode_fp4_ok(const hswa_pool *pool, const hswa_layer *layer, const void *q
            ((uintptr_t)layer->k_scale & 15) == 0 && ((uintptr_t)layer->v_scale & 15) == 0;
 }
 
-template <int kTok>
-int decode_fp4_ctas_per_sm() {
+// Workers of a launch of decode_mma_fp4_d128 on the whole GPU; -1 on failure.
+template <class Shape>
+int fp4_workers() {
     static int cache[kMaxDevices] = {};
-    return kernel_setup(decode_mma_fp4_d128<kTok>, kDecodeSmem4Bytes, 32 * kFp4Warps, cache);
+    const int per_sm = kernel_setup(decode_mma_fp4_d128<Shape>, decode_smem4_bytes<Shape>(), 32 * Shape::kWarps, cache);
+    static_assert(Shape::kCtas * Shape::kWarps <= kFp4WorkersPerSm, "the workspace has records for that many");
+    return per_sm <= 0 ? -1 : sm_count() * std::min(per_sm, Shape::kCtas) * Shape::kWarps;
+}
+
+template <class Shape>
+cudaError_t launch_decode_fp4(int workers, cudaStream_t st, const DecodeArgs &a) {
+    return launch_pdl(decode_mma_fp4_d128<Shape>, dim3(workers / Shape::kWarps), dim3(32 * Shape::kWarps),
+                      decode_smem4_bytes<Shape>(), st, a);
 }
 
 // Query tokens per sequence from which an FP4 decode runs on the tensor-core
-// kernel; below it decode_mma_fp4_d128 takes them two at a time, one launch
-// after the other.
+// kernel; below it decode_mma_fp4_d128 takes them in one launch.
 constexpr int kTcMinTokensFp4 = 5;
 
 size_t desc_bytes(int n_seqs) { return ((size_t)(n_seqs + 1) * sizeof(int4) + 255) & ~(size_t)255; }
@@ -2709,7 +2717,7 @@ extern "C" size_t hswa_decode_multi_workspace_size(const hswa_pool *pool, int n_
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         sms = 192;  // no device visible: size for the largest part
     // FP4 pools: every warp leaves records of its own
-    const int per_sm = pool->cfg.dtype == HSWA_DTYPE_FP4 && n_tok < kTcMinTokensFp4 ? kFp4CtasPerSm * kFp4Warps : kMaxCtasPerSm;
+    const int per_sm = pool->cfg.dtype == HSWA_DTYPE_FP4 && n_tok < kTcMinTokensFp4 ? kFp4WorkersPerSm : kMaxCtasPerSm;
     return desc_bytes(n_seqs) + (size_t)sms * per_sm * 2 * n_tok * sizeof(Partial);
 }
 
@@ -2744,7 +2752,6 @@ int fill_args(DecodeArgs &a, const hswa_pool *pool, const hswa_layer *layer, con
     a.window = layer->kind == HSWA_KIND_SWA ? layer->window : 0;
     a.num_pages = num_pages;
     a.n_tok = 1;
-    a.tok0 = 0;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.err = error_word();
     a.page_lse = a.seq_lse = a.piece_lse = nullptr;
@@ -2820,18 +2827,18 @@ int decode_fp4(const hswa_pool *pool, const hswa_layer *layer, const void *q, vo
     if (!layer->k_scale || !layer->v_scale) return HSWA_ERR_INVALID_ARG;
     const int32_t num_pages = layer->kind == HSWA_KIND_SWA ? c.swa_pages : c.full_pages;
     const uint64_t rows = (uint64_t)num_pages * c.n_kv_heads * c.page_size;
-    // the tensor map's rows are 32-bit coordinates
-    const bool fast = decode_fp4_ok(pool, layer, q, o) && rows < (1ull << 31) && (int64_t)n_seqs * n_tok <= 65535;
+    // rows are counted in 32 bits
+    const bool fast = decode_fp4_ok(pool, layer, q, o) && rows < (1ull << 31) && (int64_t)n_seqs * n_tok <= 65535 && c.n_kv_heads < 32768;
     const bool tc = n_tok >= kTcMinTokensFp4;
-    int n_ctas = 0, workers = 0;
+    int workers = 0;
     if (fast) {
         const int sms = sm_count();
         if (sms <= 0) return HSWA_ERR_CUDA;
-        const int per_sm = tc ? decode_tc_ctas_per_sm<DecodeTc4Smem>(n_tok)
-                              : std::min(decode_fp4_ctas_per_sm<1>(), n_tok > 1 ? decode_fp4_ctas_per_sm<2>() : kFp4CtasPerSm);
-        if (per_sm <= 0) return HSWA_ERR_CUDA;
-        n_ctas = sms * std::min(per_sm, kFp4CtasPerSm);
-        workers = tc ? n_ctas : n_ctas * kFp4Warps;
+        workers = tc           ? sms * std::min(decode_tc_ctas_per_sm<DecodeTc4Smem>(n_tok), 1)
+                  : n_tok == 1 ? fp4_workers<Fp4One>()
+                  : n_tok == 2 ? fp4_workers<Fp4Two>()
+                               : fp4_workers<Fp4Four>();
+        if (workers <= 0) return HSWA_ERR_CUDA;
         if (!ws || ((uintptr_t)ws & 255) ||
             ws_bytes < desc_bytes(n_seqs) + (size_t)workers * 2 * n_tok * sizeof(Partial))
             return HSWA_ERR_INVALID_ARG;
@@ -2846,20 +2853,17 @@ int decode_fp4(const hswa_pool *pool, const hswa_layer *layer, const void *q, vo
     DecodeArgs a;
     fill_args(a, pool, layer, q, o, d_bt, d_seq_len, n_seqs, scale, ws);
     a.n_tok = n_tok;
-    CUtensorMap tv, tq;
-    if (tc ? !make_q_tmap(&tq, q, c, n_seqs, n_tok)
-           : !make_tmap_2d(&tv, layer->v_pool, rows, kD / 2, kP, kD / 2, CU_TENSOR_MAP_DATA_TYPE_UINT8,
-                           CU_TENSOR_MAP_SWIZZLE_64B))
-        return HSWA_ERR_CUDA;
-    if (tc) tv = tq;  // pages go by plain bulk copies
+    CUtensorMap tq;
+    if (tc && !make_q_tmap(&tq, q, c, n_seqs, n_tok)) return HSWA_ERR_CUDA;
     set_last_kernel(tc ? "decode_tc_fp4_d128" : slots ? "append_kv_fp4+decode_mma_fp4_d128" : "decode_mma_fp4_d128");
     cudaError_t e = launch_pdl(decode_plan, dim3(1), dim3(plan_threads(n_seqs)), 0, st, d_seq_len, n_seqs, c.n_kv_heads, kP,
                                a.window, n_tok, static_cast<int4 *>(ws), INT64_MAX, a.err);
-    if (e == cudaSuccess && tc) e = launch_decode_tc<DecodeTc4Smem>(n_tok, n_ctas, st, tq, tv, tv, a);
-    if (!tc)
-        for (; e == cudaSuccess && a.tok0 < n_tok; a.tok0 += 2)
-            e = a.tok0 + 1 < n_tok ? launch_pdl(decode_mma_fp4_d128<2>, dim3(n_ctas), dim3(32 * kFp4Warps), kDecodeSmem4Bytes, st, tv, a)
-                                   : launch_pdl(decode_mma_fp4_d128<1>, dim3(n_ctas), dim3(32 * kFp4Warps), kDecodeSmem4Bytes, st, tv, a);
+    if (e == cudaSuccess)
+        e = tc           ? launch_decode_tc<DecodeTc4Smem>(n_tok, workers, st, tq, tq, tq, a)  // pages go by plain bulk copies
+           
+            : n_tok == 1 ? launch_decode_fp4<Fp4One>(workers, st, a)
+            : n_tok == 2 ? launch_decode_fp4<Fp4Two>(workers, st, a)
+                         : launch_decode_fp4<Fp4Four>(workers, st, a);
     if (e == cudaSuccess) e = launch_combine(c, a, workers, st);
     return e == cudaSuccess ? HSWA_OK : cuda_fail(e, "decode over an FP4 pool");
 }

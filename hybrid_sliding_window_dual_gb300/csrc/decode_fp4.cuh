@@ -30,22 +30,45 @@
 //     that the 8-byte loads of V (64-byte swizzle) meet different banks.
 #pragma once
 
-constexpr int kFp4Warps = 4;    // workers per CTA
-constexpr int kFp4Stages = 2;   // units in flight per worker
-struct Fp4Unit {
-    uint8_t k[kK4Bytes];   // [64 keys][64 B]
-    uint8_t v[kK4Bytes];   // [64 keys][64 B], 64-byte swizzle
-    uint8_t ks[kS4Bytes];  // [64 keys][8]
-    uint8_t vs[kS4Bytes];
+// kTok query tokens per launch (1, 2 or 4), kKeys keys taken at once, kWarps
+// workers per CTA, kParts parts in flight per worker, kCtas CTAs per SM.
+template <int kTok_, int kKeys_, int kWarps_, int kParts_, int kCtas_>
+struct Fp4Shape {
+    static constexpr int kTok = kTok_, kKeys = kKeys_, kWarps = kWarps_, kParts = kParts_, kCtas = kCtas_;
+    static constexpr int kSteps = kP / kKeys;      // of a unit
+    static constexpr int kTiles = kKeys / 8;       // of 8 keys
+    static constexpr int kPairs = (kTok + 1) / 2;  // tokens share the 16 rows of a tile two by two
+    static constexpr bool kSharedQ = kTok > 1;     // Q's fragments in shared memory
 };
-static_assert(sizeof(Fp4Unit) % 1024 == 0, "swizzled tiles stay aligned");
+using Fp4One = Fp4Shape<1, 64, 4, 4, 3>;
+using Fp4Two = Fp4Shape<2, 64, 4, 4, 2>;
+using Fp4Four = Fp4Shape<4, 32, 4, 6, 2>;
+constexpr int kFp4WorkersPerSm = 16;  // the most of these
+constexpr int kFp4Ahead = 8;          // units whose descriptors are made at once
 
-struct DecodeSmem4 {
-    Fp4Unit unit[kFp4Warps][kFp4Stages];
-    StageDesc desc[kFp4Warps][kFp4Stages];
-    uint64_t full[kFp4Warps][kFp4Stages];
+// K or V of kKeys keys.
+template <int kKeys>
+struct alignas(128) Fp4Part {
+    static constexpr uint32_t kCodeBytes = kKeys * kD / 2, kScaleBytes = kKeys * kD / kFp4Block;
+    uint8_t codes[kCodeBytes];    // [keys][64 B]; V with the 64-byte swizzle
+    uint8_t scales[kScaleBytes];  // [keys][8]
 };
-constexpr size_t kDecodeSmem4Bytes = sizeof(DecodeSmem4) + 1024;
+
+struct Fp4Desc {
+    int32_t row;    // first row of the page and kv head in the pool, -1: nothing to load
+    int32_t range;  // keys of the page in the sequence's range: first | last + 1 << 8 | flags << 16
+    int32_t seq;    // sequence | kv head << 16
+    int32_t rel;    // the sequence's length from the page's first key on
+};
+
+template <class Shape>
+struct DecodeSmem4 {
+    Fp4Part<Shape::kKeys> part[Shape::kWarps][Shape::kParts];
+    uint4 q[Shape::kSharedQ ? Shape::kWarps : 1][Shape::kSharedQ ? Shape::kPairs : 1][8][Shape::kSharedQ ? 32 : 1];
+    Fp4Desc desc[Shape::kWarps][2 * kFp4Ahead];
+};
+template <class Shape>
+constexpr size_t decode_smem4_bytes() { return sizeof(DecodeSmem4<Shape>) + 128; }
 
 // The MMAs here are not volatile: the compiler may move them among the
 // conversions of other tiles.
@@ -57,309 +80,443 @@ __device__ __forceinline__ void mma4(float (&d)[4], uint32_t a0, uint32_t a1, ui
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The units [u, u1) of a worker, one after the other (uniform over the warp).
-struct Fp4Walk {
-    int64_t u, u1, u0;
-    int64_t piece_end;
-    int32_t s, g, p, npg, pf, lo, hi;
-    int32_t batch, mine;  // table entries of pages 32 batch .. 32 batch + 31 of the sequence, one per lane
-    int32_t flags, slot;
-    int4 d, dn;
+constexpr int32_t kSecond = 16;  // a piece whose record is its worker's second
 
-    __device__ Fp4Walk(const DecodeArgs &a, int64_t u0_, int64_t u1_) : u(u0_), u1(u1_), u0(u0_), piece_end(u0_) {
-        s = 0, batch = -1, mine = -1;
-        d = dn = make_int4(0, 0, 0, 0);
-        if (u0 < u1) {
-            s = find_seq(a.sdesc, a.n_seqs, u0);
-            d = a.sdesc[s];
-            dn = a.sdesc[s + 1];
+// 16 bytes global -> shared, without a register between.
+__device__ __forceinline__ void copy16(uint32_t to, const uint8_t *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
+// Makes the descriptors of a worker's units [u0, u1), 8 at a time, a lane
+// each. A unit's table entry is loaded when those before it are written down.
+struct Fp4Units {
+    int32_t u0, u1, base, s;  // the next 8 units are base ..; s: the sequence of an earlier one
+    int32_t page;
+    Fp4Desc x;
+
+    __device__ __forceinline__ void fetch(const DecodeArgs &a) {
+        const int lane = threadIdx.x & 31;
+        const int32_t u = base + lane;
+        int32_t mine = s;
+        if (lane < kFp4Ahead && u < u1) {
+            int4 d = a.sdesc[mine];
+            while (u >= d.x + d.w) d = a.sdesc[++mine];
+            const int32_t npg = d.w / a.hkv, pf = d.y / kP;
+            const int32_t g = (u - d.x) / npg, p = u - d.x - g * npg;
+            const int32_t seg = u - p;  // the segment's first unit
+            const int32_t key0 = (pf + p) * kP;
+            page = pf + p < a.bt_stride ? a.bt[(int64_t)mine * a.bt_stride + pf + p] : -1;
+            const int32_t flags = (u == seg || u == u0 ? kFirst : 0) | (p == npg - 1 || u == u1 - 1 ? kLast : 0) |
+                                  (seg >= u0 && seg + npg <= u1 ? kDirect : 0) | (seg > u0 ? kSecond : 0);
+            x.range = max(d.y - key0, 0) | min(d.z - key0, kP) << 8 | flags << 16;
+            x.seq = mine | g << 16;
+            x.rel = d.z - key0;
         }
+        s = __shfl_sync(0xffffffffu, mine, max(min(kFp4Ahead, u1 - base) - 1, 0));
     }
-    __device__ bool more() const { return u < u1; }
-
-    // The next unit: its descriptor and page.
-    __device__ int32_t next(const DecodeArgs &a, StageDesc &out) {
-        int32_t first = 0;
-        if (u == piece_end) {
-            first = kFirst;
-            while (u >= (int64_t)d.x + d.w) {  // next sequence with units
-                ++s;
-                d = dn;
-                dn = a.sdesc[s + 1];
-                batch = -1;
-            }
-            lo = d.y, hi = d.z;
-            pf = lo / kP;
-            npg = d.w / a.hkv;
-            const int32_t at = (int32_t)(u - d.x);
-            g = at / npg;
-            p = at - g * npg;
-            const int64_t seg_end = u - p + npg;
-            piece_end = seg_end < u1 ? seg_end : u1;
-            flags = p == 0 && piece_end == seg_end ? kDirect : 0;
-            slot = u == u0 ? 0 : 1;
+    __device__ __forceinline__ Fp4Units(const DecodeArgs &a, int32_t u0_, int32_t u1_) : u0(u0_), u1(u1_), base(u0_) {
+        s = find_seq(a.sdesc, a.n_seqs, u0);
+        fetch(a);
+    }
+    // Write the next 8 down.
+    __device__ __forceinline__ void put(const DecodeArgs &a, Fp4Desc *desc) {
+        const int lane = threadIdx.x & 31;
+        if (lane < kFp4Ahead && base + lane < u1) {
+            const bool valid = page >= 0 && page < a.num_pages;
+            if (!valid) set_error(a.err, HSWA_ERR_BOUNDS);
+            x.row = valid ? (page * a.hkv + (x.seq >> 16)) * kP : -1;
+            if (!valid) x.range |= kSkip << 16;
+            desc[(base - u0 + lane) % (2 * kFp4Ahead)] = x;
         }
-        if ((p >> 5) != batch) {
-            batch = p >> 5;
-            const int32_t q = (p & ~31) + (threadIdx.x & 31);
-            mine = q < npg && pf + q < a.bt_stride ? a.bt[(int64_t)s * a.bt_stride + pf + q] : -1;
-        }
-        const int32_t page = __shfl_sync(0xffffffffu, mine, p & 31);
-        const int32_t key0 = (pf + p) * kP;
-        const bool valid = page >= 0 && page < a.num_pages;
-        out.seq = s;
-        out.kvh = g;
-        out.lo = lo - key0 > 0 ? lo - key0 : 0;
-        out.hi = hi - key0 < kP ? hi - key0 : kP;
-        out.slot = slot;
-        out.key0 = key0;
-        out.len = hi;
-        out.flags = flags | first | (u + 1 == piece_end ? kLast : 0) | (valid ? 0 : kSkip);
-        ++u;
-        ++p;
-        return valid ? page : -1;
+        base += kFp4Ahead;
+        fetch(a);
+        __syncwarp();
     }
 };
 
-// One worker. kTok = 1 or 2 query tokens, from token a.tok0 of each sequence.
-template <int kTok>
-__device__ void decode_fp4_worker(DecodeSmem4 &sm, const CUtensorMap *tv, const DecodeArgs &a, int64_t u0, int64_t u1,
+// 16 elements of o, over the sum of P.
+__device__ __forceinline__ void fp4_store(__nv_bfloat16 *to, const float (&f)[16], float L) {
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+        reinterpret_cast<uint4 *>(to)[y] =
+            make_uint4(pack_bf16(f[8 * y] * inv, f[8 * y + 1] * inv), pack_bf16(f[8 * y + 2] * inv, f[8 * y + 3] * inv),
+                       pack_bf16(f[8 * y + 4] * inv, f[8 * y + 5] * inv), pack_bf16(f[8 * y + 6] * inv, f[8 * y + 7] * inv));
+}
+
+// One worker.
+template <class Shape>
+__device__ void decode_fp4_worker(DecodeSmem4<Shape> &sm, const DecodeArgs &a, int32_t u0, int32_t u1,
                                   int32_t worker) {
+    constexpr int kTok = Shape::kTok, kPairs = Shape::kPairs, kParts = Shape::kParts, kTiles = Shape::kTiles;
+    constexpr int kSteps = Shape::kSteps, kKeys = Shape::kKeys;
+    using Part = Fp4Part<kKeys>;
+    if (u0 >= u1) return;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int gr = lane >> 2, t = lane & 3;
-    Fp4Walk walk(a, u0, u1);
-    const uint8_t *kp = reinterpret_cast<const uint8_t *>(a.k_pool);
-    const uint8_t *ksp = reinterpret_cast<const uint8_t *>(a.k_scale), *vsp = reinterpret_cast<const uint8_t *>(a.v_scale);
-    const int64_t n = u1 - u0;
-    int64_t issued = 0;
-    const auto issue = [&] {
-        const int st = (int)(issued % kFp4Stages);
-        StageDesc d;
-        const int32_t page = walk.next(a, d);
-        if (lane == 0) {
-            sm.desc[w][st] = d;
-            uint64_t *full = &sm.full[w][st];
-            if (page >= 0) {
-                Fp4Unit &x = sm.unit[w][st];
-                const int64_t blk = (int64_t)page * a.hkv + d.kvh;  // (page, kv head) block
-                mbar_arrive_expect_tx(full, kUnit4Bytes);
-                bulk_g2s(x.k, kp + blk * kK4Bytes, kK4Bytes, full);
-                tma_load_2d(x.v, tv, 0, (int32_t)(blk * kP), full);
-                bulk_g2s(x.ks, ksp + blk * kS4Bytes, kS4Bytes, full);
-                bulk_g2s(x.vs, vsp + blk * kS4Bytes, kS4Bytes, full);
-            } else {
-                set_error(a.err, HSWA_ERR_BOUNDS);
-                mbar_arrive(full);
+    // this lane's 16 bytes of a run of 8 rows of codes, in the pool and in a
+    // part (V: its 16-byte chunks turned round by the row's bits 1 and 2), and of scales
+    const uint8_t *const kp = reinterpret_cast<const uint8_t *>(a.k_pool) + lane * 16, *const vp = reinterpret_cast<const uint8_t *>(a.v_pool) + lane * 16;
+    const uint8_t *const ksp = reinterpret_cast<const uint8_t *>(a.k_scale) + lane * 16, *const vsp = reinterpret_cast<const uint8_t *>(a.v_scale) + lane * 16;
+    const uint32_t parts0 = smem_u32(sm.part[w]);
+    const int32_t parts = 2 * kSteps * (u1 - u0);
+    Fp4Units units(a, u0, u1);
+    Fp4Desc *const desc = sm.desc[w];
+    int32_t described = 0;
+    // Part c: K (c even) or V of step c / 2, into buffer st; a group of copies of its own.
+    const auto issue = [&](int32_t c, int st, bool is_v) {
+        const int32_t i = (c >> 1) / kSteps;
+        if (c < parts) {
+            if (i == described) {
+                units.put(a, desc);
+                described += kFp4Ahead;
+            }
+            const int32_t first = desc[i % (2 * kFp4Ahead)].row, row = first + (c >> 1) % kSteps * kKeys;
+            if (first >= 0) {
+                const uint8_t *from = (is_v ? vp : kp) + (int64_t)row * (kD / 2);
+                const uint32_t to = parts0 + st * (uint32_t)sizeof(Part) + (is_v ? (lane & ~3) << 4 | ((lane ^ lane >> 3) & 3) << 4 : lane << 4);
+#pragma unroll
+                for (int x = 0; x < kTiles; ++x) copy16(to + x * 512, from + x * 512);
+                if (kKeys == 64 || lane < kKeys / 2)
+                    copy16(parts0 + st * (uint32_t)sizeof(Part) + Part::kCodeBytes + lane * 16, (is_v ? vsp : ksp) + (int64_t)row * (kD / kFp4Block));
             }
         }
-        __syncwarp();
-        ++issued;
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    while (issued < n && issued < kFp4Stages) issue();
-
-    uint32_t qf[kTok][8][2];  // this lane's 32 d's of head gr as f16 pairs
-    float o[2][8][4];         // kTok 1: o[0] only; else [parity of d][pair of d's]
-    float m[kTok], l[kTok];   // this lane's head: reference (log2 units) and sum of P
+    static_assert(kParts % 2 == 0, "K and V in turn");
 #pragma unroll
-    for (int j = 0; j < kTok; ++j) m[j] = -INFINITY, l[j] = 0.f;
+    for (int st = 0; st < kParts; ++st) issue(st, st, st & 1);
+
+    uint32_t qf[Shape::kSharedQ ? 1 : kTok][8][2];  // this lane's 32 d's of head gr as f16 pairs
+    float o[kPairs][2][8][4];  // kTok 1: o[0][0] only; else [pair of tokens][parity of d][pair of d's]
+    float m[kTok];             // this lane's head: reference (log2 units),
+    float2 l[kTok];            // sums of P over its keys of each parity;
+    float2 m2 = make_float2(-INFINITY, -INFINITY);  // kTok 1: both of heads 2 t, 2 t + 1
+#pragma unroll
+    for (int j = 0; j < kTok; ++j) m[j] = -INFINITY, l[j] = make_float2(0.f, 0.f);
+    // a negative scale turns q's sign instead, so that the largest score is
+    // that of the largest product; 0 becomes so little that every score is 0
+    const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);
+    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
     // the key of a tile in column gr of S; this lane's two keys of a tile are
     // 2 t + b and 2 t + 1 - b
     const int b = t & 1, krow = (gr & ~1) + ((gr ^ (gr >> 1)) & 1);
 
-    for (int64_t i = 0; i < n; ++i) {
-        const int st = (int)(i % kFp4Stages);
-        const StageDesc d = sm.desc[w][st];
-        if (d.flags & kFirst) {
+    int st = 0;
+    // the part in buffer st is there once at most kParts - 1 younger ones are not
+    const auto arrived = [&] {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kParts - 1) : "memory");
+        __syncwarp();
+    };
+    // every lane has read the buffer: it is filled again, on to the next
+    const auto release = [&](int32_t c, bool is_v) {
+        __syncwarp();
+        issue(c + kParts, st, is_v);
+        if (++st == kParts) st = 0;
+    };
+    for (int32_t i = 0; i < parts / 2; ++i) {
+        const Fp4Desc d = desc[i / kSteps % (2 * kFp4Ahead)];
+        const int32_t from = i % kSteps * kKeys;  // the step's first key of the page
+        const int32_t flags = (d.range >> 16) & (kSteps == 1 ? ~0 : i % kSteps == 0 ? ~kLast : i % kSteps == kSteps - 1 ? ~kFirst : ~(kFirst | kLast));
+        if (flags & kFirst) {
+            m2 = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
             for (int j = 0; j < kTok; ++j) {
-                const int tok = a.tok0 + j;
+                const int tok = min(j, a.n_tok - 1);  // a row too many is computed and not stored
                 const uint4 *q = reinterpret_cast<const uint4 *>(
-                    a.q + (q_row(a, d.seq, tok) * a.hq + (int64_t)d.kvh * kG + gr) * kD + 32 * t);
+                    a.q + (q_row(a, d.seq & 0xffff, tok) * a.hq + (int64_t)(d.seq >> 16) * kG + gr) * kD + 32 * t);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const uint4 f = bf16x8_to_f16x8(q[x]);
-                    qf[j][2 * x][0] = f.x, qf[j][2 * x][1] = f.y, qf[j][2 * x + 1][0] = f.z, qf[j][2 * x + 1][1] = f.w;
-                }
-                m[j] = -INFINITY, l[j] = 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[0][j][e] = o[1][j][e] = 0.f;
-        }
-        bool ok = mbar_wait(&sm.full[w][st], (uint32_t)(i / kFp4Stages) & 1, a.err);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (!(d.flags & kSkip)) {
-            const Fp4Unit &x = sm.unit[w][st];
-            float s[8][2 * kTok];  // [tile][token's two keys]
-#pragma unroll
-            for (int tile = 0; tile < 8; ++tile) {
-                const int key = 8 * tile + krow;
-                const uint4 c = *reinterpret_cast<const uint4 *>(x.k + key * 64 + t * 16);
-                const uint32_t sc = *reinterpret_cast<const uint16_t *>(x.ks + key * 8 + 2 * t);
-                const uint32_t s0 = scale_f16x2(sc & 0xff), s1 = scale_f16x2(sc >> 8);
-                const uint32_t words[4] = {c.x, c.y, c.z, c.w};
-                float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    uint32_t p0, p1, p2, p3;
-                    e2m1x8_f16(words[y], p0, p1, p2, p3);
-                    const uint32_t sy = y < 2 ? s0 : s1;
-                    p0 = hmul2_bits(p0, sy), p1 = hmul2_bits(p1, sy), p2 = hmul2_bits(p2, sy), p3 = hmul2_bits(p3, sy);
-                    if constexpr (kTok == 1) {
-                        mma4(acc, qf[0][2 * y][0], 0u, qf[0][2 * y][1], 0u, p0, p1);
-                        mma4(acc, qf[0][2 * y + 1][0], 0u, qf[0][2 * y + 1][1], 0u, p2, p3);
+                    if constexpr (Shape::kSharedQ) {
+                        // A operand: .x, .z the pair's first token, .y, .w its second
+                        uint32_t *to = reinterpret_cast<uint32_t *>(&sm.q[w][j / 2][2 * x][lane]) + (j & 1);
+                        to[0] = f.x ^ flip, to[2] = f.y ^ flip;
+                        to += 32 * 4;
+                        to[0] = f.z ^ flip, to[2] = f.w ^ flip;
                     } else {
-                        mma4(acc, qf[0][2 * y][0], qf[1][2 * y][0], qf[0][2 * y][1], qf[1][2 * y][1], p0, p1);
-                        mma4(acc, qf[0][2 * y + 1][0], qf[1][2 * y + 1][0], qf[0][2 * y + 1][1], qf[1][2 * y + 1][1], p2, p3);
+                        qf[j][2 * x][0] = f.x ^ flip, qf[j][2 * x][1] = f.y ^ flip;
+                        qf[j][2 * x + 1][0] = f.z ^ flip, qf[j][2 * x + 1][1] = f.w ^ flip;
                     }
                 }
-#pragma unroll
-                for (int e = 0; e < 2 * kTok; ++e) s[tile][e] = acc[e] * a.scale_log2;
+                m[j] = -INFINITY, l[j] = make_float2(0.f, 0.f);
             }
-            uint32_t pk[8][kTok];  // P of this lane's two keys of a tile, an f16 pair
 #pragma unroll
-            for (int j = 0; j < kTok; ++j) {
-                int32_t lo = d.lo, hi = d.hi;  // one token: the stage's range is its own
-                if (a.n_tok > 1) {
-                    const int32_t at = d.len - a.n_tok + a.tok0 + j;
-                    hi = min(d.hi, at - d.key0 + 1);
-                    if (a.window > 0) lo = max(d.lo, at - a.window + 1 - d.key0);
-                }
-                if (lo > 0 || hi < kP) {
+            for (int pr = 0; pr < kPairs; ++pr)
 #pragma unroll
-                    for (int tile = 0; tile < 8; ++tile)
+                for (int y = 0; y < 8; ++y)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int key = 8 * tile + 2 * t + (e ^ b);
-                            if (key < lo || key >= hi) s[tile][2 * j + e] = -INFINITY;
+                    for (int e = 0; e < 4; ++e) o[pr][0][y][e] = o[pr][1][y][e] = 0.f;
+        }
+        arrived();
+        uint32_t pk[kTok][kTiles];  // P of this lane's two keys of a tile, an f16 pair
+        if (!(flags & kSkip)) {
+            const Part &x = sm.part[w][st];
+            if constexpr (kTok == 1) {
+                float s[kTiles / 2][4];  // keys of two tiles as rows: heads 2 t, 2 t + 1 of one key, of the other
+                constexpr int kGroup = 2;
+#pragma unroll
+                for (int r0 = 0; r0 < kTiles / 2; r0 += kGroup) {
+                    uint4 c[2 * kGroup];
+                    uint32_t sc[2 * kGroup];
+#pragma unroll
+                    for (int z = 0; z < 2 * kGroup; ++z) {
+                        const int key = 8 * (2 * r0 + z) + krow;
+                        c[z] = *reinterpret_cast<const uint4 *>(x.codes + key * 64 + t * 16);
+                        sc[z] = *reinterpret_cast<const uint16_t *>(x.scales + key * 8 + 2 * t);
+                    }
+#pragma unroll
+                    for (int z = 0; z < kGroup; ++z) s[r0 + z][0] = s[r0 + z][1] = s[r0 + z][2] = s[r0 + z][3] = 0.f;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+#pragma unroll
+                        for (int z = 0; z < kGroup; ++z) {
+                            uint32_t k[2][4];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint4 &cz = c[2 * z + h];
+                                const uint32_t sy = scale_f16x2(y < 2 ? sc[2 * z + h] & 0xff : sc[2 * z + h] >> 8);
+                                e2m1x8_f16(y == 0 ? cz.x : y == 1 ? cz.y : y == 2 ? cz.z : cz.w, k[h][0], k[h][1], k[h][2], k[h][3]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) k[h][e] = hmul2_bits(k[h][e], sy);
+                            }
+                            mma4(s[r0 + z], k[0][0], k[1][0], k[0][1], k[1][1], qf[0][2 * y][0], qf[0][2 * y][1]);
+                            mma4(s[r0 + z], k[0][2], k[1][2], k[0][3], k[1][3], qf[0][2 * y + 1][0], qf[0][2 * y + 1][1]);
                         }
                 }
-                float top = fmaxf(s[0][2 * j], s[0][2 * j + 1]);
+                const int32_t lo = (d.range & 0xff) - from, hi = (d.range >> 8 & 0xff) - from;
+                if (lo > 0 || hi < kKeys) {
 #pragma unroll
-                for (int tile = 1; tile < 8; ++tile) top = max3(top, s[tile][2 * j], s[tile][2 * j + 1]);
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    for (int z = 0; z < kTiles; ++z) {
+                        const int key = 8 * z + krow;
+                        if (key < lo || key >= hi) s[z / 2][2 * (z & 1)] = s[z / 2][2 * (z & 1) + 1] = -INFINITY;
+                    }
+                }
+                float top0 = fmaxf(s[0][0], s[0][2]), top1 = fmaxf(s[0][1], s[0][3]);
+#pragma unroll
+                for (int z = 1; z < kTiles / 2; ++z) top0 = max3(top0, s[z][0], s[z][2]), top1 = max3(top1, s[z][1], s[z][3]);
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) {
+                    top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, off));
+                    top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, off));
+                }
                 // P carries 2^14, in the middle of f16's range, and so does its
                 // sum: the reference is 14 below the largest score
-                const float next = fmaxf(m[j], top - 14.f);
-                const float ref = next == -INFINITY ? 0.f : next;
-                if (__any_sync(0xffffffffu, next > m[j])) {
-                    const float al = next == -INFINITY ? 1.f : fast_exp2(m[j] - next);
-                    l[j] *= al;
+                const float n0 = fmaxf(m2.x, fmaf(top0, scale, -14.f)), n1 = fmaxf(m2.y, fmaf(top1, scale, -14.f));
+                if (__any_sync(0xffffffffu, n0 > m2.x || n1 > m2.y)) {
+                    const float al0 = n0 == -INFINITY ? 1.f : fast_exp2(m2.x - n0), al1 = n1 == -INFINITY ? 1.f : fast_exp2(m2.y - n1);
+                    l[0].x *= al0, l[0].y *= al1;
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) {
-                        if constexpr (kTok == 1) {
-                            o[0][y][0] *= al, o[0][y][1] *= al, o[0][y][2] *= al, o[0][y][3] *= al;
-                        } else {
-                            o[0][y][2 * j] *= al, o[0][y][2 * j + 1] *= al, o[1][y][2 * j] *= al, o[1][y][2 * j + 1] *= al;
-                        }
-                    }
-                    m[j] = next;
+                    for (int y = 0; y < 8; ++y) o[0][0][y][0] *= al0, o[0][0][y][1] *= al1, o[0][0][y][2] *= al0, o[0][0][y][3] *= al1;
+                    m2 = make_float2(n0, n1);
                 }
+                const float2 scale2 = make_float2(scale, scale);
+                const float2 ref2 = make_float2(n0 == -INFINITY ? 0.f : -n0, n1 == -INFINITY ? 0.f : -n1);
 #pragma unroll
-                for (int tile = 0; tile < 8; ++tile) {
-                    const float p0 = fast_exp2(s[tile][2 * j] - ref), p1 = fast_exp2(s[tile][2 * j + 1] - ref);
-                    l[j] += p0 + p1;
-                    pk[tile][j] = pack_f16(p0, p1);
-                }
-            }
-            // V of the lane's keys of a tile, block gr: 8 f16 pairs (d, d + 1) each
-            const auto values = [&](int tile, int e, uint32_t (&v)[8]) {
-                const int key = 8 * tile + 2 * t + (e ^ b);  // (key >> 1) & 3 is t
-                const uint2 c = *reinterpret_cast<const uint2 *>(x.v + key * 64 + (((gr >> 1) ^ t) << 4) + (gr & 1) * 8);
-                const uint32_t sv = scale_f16x2(x.vs[key * 8 + gr]);
-                e2m1x8_f16(c.x, v[0], v[1], v[2], v[3]);
-                e2m1x8_f16(c.y, v[4], v[5], v[6], v[7]);
-#pragma unroll
-                for (int y = 0; y < 8; ++y) v[y] = hmul2_bits(v[y], sv);
-            };
-            if constexpr (kTok == 1) {
-#pragma unroll
-                for (int tile = 0; tile < 8; ++tile) {
-                    uint32_t v0[8], v1[8];
-                    values(tile, 0, v0);
-                    values(tile, 1, v1);
-                    const uint32_t p = pk[tile][0];
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) mma4(o[0][y], p & 0xffff, p << 16, p >> 16, p & 0xffff0000u, v0[y], v1[y]);
+                for (int z = 0; z < kTiles; ++z) {
+                    const float2 y = __ffma2_rn(make_float2(s[z / 2][2 * (z & 1)], s[z / 2][2 * (z & 1) + 1]), scale2, ref2);
+                    const float2 pp = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                    l[0] = __fadd2_rn(l[0], pp);
+                    pk[0][z] = movmatrix_t(pack_f16(pp.x, pp.y));  // head gr, keys of columns 2 t, 2 t + 1
                 }
             } else {
+                float s[kPairs][kTiles][4];  // rows: the pair's first token (two keys), its second
+                constexpr int kGroup = 4;       // tiles whose MMAs go side by side
 #pragma unroll
-                for (int tile = 0; tile < 8; tile += 2) {
-                    uint32_t v0[8], v1[8], v2[8], v3[8];
-                    values(tile, 0, v0);
-                    values(tile, 1, v1);
-                    values(tile + 1, 0, v2);
-                    values(tile + 1, 1, v3);
+                for (int t0 = 0; t0 < kTiles; t0 += kGroup) {
+                    uint4 c[kGroup];
+                    uint32_t sc[kGroup];
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) {
-                        mma4(o[0][y], pk[tile][0], pk[tile][1], pk[tile + 1][0], pk[tile + 1][1],
-                             __byte_perm(v0[y], v1[y], 0x5410), __byte_perm(v2[y], v3[y], 0x5410));
-                        mma4(o[1][y], pk[tile][0], pk[tile][1], pk[tile + 1][0], pk[tile + 1][1],
-                             __byte_perm(v0[y], v1[y], 0x7632), __byte_perm(v2[y], v3[y], 0x7632));
+                    for (int z = 0; z < kGroup; ++z) {
+                        const int key = 8 * (t0 + z) + krow;
+                        c[z] = *reinterpret_cast<const uint4 *>(x.codes + key * 64 + t * 16);
+                        sc[z] = *reinterpret_cast<const uint16_t *>(x.scales + key * 8 + 2 * t);
+#pragma unroll
+                        for (int pr = 0; pr < kPairs; ++pr) s[pr][t0 + z][0] = s[pr][t0 + z][1] = s[pr][t0 + z][2] = s[pr][t0 + z][3] = 0.f;
+                    }
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        uint4 qa[kPairs][2];  // steps 2 y and 2 y + 1
+#pragma unroll
+                        for (int pr = 0; pr < kPairs; ++pr)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                if constexpr (Shape::kSharedQ)
+                                    qa[pr][h] = sm.q[w][pr][2 * y + h][lane];
+                                else
+                                    qa[pr][h] = make_uint4(qf[0][2 * y + h][0], 0u, qf[0][2 * y + h][1], 0u);
+                            }
+#pragma unroll
+                        for (int z = 0; z < kGroup; ++z) {
+                            const uint32_t word = y == 0 ? c[z].x : y == 1 ? c[z].y : y == 2 ? c[z].z : c[z].w;
+                            const uint32_t sy = scale_f16x2(y < 2 ? sc[z] & 0xff : sc[z] >> 8);
+                            uint32_t p0, p1, p2, p3;
+                            e2m1x8_f16(word, p0, p1, p2, p3);
+                            p0 = hmul2_bits(p0, sy), p1 = hmul2_bits(p1, sy), p2 = hmul2_bits(p2, sy), p3 = hmul2_bits(p3, sy);
+#pragma unroll
+                            for (int pr = 0; pr < kPairs; ++pr) {
+                                mma4(s[pr][t0 + z], qa[pr][0].x, qa[pr][0].y, qa[pr][0].z, qa[pr][0].w, p0, p1);
+                                mma4(s[pr][t0 + z], qa[pr][1].x, qa[pr][1].y, qa[pr][1].z, qa[pr][1].w, p2, p3);
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kTok; ++j) {
+                    float(&sj)[kTiles][4] = s[j / 2];
+                    const int e0 = 2 * (j & 1);
+                    int32_t lo = (d.range & 0xff) - from, hi = (d.range >> 8 & 0xff) - from;  // one token: the sequence's range is its own
+                    if (a.n_tok > 1) {
+                        const int32_t at = d.rel - a.n_tok + j - from;  // its position
+                        hi = min(hi, at + 1);
+                        if (a.window > 0) lo = max(lo, at - a.window + 1);
+                    }
+                    if (lo > 0 || hi < kKeys) {
+#pragma unroll
+                        for (int tile = 0; tile < kTiles; ++tile)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int key = 8 * tile + 2 * t + (e ^ b);
+                                if (key < lo || key >= hi) sj[tile][e0 + e] = -INFINITY;
+                            }
+                    }
+                    float top = fmaxf(sj[0][e0], sj[0][e0 + 1]);
+#pragma unroll
+                    for (int tile = 1; tile < kTiles; ++tile) top = max3(top, sj[tile][e0], sj[tile][e0 + 1]);
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    // P carries 2^14, in the middle of f16's range, and so does its
+                    // sum: the reference is 14 below the largest score
+                    const float next = fmaxf(m[j], fmaf(top, scale, -14.f));
+                    if (__any_sync(0xffffffffu, next > m[j])) {
+                        const float al = next == -INFINITY ? 1.f : fast_exp2(m[j] - next);
+                        l[j].x *= al, l[j].y *= al;
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            if constexpr (kTok == 1) {
+                                o[0][0][y][0] *= al, o[0][0][y][1] *= al, o[0][0][y][2] *= al, o[0][0][y][3] *= al;
+                            } else {
+                                float(&oj)[2][8][4] = o[j / 2];
+                                oj[0][y][e0] *= al, oj[0][y][e0 + 1] *= al, oj[1][y][e0] *= al, oj[1][y][e0 + 1] *= al;
+                            }
+                        }
+                        m[j] = next;
+                    }
+                    const float ref = next == -INFINITY ? 0.f : -next;
+                    const float2 scale2 = make_float2(scale, scale), ref2 = make_float2(ref, ref);
+#pragma unroll
+                    for (int tile = 0; tile < kTiles; ++tile) {
+                        const float2 y = __ffma2_rn(make_float2(sj[tile][e0], sj[tile][e0 + 1]), scale2, ref2);
+                        const float2 pp = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                        l[j] = __fadd2_rn(l[j], pp);
+                        pk[j][tile] = pack_f16(pp.x, pp.y);
                     }
                 }
             }
         }
-        __syncwarp();  // every lane has read the stage
-        if (issued < n) issue();
-
-        if (d.flags & kLast) {
+        release(2 * i, false);
+        arrived();
+        if (!(flags & kSkip)) {
+            const Part &x = sm.part[w][st];
+            // V of the lane's two keys of a tile, block gr: f16 pairs of both
+            // keys' even d's (ve) and odd d's (vo). The codes are paired before they
+            // are converted, a byte taking one code of each key.
+            const uint8_t *const at0 = x.codes + (2 * t + b) * 64 + (((gr >> 1) ^ t) << 4) + (gr & 1) * 8;  // (key >> 1) & 3 is t
+            const uint8_t *const at1 = at0 + (b ? -64 : 64);
+            const uint8_t *const sc0 = x.scales + (2 * t + b) * 8 + gr, *const sc1 = sc0 + (b ? -8 : 8);
+            const auto values = [&](int tile, uint32_t (&ve)[8], uint32_t (&vo)[8]) {
+                const uint2 c0 = *reinterpret_cast<const uint2 *>(at0 + tile * 512), c1 = *reinterpret_cast<const uint2 *>(at1 + tile * 512);
+                const uint32_t sv = (uint32_t)sc0[tile * 64] << 7 | (uint32_t)sc1[tile * 64] << 23;
+                constexpr uint32_t kLow = 0x0f0f0f0f;
+                e2m1x8_f16((c0.x & kLow) | (c1.x << 4 & ~kLow), ve[0], ve[1], ve[2], ve[3]);
+                e2m1x8_f16((c0.y & kLow) | (c1.y << 4 & ~kLow), ve[4], ve[5], ve[6], ve[7]);
+                e2m1x8_f16((c0.x >> 4 & kLow) | (c1.x & ~kLow), vo[0], vo[1], vo[2], vo[3]);
+                e2m1x8_f16((c0.y >> 4 & kLow) | (c1.y & ~kLow), vo[4], vo[5], vo[6], vo[7]);
 #pragma unroll
-            for (int j = 0; j < kTok; ++j) {
-                float L = l[j];
-                L += __shfl_xor_sync(0xffffffffu, L, 1);
-                L += __shfl_xor_sync(0xffffffffu, L, 2);
-                float f[32];  // d = 32 t .. 32 t + 31
+                for (int y = 0; y < 8; ++y) ve[y] = hmul2_bits(ve[y], sv), vo[y] = hmul2_bits(vo[y], sv);
+            };
+#pragma unroll
+            for (int tile = 0; tile < kTiles; tile += 2) {
+                uint32_t a0[8], a1[8], a2[8], a3[8];
+                values(tile, a0, a1);
+                values(tile + 1, a2, a3);
 #pragma unroll
                 for (int y = 0; y < 8; ++y) {
                     if constexpr (kTok == 1) {
-                        f[2 * y] = o[0][y][0], f[2 * y + 1] = o[0][y][2];
-                        f[16 + 2 * y] = o[0][y][1], f[17 + 2 * y] = o[0][y][3];
+                        mma4(o[0][0][y], a0[y], a1[y], a2[y], a3[y], pk[0][tile], pk[0][tile + 1]);
                     } else {
-                        f[2 * y] = o[0][y][2 * j], f[2 * y + 1] = o[1][y][2 * j];
-                        f[16 + 2 * y] = o[0][y][2 * j + 1], f[17 + 2 * y] = o[1][y][2 * j + 1];
+#pragma unroll
+                        for (int pr = 0; pr < kPairs; ++pr) {
+                            mma4(o[pr][0][y], pk[2 * pr][tile], pk[2 * pr + 1][tile], pk[2 * pr][tile + 1], pk[2 * pr + 1][tile + 1], a0[y], a2[y]);
+                            mma4(o[pr][1][y], pk[2 * pr][tile], pk[2 * pr + 1][tile], pk[2 * pr][tile + 1], pk[2 * pr + 1][tile + 1], a1[y], a3[y]);
+                        }
                     }
                 }
-                const int tok = a.tok0 + j;
-                if (d.flags & kDirect) {
-                    const float inv = L > 0.f ? 1.f / L : 0.f;
-                    uint4 *out = reinterpret_cast<uint4 *>(a.o + (q_row(a, d.seq, tok) * a.hq + (int64_t)d.kvh * kG + gr) * kD + 32 * t);
+            }
+        }
+        release(2 * i + 1, true);
+
+        if (flags & kLast) {
+            if constexpr (kTok == 1) {
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        out[y] = make_uint4(pack_bf16(f[8 * y] * inv, f[8 * y + 1] * inv), pack_bf16(f[8 * y + 2] * inv, f[8 * y + 3] * inv),
-                                            pack_bf16(f[8 * y + 4] * inv, f[8 * y + 5] * inv), pack_bf16(f[8 * y + 6] * inv, f[8 * y + 7] * inv));
-                } else {
-                    Partial &p = a.part[((int64_t)worker * 2 + d.slot) * a.n_tok + tok];
-                    if (t == 0) p.m[gr] = m[j], p.l[gr] = L;
-                    float4 *out = reinterpret_cast<float4 *>(p.o[gr] + 32 * t);
+                for (int off = 4; off < 32; off <<= 1) {
+                    l[0].x += __shfl_xor_sync(0xffffffffu, l[0].x, off);
+                    l[0].y += __shfl_xor_sync(0xffffffffu, l[0].y, off);
+                }
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) out[y] = make_float4(f[4 * y], f[4 * y + 1], f[4 * y + 2], f[4 * y + 3]);
+                for (int e = 0; e < 2; ++e) {  // head 2 t + e, d = 16 gr .. 16 gr + 15
+                    const int h = 2 * t + e;
+                    const float L = e ? l[0].y : l[0].x;
+                    float f[16];
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) f[2 * y] = o[0][0][y][e], f[2 * y + 1] = o[0][0][y][2 + e];
+                    if (flags & kDirect) {
+                        fp4_store(a.o + ((int64_t)(d.seq & 0xffff) * a.hq + (int64_t)(d.seq >> 16) * kG + h) * kD + 16 * gr, f, L);
+                    } else {
+                        Partial &p = a.part[(int64_t)worker * 2 + (flags & kSecond ? 1 : 0)];
+                        if (gr == 0) p.m[h] = e ? m2.y : m2.x, p.l[h] = L;
+                        float4 *out = reinterpret_cast<float4 *>(p.o[h] + 16 * gr);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) out[y] = make_float4(f[4 * y], f[4 * y + 1], f[4 * y + 2], f[4 * y + 3]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kTok; ++j) {
+                    if (j >= a.n_tok) break;
+                    float L = l[j].x + l[j].y;
+                    L += __shfl_xor_sync(0xffffffffu, L, 1);
+                    L += __shfl_xor_sync(0xffffffffu, L, 2);
+                    float(&oj)[2][8][4] = o[j / 2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {  // head gr, d = 32 t + 16 c ..
+                        float f[16];
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) f[2 * y] = oj[0][y][2 * (j & 1) + c], f[2 * y + 1] = oj[1][y][2 * (j & 1) + c];
+                        if (flags & kDirect) {
+                            fp4_store(a.o + (q_row(a, d.seq & 0xffff, j) * a.hq + (int64_t)(d.seq >> 16) * kG + gr) * kD + 32 * t + 16 * c, f, L);
+                        } else {
+                            Partial &p = a.part[((int64_t)worker * 2 + (flags & kSecond ? 1 : 0)) * a.n_tok + j];
+                            if (t == 0 && c == 0) p.m[gr] = m[j], p.l[gr] = L;
+                            float4 *out = reinterpret_cast<float4 *>(p.o[gr] + 32 * t + 16 * c);
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) out[y] = make_float4(f[4 * y], f[4 * y + 1], f[4 * y + 2], f[4 * y + 3]);
+                        }
+                    }
                 }
             }
         }
     }
-    // a wait gave up: never leave with copies still landing in shared memory
-    // (stages that were waited for already return at once)
-    if (lane == 0)
-        for (int64_t i = issued > kFp4Stages ? issued - kFp4Stages : 0; i < issued; ++i)
-            mbar_wait(&sm.full[w][i % kFp4Stages], (uint32_t)(i / kFp4Stages) & 1, a.err);
 }
 
-template <int kTok>
-__global__ void __launch_bounds__(32 * kFp4Warps, 3) decode_mma_fp4_d128(const __grid_constant__ CUtensorMap tv, DecodeArgs a) {
+template <class Shape>
+__global__ void __launch_bounds__(32 * Shape::kWarps, Shape::kCtas) decode_mma_fp4_d128(const __grid_constant__ DecodeArgs a) {
     extern __shared__ uint8_t raw[];
-    DecodeSmem4 &sm = *reinterpret_cast<DecodeSmem4 *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    if (threadIdx.x < kFp4Warps * kFp4Stages) mbar_init(&sm.full[0][0] + threadIdx.x, 1);
-    fence_barrier_init();
-    __syncthreads();
+    using Smem = DecodeSmem4<Shape>;
+    Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(raw) + 127) & ~uintptr_t(127));
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t U = a.sdesc[a.n_seqs].x, N = (int64_t)gridDim.x * kFp4Warps;
-    if (U == 0) return;
-    const int32_t worker = blockIdx.x * kFp4Warps + (threadIdx.x >> 5);
-    const int64_t u0 = cta_start(worker, U, N), u1 = cta_start(worker + 1, U, N);
-    decode_fp4_worker<kTok>(sm, &tv, a, u0, u1, worker);
+    const int64_t U = a.sdesc[a.n_seqs].x, N = (int64_t)gridDim.x * Shape::kWarps;
+    const int32_t worker = blockIdx.x * Shape::kWarps + (threadIdx.x >> 5);
+    decode_fp4_worker<Shape>(sm, a, (int32_t)cta_start(worker, U, N), (int32_t)cta_start(worker + 1, U, N), worker);
 }
