@@ -52,7 +52,7 @@ constexpr uint32_t kBoxBytes = 64 * 128;           // 64 rows x 128 bytes
 constexpr uint32_t kPageHeadBytes = 2 * kBoxBytes;  // one page of one kv head
 constexpr uint32_t kQBytes = kG * kD * 2;
 
-enum : int32_t { kFirst = 1, kLast = 2, kDirect = 4, kSkip = 8 };
+enum : int32_t { kFirst = 1, kLast = 2, kDirect = 4, kSkip = 8, kSecond = 16, kOdd = 32 };
 
 struct StageDesc {
     int32_t seq, kvh, lo, hi, flags, slot;
@@ -428,6 +428,7 @@ __device__ void decode_producer(Smem &sm, const CUtensorMap *tk, const CUtensorM
                     d.key0 = key0;
                     d.len = hi;
                     int32_t flags = (j == 0 ? kFirst : 0) | (j == n - 1 ? kLast : 0) | (direct ? kDirect : 0);
+                    if constexpr (Smem::kTcQ) flags |= pc & 1 ? 0 : kOdd;  // pc counts this piece already
                     const bool valid = page >= 0 && page < a.num_pages;
                     if (!valid) {
                         set_error(a.err, HSWA_ERR_BOUNDS);
@@ -1169,6 +1170,7 @@ struct DecodeTcSmem {
     static constexpr bool kTcQ = true;
     static constexpr bool kWeights = false;
     static constexpr bool kQTmem = false;  // QK reads q from shared memory
+    static constexpr int kGroups = 0, kConvThreads = 1, kConvWarp = 7;  // no converters
     static constexpr int kThreads = 224;
     static constexpr uint32_t kQHalfBytes = 128 * 128;  // 128 rows x 64 columns of 16-bit values
     uint8_t k[kStages][kPageHeadBytes];                // [d half][64 keys][128 B], 128-byte swizzle
@@ -1209,6 +1211,7 @@ struct DecodeTc8Smem {
     static constexpr bool kTcQ = true;
     static constexpr bool kWeights = false;
     static constexpr bool kQTmem = true;  // with copies (R > 1) QK reads q from TMEM column kTmemQ
+    static constexpr int kGroups = 1, kConvWarp = 7;
     static constexpr int kConvThreads = 128;  // converter warps 7 ..
     static constexpr int kThreads = 224 + kConvThreads;
     static constexpr uint32_t kQHalfBytes = 128 * 128;
@@ -1260,8 +1263,12 @@ struct DecodeTc4Smem {
     static constexpr bool kTcQ = true;
     static constexpr bool kWeights = false;
     static constexpr bool kQTmem = true;
-    static constexpr int kConvThreads = 128;
-    static constexpr int kThreads = 224 + kConvThreads;
+    // Two groups of converter warps take the pages in turn: the conversion of a
+    // page, with its waits for a stage and a buffer, takes longer than the
+    // pages' other roles.
+    static constexpr int kGroups = 2, kConvWarp = 8;
+    static constexpr int kConvThreads = 128;  // of a group
+    static constexpr int kThreads = 32 * kConvWarp + kGroups * kConvThreads;
     static constexpr uint32_t kQHalfBytes = 128 * 128;
     uint8_t q[kQBufs][2 * kQHalfBytes];
     uint8_t kc[kConv][kPageHeadBytes];  // f16 K and V, [d half][64 keys][128 B], 128-byte swizzle
@@ -1484,7 +1491,10 @@ __device__ void decode_tc_softmax(Smem &sm, const DecodeArgs &a, int64_t n) {
             const int32_t base = d.key0 + c * kK;
             int32_t hi_c = min(d.hi - c * kK, t - base + 1), lo_c = d.lo - c * kK;
             if (a.window > 0) lo_c = max(lo_c, t - a.window + 1 - base);
-            if (w >= a.n_tok || (d.flags & kSkip)) hi_c = 0;
+            // rows behind the last token see every key, whatever is in them:
+            // nothing reads them, and their warps need no mask
+            if (w >= a.n_tok) lo_c = 0, hi_c = kK;
+            if (d.flags & kSkip) hi_c = 0;
             float m0 = -INFINITY, m1 = -INFINITY;
             // most pages are seen whole by every token of the warp
             if (__any_sync(0xffffffffu, lo_c > 0 || hi_c < kK)) {
@@ -1706,22 +1716,23 @@ __device__ __forceinline__ void fp4_to_f16_row(const uint4 &c, uint32_t sc, bool
 // row, which become 4 chunks of K or of V times the scales of their two blocks.
 template <bool kQT, class Smem>
 __device__ void decode_tc_convert(Smem &sm, const DecodeArgs &a, int64_t n) {
+    static_assert(Smem::kGroups == 1 || Smem::kQBufs == 1, "a piece's parity is its q slot's");
     constexpr int kStages = Smem::kStages, kConv = Smem::kConv, kQB = Smem::kQBufs;
     constexpr int kCT = Smem::kConvThreads, kPer = (Smem::kFP4 ? 256 : 512) / kCT;  // 16-byte chunks per thread and tile
     constexpr uint32_t kQH = Smem::kQHalfBytes;
-    const int t = threadIdx.x - 7 * 32;  // 0 .. kCT - 1
+    const int t = (threadIdx.x - Smem::kConvWarp * 32) % kCT;
     const int quad = (threadIdx.x >> 5) & 3, row = 32 * quad + (threadIdx.x & 31);
     const uint32_t t_q = sm.tmem_base + ((uint32_t)(32 * quad) << 16) + kTmemQ;
     int32_t pc = -1;
     bool ok = true;
-    for (int64_t i = 0; i < n && ok; ++i) {
+    for (int64_t i = (threadIdx.x - Smem::kConvWarp * 32) / kCT; i < n && ok; i += Smem::kGroups) {
         const int st = (int)(i % kStages), b = (int)(i % kConv);
         ok = mbar_wait(&sm.full[st], (uint32_t)(i / kStages) & 1, a.err) &&
              (i < kConv || mbar_wait(&sm.conv_empty[b], (uint32_t)((i - kConv) / kConv) & 1, a.err)) &&
              !*(volatile int32_t *)&sm.abort;
         const StageDesc d = sm.desc[st];
         if (ok && (d.flags & kFirst)) {
-            ++pc;
+            pc = Smem::kGroups > 1 ? (d.flags & kOdd ? 1 : 0) : pc + 1;  // a group of several does not see every piece
             ok = mbar_wait(&sm.q_full[pc % kQB], (uint32_t)(pc / kQB) & 1, a.err);
         }
         // the TMEM stores below are warp-wide: the warp goes on or stops as one
@@ -1834,7 +1845,7 @@ __global__ void __launch_bounds__(Smem::kThreads, 1)
         for (int i = 0; i < Smem::kStages; ++i) {
             mbar_init(&sm.full[i], 1);
             // bf16: the PV thread's commit; FP8, FP4: the 128 converter threads
-            mbar_init(&sm.empty[i], Smem::kConvert ? Smem::kThreads - 224 : 1);
+            mbar_init(&sm.empty[i], Smem::kConvThreads);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sm.q_full[b], 1);
@@ -1846,10 +1857,10 @@ __global__ void __launch_bounds__(Smem::kThreads, 1)
         }
         if constexpr (Smem::kConvert) {
             for (int b = 0; b < Smem::kConv; ++b) {
-                mbar_init(&sm.conv_full[b], Smem::kThreads - 224);
+                mbar_init(&sm.conv_full[b], Smem::kConvThreads);
                 mbar_init(&sm.conv_empty[b], 1);
             }
-            for (int b = 0; b < 2; ++b) mbar_init(&sm.q_conv[b], Smem::kThreads - 224);
+            for (int b = 0; b < 2; ++b) mbar_init(&sm.q_conv[b], Smem::kConvThreads);
         }
         mbar_init(&sm.mma_done[0], 1);
         mbar_init(&sm.mma_done[1], 1);
@@ -1865,6 +1876,14 @@ __global__ void __launch_bounds__(Smem::kThreads, 1)
     pdl_launch_dependents();
     const int64_t U = a.sdesc[a.n_seqs].x, N = gridDim.x;
     const int64_t u0 = cta_start(blockIdx.x, U, N), u1 = cta_start(blockIdx.x + 1, U, N);
+    // With two converter groups the four warps of a role's group trade registers:
+    // 168 + 88 + 2 x 128 of 4 x 128.
+    if constexpr (Smem::kGroups == 2) {
+        if (warp < 4)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        else if (warp < 8)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    }
     if (warp < 4) {
         decode_tc_softmax<kR>(sm, a, u1 - u0);
     } else if (warp == 4) {
@@ -1878,7 +1897,7 @@ __global__ void __launch_bounds__(Smem::kThreads, 1)
         }
         __syncwarp();
     } else if constexpr (Smem::kConvert) {
-        decode_tc_convert<Smem::kQTmem && (kR > 1)>(sm, a, u1 - u0);
+        if (warp >= Smem::kConvWarp) decode_tc_convert<Smem::kQTmem && (kR > 1)>(sm, a, u1 - u0);
     }
     tc_fence_before();
     __syncthreads();

@@ -80,8 +80,6 @@ __device__ __forceinline__ void mma4(float (&d)[4], uint32_t a0, uint32_t a1, ui
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-constexpr int32_t kSecond = 16;  // a piece whose record is its worker's second
-
 // 16 bytes global -> shared, without a register between.
 __device__ __forceinline__ void copy16(uint32_t to, const uint8_t *from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
