@@ -32,9 +32,34 @@ struct ProbsArgs {
     const int32_t *bias_token;
     const float *bias;        // [n_seqs][n_bias]
     const uint32_t *mask;
-    int32_t n_bias, n_tok, vocab, cluster, slice;  // slice: elements per CTA, a multiple of 8
+    bool wide;                // fp32 rows start on 32 bytes
+    int32_t n_bias, n_tok, vocab, cluster, cluster_log2, slice;  // slice: elements per CTA, a multiple of 8
     int *err;
 };
+
+// 8 neighbouring fp32 values: in one access where they start on 32 bytes (two of
+// 16 bytes from each lane touch every sector of the warp's kilobyte twice).
+__device__ __forceinline__ void load8(const float *p, bool wide, float (&x)[8]) {
+    if (wide) {
+        asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                     : "l"(p)
+                     : "memory");
+    } else {
+        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+}
+__device__ __forceinline__ void store8(float *p, bool wide, const float (&x)[8]) {
+    if (wide) {
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]),
+                     "f"(x[5]), "f"(x[6]), "f"(x[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+}
 
 template <typename T>
 __device__ __forceinline__ float as_float(T x);
@@ -46,10 +71,9 @@ __device__ __forceinline__ float as_float<__nv_bfloat16>(__nv_bfloat16 x) { retu
 struct ProbsSmem {
     int32_t key[kBiasSlots];  // token of a slot, -1: free
     int32_t at[kBiasSlots];   // the last entry of the bias list with that token
-    uint32_t special[kMaxSlice / 8 / 32];  // groups of 8 tokens with a bias or a draft among them
+    uint32_t special[kMaxSlice / 32];  // the CTA's tokens with a bias or a draft
     int32_t draft[HSWA_DECODE_MAX_TOKENS];
-    float warp[32];
-    uint64_t part[kMaxCluster];  // every CTA's (maximum, sum or first index)
+    uint64_t part[kMaxCluster * 32];  // every warp's of the cluster: maximum, sum or first index
 };
 
 __device__ __forceinline__ uint32_t bias_slot(int32_t token) { return (uint32_t)token * 0x9E3779B1u >> 21; }
@@ -69,10 +93,10 @@ struct ProbsRow {
     bool specials;
     float rep, inv_rep, freq, pres;  // inv_rep 0: divide
 
-    // Token of element e of group k of this thread (kVec: 8 neighbours, else 8
+    // Token of element e of group k of thread t (kVec: 8 neighbours, else 8
     // as far apart as the CTA has threads).
-    __device__ __forceinline__ int32_t token(int32_t k, int e) const {
-        return kVec ? lo + 8 * (k * (int32_t)blockDim.x + (int32_t)threadIdx.x) + e : lo + (8 * k + e) * (int32_t)blockDim.x + (int32_t)threadIdx.x;
+    __device__ __forceinline__ int32_t token(int32_t k, int32_t t, int e) const {
+        return kVec ? lo + 8 * (k * (int32_t)blockDim.x + t) + e : lo + (8 * k + e) * (int32_t)blockDim.x + t;
     }
 
     __device__ __forceinline__ float penalized(float z, uint32_t c, int extra) const {
@@ -91,11 +115,13 @@ struct ProbsRow {
         return z;
     }
 
-    __device__ __noinline__ float special(float z, uint32_t c, int32_t v) const {
+    // z of any token but for the mask, from its logit and its count.
+    __device__ __forceinline__ float value(int32_t v, float z, uint32_t c) const {
         int extra = 0;
-        if (counts)
+        if (counts) {
             for (int j = 0; j < w; ++j) extra += sm.draft[j] == v;
-        if (counts) z = penalized(z, c, extra);
+            z = penalized(z, c, extra);
+        }
         if (a.n_bias) {
             uint32_t s = bias_slot(v);
             while (sm.key[s] != -1 && sm.key[s] != v) s = (s + 1) & (kBiasSlots - 1);
@@ -103,70 +129,118 @@ struct ProbsRow {
         }
         return z;
     }
-
-    // Group k: its 8 values of z, -inf behind the CTA's last token.
-    __device__ __forceinline__ void load(int32_t k, float (&z)[8]) const {
-        uint32_t c[8];
-        uint32_t allowed = 0xff;
-        const int32_t v0 = token(k, 0);
-        if (kVec && v0 + 8 <= hi) {
-            if constexpr (sizeof(TL) == 4) {
-                const float4 x = reinterpret_cast<const float4 *>(logits + v0)[0], y = reinterpret_cast<const float4 *>(logits + v0)[1];
-                z[0] = x.x, z[1] = x.y, z[2] = x.z, z[3] = x.w, z[4] = y.x, z[5] = y.y, z[6] = y.z, z[7] = y.w;
-            } else {
-                const uint4 x = *reinterpret_cast<const uint4 *>(logits + v0);
-                const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+    // 8 neighbouring logits.
+    __device__ __forceinline__ void read8(int32_t v0, float (&z)[8]) const {
+        if constexpr (sizeof(TL) == 4) {
+            load8(reinterpret_cast<const float *>(logits + v0), a.wide, z);
+        } else {
+            const uint4 x = *reinterpret_cast<const uint4 *>(logits + v0);
+            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) z[2 * e] = __uint_as_float(u[e] << 16), z[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-            }
+            for (int e = 0; e < 4; ++e) z[2 * e] = __uint_as_float(u[e] << 16), z[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+        }
+    }
+
+    // Group k of this thread: its 8 logits as z, and whether a token of it may
+    // need more (one that occurred, a draft, one with a bias).
+    __device__ __forceinline__ bool load(int32_t k, float (&z)[8]) const {
+        const int32_t v0 = token(k, threadIdx.x, 0);
+        uint32_t any = 0;
+        if (kVec && v0 >= hi) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = -INFINITY;
+        } else if (kVec && v0 + 8 <= hi) {
             uint4 n = make_uint4(0, 0, 0, 0);
             if (counts) n = *reinterpret_cast<const uint4 *>(counts + v0);
-            const uint32_t u[4] = {n.x, n.y, n.z, n.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) c[2 * e] = u[e] & 0xffff, c[2 * e + 1] = u[e] >> 16;
-            if (mask) allowed = reinterpret_cast<const uint8_t *>(mask)[v0 >> 3];
+            read8(v0, z);
+            any = n.x | n.y | n.z | n.w;
+            if (specials) any |= sm.special[(v0 - lo) >> 5] >> ((v0 - lo) & 31) & 0xff;
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int32_t v = token(k, e);
-                z[e] = v < hi ? as_float(logits[v]) : -INFINITY;
-                c[e] = counts && v < hi ? counts[v] : 0;
-                if (mask && !(v < hi && mask[v >> 5] >> (v & 31) & 1)) allowed &= ~(1u << e);
+                const int32_t v = token(k, threadIdx.x, e);
+                z[e] = -INFINITY;
+                if (v < hi) {
+                    z[e] = as_float(logits[v]);
+                    if (counts) any |= counts[v];
+                    if (specials) any |= sm.special[(v - lo) >> 5] >> ((v - lo) & 31) & 1;
+                }
             }
         }
-        uint32_t any = 0;
+        return any != 0;
+    }
+
+    // z of group k of thread t into z8 (shared memory), each token with what it needs.
+    __device__ __forceinline__ void fetch(int32_t k, int32_t t, float *z8) const {
+        const int32_t v0 = token(k, t, 0);
+        uint32_t own = 0;
+        if (kVec && v0 + 8 <= hi) {
+            float z[8];
+            read8(v0, z);
+            if (counts) {
+                const uint4 n = *reinterpret_cast<const uint4 *>(counts + v0);
+                const uint32_t u[4] = {n.x, n.y, n.z, n.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) any |= c[e];
-        uint32_t spec = 0;
-        if (specials) {
+                for (int e = 0; e < 4; ++e) own |= (u[e] & 0xffff ? 1u : 0u) << (2 * e) | (u[e] >> 16 ? 2u : 0u) << (2 * e);
+            }
+            if (specials) own |= sm.special[(v0 - lo) >> 5] >> ((v0 - lo) & 31) & 0xff;
 #pragma unroll
-            for (int e = 0; e < 8; e += kVec ? 8 : 1) {
-                const int32_t r = (token(k, e) - lo) >> 3;
-                if (token(k, e) < hi) spec |= (sm.special[r >> 5] >> (r & 31) & 1) << e;
+            for (int e = 0; e < 8; ++e) z8[e] = z[e];
+        } else {
+            for (int e = 0; e < 8; ++e) {
+                const int32_t v = token(k, t, e);
+                if (v < hi) own |= 1u << e;  // whatever it needs
+                z8[e] = v < hi ? as_float(logits[v]) : -INFINITY;
             }
         }
-        if (spec) {
+        while (own) {
+            const int e = __ffs((int)own) - 1;
+            own &= own - 1;
+            const int32_t v = token(k, t, e);
+            z8[e] = value(v, z8[e], counts ? counts[v] : 0);
+        }
+    }
+
+    // Group k's 8 bits of the mask.
+    __device__ __forceinline__ uint32_t allowed(int32_t k) const {
+        uint32_t bits = 0;
+        if constexpr (kVec) {
+            const int32_t v0 = token(k, threadIdx.x, 0);
+            if (v0 < hi) bits = reinterpret_cast<const uint8_t *>(mask)[v0 >> 3];
+        } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int32_t v = token(k, e);
-                if (v < hi) z[e] = special(z[e], c[e], v);
+                const int32_t v = token(k, threadIdx.x, e);
+                if (v < hi) bits |= (mask[v >> 5] >> (v & 31) & 1) << e;
             }
-        } else if (any) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = penalized(z[e], c[e], 0);
         }
+        return bits;
+    }
+
+    // All of it, where nothing is kept between.
+    __device__ __forceinline__ void whole(int32_t k, float (&z)[8]) const {
+        if (load(k, z)) {
+#pragma unroll 1
+            for (int e = 0; e < 8; ++e) {
+                const int32_t v = token(k, threadIdx.x, e);
+                const float x = v < hi ? value(v, as_float(logits[v]), counts ? counts[v] : 0) : -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (!(allowed >> e & 1) || z[e] != z[e]) z[e] = -INFINITY;
+                for (int y = 0; y < 8; ++y)
+                    if (y == e) z[y] = x;
+            }
+        }
+        const uint32_t bits = mask ? allowed(k) : 0xff;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] = bits >> e & 1 ? fmaxf(z[e], -INFINITY) : -INFINITY;  // NaN too
     }
 };
 
 template <typename TP, bool kVec>
-__device__ __forceinline__ void store_probs(TP *p, int32_t v0, int32_t step, int32_t hi, const float (&x)[8]) {
+__device__ __forceinline__ void store_probs(TP *p, int32_t v0, int32_t step, int32_t hi, bool wide, const float (&x)[8]) {
+    if (kVec && v0 >= hi) return;
     if (kVec && v0 + 8 <= hi) {
         if constexpr (sizeof(TP) == 4) {
-            reinterpret_cast<float4 *>(p + v0)[0] = make_float4(x[0], x[1], x[2], x[3]);
-            reinterpret_cast<float4 *>(p + v0)[1] = make_float4(x[4], x[5], x[6], x[7]);
+            store8(reinterpret_cast<float *>(p + v0), wide, x);
         } else {
             *reinterpret_cast<uint4 *>(p + v0) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
         }
@@ -184,81 +258,70 @@ __device__ __forceinline__ void store_probs(TP *p, int32_t v0, int32_t step, int
     }
 }
 
-__device__ __forceinline__ float block_max(float x, float *warp) {
-    for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-    if ((threadIdx.x & 31) == 0) warp[threadIdx.x >> 5] = x;
-    __syncthreads();
-    const int n = blockDim.x >> 5, lane = threadIdx.x & 31;
-    x = lane < n ? warp[lane] : -INFINITY;
-    for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-    __syncthreads();
-    return x;
+__device__ __forceinline__ float warp_max(float x) {  // passes NaN over
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
 }
-
-__device__ __forceinline__ float block_sum(float x, float *warp) {
+__device__ __forceinline__ float warp_sum(float x) {
     for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    if ((threadIdx.x & 31) == 0) warp[threadIdx.x >> 5] = x;
-    __syncthreads();
-    const int n = blockDim.x >> 5, lane = threadIdx.x & 31;
-    x = lane < n ? warp[lane] : 0.f;
-    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    __syncthreads();
     return x;
 }
 
-__device__ __forceinline__ int32_t block_min(int32_t x, float *warp) {
-    x = __reduce_min_sync(0xffffffffu, x);
-    if ((threadIdx.x & 31) == 0) warp[threadIdx.x >> 5] = __int_as_float(x);
-    __syncthreads();
-    const int n = blockDim.x >> 5, lane = threadIdx.x & 31;
-    x = __reduce_min_sync(0xffffffffu, lane < n ? __float_as_int(warp[lane]) : INT32_MAX);
-    __syncthreads();
-    return x;
-}
-
-// exp((z - top) / T) of a row's value: k is log2 e / T. A top of +inf shares
-// the probability among the infinite values.
+// exp((z - top) / T): k is log2 e / T, finite and above 0. A top of +inf
+// shares the probability among the infinite values; -inf is that of no value at all.
 __device__ __forceinline__ float weight(float z, float top, float k) {
-    if (z == -INFINITY) return 0.f;
     if (top == INFINITY) return z == INFINITY ? 1.f : 0.f;
-    return fast_exp2((z - top) * k);
+    return fast_exp2((z - (top == -INFINITY ? 0.f : top)) * k);
 }
 
 // A cluster per row, kGroups groups of 8 values per thread in registers between
 // the one read and the one write; rows longer than that (kLoop) are read three
-// times, for the maximum, the sum and the result.
+// times, for the maximum, the sum and the result. Warps work on their own (their
+// maximum, the sum relative to it) and meet once, at the cluster's barrier, with
+// every warp's pair in every CTA.
+//
+// What few tokens need (penalties, drafts, biases) is not done where they lie,
+// where a warp would do it for all its values: groups with such a token go on the
+// warp's list, its lanes take one each, and the owners fetch the results.
 template <typename TL, typename TP, bool kVec, int kThreads, int kGroups, bool kLoop>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_probs(const ProbsArgs a) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_probs(const __grid_constant__ ProbsArgs a) {
+    constexpr int kWarps = kThreads / 32;
     __shared__ ProbsSmem sm;
-    const int tid = threadIdx.x;
+    constexpr int kList = 32;  // groups at once, one a lane
+    __shared__ uint8_t list[kLoop ? 1 : kWarps][kList];  // group k of lane t: 32 k + t
+    __shared__ __align__(16) float fetched[kLoop ? 1 : kWarps][kList][8];
+    static_assert(kGroups <= 8, "an entry of the list is a byte");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     cluster_arrive();
     pdl_wait();
     pdl_launch_dependents();
-    const int32_t rank = blockIdx.x % a.cluster;
-    const int64_t row = blockIdx.x / a.cluster;
-    const int32_t seq = (int32_t)(row / a.n_tok), w = (int32_t)(row % a.n_tok);
+    const uint32_t rank = blockIdx.x & (a.cluster - 1), row = blockIdx.x >> a.cluster_log2;
+    const uint32_t seq = row / (uint32_t)a.n_tok;
+    const int32_t w = (int32_t)(row - seq * a.n_tok);
     float temperature = 1.f, rep = 1.f, freq = 0.f, pres = 0.f;
     if (a.params) {
-        const float *x = a.params + (int64_t)seq * 4;
+        const float *x = a.params + (size_t)seq * 4;
         temperature = x[0], rep = x[1] > 0.f ? x[1] : 1.f, freq = x[2], pres = x[3];
     }
     const bool penalties = a.counts && !(rep == 1.f && freq == 0.f && pres == 0.f);
-    const int32_t lo = min(rank * a.slice, a.vocab), hi = min(lo + a.slice, a.vocab);
+    const int32_t lo = min((int32_t)rank * a.slice, a.vocab), hi = min(lo + a.slice, a.vocab);
     const bool drafts = penalties && a.draft && w > 0;
-    ProbsRow<TL, kVec> r{a, sm, static_cast<const TL *>(a.logits) + row * a.logits_stride,
-                         penalties ? a.counts + seq * a.count_stride : nullptr,
-                         a.mask ? a.mask + row * a.mask_stride : nullptr,
-                         a.bias + (int64_t)seq * a.n_bias, lo, hi, drafts ? w : 0, a.n_bias > 0 || drafts,
-                         rep, rep >= 0x1p-64f && rep <= 0x1p64f ? __frcp_rn(rep) : 0.f, freq, pres};
+    const ProbsRow<TL, kVec> r{a, sm, static_cast<const TL *>(a.logits) + row * a.logits_stride,
+                               penalties ? a.counts + seq * a.count_stride : nullptr,
+                               a.mask ? a.mask + row * a.mask_stride : nullptr,
+                               a.bias + (size_t)seq * a.n_bias, lo, hi, drafts ? w : 0, a.n_bias > 0 || drafts,
+                               rep, rep >= 0x1p-64f && rep <= 0x1p64f ? __frcp_rn(rep) : 0.f, freq, pres};
     if (r.specials) {
-        for (int i = tid; i < kBiasSlots; i += kThreads) sm.key[i] = sm.at[i] = -1;
-        for (int i = tid; i < (a.slice / 8 + 31) / 32; i += kThreads) sm.special[i] = 0;
+        if (a.n_bias)
+            for (int i = tid; i < kBiasSlots; i += kThreads) sm.key[i] = sm.at[i] = -1;
+        for (int i = tid; i < (a.slice + 31) / 32; i += kThreads) sm.special[i] = 0;
         __syncthreads();
         for (int i = tid; i < a.n_bias; i += kThreads) {
             const int32_t v = a.bias_token[(int64_t)seq * a.n_bias + i];
             if (v >= a.vocab) set_error(a.err, HSWA_ERR_BOUNDS);
             if (v < lo || v >= hi) continue;
-            atomicOr(&sm.special[(v - lo) >> 8], 1u << ((v - lo) >> 3 & 31));
+            atomicOr(&sm.special[(v - lo) >> 5], 1u << ((v - lo) & 31));
             uint32_t s = bias_slot(v);
             for (;;) {  // at most half of the slots are taken
                 const int32_t was = atomicCAS(&sm.key[s], -1, v);
@@ -270,40 +333,101 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_probs(const 
         if (drafts && tid < w) {
             const int32_t v = a.draft[(int64_t)seq * (a.n_tok - 1) + tid];
             sm.draft[tid] = v;
-            if (v >= lo && v < hi) atomicOr(&sm.special[(v - lo) >> 8], 1u << ((v - lo) >> 3 & 31));
+            if (v >= lo && v < hi) atomicOr(&sm.special[(v - lo) >> 5], 1u << ((v - lo) & 31));
         }
         __syncthreads();
     }
     const int32_t groups = kLoop ? (a.slice / 8 + kThreads - 1) / kThreads : kGroups;
     const bool greedy = !(temperature > 0.f);
-    const float k = greedy ? 0.f : fminf(1.4426950408889634f / temperature, FLT_MAX);
+    const float k = greedy ? 1.f : fminf(fmaxf(1.4426950408889634f / temperature, 0x1p-149f), FLT_MAX);
 
     float z[kGroups][8];
     float top = -INFINITY;
     if constexpr (kLoop) {
         for (int32_t g = 0; g < groups; ++g) {
-            r.load(g, z[0]);
+            r.whole(g, z[0]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) top = fmaxf(top, z[0][e]);
         }
     } else {
+        uint32_t own = 0;  // bit g: group g goes on the list
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) own |= (r.load(g, z[g]) ? 1u : 0u) << g;
+        uint64_t bits = ~0ull;
+        if (r.mask) {
+            bits = 0;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                const uint32_t b = r.allowed(g);
+                bits |= (uint64_t)b << (8 * g);
+                if (b == 0) own &= ~(1u << g);
+            }
+        }
+        if (__any_sync(0xffffffffu, own != 0)) {
+            const int n = __popc(own);
+            int upto = n;  // of the warp's lanes
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, upto, off);
+                if (lane >= off) upto += y;
+            }
+            const int n_list = __shfl_sync(0xffffffffu, upto, 31), slot = upto - n;
+            for (int from = 0; from < n_list; from += kList) {
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    const int at = slot + __popc(own & ((1u << g) - 1)) - from;
+                    if ((own >> g & 1) && at >= 0 && at < kList) list[warp][at] = (uint8_t)(32 * g + lane);
+                }
+                __syncwarp();
+                if (from + lane < n_list) {
+                    const int id = list[warp][lane];
+                    r.fetch(id >> 5, 32 * warp + (id & 31), fetched[warp][lane]);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    const int at = slot + __popc(own & ((1u << g) - 1)) - from;
+                    if ((own >> g & 1) && at >= 0 && at < kList) {
+                        const float4 x0 = *reinterpret_cast<const float4 *>(&fetched[warp][at][0]), x1 = *reinterpret_cast<const float4 *>(&fetched[warp][at][4]);
+                        z[g][0] = x0.x, z[g][1] = x0.y, z[g][2] = x0.z, z[g][3] = x0.w, z[g][4] = x1.x, z[g][5] = x1.y, z[g][6] = x1.z, z[g][7] = x1.w;
+                    }
+                }
+                __syncwarp();
+            }
+        }
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-            r.load(g, z[g]);
+            if (r.mask) {
+                const uint32_t b = (uint32_t)(bits >> (8 * g));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, z[g][e]);
+                for (int e = 0; e < 8; ++e) z[g][e] = b >> e & 1 ? z[g][e] : -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) top = fmaxf(fmaxf(top, z[g][e]), z[g][e + 1]);  // passes NaN over
         }
     }
-    top = block_max(top, sm.warp);  // of this CTA's tokens
-    // this CTA's sum relative to it, or the first token that has it
+    top = warp_max(top);
+    // the warp's sum relative to it, or the first token that has it
     float sum = 0.f;
     int32_t first = INT32_MAX;
+    const bool plain = top < INFINITY;
+    const float ref = top == -INFINITY ? 0.f : -top;
     const auto take = [&](int32_t g, float (&x)[8]) {
+        if (greedy) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (greedy) {
-                if (x[e] == top && x[e] > -INFINITY) first = min(first, r.token(g, e));
-            } else {
+            for (int e = 0; e < 8; ++e)
+                if (x[e] == top && x[e] > -INFINITY) first = min(first, r.token(g, tid, e));
+        } else if (plain) {
+            float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const float2 y = __fmul2_rn(__fadd2_rn(make_float2(x[e], x[e + 1]), make_float2(ref, ref)), make_float2(k, k));
+                x[e] = fmaxf(fast_exp2(y.x), 0.f), x[e + 1] = fmaxf(fast_exp2(y.y), 0.f);  // NaN becomes 0
+                part = __fadd2_rn(part, make_float2(x[e], x[e + 1]));
+            }
+            sum += part.x + part.y;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
                 x[e] = weight(x[e], top, k);
                 sum += x[e];
             }
@@ -311,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_probs(const 
     };
     if constexpr (kLoop) {
         for (int32_t g = 0; g < groups; ++g) {
-            r.load(g, z[0]);
+            r.whole(g, z[0]);
             take(g, z[0]);
         }
     } else {
@@ -319,41 +443,57 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_probs(const 
         for (int g = 0; g < kGroups; ++g) take(g, z[g]);
     }
     if (greedy)
-        first = block_min(first, sm.warp);
+        first = __reduce_min_sync(0xffffffffu, first);
     else
-        sum = block_sum(sum, sm.warp);
-    float all = top, total = sum, mine = 1.f;
-    if (a.cluster > 1) {
-        cluster_wait();  // every CTA of the cluster has started
-        if (tid < a.cluster)
-            st_cluster_u64(&sm.part[rank], tid, (uint64_t)__float_as_uint(top) << 32 | (greedy ? (uint32_t)first : __float_as_uint(sum)));
-        cluster_arrive();
-        cluster_wait();
-        for (int i = 0; i < a.cluster; ++i) all = fmaxf(all, __uint_as_float((uint32_t)(sm.part[i] >> 32)));
-        total = 0.f;
-        first = INT32_MAX;
-        for (int i = 0; i < a.cluster; ++i) {
-            const float t = __uint_as_float((uint32_t)(sm.part[i] >> 32));
-            if (greedy)
-                first = t == all ? min(first, (int32_t)(uint32_t)sm.part[i]) : first;
-            else
-                total += __uint_as_float((uint32_t)sm.part[i]) * weight(t, all, k);
-        }
-        mine = weight(top, all, k);
-    } else {
-        cluster_wait();
+        sum = warp_sum(sum);
+    cluster_wait();  // every CTA of the cluster has started
+    const uint64_t pair = (uint64_t)__float_as_uint(top) << 32 | (greedy ? (uint32_t)first : __float_as_uint(sum));
+    if (lane < a.cluster) st_cluster_u64(&sm.part[rank * kWarps + warp], lane, pair);
+    cluster_arrive();
+    cluster_wait();
+    // all warps' pairs, kPer of them a lane
+    constexpr int kPer = kMaxCluster * kWarps / 32;
+    const int n_parts = a.cluster * kWarps;
+    uint64_t parts[kPer];
+    float all = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        parts[i] = lane + 32 * i < n_parts ? sm.part[lane + 32 * i] : (uint64_t)0xff800000u << 32;
+        all = fmaxf(all, __uint_as_float((uint32_t)(parts[i] >> 32)));
+    }
+    all = warp_max(all);
+    float total = 0.f;
+    first = INT32_MAX;
+    if (greedy) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (__uint_as_float((uint32_t)(parts[i] >> 32)) == all) first = min(first, (int32_t)(uint32_t)parts[i]);
+        first = __reduce_min_sync(0xffffffffu, first);
+        if (all == -INFINITY) first = INT32_MAX;
+    } else if (all > -INFINITY) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) total += __uint_as_float((uint32_t)parts[i]) * weight(__uint_as_float((uint32_t)(parts[i] >> 32)), all, k);
+        total = warp_sum(total);
     }
     // nothing allowed: no probability at all
-    const float f = total > 0.f ? mine / total : 0.f;
+    const float f = total > 0.f && top > -INFINITY ? weight(top, all, k) / total : 0.f;
     TP *p = static_cast<TP *>(a.p) + row * a.p_stride;
     const auto put = [&](int32_t g, float (&x)[8]) {
+        if (greedy) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = greedy ? (r.token(g, e) == first ? 1.f : 0.f) : x[e] * f;
-        store_probs<TP, kVec>(p, r.token(g, 0), kVec ? 1 : kThreads, hi, x);
+            for (int e = 0; e < 8; ++e) x[e] = r.token(g, tid, e) == first ? 1.f : 0.f;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const float2 y = __fmul2_rn(make_float2(x[e], x[e + 1]), make_float2(f, f));
+                x[e] = y.x, x[e + 1] = y.y;
+            }
+        }
+        store_probs<TP, kVec>(p, r.token(g, tid, 0), kVec ? 1 : kThreads, hi, a.wide, x);
     };
     if constexpr (kLoop) {
         for (int32_t g = 0; g < groups; ++g) {
-            r.load(g, z[0]);
+            r.whole(g, z[0]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) z[0][e] = greedy ? 0.f : weight(z[0][e], top, k);
             put(g, z[0]);
@@ -522,8 +662,10 @@ extern "C" int hswa_logits_probs(int logits_dtype, const void *logits, int64_t l
            (slice_of(a.cluster) > 512 * 8 * 5 || (rows * a.cluster * 2 <= 2 * sms && slice_of(a.cluster) >= 2048)))
         a.cluster *= 2;
     a.slice = slice_of(a.cluster);
+    a.cluster_log2 = a.cluster == 8 ? 3 : a.cluster / 2;
     const bool vec = (x0 & 15) == 0 && (y0 & 15) == 0 && logits_stride * el % 16 == 0 && p_stride * ep % 16 == 0 &&
                      (!counts || (((uintptr_t)counts & 15) == 0 && count_stride % 8 == 0));
+    a.wide = (el == 2 || ((x0 & 31) == 0 && logits_stride % 8 == 0)) && (ep == 2 || ((y0 & 31) == 0 && p_stride % 8 == 0));
     set_last_kernel(vec ? "logits_probs" : "logits_probs_any");
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
