@@ -216,35 +216,90 @@ __device__ __forceinline__ void unpack_bf16x8(const uint4 &c, float *x) {
     }
 }
 
-// FP4 append: a thread per block of 16 elements, K's and V's; neighbouring
-// threads hold neighbouring blocks of a row, then rows of neighbouring heads,
-// so that a warp reads 1 KB runs and writes 256-byte runs of codes.
-__global__ void __launch_bounds__(256) append_kv_fp4_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v,
-                                                            uint2 *kp, uint2 *vp, uint8_t *ks, uint8_t *vs,
-                                                            const int32_t *__restrict__ slots, int64_t n_tokens,
-                                                            int32_t hkv, int32_t page, int32_t blocks,
-                                                            int64_t pool_slots, int *err) {
-    const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-    const int32_t per_tok = hkv * blocks;
-    if (i >= n_tokens * per_tok) return;
-    const int64_t t = i / per_tok;
-    const int32_t r = (int32_t)(i - t * per_tok), g = r / blocks, b = r - g * blocks;
-    const int32_t slot = slots[t];
-    if (slot < 0) return;
-    if (slot >= pool_slots) {
-        set_error(err, HSWA_ERR_BOUNDS);
-        return;
+// Division by a number of the launch: a shift where it is a power of two.
+struct Divisor {
+    uint32_t d;
+    int32_t shift;  // -1: no power of two
+    explicit Divisor(uint32_t x) : d(x), shift(-1) {
+        if ((x & (x - 1)) == 0)
+            for (shift = 0; (1u << shift) < x;) ++shift;
     }
-    const uint4 in[4] = {k[2 * i], k[2 * i + 1], v[2 * i], v[2 * i + 1]};
-    const int64_t at = (((int64_t)(slot / page) * hkv + g) * page + slot % page) * blocks + b;
+    __device__ __forceinline__ uint32_t div(uint32_t x) const { return shift >= 0 ? x >> shift : x / d; }
+};
+
+// The blocks of 16 elements that a CTA of the FP4 kernels moves: those of
+// `tokens` neighbouring tokens, head by head, so that a warp reads runs of blocks
+// on one side and, where the tokens' slots follow each other, writes whole
+// sectors of codes and of scales on the other.
+struct Fp4Blocks {
+    const int32_t *slots;
+    int64_t n_tokens, pool_slots;
+    uint32_t total, hkv;  // blocks per CTA (idle ones of the last CTA among them)
+    Divisor tokens, page, blocks;
+    bool wide;  // bf16 rows start on 32 bytes
+    // Block u of the CTA: where it lies in [T][Hkv][blocks], in the pool (for a
+    // slot that is one), and its slot. False: behind the last token.
+    __device__ __forceinline__ bool at(uint32_t u, int64_t &row, int64_t &pool, int32_t &slot) const {
+        const uint32_t x = blocks.div(u), b = u - x * blocks.d, g = tokens.div(x);
+        const int64_t t = (int64_t)blockIdx.x * tokens.d + (x - g * tokens.d);
+        if (t >= n_tokens) return false;
+        slot = slots[t];
+        row = (t * hkv + g) * blocks.d + b;
+        const uint32_t pg = page.div((uint32_t)slot);
+        pool = (((int64_t)pg * hkv + g) * page.d + ((uint32_t)slot - pg * page.d)) * blocks.d + b;
+        return true;
+    }
+};
+
+// 32 bytes of 16 bf16.
+__device__ __forceinline__ void load_block(const uint4 *p, bool wide, uint4 &lo, uint4 &hi) {
+    if (wide)
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(lo.x), "=r"(lo.y), "=r"(lo.z), "=r"(lo.w), "=r"(hi.x), "=r"(hi.y), "=r"(hi.z), "=r"(hi.w)
+                     : "l"(p));
+    else
+        lo = p[0], hi = p[1];
+}
+__device__ __forceinline__ void store_block(uint4 *p, bool wide, const uint4 &lo, const uint4 &hi) {
+    if (wide)
+        asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(lo.x), "r"(lo.y), "r"(lo.z),
+                     "r"(lo.w), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w), "l"(p)
+                     : "memory");
+    else
+        p[0] = lo, p[1] = hi;
+}
+
+// A thread per block of 16 elements, K's and V's. Memory bounds both kernels:
+// 32768 tokens of 8 heads of 128 stored and read back take 57 us, 0.9 of a plain
+// copy's rate. Two blocks a thread were slower (73; fewer warps in flight), CTAs
+// of 256 threads 64 and of 512 71 (with 128: 63), and registers for 12 CTAs an
+// SM are worth another us.
+constexpr int kFp4Threads = 128;
+
+__global__ void __launch_bounds__(kFp4Threads, 12) append_kv_fp4_kernel(const uint4 *k, const uint4 *v, uint2 *kp, uint2 *vp,
+                                                                    uint8_t *ks, uint8_t *vs, const Fp4Blocks a, int *err) {
+    pdl_wait();
+    for (uint32_t u = threadIdx.x; u < a.total; u += kFp4Threads) {
+        int64_t row, at;
+        int32_t slot;
+        if (!a.at(u, row, at, slot)) continue;
+        uint4 in[4];
+        load_block(k + 2 * row, a.wide, in[0], in[1]);
+        load_block(v + 2 * row, a.wide, in[2], in[3]);
+        if (slot < 0) continue;
+        if (slot >= a.pool_slots) {
+            set_error(err, HSWA_ERR_BOUNDS);
+            continue;
+        }
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        float x[16];
-        unpack_bf16x8(in[2 * which], x);
-        unpack_bf16x8(in[2 * which + 1], x + 8);
-        const uint32_t scale = fp4_scale(amax16(x));
-        (which ? vp : kp)[at] = fp4_codes(x, scale);
-        (which ? vs : ks)[at] = (uint8_t)scale;
+        for (int which = 0; which < 2; ++which) {
+            float x[16];
+            unpack_bf16x8(in[2 * which], x);
+            unpack_bf16x8(in[2 * which + 1], x + 8);
+            const uint32_t scale = fp4_scale(amax16(x));
+            (which ? vp : kp)[at] = fp4_codes(x, scale);
+            (which ? vs : ks)[at] = (uint8_t)scale;
+        }
     }
 }
 
@@ -287,29 +342,27 @@ __device__ __forceinline__ void fp4_block_bf16(uint2 codes, uint8_t scale, uint4
     hi = make_uint4(p[4], p[5], p[6], p[7]);
 }
 
-__global__ void __launch_bounds__(256) read_kv_fp4_kernel(uint4 *__restrict__ k, uint4 *__restrict__ v,
-                                                          const uint2 *__restrict__ kp, const uint2 *__restrict__ vp,
-                                                          const uint8_t *__restrict__ ks, const uint8_t *__restrict__ vs,
-                                                          const int32_t *__restrict__ slots, int64_t n_tokens, int32_t hkv,
-                                                          int32_t page, int32_t blocks, int64_t pool_slots, int *err) {
-    const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-    const int32_t per_tok = hkv * blocks;
-    if (i >= n_tokens * per_tok) return;
-    const int64_t t = i / per_tok;
-    const int32_t r = (int32_t)(i - t * per_tok), g = r / blocks, b = r - g * blocks;
-    const int32_t slot = slots[t];
-    uint4 lo[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, hi[2] = {lo[0], lo[0]};
-    if (slot >= 0 && slot < pool_slots) {
-        const int64_t at = (((int64_t)(slot / page) * hkv + g) * page + slot % page) * blocks + b;
-        const uint2 ck = kp[at], cv = vp[at];
-        const uint8_t sk = ks[at], sv = vs[at];
-        fp4_block_bf16(ck, sk, lo[0], hi[0]);
-        fp4_block_bf16(cv, sv, lo[1], hi[1]);
-    } else if (slot >= 0) {
-        set_error(err, HSWA_ERR_BOUNDS);
+__global__ void __launch_bounds__(kFp4Threads) read_kv_fp4_kernel(uint4 *k, uint4 *v, const uint2 *kp, const uint2 *vp,
+                                                                  const uint8_t *ks, const uint8_t *vs, const Fp4Blocks a,
+                                                                  int *err) {
+    pdl_wait();
+    for (uint32_t u = threadIdx.x; u < a.total; u += kFp4Threads) {
+        int64_t row, at;
+        int32_t slot;
+        if (!a.at(u, row, at, slot)) continue;
+        uint2 code[2] = {make_uint2(0, 0), make_uint2(0, 0)};
+        uint8_t scale[2] = {0, 0};
+        if (slot >= 0 && slot < a.pool_slots)
+            code[0] = kp[at], code[1] = vp[at], scale[0] = ks[at], scale[1] = vs[at];
+        else if (slot >= 0)
+            set_error(err, HSWA_ERR_BOUNDS);
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            uint4 lo, hi;
+            fp4_block_bf16(code[which], scale[which], lo, hi);
+            store_block((which ? v : k) + 2 * row, a.wide, lo, hi);
+        }
     }
-    k[2 * i] = lo[0], k[2 * i + 1] = hi[0];
-    v[2 * i] = lo[1], v[2 * i + 1] = hi[1];
 }
 
 // FP8 pools (d = 128): a warp per (token, kv head), 4 elements a lane; code *
@@ -358,11 +411,22 @@ int64_t pool_slots(const hswa_config &c, const hswa_layer *layer) {
     return (int64_t)(layer->kind == HSWA_KIND_SWA ? c.swa_pages : c.full_pages) * c.page_size;
 }
 
-// FP4 rows are whole blocks, codes 8 bytes each; a launch has at most 2^31 - 1 CTAs.
-bool fp4_layout_ok(const hswa_config &c, const hswa_layer *layer, int n_tokens) {
+// FP4 rows are whole blocks, codes 8 bytes each; a CTA's blocks are counted in 32 bits.
+bool fp4_layout_ok(const hswa_config &c, const hswa_layer *layer) {
     return c.head_dim % kFp4Block == 0 && (((uintptr_t)layer->k_pool | (uintptr_t)layer->v_pool) & 7) == 0 &&
-           (int64_t)n_tokens * c.n_kv_heads * (c.head_dim / kFp4Block) / 256 < INT32_MAX;
+           (int64_t)c.n_kv_heads * (c.head_dim / kFp4Block) < (1 << 30);
 }
+
+// As many tokens per CTA as its threads take at once; one, where that leaves SMs idle.
+Fp4Blocks fp4_blocks(const hswa_config &c, const hswa_layer *layer, const int32_t *d_slots, int n_tokens, const void *k,
+                     const void *v) {
+    const int64_t blocks = c.head_dim / kFp4Block, per_tok = c.n_kv_heads * blocks;
+    const int64_t t = std::max<int64_t>(1, std::min<int64_t>(kFp4Threads / per_tok, n_tokens / std::max(1, sm_count())));
+    return {d_slots, n_tokens, pool_slots(c, layer), (uint32_t)(t * per_tok), (uint32_t)c.n_kv_heads, Divisor((uint32_t)t),
+            Divisor((uint32_t)c.page_size), Divisor((uint32_t)blocks), (((uintptr_t)k | (uintptr_t)v) & 31) == 0};
+}
+
+dim3 fp4_grid(const Fp4Blocks &a) { return dim3((unsigned)((a.n_tokens + a.tokens.d - 1) / a.tokens.d)); }
 
 }  // namespace
 }  // namespace hswa
@@ -391,16 +455,14 @@ extern "C" int hswa_append_kv(const hswa_pool *pool, const hswa_layer *layer, co
     }
     if (c.dtype == HSWA_DTYPE_FP4) {
         if (!layer->k_scale || !layer->v_scale) return HSWA_ERR_INVALID_ARG;
-        if (!fp4_layout_ok(c, layer, n_tokens) || !aligned16(k) || !aligned16(v)) return HSWA_ERR_UNSUPPORTED;
+        if (!fp4_layout_ok(c, layer) || !aligned16(k) || !aligned16(v)) return HSWA_ERR_UNSUPPORTED;
         if (n_tokens == 0) return HSWA_OK;
-        const int32_t blocks = c.head_dim / kFp4Block;
-        const int64_t work = (int64_t)n_tokens * c.n_kv_heads * blocks;
+        const Fp4Blocks a = fp4_blocks(c, layer, d_slots, n_tokens, k, v);
         set_last_kernel("append_kv_fp4");
-        append_kv_fp4_kernel<<<(unsigned)((work + 255) / 256), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-            (const uint4 *)k, (const uint4 *)v, (uint2 *)layer->k_pool, (uint2 *)layer->v_pool, (uint8_t *)layer->k_scale,
-            (uint8_t *)layer->v_scale, d_slots, n_tokens, c.n_kv_heads, c.page_size, blocks, pool_slots(c, layer),
-            error_word());
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_pdl(append_kv_fp4_kernel, fp4_grid(a), dim3(kFp4Threads), 0,
+                                         reinterpret_cast<cudaStream_t>(stream), (const uint4 *)k, (const uint4 *)v,
+                                         (uint2 *)layer->k_pool, (uint2 *)layer->v_pool, (uint8_t *)layer->k_scale,
+                                         (uint8_t *)layer->v_scale, a, error_word());
         return e == cudaSuccess ? HSWA_OK : cuda_fail(e, "append_kv_fp4");
     }
     const int64_t row_bytes = (int64_t)c.head_dim * esize(c);
@@ -427,25 +489,27 @@ extern "C" int hswa_read_kv(const hswa_pool *pool, const hswa_layer *layer, cons
     const bool fp8 = c.dtype == HSWA_DTYPE_FP8_E4M3, fp4 = c.dtype == HSWA_DTYPE_FP4;
     if ((fp8 || fp4) && (!layer->k_scale || !layer->v_scale)) return HSWA_ERR_INVALID_ARG;
     const int64_t row_bytes = (int64_t)c.head_dim * esize(c);
-    if (!aligned16(k) || !aligned16(v) || (fp8 && c.head_dim != 128) || (fp4 && !fp4_layout_ok(c, layer, n_tokens)) ||
+    if (!aligned16(k) || !aligned16(v) || (fp8 && c.head_dim != 128) || (fp4 && !fp4_layout_ok(c, layer)) ||
         (!fp8 && !fp4 && (row_bytes % 16 || !aligned16(layer->k_pool) || !aligned16(layer->v_pool))))
         return HSWA_ERR_UNSUPPORTED;
-    const int32_t units = fp8 ? 32 : fp4 ? c.head_dim / kFp4Block : (int32_t)(row_bytes / 16);
+    const int32_t units = fp8 ? 32 : (int32_t)(row_bytes / 16);
     const int64_t ctas = ((int64_t)n_tokens * c.n_kv_heads * units + 255) / 256;
     if (ctas > INT32_MAX) return HSWA_ERR_UNSUPPORTED;
     if (n_tokens == 0) return HSWA_OK;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     set_last_kernel(fp8 ? "read_kv_fp8" : fp4 ? "read_kv_fp4" : "read_kv");
+    if (fp4) {
+        const Fp4Blocks a = fp4_blocks(c, layer, d_slots, n_tokens, k, v);
+        const cudaError_t e = launch_pdl(read_kv_fp4_kernel, fp4_grid(a), dim3(kFp4Threads), 0, st, (uint4 *)k, (uint4 *)v,
+                                         (const uint2 *)layer->k_pool, (const uint2 *)layer->v_pool,
+                                         (const uint8_t *)layer->k_scale, (const uint8_t *)layer->v_scale, a, error_word());
+        return e == cudaSuccess ? HSWA_OK : cuda_fail(e, "hswa_read_kv");
+    }
     if (fp8)
         read_kv_fp8_kernel<<<(unsigned)ctas, 256, 0, st>>>((uint2 *)k, (uint2 *)v, (const uint8_t *)layer->k_pool,
                                                            (const uint8_t *)layer->v_pool, layer->k_scale, layer->v_scale,
                                                            d_slots, n_tokens, c.n_kv_heads, c.page_size,
                                                            pool_slots(c, layer), error_word());
-    else if (fp4)
-        read_kv_fp4_kernel<<<(unsigned)ctas, 256, 0, st>>>((uint4 *)k, (uint4 *)v, (const uint2 *)layer->k_pool,
-                                                           (const uint2 *)layer->v_pool, (const uint8_t *)layer->k_scale,
-                                                           (const uint8_t *)layer->v_scale, d_slots, n_tokens, c.n_kv_heads,
-                                                           c.page_size, units, pool_slots(c, layer), error_word());
     else
         read_kv_kernel<<<(unsigned)ctas, 256, 0, st>>>((chunk_t *)k, (chunk_t *)v, (const chunk_t *)layer->k_pool,
                                                        (const chunk_t *)layer->v_pool, d_slots, n_tokens, c.n_kv_heads,

@@ -1170,7 +1170,7 @@ struct DecodeTcSmem {
     static constexpr bool kTcQ = true;
     static constexpr bool kWeights = false;
     static constexpr bool kQTmem = false;  // QK reads q from shared memory
-    static constexpr int kGroups = 0, kConvThreads = 1, kConvWarp = 7;  // no converters
+    [[maybe_unused]] static constexpr int kGroups = 0, kConvThreads = 1, kConvWarp = 7;  // no converters
     static constexpr int kThreads = 224;
     static constexpr uint32_t kQHalfBytes = 128 * 128;  // 128 rows x 64 columns of 16-bit values
     uint8_t k[kStages][kPageHeadBytes];                // [d half][64 keys][128 B], 128-byte swizzle

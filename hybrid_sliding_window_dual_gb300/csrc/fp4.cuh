@@ -18,6 +18,7 @@ namespace hswa {
 
 constexpr int kFp4Block = 16;
 constexpr float kFp4MaxScale = 10240.f;  // 6 times it is an f16; the next scale's would not be
+constexpr uint32_t kFp4MaxScaleByte = 0xe2;
 
 // The 8 codes of a word as f16 pairs: elements (0, 1), (2, 3), (4, 5), (6, 7).
 __device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t &p0, uint32_t &p1, uint32_t &p2, uint32_t &p3) {
@@ -62,27 +63,37 @@ __device__ __forceinline__ uint32_t fp4_scale(float amax) {
 }
 
 // x / scale for a code: the nearest E2M1 value to it is that of the exact
-// quotient. q + (x - s q) / s is x / s to far less than a step of fp32, so that
+// quotient. q - (s q - x) / s is x / s to far less than a step of fp32, so that
 // it rounds to a border between codes only if x / s is on one: such borders
 // times a scale have at most 7 significant bits, and no other fp32 x is nearer
-// to that product than half a step of the quotient's. The clamp to the largest
-// code keeps infinities out of the remainder.
+// to that product than half a step of the quotient's. A -0 keeps its sign. x
+// is finite, and no more than a few scales unless the scale is the largest.
 struct Fp4Divider {
-    float s, r, top;
+    float s, r;
     __device__ __forceinline__ explicit Fp4Divider(uint32_t scale) : s(scale_value((uint8_t)scale)) {
         r = __frcp_rn(s);
-        top = 6.f * s;
     }
     __device__ __forceinline__ float operator()(float x) const {
-        const float v = fminf(fmaxf(x, -top), top), q = v * r;
-        return copysignf(fmaf(fmaf(-s, q, v), r, q), v);  // -0 keeps its sign
+        const float q = x * r;
+        return fmaf(-fmaf(s, q, -x), r, q);
     }
 };
 
+// Under the largest scale values past 6 of it, infinities among them, become
+// 6 of it. (The conversion saturates, but the remainder of an infinity is none.)
+__device__ __forceinline__ float fp4_clamp(float x) { return fminf(fmaxf(x, -6.f * kFp4MaxScale), 6.f * kFp4MaxScale); }
+
 // 8 values as codes under a scale byte: the nearest E2M1 value to x / scale
 // (ties to the even code), at most 6; all codes 0 under scale 0.
-__device__ __forceinline__ uint32_t fp4_codes8(const float *x, uint32_t scale) {
+__device__ __forceinline__ uint32_t fp4_codes8(const float *in, uint32_t scale) {
     if (scale == 0) return 0;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = in[i];
+    if (__builtin_expect(scale == kFp4MaxScaleByte, 0)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = fp4_clamp(x[i]);
+    }
     const Fp4Divider div(scale);
     uint32_t w = 0;
 #pragma unroll
@@ -98,7 +109,7 @@ __device__ __forceinline__ uint2 fp4_codes(const float (&x)[16], uint32_t scale)
 // One value's code.
 __device__ __forceinline__ uint32_t fp4_code(float x, uint32_t scale) {
     if (scale == 0) return 0;
-    return __nv_cvt_float2_to_fp4x2(make_float2(Fp4Divider(scale)(x), 0.f), __NV_E2M1, cudaRoundNearest) & 15;
+    return __nv_cvt_float2_to_fp4x2(make_float2(Fp4Divider(scale)(scale == kFp4MaxScaleByte ? fp4_clamp(x) : x), 0.f), __NV_E2M1, cudaRoundNearest) & 15;
 }
 
 __device__ __forceinline__ float amax16(const float (&x)[16]) {

@@ -514,9 +514,93 @@ struct CountArgs {
 };
 
 constexpr int kCountSlice = 8192, kCountThreads = 512;
+constexpr int kCountAhead = 8;  // tokens of a thread in flight
 
-// A CTA per sequence and slice of the vocabulary: it goes through the
-// sequence's tokens, counts its own in shared memory (bit 31: in the prompt)
+// A cluster per sequence. Each CTA reads an eighth of the tokens and counts them
+// where they belong: 64 tokens of the vocabulary in turn lie with each CTA, in its
+// shared memory, so that what it writes back are whole 128-byte lines. kPacked:
+// at most 32767 tokens, whose counts need 15 bits, as the result has them. No
+// order of the additions shows in the result.
+template <bool kPacked>
+__global__ void __launch_bounds__(kCountThreads) count_cluster(const CountArgs a) {
+    extern __shared__ __align__(16) uint32_t counted[];
+    const uint32_t rank = blockIdx.x % kMaxCluster;
+    const int64_t s = blockIdx.x / kMaxCluster;
+    const int32_t mine = (a.vocab + 511) / 512 * 64;  // counts of this CTA
+    for (int i = threadIdx.x; i < mine / (kPacked ? 8 : 4); i += kCountThreads)
+        reinterpret_cast<uint4 *>(counted)[i] = make_uint4(0, 0, 0, 0);
+    cluster_arrive();  // nobody counts before all are zero
+    pdl_wait();
+    pdl_launch_dependents();
+    const int32_t *tokens = a.tokens + s * a.token_stride;
+    const int32_t prompt = a.n_prompt ? a.n_prompt[s] : 0;
+    bool waited = false;
+    for (int32_t i0 = rank * kCountThreads + threadIdx.x; i0 - (int32_t)threadIdx.x < a.n_tokens;) {
+        int32_t v[kCountAhead];
+#pragma unroll
+        for (int e = 0; e < kCountAhead; ++e) {
+            const int64_t i = i0 + (int64_t)e * kCountThreads * kMaxCluster;
+            v[e] = i < a.n_tokens ? tokens[i] : -1;
+        }
+        if (!waited) cluster_wait();
+        waited = true;
+#pragma unroll
+        for (int e = 0; e < kCountAhead; ++e) {
+            const int64_t i = i0 + (int64_t)e * kCountThreads * kMaxCluster;
+            if (v[e] >= a.vocab) set_error(a.err, HSWA_ERR_BOUNDS);
+            if (v[e] < 0 || v[e] >= a.vocab) continue;
+            const uint32_t at = (v[e] >> 9) * 64 + (v[e] & 63);
+            const uint32_t to = cluster_addr(counted + (kPacked ? at / 2 : at), v[e] >> 6 & 7);
+            const uint32_t shift = kPacked ? 16 * (at & 1) : 0;
+            if (i < prompt)
+                asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(to), "r"(kPacked ? 0x8000u << shift : 1u << 31) : "memory");
+            else
+                asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(to), "r"(1u << shift) : "memory");
+        }
+        const int64_t next = i0 + (int64_t)kCountAhead * kCountThreads * kMaxCluster;
+        if (next - threadIdx.x >= a.n_tokens) break;
+        i0 = (int32_t)next;
+    }
+    if (!waited) cluster_wait();
+    cluster_arrive();
+    cluster_wait();
+    uint16_t *row = a.counts + s * a.count_stride;
+    const bool vec = ((uintptr_t)a.counts & 15) == 0 && a.count_stride % 8 == 0;
+    for (int u = threadIdx.x; u < mine / 8; u += kCountThreads) {
+        const int32_t v = (u >> 3) * 512 + rank * 64 + (u & 7) * 8;
+        if (v >= a.vocab) continue;
+        uint32_t x[4];  // 8 counts, 15 bits and the prompt's
+        if constexpr (kPacked) {
+            const uint4 q = reinterpret_cast<const uint4 *>(counted)[u];
+            x[0] = q.x, x[1] = q.y, x[2] = q.z, x[3] = q.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint2 q = reinterpret_cast<const uint2 *>(counted)[4 * u + e];
+                x[e] = (min(q.x & 0x7fffffffu, 0x7fffu) | q.x >> 31 << 15) | (min(q.y & 0x7fffffffu, 0x7fffu) | q.y >> 31 << 15) << 16;
+            }
+        }
+        if (a.clear && vec && v + 8 <= a.vocab) {
+            *reinterpret_cast<uint4 *>(row + v) = make_uint4(x[0], x[1], x[2], x[3]);
+            continue;
+        }
+        if (!a.clear && (x[0] | x[1] | x[2] | x[3]) == 0) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (v + e >= a.vocab) continue;
+            uint32_t y = x[e / 2] >> (16 * (e & 1)) & 0xffff;
+            if (!a.clear) {
+                if (y == 0) continue;
+                const uint32_t was = row[v + e];
+                y = ((y | was) & 0x8000) | min((y & 0x7fff) + (was & 0x7fff), 0x7fffu);
+            }
+            row[v + e] = (uint16_t)y;
+        }
+    }
+}
+
+// The same for vocabularies whose counts a cluster does not hold. A CTA per
+// sequence and slice of the vocabulary: it goes through the sequence's tokens, counts its own in shared memory (bit 31: in the prompt)
 // and writes the slice. No order of the additions shows in the result.
 __global__ void __launch_bounds__(kCountThreads) count_slices(const CountArgs a) {
     __shared__ uint32_t n[kCountSlice];
@@ -527,16 +611,15 @@ __global__ void __launch_bounds__(kCountThreads) count_slices(const CountArgs a)
     __syncthreads();
     const int32_t *tokens = a.tokens + s * a.token_stride;
     const int32_t prompt = a.n_prompt ? a.n_prompt[s] : 0;
-    constexpr int kAhead = 8;
-    for (int32_t i0 = threadIdx.x; i0 < a.n_tokens; i0 += kCountThreads * kAhead) {
-        int32_t v[kAhead];
+    for (int32_t i0 = threadIdx.x; i0 < a.n_tokens; i0 += kCountThreads * kCountAhead) {
+        int32_t v[kCountAhead];
 #pragma unroll
-        for (int e = 0; e < kAhead; ++e) {
+        for (int e = 0; e < kCountAhead; ++e) {
             const int32_t i = i0 + e * kCountThreads;
             v[e] = i < a.n_tokens ? tokens[i] : -1;
         }
 #pragma unroll
-        for (int e = 0; e < kAhead; ++e) {
+        for (int e = 0; e < kCountAhead; ++e) {
             const int32_t i = i0 + e * kCountThreads;
             if (v[e] >= a.vocab && lo == 0) set_error(a.err, HSWA_ERR_BOUNDS);
             if (v[e] < lo || v[e] - lo >= size) continue;
@@ -581,6 +664,31 @@ __global__ void __launch_bounds__(256) count_few(const CountArgs a) {
 }
 
 constexpr int kFewTokens = 64;  // of a sequence
+
+constexpr size_t kCountSmem = 96 << 10;  // at most, of a CTA: two on an SM
+
+// Bytes of shared memory of a CTA of the cluster.
+size_t count_smem(int vocab, bool packed) { return (size_t)(vocab + 511) / 512 * 64 * (packed ? 2 : 4); }
+
+template <bool kPacked>
+cudaError_t launch_count(const CountArgs &a, cudaStream_t st) {
+    static int setup[kMaxDevices] = {};
+    if (kernel_setup(count_cluster<kPacked>, kCountSmem, kCountThreads, setup) < 0) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.n_seqs * kMaxCluster);
+    cfg.blockDim = dim3(kCountThreads);
+    cfg.dynamicSmemBytes = count_smem(a.vocab, kPacked);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kMaxCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, count_cluster<kPacked>, a);
+}
 
 template <typename TL, typename TP, bool kVec, int kThreads, int kGroups, bool kLoop>
 cudaError_t launch(const ProbsArgs &a, int64_t rows, cudaStream_t st) {
@@ -701,6 +809,10 @@ extern "C" int hswa_count_tokens(uint16_t *counts, int64_t count_stride, const i
     if (!clear && n_tokens <= kFewTokens) {
         set_last_kernel("count_few");
         e = launch_pdl(count_few, dim3((unsigned)(((int64_t)n_seqs * n_tokens + 255) / 256)), dim3(256), 0, st, a);
+    } else if (const bool packed = n_tokens <= 0x7fff;
+               count_smem(vocab, packed) <= kCountSmem && n_seqs <= INT32_MAX / kMaxCluster) {
+        set_last_kernel("count_cluster");
+        e = packed ? launch_count<true>(a, st) : launch_count<false>(a, st);
     } else {
         set_last_kernel("count_slices");
         e = launch_pdl(count_slices, dim3((unsigned)(n_seqs * slices)), dim3(kCountThreads), 0, st, a);

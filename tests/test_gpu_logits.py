@@ -230,7 +230,7 @@ def count(tokens, n_prompt, V, before=None, clear=True, pad=0, expect=0):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("pad", [0, 3])
-@pytest.mark.parametrize("S,n,V", [(1, 1, 1), (3, 4, 17), (5, 64, 8192), (5, 65, 8193), (2, 1000, 20000), (64, 4, 1000), (3, 40000, 131072), (2, 3, 1 << 20)])
+@pytest.mark.parametrize("S,n,V", [(1, 1, 1), (3, 4, 17), (5, 64, 8192), (5, 65, 8193), (2, 1000, 20000), (64, 4, 1000), (3, 40000, 131072), (2, 3, 1 << 20), (2, 5000, 393217), (2, 40000, 200000), (2, 5000, 390000)])
 def test_count_tokens(S, n, V, pad):
     rng = np.random.default_rng(S + n)
     tokens = np.where(rng.random((S, n)) < 0.1, -1, np.minimum(rng.exponential(V / 50 + 1, (S, n)), V - 1)).astype(np.int32)
@@ -247,10 +247,11 @@ def test_count_tokens(S, n, V, pad):
 @pytest.mark.gpu
 def test_count_tokens_many_of_one_and_outside():
     """More than 32767 times one token; tokens past the vocabulary."""
-    tokens = np.full((2, 40000), 5, np.int32)
     zero = torch.zeros(2, 300, dtype=torch.int16, device="cuda")
     for clear in (True, False):
-        count(tokens, None, 300, zero, clear)
+        for n in (40000, 32768, 32767):
+            count(np.full((2, n), 5, np.int32), None, 300, zero, clear)
+            count(np.full((2, n), 4, np.int32), np.array([1, n], np.int32), 300, zero, clear)
         few = np.array([[299, 300, 2, 2, 2], [1 << 30, -(1 << 31), 0, 0, 1]], np.int32)
         count(few, np.array([3, 9], np.int32), 300, zero, clear, expect=H.HSWA_ERR_BOUNDS)
     empty = torch.empty(2, 0, dtype=torch.int32, device="cuda")
