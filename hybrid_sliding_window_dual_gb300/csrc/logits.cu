@@ -61,6 +61,24 @@ __device__ __forceinline__ void store8(float *p, bool wide, const float (&x)[8])
     }
 }
 
+// Loads where `on` says so, x as it was otherwise. Without branches, so that a
+// thread has those of all its groups in flight.
+__device__ __forceinline__ void load8_if(bool on, const float *p, bool wide, float (&x)[8]) {
+    asm volatile("{\n\t.reg .pred w, n;\n\t.reg .b32 f;\n\t"
+                 "and.b32 f, %9, %10;\n\tsetp.ne.u32 w, f, 0;\n\t"
+                 "not.b32 f, %10;\n\tand.b32 f, f, %9;\n\tand.b32 f, f, 1;\n\tsetp.ne.u32 n, f, 0;\n\t"
+                 "@w ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+                 "@n ld.global.v4.f32 {%0, %1, %2, %3}, [%8];\n\t"
+                 "@n ld.global.v4.f32 {%4, %5, %6, %7}, [%8 + 16];\n\t}"
+                 : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7])
+                 : "l"(p), "r"((uint32_t)on), "r"((uint32_t)wide));
+}
+__device__ __forceinline__ void load16b_if(bool on, const void *p, uint32_t (&x)[4]) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t@q ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3])
+                 : "l"(p), "r"((uint32_t)on));
+}
+
 template <typename T>
 __device__ __forceinline__ float as_float(T x);
 template <>
@@ -168,6 +186,65 @@ struct ProbsRow {
             }
         }
         return any != 0;
+    }
+
+    // load() for all groups of the thread whose bits (8 a group) are not all 0, the
+    // others' z being -inf: bit k of the result is group k's.
+    template <int kGroups>
+    __device__ __forceinline__ uint32_t load_all(uint64_t bits, float (&z)[kGroups][8]) const {
+        uint32_t own = 0;
+        if constexpr (kVec) {
+            uint32_t on = 0;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+                on |= (token(g, threadIdx.x, 8) <= hi && (bits >> (8 * g) & 0xff) ? 1u : 0u) << g;
+            const auto occurred = [&] {
+                if (!counts) return;
+                uint32_t n[kGroups][4];
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    n[g][0] = n[g][1] = n[g][2] = n[g][3] = 0;
+                    load16b_if(on >> g & 1, counts + token(g, threadIdx.x, 0), n[g]);
+                }
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) own |= (n[g][0] | n[g][1] | n[g][2] | n[g][3] ? 1u : 0u) << g;
+            };
+            if constexpr (sizeof(TL) == 4) {
+                occurred();  // first: registers for both are not there
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) z[g][e] = -INFINITY;
+                    load8_if(on >> g & 1, reinterpret_cast<const float *>(logits + token(g, threadIdx.x, 0)), a.wide, z[g]);
+                }
+            } else {
+                uint32_t x[kGroups][4];
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    x[g][0] = x[g][1] = x[g][2] = x[g][3] = 0xff80ff80;  // -inf
+                    load16b_if(on >> g & 1, logits + token(g, threadIdx.x, 0), x[g]);
+                }
+                occurred();
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[g][2 * e] = __uint_as_float(x[g][e] << 16), z[g][2 * e + 1] = __uint_as_float(x[g][e] & 0xffff0000u);
+            }
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                const int32_t v0 = token(g, threadIdx.x, 0);
+                if (specials && (on >> g & 1)) own |= (sm.special[(v0 - lo) >> 5] >> ((v0 - lo) & 31) & 0xff ? 1u : 0u) << g;
+                if (v0 < hi && v0 + 8 > hi && (bits >> (8 * g) & 0xff)) own |= (load(g, z[g]) ? 1u : 0u) << g;  // the row's last
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) z[g][e] = -INFINITY;
+                if (bits >> (8 * g) & 0xff) own |= (load(g, z[g]) ? 1u : 0u) << g;
+            }
+        }
+        return own;
     }
 
     // z of group k of thread t into z8 (shared memory), each token with what it needs.
@@ -350,19 +427,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_probs(const 
             for (int e = 0; e < 8; ++e) top = fmaxf(top, z[0][e]);
         }
     } else {
-        uint32_t own = 0;  // bit g: group g goes on the list
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) own |= (r.load(g, z[g]) ? 1u : 0u) << g;
         uint64_t bits = ~0ull;
         if (r.mask) {
             bits = 0;
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                const uint32_t b = r.allowed(g);
-                bits |= (uint64_t)b << (8 * g);
-                if (b == 0) own &= ~(1u << g);
-            }
+            for (int g = 0; g < kGroups; ++g) bits |= (uint64_t)r.allowed(g) << (8 * g);
         }
+        const uint32_t own = r.load_all(bits, z);  // bit g: group g goes on the list
         if (__any_sync(0xffffffffu, own != 0)) {
             const int n = __popc(own);
             int upto = n;  // of the warp's lanes
