@@ -148,6 +148,11 @@ class DualPoolSession:
 
     def read(self, layer, d_slots, k, v):
         """K and V rows at slots as values: k, v [T, n_kv_heads, head_dim]."""
+        dtype = torch.bfloat16 if self.fp8 or self.fp4 else self.k[layer].dtype
+        shape = (d_slots.shape[0], self.cfg.n_kv_heads, self.cfg.head_dim)
+        for x in (k, v):
+            if x.shape != shape or x.dtype != dtype or not x.is_contiguous():
+                raise ValueError("k and v must be contiguous rows of the pool's values, one per slot")
         B.hswa_read_kv(self.pool, self.layers[layer], d_slots, d_slots.shape[0], k, v, self.stream)
 
     def rope_append(self, layer, rope, q, k, v, d_pos, d_slots, q_out):
@@ -206,6 +211,8 @@ class DualPoolSession:
             raise ValueError("counts must hold a row of 16-bit values per sequence")
         if tokens.dtype != torch.int32 or (n > 1 and tokens.stride(1) != 1):
             raise ValueError("tokens must be rows of int32")
+        if n_prompt is not None and (n_prompt.dtype != torch.int32 or n_prompt.shape != (n_seqs,) or not n_prompt.is_contiguous()):
+            raise ValueError("n_prompt must hold an int32 per sequence")
         vocab = counts.shape[1]
         B.hswa_count_tokens(counts, counts.stride(0) if n_seqs > 1 else vocab, tokens, tokens.stride(0) if n_seqs > 1 else n,
                             n_prompt, n_seqs, n, vocab, clear, self.stream)
@@ -223,14 +230,16 @@ class DualPoolSession:
             raise ValueError("counts must hold a row of 16-bit values per sequence")
         if (bias_token is None) != (bias is None) or (bias is not None and bias.shape != bias_token.shape):
             raise ValueError("a bias for each token of the list")
-        for x, shape in ((params, (n_seqs, 4)), (d_draft, (n_seqs, n_tok - 1)), (bias_token, (n_seqs, 0 if bias is None else bias.shape[1]))):
-            if x is not None and (x.shape != shape or not x.is_contiguous()):
-                raise ValueError("params, drafts and biases must be contiguous rows, one per sequence")
+        n_bias = 0 if bias is None else bias.shape[1]
+        for x, shape, of in ((params, (n_seqs, 4), torch.float32), (d_draft, (n_seqs, n_tok - 1), torch.int32), (bias_token, (n_seqs, n_bias), torch.int32),
+                             (bias, (n_seqs, n_bias), torch.float32)):
+            if x is not None and (x.shape != shape or x.dtype != of or not x.is_contiguous()):
+                raise ValueError("params and biases (float32), drafts and biased tokens (int32) must be contiguous rows, one per sequence")
         if mask is not None and (mask.dtype.itemsize != 4 or mask.shape != (n_seqs * n_tok, -(-vocab // 32)) or (mask.shape[1] > 1 and mask.stride(1) != 1)):
             raise ValueError("mask must hold a row of 32-bit words per query token")
         B.hswa_logits_probs(dtype[logits.dtype], logits, self._row_stride(logits), dtype[p.dtype], p, self._row_stride(p),
                             params, counts, 0 if counts is None else counts.stride(0) if n_seqs > 1 else vocab, d_draft,
-                            bias_token, bias, 0 if bias is None else bias.shape[1], mask,
+                            bias_token, bias, n_bias, mask,
                             0 if mask is None else mask.stride(0) if mask.shape[0] > 1 else mask.shape[1], n_seqs, n_tok,
                             vocab, self.stream)
 

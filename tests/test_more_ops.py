@@ -251,11 +251,19 @@ def test_session_shapes():
     for args in (dict(logits=logits.double(), p=logits), dict(logits=logits, p=f(2, 3, 49)), dict(logits=logits, p=logits, params=f(2, 3)), dict(logits=logits, p=logits, counts=f(2, 50, **i32)),
                  dict(logits=logits, p=logits, counts=f(3, 50, **i16)), dict(logits=logits, p=logits, counts=f(2, 100, **i16)[:, ::2]), dict(logits=logits, p=logits, d_draft=f(2, 3, **i32)),
                  dict(logits=logits, p=logits, bias_token=f(2, 4, **i32)), dict(logits=logits, p=logits, bias_token=f(2, 4, **i32), bias=f(2, 5)),
-                 dict(logits=logits, p=logits, mask=f(2, 2, **i32)), dict(logits=logits, p=logits, mask=f(6, 3, **i32)), dict(logits=f(2, 3, 100)[:, :, ::2], p=logits)):
+                 dict(logits=logits, p=logits, mask=f(2, 2, **i32)), dict(logits=logits, p=logits, mask=f(6, 3, **i32)), dict(logits=f(2, 3, 100)[:, :, ::2], p=logits),
+                 dict(logits=logits, p=logits, params=f(2, 4).double()), dict(logits=logits, p=logits, d_draft=f(2, 2).long()),
+                 dict(logits=logits, p=logits, bias_token=f(2, 4).long(), bias=f(2, 4)), dict(logits=logits, p=logits, bias_token=f(2, 4, **i32), bias=f(2, 4).half())):
         with pytest.raises(ValueError):
             s.probs(**args)
     for counts, tokens in ((f(2, 50, **i32), f(2, 7, **i32)), (f(3, 50, **i16), f(2, 7, **i32)), (f(2, 50, **i16), f(2, 7)), (f(2, 100, **i16)[:, ::2], f(2, 7, **i32)),
                            (f(2, 50, **i16), f(2, 14, **i32)[:, ::2])):
         with pytest.raises(ValueError):
             s.count_tokens(counts, tokens)
+    for prompt in (f(2), f(3, **i32), f(4, **i32)[::2]):
+        with pytest.raises(ValueError):
+            s.count_tokens(f(2, 50, **i16), f(2, 7, **i32), prompt)
+    for k, v in ((f(3, 2, 32), f(3, 2, 32)), (f(3, 2, 32).bfloat16(), f(2, 2, 32).bfloat16()), (f(3, 32, 2).bfloat16().transpose(1, 2), f(3, 2, 32).bfloat16())):
+        with pytest.raises(ValueError):
+            s.read(0, f(3, **i32), k, v)
     s.close()
