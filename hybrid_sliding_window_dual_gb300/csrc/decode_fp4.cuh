@@ -1,33 +1,39 @@
-// Decode over FP4 pools (d = 128, 8 query heads per kv head, page 64): part of
-// decode.cu, whose plan, partial records and merge it shares.
+// Decode of 1 to 4 tokens over FP4 pools (d = 128, 8 query heads per kv head,
+// page 64): part of decode.cu, whose plan, partial records and merge it shares.
 //
-// The bytes of a page and kv head are 9 KB, 1.83 times fewer than in FP8, and
-// the work to turn codes into MMA operands is the same, so that here the
-// instructions of an element, not the loads, decide how near the kernel comes
-// to the memory's rate. Every choice below saves some:
+// A page and kv head are 9 KB, 1.83 times less than in FP8, and the work to
+// turn codes into MMA operands is the same, so that here the instructions of an
+// element, not the loads, decide how near the kernel comes to the memory's rate:
+// conversions, their products with scales, and the MMAs, which an SM's quarter
+// issues one after the other (64 sequences of 1K to 32K tokens, one token each:
+// 209 us, 0.9 of a plain copy's rate; four each 570, where the MMAs alone are
+// 240). Every choice below saves some; times are that first case's.
 //   * A warp is a worker of its own. It takes an equal share of the units (a
-//     page of a kv head), streams them through its own ring of kFp4Stages
-//     stages and leaves its own partial records: no barriers between warps,
-//     no producer, one wait for 64 keys.
+//     page of a kv head), streams them through its own ring of kParts parts
+//     and leaves its own partial records: no barriers between warps, no
+//     producer. 12 workers on an SM are best; with 8 an exposed latency shows,
+//     16 spill.
+//   * Parts come by cp.async of all lanes, 16 bytes each, waited for by count
+//     (an elected lane's bulk copies and a barrier per part: 247 us against
+//     236). A unit's descriptor is made once, 8 units at a time, a lane each.
 //   * Codes become f16 pairs by the conversion instruction, two at a time, and
 //     are multiplied by their block's scale as pairs, which is exact (see
-//     fp4.cuh). No layout change follows: both pools keep a token's codes in a
-//     row, and the MMAs are arranged so that those pairs are operands as they
-//     stand.
-//   * S = Q K^T: keys are the columns of B. Lane (g, t) holds 32 d's of one
-//     key per 8-key tile (one 16-byte load, two scales); the contraction takes
+//     fp4.cuh).
+//   * Both pools keep a token's codes in a row. S: lane (g, t) holds 32 d's of
+//     one key per 8 keys (one 16-byte load, two scales); the contraction takes
 //     d = 32 t + 4 s + 0..3 in step s from lane t, and Q's fragments follow.
-//   * O += P V, one token: a pair holds two d's of one key where B wants two
-//     rows of the contraction. So the contraction runs over (key, parity of
-//     d): 8 keys a step, and the rows of the tile are (head, parity): the
-//     A operand is P where the parities agree and 0 elsewhere, which makes the
-//     MMA's 16 rows useful with 8 heads. Lane (g, t) then holds head g and
-//     d = 32 t .. 32 t + 31 of O.
-//   * Two tokens: the 16 rows are (token, head), and the pairs of two keys are
-//     turned round by two byte permutes.
-//   * S leaves each lane two keys of a tile, and the same two are the keys of
-//     its A and B fragments of PV: P needs no shuffle. Which two is chosen so
-//     that the 8-byte loads of V (64-byte swizzle) meet different banks.
+//   * One token: keys are the 16 rows of S^T = K Q^T and d's those of
+//     O^T += V^T P^T, with the 8 heads as columns: no row is idle (heads as
+//     rows: 271 us against 238). S^T leaves a lane one key of two heads; the
+//     transpose of an 8 x 8 tile of pairs gives it P^T's fragment.
+//   * Two to four: (token, head) are the rows. S leaves each lane two keys of a
+//     tile, and the same two are those of its fragments of PV: P needs no
+//     shuffle. Q's fragments lie in shared memory.
+//   * PV wants pairs of two keys where the pool has pairs of two d's: the codes
+//     of two keys are paired before the conversion, four logic operations for
+//     16 elements (253 us -> 247).
+//   * Which keys of a tile a lane holds is chosen so that the 8-byte loads of V
+//     (its 16-byte chunks turned round by the row) meet different banks.
 #pragma once
 
 // kTok query tokens per launch (1, 2 or 4), kKeys keys taken at once, kWarps
@@ -38,7 +44,6 @@ struct Fp4Shape {
     static constexpr int kSteps = kP / kKeys;      // of a unit
     static constexpr int kTiles = kKeys / 8;       // of 8 keys
     static constexpr int kPairs = (kTok + 1) / 2;  // tokens share the 16 rows of a tile two by two
-    static constexpr bool kSharedQ = kTok > 1;     // Q's fragments in shared memory
 };
 using Fp4One = Fp4Shape<1, 64, 4, 4, 3>;
 using Fp4Two = Fp4Shape<2, 64, 4, 4, 2>;
@@ -64,7 +69,8 @@ struct Fp4Desc {
 template <class Shape>
 struct DecodeSmem4 {
     Fp4Part<Shape::kKeys> part[Shape::kWarps][Shape::kParts];
-    uint4 q[Shape::kSharedQ ? Shape::kWarps : 1][Shape::kSharedQ ? Shape::kPairs : 1][8][Shape::kSharedQ ? 32 : 1];
+    // Q's fragments, where registers do not hold them
+    uint4 q[Shape::kTok > 1 ? Shape::kWarps : 1][Shape::kPairs][8][Shape::kTok > 1 ? 32 : 1];
     Fp4Desc desc[Shape::kWarps][2 * kFp4Ahead];
 };
 template <class Shape>
@@ -185,11 +191,11 @@ __device__ void decode_fp4_worker(DecodeSmem4<Shape> &sm, const DecodeArgs &a, i
 #pragma unroll
     for (int st = 0; st < kParts; ++st) issue(st, st, st & 1);
 
-    uint32_t qf[Shape::kSharedQ ? 1 : kTok][8][2];  // this lane's 32 d's of head gr as f16 pairs
+    uint32_t qf[8][2];         // kTok 1: this lane's 32 d's of head gr as f16 pairs
     float o[kPairs][2][8][4];  // kTok 1: o[0][0] only; else [pair of tokens][parity of d][pair of d's]
     float m[kTok];             // this lane's head: reference (log2 units),
-    float2 l[kTok];            // sums of P over its keys of each parity;
-    float2 m2 = make_float2(-INFINITY, -INFINITY);  // kTok 1: both of heads 2 t, 2 t + 1
+    float2 l[kTok];            // sums of P over its keys (two sums; kTok 1: of heads 2 t, 2 t + 1);
+    float2 m2 = make_float2(-INFINITY, -INFINITY);  // kTok 1: references of heads 2 t, 2 t + 1
 #pragma unroll
     for (int j = 0; j < kTok; ++j) m[j] = -INFINITY, l[j] = make_float2(0.f, 0.f);
     // a negative scale turns q's sign instead, so that the largest score is
@@ -226,15 +232,15 @@ __device__ void decode_fp4_worker(DecodeSmem4<Shape> &sm, const DecodeArgs &a, i
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const uint4 f = bf16x8_to_f16x8(q[x]);
-                    if constexpr (Shape::kSharedQ) {
+                    if constexpr (kTok > 1) {
                         // A operand: .x, .z the pair's first token, .y, .w its second
                         uint32_t *to = reinterpret_cast<uint32_t *>(&sm.q[w][j / 2][2 * x][lane]) + (j & 1);
                         to[0] = f.x ^ flip, to[2] = f.y ^ flip;
                         to += 32 * 4;
                         to[0] = f.z ^ flip, to[2] = f.w ^ flip;
                     } else {
-                        qf[j][2 * x][0] = f.x ^ flip, qf[j][2 * x][1] = f.y ^ flip;
-                        qf[j][2 * x + 1][0] = f.z ^ flip, qf[j][2 * x + 1][1] = f.w ^ flip;
+                        qf[2 * x][0] = f.x ^ flip, qf[2 * x][1] = f.y ^ flip;
+                        qf[2 * x + 1][0] = f.z ^ flip, qf[2 * x + 1][1] = f.w ^ flip;
                     }
                 }
                 m[j] = -INFINITY, l[j] = make_float2(0.f, 0.f);
@@ -278,8 +284,8 @@ __device__ void decode_fp4_worker(DecodeSmem4<Shape> &sm, const DecodeArgs &a, i
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) k[h][e] = hmul2_bits(k[h][e], sy);
                             }
-                            mma4(s[r0 + z], k[0][0], k[1][0], k[0][1], k[1][1], qf[0][2 * y][0], qf[0][2 * y][1]);
-                            mma4(s[r0 + z], k[0][2], k[1][2], k[0][3], k[1][3], qf[0][2 * y + 1][0], qf[0][2 * y + 1][1]);
+                            mma4(s[r0 + z], k[0][0], k[1][0], k[0][1], k[1][1], qf[2 * y][0], qf[2 * y][1]);
+                            mma4(s[r0 + z], k[0][2], k[1][2], k[0][3], k[1][3], qf[2 * y + 1][0], qf[2 * y + 1][1]);
                         }
                 }
                 const int32_t lo = (d.range & 0xff) - from, hi = (d.range >> 8 & 0xff) - from;
@@ -338,12 +344,7 @@ __device__ void decode_fp4_worker(DecodeSmem4<Shape> &sm, const DecodeArgs &a, i
 #pragma unroll
                         for (int pr = 0; pr < kPairs; ++pr)
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                if constexpr (Shape::kSharedQ)
-                                    qa[pr][h] = sm.q[w][pr][2 * y + h][lane];
-                                else
-                                    qa[pr][h] = make_uint4(qf[0][2 * y + h][0], 0u, qf[0][2 * y + h][1], 0u);
-                            }
+                            for (int h = 0; h < 2; ++h) qa[pr][h] = sm.q[w][pr][2 * y + h][lane];
 #pragma unroll
                         for (int z = 0; z < kGroup; ++z) {
                             const uint32_t word = y == 0 ? c[z].x : y == 1 ? c[z].y : y == 2 ? c[z].z : c[z].w;
@@ -363,12 +364,10 @@ __device__ void decode_fp4_worker(DecodeSmem4<Shape> &sm, const DecodeArgs &a, i
                 for (int j = 0; j < kTok; ++j) {
                     float(&sj)[kTiles][4] = s[j / 2];
                     const int e0 = 2 * (j & 1);
-                    int32_t lo = (d.range & 0xff) - from, hi = (d.range >> 8 & 0xff) - from;  // one token: the sequence's range is its own
-                    if (a.n_tok > 1) {
-                        const int32_t at = d.rel - a.n_tok + j - from;  // its position
-                        hi = min(hi, at + 1);
-                        if (a.window > 0) lo = max(lo, at - a.window + 1);
-                    }
+                    int32_t lo = (d.range & 0xff) - from, hi = (d.range >> 8 & 0xff) - from;
+                    const int32_t at = d.rel - a.n_tok + j - from;  // its position
+                    hi = min(hi, at + 1);
+                    if (a.window > 0) lo = max(lo, at - a.window + 1);
                     if (lo > 0 || hi < kKeys) {
 #pragma unroll
                         for (int tile = 0; tile < kTiles; ++tile)
@@ -391,12 +390,8 @@ __device__ void decode_fp4_worker(DecodeSmem4<Shape> &sm, const DecodeArgs &a, i
                         l[j].x *= al, l[j].y *= al;
 #pragma unroll
                         for (int y = 0; y < 8; ++y) {
-                            if constexpr (kTok == 1) {
-                                o[0][0][y][0] *= al, o[0][0][y][1] *= al, o[0][0][y][2] *= al, o[0][0][y][3] *= al;
-                            } else {
-                                float(&oj)[2][8][4] = o[j / 2];
-                                oj[0][y][e0] *= al, oj[0][y][e0 + 1] *= al, oj[1][y][e0] *= al, oj[1][y][e0 + 1] *= al;
-                            }
+                            float(&oj)[2][8][4] = o[j / 2];
+                            oj[0][y][e0] *= al, oj[0][y][e0 + 1] *= al, oj[1][y][e0] *= al, oj[1][y][e0 + 1] *= al;
                         }
                         m[j] = next;
                     }

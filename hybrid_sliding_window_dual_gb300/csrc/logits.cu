@@ -73,6 +73,12 @@ __device__ __forceinline__ void load8_if(bool on, const float *p, bool wide, flo
                  : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7])
                  : "l"(p), "r"((uint32_t)on), "r"((uint32_t)wide));
 }
+__device__ __forceinline__ void load_if(bool on, const float *p, float &x) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.f32 %0, [%1];\n\t}" : "+f"(x) : "l"(p), "r"((uint32_t)on));
+}
+__device__ __forceinline__ void load_if(bool on, const void *p, uint16_t &x) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.u16 %0, [%1];\n\t}" : "+h"(x) : "l"(p), "r"((uint32_t)on));
+}
 __device__ __forceinline__ void load16b_if(bool on, const void *p, uint32_t (&x)[4]) {
     asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t@q ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
                  : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3])
@@ -237,11 +243,42 @@ struct ProbsRow {
                 if (v0 < hi && v0 + 8 > hi && (bits >> (8 * g) & 0xff)) own |= (load(g, z[g]) ? 1u : 0u) << g;  // the row's last
             }
         } else {
+            const auto on = [&](int g, int e) { return token(g, threadIdx.x, e) < hi && (bits >> (8 * g + e) & 1); };
+            if (counts) {
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
+                for (int g = 0; g < kGroups; ++g) {
+                    uint16_t n[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) z[g][e] = -INFINITY;
-                if (bits >> (8 * g) & 0xff) own |= (load(g, z[g]) ? 1u : 0u) << g;
+                    for (int e = 0; e < 8; ++e) n[e] = 0, load_if(on(g, e), counts + token(g, threadIdx.x, e), n[e]);
+                    own |= (n[0] | n[1] | n[2] | n[3] | n[4] | n[5] | n[6] | n[7] ? 1u : 0u) << g;
+                }
+            }
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    z[g][e] = -INFINITY;
+                    if constexpr (sizeof(TL) == 4) {
+                        load_if(on(g, e), reinterpret_cast<const float *>(logits + token(g, threadIdx.x, e)), z[g][e]);
+                    } else {
+                        uint16_t x = 0xff80;
+                        load_if(on(g, e), logits + token(g, threadIdx.x, e), x);
+                        z[g][e] = __uint_as_float((uint32_t)x << 16);
+                    }
+                }
+            if (specials) {
+                // a warp's tokens of one (group, element) are a word of the bits; mostly none is set
+                const int lane = threadIdx.x & 31, words = blockDim.x / 32, first = threadIdx.x / 32;
+                uint32_t some = 0;
+                for (int i = lane; i < 8 * kGroups; i += 32)
+                    if (lo + i * (int32_t)blockDim.x < hi) some |= sm.special[i * words + first];
+                if (__any_sync(0xffffffffu, some != 0)) {
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (on(g, e)) own |= (sm.special[(8 * g + e) * words + first] >> lane & 1) << g;
+                }
             }
         }
         return own;
@@ -587,91 +624,8 @@ struct CountArgs {
 constexpr int kCountSlice = 8192, kCountThreads = 512;
 constexpr int kCountAhead = 8;  // tokens of a thread in flight
 
-// A cluster per sequence. Each CTA reads an eighth of the tokens and counts them
-// where they belong: 64 tokens of the vocabulary in turn lie with each CTA, in its
-// shared memory, so that what it writes back are whole 128-byte lines. kPacked:
-// at most 32767 tokens, whose counts need 15 bits, as the result has them. No
-// order of the additions shows in the result.
-template <bool kPacked>
-__global__ void __launch_bounds__(kCountThreads) count_cluster(const CountArgs a) {
-    extern __shared__ __align__(16) uint32_t counted[];
-    const uint32_t rank = blockIdx.x % kMaxCluster;
-    const int64_t s = blockIdx.x / kMaxCluster;
-    const int32_t mine = (a.vocab + 511) / 512 * 64;  // counts of this CTA
-    for (int i = threadIdx.x; i < mine / (kPacked ? 8 : 4); i += kCountThreads)
-        reinterpret_cast<uint4 *>(counted)[i] = make_uint4(0, 0, 0, 0);
-    cluster_arrive();  // nobody counts before all are zero
-    pdl_wait();
-    pdl_launch_dependents();
-    const int32_t *tokens = a.tokens + s * a.token_stride;
-    const int32_t prompt = a.n_prompt ? a.n_prompt[s] : 0;
-    bool waited = false;
-    for (int32_t i0 = rank * kCountThreads + threadIdx.x; i0 - (int32_t)threadIdx.x < a.n_tokens;) {
-        int32_t v[kCountAhead];
-#pragma unroll
-        for (int e = 0; e < kCountAhead; ++e) {
-            const int64_t i = i0 + (int64_t)e * kCountThreads * kMaxCluster;
-            v[e] = i < a.n_tokens ? tokens[i] : -1;
-        }
-        if (!waited) cluster_wait();
-        waited = true;
-#pragma unroll
-        for (int e = 0; e < kCountAhead; ++e) {
-            const int64_t i = i0 + (int64_t)e * kCountThreads * kMaxCluster;
-            if (v[e] >= a.vocab) set_error(a.err, HSWA_ERR_BOUNDS);
-            if (v[e] < 0 || v[e] >= a.vocab) continue;
-            const uint32_t at = (v[e] >> 9) * 64 + (v[e] & 63);
-            const uint32_t to = cluster_addr(counted + (kPacked ? at / 2 : at), v[e] >> 6 & 7);
-            const uint32_t shift = kPacked ? 16 * (at & 1) : 0;
-            if (i < prompt)
-                asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(to), "r"(kPacked ? 0x8000u << shift : 1u << 31) : "memory");
-            else
-                asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(to), "r"(1u << shift) : "memory");
-        }
-        const int64_t next = i0 + (int64_t)kCountAhead * kCountThreads * kMaxCluster;
-        if (next - threadIdx.x >= a.n_tokens) break;
-        i0 = (int32_t)next;
-    }
-    if (!waited) cluster_wait();
-    cluster_arrive();
-    cluster_wait();
-    uint16_t *row = a.counts + s * a.count_stride;
-    const bool vec = ((uintptr_t)a.counts & 15) == 0 && a.count_stride % 8 == 0;
-    for (int u = threadIdx.x; u < mine / 8; u += kCountThreads) {
-        const int32_t v = (u >> 3) * 512 + rank * 64 + (u & 7) * 8;
-        if (v >= a.vocab) continue;
-        uint32_t x[4];  // 8 counts, 15 bits and the prompt's
-        if constexpr (kPacked) {
-            const uint4 q = reinterpret_cast<const uint4 *>(counted)[u];
-            x[0] = q.x, x[1] = q.y, x[2] = q.z, x[3] = q.w;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint2 q = reinterpret_cast<const uint2 *>(counted)[4 * u + e];
-                x[e] = (min(q.x & 0x7fffffffu, 0x7fffu) | q.x >> 31 << 15) | (min(q.y & 0x7fffffffu, 0x7fffu) | q.y >> 31 << 15) << 16;
-            }
-        }
-        if (a.clear && vec && v + 8 <= a.vocab) {
-            *reinterpret_cast<uint4 *>(row + v) = make_uint4(x[0], x[1], x[2], x[3]);
-            continue;
-        }
-        if (!a.clear && (x[0] | x[1] | x[2] | x[3]) == 0) continue;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (v + e >= a.vocab) continue;
-            uint32_t y = x[e / 2] >> (16 * (e & 1)) & 0xffff;
-            if (!a.clear) {
-                if (y == 0) continue;
-                const uint32_t was = row[v + e];
-                y = ((y | was) & 0x8000) | min((y & 0x7fff) + (was & 0x7fff), 0x7fffu);
-            }
-            row[v + e] = (uint16_t)y;
-        }
-    }
-}
-
-// The same for vocabularies whose counts a cluster does not hold. A CTA per
-// sequence and slice of the vocabulary: it goes through the sequence's tokens, counts its own in shared memory (bit 31: in the prompt)
+// Many tokens: a CTA per sequence and slice of the vocabulary goes through the
+// sequence's tokens, counts its own in shared memory (bit 31: in the prompt)
 // and writes the slice. No order of the additions shows in the result.
 __global__ void __launch_bounds__(kCountThreads) count_slices(const CountArgs a) {
     __shared__ uint32_t n[kCountSlice];
@@ -713,53 +667,64 @@ __global__ void __launch_bounds__(kCountThreads) count_slices(const CountArgs a)
     }
 }
 
-// A few tokens added to counts that stay: a thread each.
-__global__ void __launch_bounds__(256) count_few(const CountArgs a) {
+// Rows of counts from nothing.
+__global__ void __launch_bounds__(256) count_clear(const CountArgs a) {
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t at = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-    if (at >= (int64_t)a.n_seqs * a.n_tokens) return;
-    const int32_t s = (int32_t)(at / a.n_tokens), i = (int32_t)(at % a.n_tokens);
-    const int32_t v = a.tokens[s * a.token_stride + i];
-    if (v >= a.vocab) set_error(a.err, HSWA_ERR_BOUNDS);
-    if (v < 0 || v >= a.vocab) return;
-    const bool prompt = a.n_prompt && i < a.n_prompt[s];
-    unsigned short *n = a.counts + s * a.count_stride + v, was = *n;
-    for (;;) {
-        const unsigned short next = prompt ? was | 0x8000 : (was & 0x7fff) == 0x7fff ? was : was + 1;
-        if (next == was) return;
-        const unsigned short seen = atomicCAS(n, was, next);
-        if (seen == was) return;
-        was = seen;
+    constexpr int kPer = 256 * 8 * 2;  // counts of a CTA
+    const int32_t parts = (a.vocab + kPer - 1) / kPer, v0 = blockIdx.x % parts * kPer;
+    uint16_t *row = a.counts + (int64_t)(blockIdx.x / parts) * a.count_stride;
+    const bool vec = ((uintptr_t)a.counts & 15) == 0 && a.count_stride % 8 == 0;
+    for (int i = threadIdx.x; i < kPer / 8; i += 256) {
+        const int32_t v = v0 + 8 * i;
+        if (vec && v + 8 <= a.vocab) {
+            *reinterpret_cast<uint4 *>(row + v) = make_uint4(0, 0, 0, 0);
+        } else {
+            for (int e = 0; e < 8; ++e)
+                if (v + e < a.vocab) row[v + e] = 0;
+        }
     }
 }
 
-constexpr int kFewTokens = 64;  // of a sequence
-
-constexpr size_t kCountSmem = 96 << 10;  // at most, of a CTA: two on an SM
-
-// Bytes of shared memory of a CTA of the cluster.
-size_t count_smem(int vocab, bool packed) { return (size_t)(vocab + 511) / 512 * 64 * (packed ? 2 : 4); }
-
-template <bool kPacked>
-cudaError_t launch_count(const CountArgs &a, cudaStream_t st) {
-    static int setup[kMaxDevices] = {};
-    if (kernel_setup(count_cluster<kPacked>, kCountSmem, kCountThreads, setup) < 0) return cudaErrorInvalidConfiguration;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.n_seqs * kMaxCluster);
-    cfg.blockDim = dim3(kCountThreads);
-    cfg.dynamicSmemBytes = count_smem(a.vocab, kPacked);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kMaxCluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, count_cluster<kPacked>, a);
+// Tokens [from, to) of every sequence added to counts that are there: a thread
+// each. Additions and ors that need no answer, unless a count could pass 32767.
+__global__ void __launch_bounds__(256) count_each(const CountArgs a, int32_t from, int32_t to) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t at = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+    if (at >= (int64_t)a.n_seqs * (to - from)) return;
+    const int32_t s = (int32_t)(at / (to - from)), i = from + (int32_t)(at % (to - from));
+    const int32_t v = a.tokens[s * a.token_stride + i];
+    if (v >= a.vocab) set_error(a.err, HSWA_ERR_BOUNDS);
+    if (v < 0 || v >= a.vocab) return;
+    const int32_t prompt = a.n_prompt ? a.n_prompt[s] : 0;
+    // the word that the count is half of (the other half stays as it is)
+    const uintptr_t n = reinterpret_cast<uintptr_t>(a.counts + s * a.count_stride + v);
+    uint32_t *word = reinterpret_cast<uint32_t *>(n & ~(uintptr_t)3);
+    const int shift = n & 2 ? 16 : 0;
+    if (i < prompt) {
+        atomicOr(word, 0x8000u << shift);
+        return;
+    }
+    uint32_t was = *(volatile uint32_t *)word;
+    if ((int32_t)(was >> shift & 0x7fff) + to - max(from, prompt) <= 0x7fff) {
+        atomicAdd(word, 1u << shift);  // all that this launch adds cannot take it past 32767
+    } else {
+        while ((was >> shift & 0x7fff) != 0x7fff) {
+            const uint32_t seen = atomicCAS(word, was, was + (1u << shift));
+            if (seen == was) break;
+            was = seen;
+        }
+    }
 }
+
+// Atomics on the counts themselves (64 sequences of 4096 tokens added 6.1 us, all
+// the same token 12; a cluster that counts in its shared memory and adds to the
+// rows 15 and 17, slices 20 and 10). One launch takes up to 2^15 tokens, which cannot
+// overflow a count from nothing (one of so many being a prompt's); of more, each
+// takes so many that few counts come near it: those need a compare-and-swap, 0.9
+// us for each of the same token. Above kEachTokens tokens slices.
+constexpr int kEachTokens = 65536, kEachOnce = 1 << 15, kEachPart = 16384;
 
 template <typename TL, typename TP, bool kVec, int kThreads, int kGroups, bool kLoop>
 cudaError_t launch(const ProbsArgs &a, int64_t rows, cudaStream_t st) {
@@ -782,6 +747,7 @@ template <typename TL, typename TP, bool kVec>
 cudaError_t launch_row(const ProbsArgs &a, int64_t rows, cudaStream_t st) {
     const int32_t groups = (a.slice / 8 + 511) / 512;  // of 512 threads
     if (groups <= 2) return launch<TL, TP, kVec, 512, 2, false>(a, rows, st);
+    if (groups <= 4 && rows * a.cluster <= sm_count()) return launch<TL, TP, kVec, 1024, 2, false>(a, rows, st);
     if (groups <= 5) return launch<TL, TP, kVec, 512, 5, false>(a, rows, st);
     if (groups <= 10) return launch<TL, TP, kVec, 1024, 5, false>(a, rows, st);
     return launch<TL, TP, kVec, 1024, 1, true>(a, rows, st);
@@ -876,14 +842,16 @@ extern "C" int hswa_count_tokens(uint16_t *counts, int64_t count_stride, const i
     a.n_seqs = n_seqs, a.n_tokens = n_tokens, a.vocab = vocab, a.slices = slices, a.clear = clear != 0;
     a.err = error_word();
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (!clear && n_tokens <= kFewTokens) {
-        set_last_kernel("count_few");
-        e = launch_pdl(count_few, dim3((unsigned)(((int64_t)n_seqs * n_tokens + 255) / 256)), dim3(256), 0, st, a);
-    } else if (const bool packed = n_tokens <= 0x7fff;
-               count_smem(vocab, packed) <= kCountSmem && n_seqs <= INT32_MAX / kMaxCluster) {
-        set_last_kernel("count_cluster");
-        e = packed ? launch_count<true>(a, st) : launch_count<false>(a, st);
+    cudaError_t e = cudaSuccess;
+    const int64_t clears = (int64_t)n_seqs * ((vocab + 4095) / 4096);
+    if (n_tokens <= kEachTokens && clears <= INT32_MAX) {
+        set_last_kernel(n_tokens ? clear ? "count_clear+count_each" : "count_each" : "count_clear");
+        if (clear) e = launch_pdl(count_clear, dim3((unsigned)clears), dim3(256), 0, st, a);
+        const int32_t part = n_tokens <= kEachOnce ? kEachOnce : kEachPart;
+        for (int32_t from = 0; from < n_tokens && e == cudaSuccess; from += part) {
+            const int32_t to = std::min(from + part, n_tokens);
+            e = launch_pdl(count_each, dim3((unsigned)(((int64_t)n_seqs * (to - from) + 255) / 256)), dim3(256), 0, st, a, from, to);
+        }
     } else {
         set_last_kernel("count_slices");
         e = launch_pdl(count_slices, dim3((unsigned)(n_seqs * slices)), dim3(kCountThreads), 0, st, a);

@@ -230,7 +230,7 @@ def count(tokens, n_prompt, V, before=None, clear=True, pad=0, expect=0):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("pad", [0, 3])
-@pytest.mark.parametrize("S,n,V", [(1, 1, 1), (3, 4, 17), (5, 64, 8192), (5, 65, 8193), (2, 1000, 20000), (64, 4, 1000), (3, 40000, 131072), (2, 3, 1 << 20), (2, 5000, 393217), (2, 40000, 200000), (2, 5000, 390000)])
+@pytest.mark.parametrize("S,n,V", [(1, 1, 1), (3, 4, 17), (5, 64, 8192), (5, 65, 8193), (2, 1000, 20000), (64, 4, 1000), (3, 40000, 131072), (2, 3, 1 << 20), (2, 5000, 393217), (2, 40000, 200000), (2, 5000, 390000), (1, 65537, 9000), (9, 33000, 1001)])
 def test_count_tokens(S, n, V, pad):
     rng = np.random.default_rng(S + n)
     tokens = np.where(rng.random((S, n)) < 0.1, -1, np.minimum(rng.exponential(V / 50 + 1, (S, n)), V - 1)).astype(np.int32)
