@@ -1,5 +1,5 @@
-// Copy kernels of the dual KV pool: slot-mapped KV append and the
-// in-window SWA gather / scatter.
+// Copy kernels of the dual KV pool: slot-mapped KV append and read-back, and
+// the in-window SWA gather / scatter.
 //
 // "MiMo-V2.5 Series Inference Full-Link Optimization", Sec. 2.1 (KVCache
 // Dual Pool): Full layers keep every token in the Full pool, SWA layers keep
@@ -7,7 +7,7 @@
 // "Tiered KV Cache Offloading in vLLM", hybrid models: sliding-window layers
 // reload only the tokens inside their window.
 //
-// All three kernels are HBM- (or host-link-) bound 16-byte copies: a warp
+// All kernels are HBM- (or host-link-) bound 16-byte copies: a warp
 // moves whole 16-byte chunks of a token's K or V row, so a row of
 // d * sizeof(dtype) bytes is read and written with full 32-byte sectors.
 #include <algorithm>

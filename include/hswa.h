@@ -116,10 +116,11 @@ extern "C" {
  * (infinities too; what a NaN becomes is not defined, but finite), and every
  * stored value is exact in fp16 and in bf16. d must be a multiple of 16.
  * Supported by hswa_append_kv, hswa_rope_append, hswa_read_kv, hswa_decode,
- * hswa_decode_append, hswa_decode_multi, hswa_prefill_chunk and
- * hswa_prefill_chunk_ws, any head ratio and page size, head_dim at most 256
- * (fastest with d = 128, 8 query heads per kv head, P = 64); other calls
- * on layers return HSWA_ERR_UNSUPPORTED. */
+ * hswa_decode_append, hswa_decode_multi and hswa_prefill_chunk_ws
+ * (hswa_prefill_chunk where the workspace size of that is 0), any head ratio and
+ * page size, head_dim at most 256 (fastest with d = 128, 8 query heads per kv
+ * head, P = 64, pools and q on 16 bytes); other calls on layers return
+ * HSWA_ERR_UNSUPPORTED. */
 #define HSWA_DTYPE_FP4 3
 
 /* A CUDA stream (the same handle as cudaStream_t); NULL = default stream. */
@@ -349,7 +350,8 @@ int hswa_sync_tables(hswa_pool *pool, int32_t *d_full_bt, int32_t *d_swa_bt, int
  * k, v: device [n_tokens][Hkv][d] in the pool dtype. d_slots: device int32,
  * the full_slot (Full layer) or swa_slot (SWA layer) array from
  * hswa_reserve. A slot past the pool sets HSWA_ERR_BOUNDS on the device
- * and is skipped. */
+ * and is skipped. Slots are distinct: of two tokens with one slot either's
+ * elements may stay, block by block. */
 int hswa_append_kv(const hswa_pool *pool, const hswa_layer *layer, const void *k, const void *v,
                    const int32_t *d_slots, int n_tokens, hswa_stream_t stream);
 
@@ -609,8 +611,8 @@ int hswa_count_tokens(uint16_t *counts, int64_t count_stride, const int32_t *tok
  * uint32 [n_seqs * n_tok], rows mask_stride (>= ceil(vocab / 32)) words apart, bit v % 32
  * of word v / 32 set where v is allowed; NULL: all are. vocab at most
  * HSWA_VERIFY_MAX_VOCAB, n_bias at most HSWA_LOGITS_MAX_BIAS, n_tok in [1,
- * HSWA_DECODE_MAX_TOKENS]. Fastest with rows on 16-byte boundaries and a
- * vocabulary of at most 163840. */
+ * HSWA_DECODE_MAX_TOKENS]. Fastest with rows on 16-byte boundaries (fp32: 32)
+ * and a vocabulary of at most 163840; above 327680 rows are read three times. */
 int hswa_logits_probs(int logits_dtype, const void *logits, int64_t logits_stride, int p_dtype, void *p,
                       int64_t p_stride, const float *params, const uint16_t *counts, int64_t count_stride,
                       const int32_t *d_draft, const int32_t *bias_token, const float *bias, int n_bias,
@@ -633,7 +635,9 @@ int hswa_prefill_chunk(const hswa_pool *pool, const hswa_layer *layer, const voi
 
 /* Bytes of workspace hswa_prefill_chunk_ws needs for any chunk of n_seqs
  * sequences with at most max_q_len new tokens each: 0 for bf16 and fp32
- * pools (they need none); for an FP8 pool, room for an fp16 copy of every
+ * pools (they need none), and for FP4 pools of other shapes than d = 128, P = 64
+ * and an even number of query heads per kv head; for other FP4 pools and for
+ * an FP8 pool, room for an fp16 copy of every
  * page such a chunk can read (all of a sequence's table row for a Full
  * layer, ceil((W - 1 + max_q_len) / P) + 1 pages for an SWA layer), a block
  * table onto the copies, a per-sequence offset table and an fp16 copy of
@@ -643,13 +647,13 @@ int hswa_prefill_chunk(const hswa_pool *pool, const hswa_layer *layer, const voi
 size_t hswa_prefill_workspace_size(const hswa_pool *pool, const hswa_layer *layer, int n_seqs,
                                    int max_q_len);
 
-/* Bytes of workspace a given chunk needs on an FP8 pool: the same layout as
+/* Bytes of workspace a given chunk needs on an FP8 or FP4 pool: the same layout as
  * above holding exactly the pages the chunk reads (logical pages 0 ..
  * (prefix + n - 1) / P of each sequence for a Full layer, from
  * (prefix - W + 1) / P for an SWA layer) and its q_start[n_seqs] query
  * rows. prefix_len (host int32 [n_seqs]) and q_start (host int32
  * [n_seqs + 1]) hold the values the device arrays of the call will hold.
- * 0 for bf16 and fp32 pools. On the chunked-prefill workload (8 sequences,
+ * 0 where the size above is. On the chunked-prefill workload (8 sequences,
  * prefixes of 8K-64K tokens, 4096 new tokens each, 64 / 8 heads, table rows
  * of 972 pages) the Full layer needs 4,897 page copies: 1.82 GB with the
  * 0.54 GB q copy, against 2.58 GB for the upper bound. */
@@ -671,9 +675,10 @@ size_t hswa_prefill_workspace_size_exact(const hswa_pool *pool, const hswa_layer
  * chunk, hswa_prefill_workspace_size bytes every page of any chunk of those
  * sizes. A ws too small for the tables, the q copy and one page copy is
  * HSWA_ERR_INVALID_ARG; pages past what ws holds are not staged, read as
- * zeros and set HSWA_ERR_BOUNDS (hswa_check). Ignored (may be NULL) for
- * bf16 and fp32 pools. hswa_prefill_chunk on an FP8 pool returns
- * HSWA_ERR_INVALID_ARG (no workspace). */
+ * zeros and set HSWA_ERR_BOUNDS (hswa_check). FP4 pools are staged in the same way
+ * (their values are exact in fp16) where hswa_prefill_workspace_size is not 0.
+ * ws is ignored (may be NULL) where that is 0. hswa_prefill_chunk returns
+ * HSWA_ERR_INVALID_ARG (no workspace) where it is not. */
 int hswa_prefill_chunk_ws(const hswa_pool *pool, const hswa_layer *layer, const void *q, void *o,
                           const int32_t *d_bt, const int32_t *d_prefix_len, const int32_t *d_q_start,
                           int n_seqs, int total_q, int max_q_len, float scale, void *ws, size_t ws_bytes,
