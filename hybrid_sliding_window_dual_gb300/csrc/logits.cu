@@ -104,7 +104,7 @@ __device__ __forceinline__ uint32_t bias_slot(int32_t token) { return (uint32_t)
 static_assert(kBiasSlots == 1 << 11, "the hash keeps 11 bits");
 
 // The row of a CTA, and what happens to its logits.
-template <typename TL, bool kVec>
+template <typename TL, bool kVec, int kThreads>
 struct ProbsRow {
     const ProbsArgs &a;
     const ProbsSmem &sm;
@@ -117,10 +117,14 @@ struct ProbsRow {
     bool specials;
     float rep, inv_rep, freq, pres;  // inv_rep 0: divide
 
-    // Token of element e of group k of thread t (kVec: 8 neighbours, else 8
-    // as far apart as the CTA has threads).
+    // Element e of group k, counted from a thread's first (kVec: 8 neighbours, else
+    // 8 as far apart as the CTA has threads).
+    static __device__ __forceinline__ constexpr int32_t offset(int32_t k, int e) {
+        return kVec ? 8 * k * kThreads + e : (8 * k + e) * kThreads;
+    }
+    // Its token in thread t.
     __device__ __forceinline__ int32_t token(int32_t k, int32_t t, int e) const {
-        return kVec ? lo + 8 * (k * (int32_t)blockDim.x + t) + e : lo + (8 * k + e) * (int32_t)blockDim.x + t;
+        return lo + (kVec ? 8 * t : t) + offset(k, e);
     }
 
     __device__ __forceinline__ float penalized(float z, uint32_t c, int extra) const {
@@ -199,18 +203,21 @@ struct ProbsRow {
     template <int kGroups>
     __device__ __forceinline__ uint32_t load_all(uint64_t bits, float (&z)[kGroups][8]) const {
         uint32_t own = 0;
+        const int32_t first = token(0, threadIdx.x, 0), left = hi - first;
+        const TL *const from = logits + first;
+        const uint16_t *const counted = counts + first;  // not read without counts
         if constexpr (kVec) {
             uint32_t on = 0;
 #pragma unroll
             for (int g = 0; g < kGroups; ++g)
-                on |= (token(g, threadIdx.x, 8) <= hi && (bits >> (8 * g) & 0xff) ? 1u : 0u) << g;
+                on |= (offset(g, 8) <= left && (bits >> (8 * g) & 0xff) ? 1u : 0u) << g;
             const auto occurred = [&] {
                 if (!counts) return;
                 uint32_t n[kGroups][4];
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
                     n[g][0] = n[g][1] = n[g][2] = n[g][3] = 0;
-                    load16b_if(on >> g & 1, counts + token(g, threadIdx.x, 0), n[g]);
+                    load16b_if(on >> g & 1, counted + offset(g, 0), n[g]);
                 }
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) own |= (n[g][0] | n[g][1] | n[g][2] | n[g][3] ? 1u : 0u) << g;
@@ -221,14 +228,14 @@ struct ProbsRow {
                 for (int g = 0; g < kGroups; ++g) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) z[g][e] = -INFINITY;
-                    load8_if(on >> g & 1, reinterpret_cast<const float *>(logits + token(g, threadIdx.x, 0)), a.wide, z[g]);
+                    load8_if(on >> g & 1, reinterpret_cast<const float *>(from + offset(g, 0)), a.wide, z[g]);
                 }
             } else {
                 uint32_t x[kGroups][4];
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
                     x[g][0] = x[g][1] = x[g][2] = x[g][3] = 0xff80ff80;  // -inf
-                    load16b_if(on >> g & 1, logits + token(g, threadIdx.x, 0), x[g]);
+                    load16b_if(on >> g & 1, from + offset(g, 0), x[g]);
                 }
                 occurred();
 #pragma unroll
@@ -238,18 +245,18 @@ struct ProbsRow {
             }
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
-                const int32_t v0 = token(g, threadIdx.x, 0);
-                if (specials && (on >> g & 1)) own |= (sm.special[(v0 - lo) >> 5] >> ((v0 - lo) & 31) & 0xff ? 1u : 0u) << g;
-                if (v0 < hi && v0 + 8 > hi && (bits >> (8 * g) & 0xff)) own |= (load(g, z[g]) ? 1u : 0u) << g;  // the row's last
+                const int32_t at = first - lo + offset(g, 0);
+                if (specials && (on >> g & 1)) own |= (sm.special[at >> 5] >> (at & 31) & 0xff ? 1u : 0u) << g;
+                if (offset(g, 0) < left && offset(g, 8) > left && (bits >> (8 * g) & 0xff)) own |= (load(g, z[g]) ? 1u : 0u) << g;  // the row's last
             }
         } else {
-            const auto on = [&](int g, int e) { return token(g, threadIdx.x, e) < hi && (bits >> (8 * g + e) & 1); };
+            const auto on = [&](int g, int e) { return offset(g, e) < left && (bits >> (8 * g + e) & 1); };
             if (counts) {
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
                     uint16_t n[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) n[e] = 0, load_if(on(g, e), counts + token(g, threadIdx.x, e), n[e]);
+                    for (int e = 0; e < 8; ++e) n[e] = 0, load_if(on(g, e), counted + offset(g, e), n[e]);
                     own |= (n[0] | n[1] | n[2] | n[3] | n[4] | n[5] | n[6] | n[7] ? 1u : 0u) << g;
                 }
             }
@@ -259,25 +266,26 @@ struct ProbsRow {
                 for (int e = 0; e < 8; ++e) {
                     z[g][e] = -INFINITY;
                     if constexpr (sizeof(TL) == 4) {
-                        load_if(on(g, e), reinterpret_cast<const float *>(logits + token(g, threadIdx.x, e)), z[g][e]);
+                        load_if(on(g, e), reinterpret_cast<const float *>(from + offset(g, e)), z[g][e]);
                     } else {
                         uint16_t x = 0xff80;
-                        load_if(on(g, e), logits + token(g, threadIdx.x, e), x);
+                        load_if(on(g, e), from + offset(g, e), x);
                         z[g][e] = __uint_as_float((uint32_t)x << 16);
                     }
                 }
             if (specials) {
                 // a warp's tokens of one (group, element) are a word of the bits; mostly none is set
-                const int lane = threadIdx.x & 31, words = blockDim.x / 32, first = threadIdx.x / 32;
+                constexpr int kWords = kThreads / 32;
+                const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
                 uint32_t some = 0;
                 for (int i = lane; i < 8 * kGroups; i += 32)
-                    if (lo + i * (int32_t)blockDim.x < hi) some |= sm.special[i * words + first];
+                    if (lo + i * kThreads < hi) some |= sm.special[i * kWords + warp];
                 if (__any_sync(0xffffffffu, some != 0)) {
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g)
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            if (on(g, e)) own |= (sm.special[(8 * g + e) * words + first] >> lane & 1) << g;
+                            if (on(g, e)) own |= (sm.special[(8 * g + e) * kWords + warp] >> lane & 1) << g;
                 }
             }
         }
@@ -301,10 +309,15 @@ struct ProbsRow {
 #pragma unroll
             for (int e = 0; e < 8; ++e) z8[e] = z[e];
         } else {
+#pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int32_t v = token(k, t, e);
-                if (v < hi) own |= 1u << e;  // whatever it needs
-                z8[e] = v < hi ? as_float(logits[v]) : -INFINITY;
+                float z = -INFINITY;
+                if (v < hi) {
+                    z = as_float(logits[v]);
+                    if ((counts && counts[v]) || (specials && (sm.special[(v - lo) >> 5] >> ((v - lo) & 31) & 1))) own |= 1u << e;
+                }
+                z8[e] = z;
             }
         }
         while (own) {
@@ -430,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_probs(const 
     const bool penalties = a.counts && !(rep == 1.f && freq == 0.f && pres == 0.f);
     const int32_t lo = min((int32_t)rank * a.slice, a.vocab), hi = min(lo + a.slice, a.vocab);
     const bool drafts = penalties && a.draft && w > 0;
-    const ProbsRow<TL, kVec> r{a, sm, static_cast<const TL *>(a.logits) + row * a.logits_stride,
+    const ProbsRow<TL, kVec, kThreads> r{a, sm, static_cast<const TL *>(a.logits) + row * a.logits_stride,
                                penalties ? a.counts + seq * a.count_stride : nullptr,
                                a.mask ? a.mask + row * a.mask_stride : nullptr,
                                a.bias + (size_t)seq * a.n_bias, lo, hi, drafts ? w : 0, a.n_bias > 0 || drafts,
