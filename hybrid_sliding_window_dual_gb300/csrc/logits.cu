@@ -362,24 +362,25 @@ struct ProbsRow {
     }
 };
 
+// A group of results from p on, `left` of the row's values from there; step
+// apart where they are not neighbours.
 template <typename TP, bool kVec>
-__device__ __forceinline__ void store_probs(TP *p, int32_t v0, int32_t step, int32_t hi, bool wide, const float (&x)[8]) {
-    if (kVec && v0 >= hi) return;
-    if (kVec && v0 + 8 <= hi) {
+__device__ __forceinline__ void store_probs(TP *p, int32_t step, int32_t left, bool wide, const float (&x)[8]) {
+    if (kVec && left <= 0) return;
+    if (kVec && left >= 8) {
         if constexpr (sizeof(TP) == 4) {
-            store8(reinterpret_cast<float *>(p + v0), wide, x);
+            store8(reinterpret_cast<float *>(p), wide, x);
         } else {
-            *reinterpret_cast<uint4 *>(p + v0) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+            *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
         }
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int32_t v = v0 + e * step;
-            if (v < hi) {
+            if (e * step < left) {
                 if constexpr (sizeof(TP) == 4)
-                    p[v] = x[e];
+                    p[e * step] = x[e];
                 else
-                    p[v] = __float2bfloat16_rn(x[e]);
+                    p[e * step] = __float2bfloat16_rn(x[e]);
             }
         }
     }
@@ -607,7 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_probs(const 
     }
     // nothing allowed: no probability at all
     const float f = total > 0.f && top > -INFINITY ? weight(top, all, k) / total : 0.f;
-    TP *p = static_cast<TP *>(a.p) + row * a.p_stride;
+    const int32_t at = r.token(0, tid, 0), left = hi - at;
+    TP *p = static_cast<TP *>(a.p) + row * a.p_stride + at;
     const auto put = [&](int32_t g, float (&x)[8]) {
         if (greedy) {
 #pragma unroll
@@ -619,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_probs(const 
                 x[e] = y.x, x[e + 1] = y.y;
             }
         }
-        store_probs<TP, kVec>(p, r.token(g, tid, 0), kVec ? 1 : kThreads, hi, a.wide, x);
+        store_probs<TP, kVec>(p + r.offset(g, 0), kVec ? 1 : kThreads, left - r.offset(g, 0), a.wide, x);
     };
     if constexpr (kLoop) {
         for (int32_t g = 0; g < groups; ++g) {
@@ -774,6 +776,7 @@ cudaError_t launch_row(const ProbsArgs &a, int64_t rows, cudaStream_t st) {
     const int32_t groups = (a.slice / 8 + 511) / 512;  // of 512 threads
     if (groups <= 2) return launch<TL, TP, kVec, 512, 2, false>(a, rows, st);
     if (groups <= 4 && rows * a.cluster <= sm_count()) return launch<TL, TP, kVec, 1024, 2, false>(a, rows, st);
+    if (groups <= 4) return launch<TL, TP, kVec, 512, 4, false>(a, rows, st);
     if (groups <= 5) return launch<TL, TP, kVec, 512, 5, false>(a, rows, st);
     if (groups <= 10) return launch<TL, TP, kVec, 1024, 5, false>(a, rows, st);
     return launch<TL, TP, kVec, 1024, 1, true>(a, rows, st);
