@@ -97,6 +97,7 @@ struct ProbsSmem {
     int32_t at[kBiasSlots];   // the last entry of the bias list with that token
     uint32_t special[kMaxSlice / 32];  // the CTA's tokens with a bias or a draft
     int32_t draft[HSWA_DECODE_MAX_TOKENS];
+    uint64_t row;                     // those of all
     uint64_t part[kMaxCluster * 32];  // every warp's of the cluster: maximum, sum or first index
 };
 
@@ -495,18 +496,18 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_probs(const 
         }
         const uint32_t own = r.load_all(bits, z);  // bit g: group g goes on the list
         if (__any_sync(0xffffffffu, own != 0)) {
-            const int n = __popc(own);
-            int upto = n;  // of the warp's lanes
-            for (int off = 1; off < 32; off <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, upto, off);
-                if (lane >= off) upto += y;
+            int place[kGroups], n_list = 0;  // of this lane's groups on the list
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                const uint32_t takers = __ballot_sync(0xffffffffu, own >> g & 1);
+                place[g] = n_list + __popc(takers & ((1u << lane) - 1));
+                n_list += __popc(takers);
             }
-            const int n_list = __shfl_sync(0xffffffffu, upto, 31), slot = upto - n;
             for (int from = 0; from < n_list; from += kList) {
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
-                    const int at = slot + __popc(own & ((1u << g) - 1)) - from;
-                    if ((own >> g & 1) && at >= 0 && at < kList) list[warp][at] = (uint8_t)(32 * g + lane);
+                    const int at = place[g] - from;
+                    if ((own >> g & 1) && (uint32_t)at < kList) list[warp][at] = (uint8_t)(32 * g + lane);
                 }
                 __syncwarp();
                 if (from + lane < n_list) {
@@ -516,8 +517,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_probs(const 
                 __syncwarp();
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
-                    const int at = slot + __popc(own & ((1u << g) - 1)) - from;
-                    if ((own >> g & 1) && at >= 0 && at < kList) {
+                    const int at = place[g] - from;
+                    if ((own >> g & 1) && (uint32_t)at < kList) {
                         const float4 x0 = *reinterpret_cast<const float4 *>(&fetched[warp][at][0]), x1 = *reinterpret_cast<const float4 *>(&fetched[warp][at][4]);
                         z[g][0] = x0.x, z[g][1] = x0.y, z[g][2] = x0.z, z[g][3] = x0.w, z[g][4] = x1.x, z[g][5] = x1.y, z[g][6] = x1.z, z[g][7] = x1.w;
                     }
@@ -582,30 +583,39 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_probs(const 
     if (lane < a.cluster) st_cluster_u64(&sm.part[rank * kWarps + warp], lane, pair);
     cluster_arrive();
     cluster_wait();
-    // all warps' pairs, kPer of them a lane
-    constexpr int kPer = kMaxCluster * kWarps / 32;
-    const int n_parts = a.cluster * kWarps;
-    uint64_t parts[kPer];
-    float all = -INFINITY;
+    // all warps' pairs, kPer of them a lane of one warp
+    if (warp == 0) {
+        constexpr int kPer = kMaxCluster * kWarps / 32;
+        const int n_parts = a.cluster * kWarps;
+        uint64_t parts[kPer];
+        float all = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        parts[i] = lane + 32 * i < n_parts ? sm.part[lane + 32 * i] : (uint64_t)0xff800000u << 32;
-        all = fmaxf(all, __uint_as_float((uint32_t)(parts[i] >> 32)));
+        for (int i = 0; i < kPer; ++i) {
+            parts[i] = lane + 32 * i < n_parts ? sm.part[lane + 32 * i] : (uint64_t)0xff800000u << 32;
+            all = fmaxf(all, __uint_as_float((uint32_t)(parts[i] >> 32)));
+        }
+        all = warp_max(all);
+        uint32_t x = (uint32_t)INT32_MAX;
+        if (greedy) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (__uint_as_float((uint32_t)(parts[i] >> 32)) == all) x = min(x, (uint32_t)parts[i]);
+            x = __reduce_min_sync(0xffffffffu, x);
+            if (all == -INFINITY) x = (uint32_t)INT32_MAX;
+        } else {
+            float total = 0.f;
+            if (all > -INFINITY) {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) total += __uint_as_float((uint32_t)parts[i]) * weight(__uint_as_float((uint32_t)(parts[i] >> 32)), all, k);
+                total = warp_sum(total);
+            }
+            x = __float_as_uint(total);
+        }
+        if (lane == 0) sm.row = (uint64_t)__float_as_uint(all) << 32 | x;
     }
-    all = warp_max(all);
-    float total = 0.f;
-    first = INT32_MAX;
-    if (greedy) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (__uint_as_float((uint32_t)(parts[i] >> 32)) == all) first = min(first, (int32_t)(uint32_t)parts[i]);
-        first = __reduce_min_sync(0xffffffffu, first);
-        if (all == -INFINITY) first = INT32_MAX;
-    } else if (all > -INFINITY) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) total += __uint_as_float((uint32_t)parts[i]) * weight(__uint_as_float((uint32_t)(parts[i] >> 32)), all, k);
-        total = warp_sum(total);
-    }
+    __syncthreads();
+    const float all = __uint_as_float((uint32_t)(sm.row >> 32)), total = greedy ? 0.f : __uint_as_float((uint32_t)sm.row);
+    first = (int32_t)(uint32_t)sm.row;
     // nothing allowed: no probability at all
     const float f = total > 0.f && top > -INFINITY ? weight(top, all, k) / total : 0.f;
     const int32_t at = r.token(0, tid, 0), left = hi - at;
