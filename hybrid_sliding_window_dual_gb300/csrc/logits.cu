@@ -34,6 +34,7 @@ struct ProbsArgs {
     const uint32_t *mask;
     bool wide;                // fp32 rows start on 32 bytes
     int32_t n_bias, n_tok, vocab, cluster, cluster_log2, slice;  // slice: elements per CTA, a multiple of 8
+    int32_t rows, ahead;  // ahead: rows that run at once, 0 if all do
     int *err;
 };
 
@@ -91,6 +92,11 @@ template <>
 __device__ __forceinline__ float as_float<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ float as_float<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// Bytes (less a last partial 16) from a 16-byte boundary on into L2.
+__device__ __forceinline__ void prefetch_l2(const void *p, int32_t bytes) {
+    if (bytes >= 16) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes & ~15));
+}
 
 struct ProbsSmem {
     int32_t key[kBiasSlots];  // token of a slot, -1: free
@@ -414,14 +420,16 @@ __device__ __forceinline__ float weight(float z, float top, float k) {
 // where a warp would do it for all its values: groups with such a token go on the
 // warp's list, its lanes take one each, and the owners fetch the results.
 //
-// 256 rows of 150000, bf16 to fp32: 93 us with penalties, 63 without, 35 at a
-// plain copy's rate. An SM holds 32 warps (a thread's 40 values are registers), whose
-// loads, list, exponentials and stores are phases between barriers: the issue
-// slots are 40 % used (37 instructions a value, 23 without penalties), and so
-// is the memory. What it took: loads of all groups in flight at once (without
-// counts 74 us before), fp32 rows 32 bytes a lane, redux for the maximum, lists by
-// groups (tokens by themselves 101). Rows streamed twice through shared
-// memory instead of kept took 115, three reads (kLoop) 585.
+// 256 rows of 150000, bf16 to fp32: 79 us with penalties, 57 without, 35 at a
+// plain copy's rate. An SM holds two CTAs (a thread's 40 values are registers), and
+// loads, list, exponentials, the cluster's barrier and stores follow each other
+// in both: issue slots and memory are each busy for less than half of the
+// time (34 instructions a value, 20 without penalties). What it took: loads of all
+// groups in flight at once (without counts 74 us before, 63 after), fp32 rows 32
+// bytes a lane, redux for the maximum, lists by groups (tokens by themselves 101,
+// groups 96), constant offsets between groups (93 to 81), the next rows on their
+// way to L2 (81 to 79). Rows streamed twice through shared memory instead of kept
+// took 115, three reads (kLoop) 585, clusters of 16 CTAs of 256 threads 85.
 template <typename TL, typename TP, bool kVec, int kThreads, int kGroups, bool kLoop>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_probs(const __grid_constant__ ProbsArgs a) {
     constexpr int kWarps = kThreads / 32;
@@ -495,6 +503,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_probs(const 
             for (int g = 0; g < kGroups; ++g) bits |= (uint64_t)r.allowed(g) << (8 * g);
         }
         const uint32_t own = r.load_all(bits, z);  // bit g: group g goes on the list
+        if constexpr (kVec) {
+            // what a CTA in this one's place will read: on its way to L2 while this one computes
+            if (tid == 0 && a.ahead > 0 && (int64_t)row + a.ahead < a.rows) {
+                const int64_t next = (int64_t)row + a.ahead;
+                prefetch_l2(r.logits + a.ahead * a.logits_stride + lo, (hi - lo) * (int32_t)sizeof(TL));
+                if (r.counts) prefetch_l2(a.counts + next / a.n_tok * a.count_stride + lo, (hi - lo) * 2);
+            }
+        }
         if (__any_sync(0xffffffffu, own != 0)) {
             int place[kGroups], n_list = 0;  // of this lane's groups on the list
 #pragma unroll
@@ -778,9 +794,10 @@ cudaError_t launch(const ProbsArgs &a, int64_t rows, cudaStream_t st) {
 }
 
 // Registers for as few groups as hold a slice: an idle group costs its
-// instructions (8 x 4 rows of 8000 5.4 us with 2 groups, 6.8 with 5). Few rows take 1024
-// threads with half the groups (4 rows of 100003 11.6 us against 14.5); many are
-// faster with CTAs of 512, two an SM (256 rows of 150000 93 us against 100).
+// instructions (8 x 4 rows of 8000 5.4 us with 2 groups, 6.8 with 5; 256 of 131000
+// 85 with 4, 91 with 5). Few rows take 1024 threads with half the groups (4 rows of
+// 100003 11.6 us against 14.5); many are faster with CTAs of 512, two an SM (256
+// rows of 150000 93 us against 100).
 template <typename TL, typename TP, bool kVec>
 cudaError_t launch_row(const ProbsArgs &a, int64_t rows, cudaStream_t st) {
     const int32_t groups = (a.slice / 8 + 511) / 512;  // of 512 threads
@@ -835,6 +852,7 @@ extern "C" int hswa_logits_probs(int logits_dtype, const void *logits, int64_t l
     a.bias_token = bias_token, a.bias = bias;
     a.mask = mask;
     a.n_bias = n_bias, a.n_tok = n_tok, a.vocab = vocab;
+    a.rows = (int32_t)rows;
     a.err = error_word();
     // CTAs per row: few rows spread over the GPU, in slices of at least 1024
     // values; many rows take as many as keep a thread's values in registers.
@@ -846,6 +864,7 @@ extern "C" int hswa_logits_probs(int logits_dtype, const void *logits, int64_t l
            (slice_of(a.cluster) > 512 * 8 * 5 || (rows * a.cluster * 2 <= 2 * sms && slice_of(a.cluster) >= 2048)))
         a.cluster *= 2;
     a.slice = slice_of(a.cluster);
+    a.ahead = rows * a.cluster > 2 * sms ? 2 * sms / a.cluster : 0;
     a.cluster_log2 = a.cluster == 8 ? 3 : a.cluster / 2;
     const bool vec = (x0 & 15) == 0 && (y0 & 15) == 0 && logits_stride * el % 16 == 0 && p_stride * ep % 16 == 0 &&
                      (!counts || (((uintptr_t)counts & 15) == 0 && count_stride % 8 == 0));
