@@ -2710,15 +2710,22 @@ bool decode_fp4_ok(const hswa_pool *pool, const hswa_layer *layer, const void *q
 template <class Shape>
 int fp4_workers() {
     static int cache[kMaxDevices] = {};
-    const int per_sm = kernel_setup(decode_mma_fp4_d128<Shape>, decode_smem4_bytes<Shape>(), 32 * Shape::kWarps, cache);
+    int per_sm = kernel_setup(decode_mma_fp4_d128<Shape, false>, decode_smem4_bytes<Shape>(), 32 * Shape::kWarps, cache);
+    if constexpr (Shape::kTok <= 2) {
+        static int planning[kMaxDevices] = {};
+        per_sm = std::min(per_sm, kernel_setup(decode_mma_fp4_d128<Shape, true>, decode_smem4_bytes<Shape>(), 32 * Shape::kWarps, planning));
+    }
     static_assert(Shape::kCtas * Shape::kWarps <= kFp4WorkersPerSm, "the workspace has records for that many");
     return per_sm <= 0 ? -1 : sm_count() * std::min(per_sm, Shape::kCtas) * Shape::kWarps;
 }
 
 template <class Shape>
 cudaError_t launch_decode_fp4(int workers, cudaStream_t st, const DecodeArgs &a) {
-    return launch_pdl(decode_mma_fp4_d128<Shape>, dim3(workers / Shape::kWarps), dim3(32 * Shape::kWarps),
-                      decode_smem4_bytes<Shape>(), st, a);
+    const dim3 grid(workers / Shape::kWarps), block(32 * Shape::kWarps);
+    if constexpr (Shape::kTok <= 2)
+        if (fp4_plans<Shape>(a.n_seqs))
+            return launch_pdl(decode_mma_fp4_d128<Shape, true>, grid, block, decode_smem4_bytes<Shape>(), st, a);
+    return launch_pdl(decode_mma_fp4_d128<Shape, false>, grid, block, decode_smem4_bytes<Shape>(), st, a);
 }
 
 // Query tokens per sequence from which an FP4 decode runs on the tensor-core
@@ -2880,8 +2887,10 @@ int decode_fp4(const hswa_pool *pool, const hswa_layer *layer, const void *q, vo
     CUtensorMap tq;
     if (tc && !make_q_tmap(&tq, q, c, n_seqs, n_tok)) return HSWA_ERR_CUDA;
     set_last_kernel(tc ? "decode_tc_fp4_d128" : slots ? "append_kv_fp4+decode_mma_fp4_d128" : "decode_mma_fp4_d128");
-    cudaError_t e = launch_pdl(decode_plan, dim3(1), dim3(plan_threads(n_seqs)), 0, st, d_seq_len, n_seqs, c.n_kv_heads, kP,
-                               a.window, n_tok, static_cast<int4 *>(ws), INT64_MAX, a.err);
+    cudaError_t e = cudaSuccess;
+    if (tc || !(n_tok == 1 ? fp4_plans<Fp4One>(n_seqs) : n_tok == 2 ? fp4_plans<Fp4Two>(n_seqs) : fp4_plans<Fp4Four>(n_seqs)))
+        e = launch_pdl(decode_plan, dim3(1), dim3(plan_threads(n_seqs)), 0, st, d_seq_len, n_seqs, c.n_kv_heads, kP, a.window,
+                       n_tok, static_cast<int4 *>(ws), INT64_MAX, a.err);
     if (e == cudaSuccess)
         e = tc           ? launch_decode_tc<DecodeTc4Smem>(n_tok, workers, st, tq, tq, tq, a)  // pages go by plain bulk copies
             : n_tok == 1 ? launch_decode_fp4<Fp4One>(workers, st, a)

@@ -50,6 +50,7 @@ using Fp4Two = Fp4Shape<2, 64, 4, 4, 2>;
 using Fp4Four = Fp4Shape<4, 32, 4, 6, 2>;
 constexpr int kFp4WorkersPerSm = 16;  // the most of these
 constexpr int kFp4Ahead = 8;          // units whose descriptors are made at once
+constexpr int kFp4PlanSeqs = 32;      // sequences whose descriptors every CTA makes for itself
 
 // K or V of kKeys keys.
 template <int kKeys>
@@ -72,6 +73,7 @@ struct DecodeSmem4 {
     // Q's fragments, where registers do not hold them
     uint4 q[Shape::kTok > 1 ? Shape::kWarps : 1][Shape::kPairs][8][Shape::kTok > 1 ? 32 : 1];
     Fp4Desc desc[Shape::kWarps][2 * kFp4Ahead];
+    int4 plan[kFp4PlanSeqs + 1];
 };
 template <class Shape>
 constexpr size_t decode_smem4_bytes() { return sizeof(DecodeSmem4<Shape>) + 128; }
@@ -94,6 +96,7 @@ __device__ __forceinline__ void copy16(uint32_t to, const uint8_t *from) {
 // Makes the descriptors of a worker's units [u0, u1), 8 at a time, a lane
 // each. A unit's table entry is loaded when those before it are written down.
 struct Fp4Units {
+    const int4 *sdesc;
     int32_t u0, u1, base, s;  // the next 8 units are base ..; s: the sequence of an earlier one
     int32_t page;
     Fp4Desc x;
@@ -103,8 +106,8 @@ struct Fp4Units {
         const int32_t u = base + lane;
         int32_t mine = s;
         if (lane < kFp4Ahead && u < u1) {
-            int4 d = a.sdesc[mine];
-            while (u >= d.x + d.w) d = a.sdesc[++mine];
+            int4 d = sdesc[mine];
+            while (u >= d.x + d.w) d = sdesc[++mine];
             const int32_t npg = d.w / a.hkv, pf = d.y / kP;
             const int32_t g = (u - d.x) / npg, p = u - d.x - g * npg;
             const int32_t seg = u - p;  // the segment's first unit
@@ -118,8 +121,9 @@ struct Fp4Units {
         }
         s = __shfl_sync(0xffffffffu, mine, max(min(kFp4Ahead, u1 - base) - 1, 0));
     }
-    __device__ __forceinline__ Fp4Units(const DecodeArgs &a, int32_t u0_, int32_t u1_) : u0(u0_), u1(u1_), base(u0_) {
-        s = find_seq(a.sdesc, a.n_seqs, u0);
+    __device__ __forceinline__ Fp4Units(const DecodeArgs &a, const int4 *sdesc_, int32_t u0_, int32_t u1_)
+        : sdesc(sdesc_), u0(u0_), u1(u1_), base(u0_) {
+        s = find_seq(sdesc, a.n_seqs, u0);
         fetch(a);
     }
     // Write the next 8 down.
@@ -150,8 +154,8 @@ __device__ __forceinline__ void fp4_store(__nv_bfloat16 *to, const float (&f)[16
 
 // One worker.
 template <class Shape>
-__device__ void decode_fp4_worker(DecodeSmem4<Shape> &sm, const DecodeArgs &a, int32_t u0, int32_t u1,
-                                  int32_t worker) {
+__device__ void decode_fp4_worker(DecodeSmem4<Shape> &sm, const DecodeArgs &a, const int4 *sdesc, int32_t u0,
+                                  int32_t u1, int32_t worker) {
     constexpr int kTok = Shape::kTok, kPairs = Shape::kPairs, kParts = Shape::kParts, kTiles = Shape::kTiles;
     constexpr int kSteps = Shape::kSteps, kKeys = Shape::kKeys;
     using Part = Fp4Part<kKeys>;
@@ -164,7 +168,7 @@ __device__ void decode_fp4_worker(DecodeSmem4<Shape> &sm, const DecodeArgs &a, i
     const uint8_t *const ksp = reinterpret_cast<const uint8_t *>(a.k_scale) + lane * 16, *const vsp = reinterpret_cast<const uint8_t *>(a.v_scale) + lane * 16;
     const uint32_t parts0 = smem_u32(sm.part[w]);
     const int32_t parts = 2 * kSteps * (u1 - u0);
-    Fp4Units units(a, u0, u1);
+    Fp4Units units(a, sdesc, u0, u1);
     Fp4Desc *const desc = sm.desc[w];
     int32_t described = 0;
     // Part c: K (c even) or V of step c / 2, into buffer st; a group of copies of its own.
@@ -502,14 +506,46 @@ __device__ void decode_fp4_worker(DecodeSmem4<Shape> &sm, const DecodeArgs &a, i
     }
 }
 
+// decode_plan by one warp, for at most kFp4PlanSeqs sequences: descriptors into
+// plan, and from the first CTA into the workspace, for the merge.
+__device__ __forceinline__ void fp4_plan(const DecodeArgs &a, int4 *plan) {
+    const int lane = threadIdx.x & 31;
+    int32_t u = 0, lo = 0, hi = 0;
+    if (lane < a.n_seqs) key_range(a.seq_len[lane], a.window, a.n_tok, lo, hi);
+    if (hi > lo) u = a.hkv * ((hi - 1) / kP - lo / kP + 1);
+    int32_t x = u;
+    for (int off = 1; off < 32; off <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+    }
+    const int32_t all = __shfl_sync(0xffffffffu, x, 31);
+    for (int4 *out : {plan, blockIdx.x == 0 ? const_cast<int4 *>(a.sdesc) : nullptr}) {
+        if (!out) continue;
+        if (lane < a.n_seqs) out[lane] = make_int4(x - u, lo, hi, u);
+        if (lane == 0) out[a.n_seqs] = make_int4(all, 0, 0, 0);
+    }
+}
+static_assert(kFp4PlanSeqs <= 32, "a lane each");
+
+// kPlan: without decode_plan before it, one launch less (3 sequences of 700 to
+// 2500 tokens 12.5 us against 13.3). With 64 sequences it was 1 us slower, and with
+// Fp4Four's registers 10 (570 us).
 template <class Shape>
+bool fp4_plans(int n_seqs) { return Shape::kTok <= 2 && n_seqs <= kFp4PlanSeqs; }
+template <class Shape, bool kPlan>
 __global__ void __launch_bounds__(32 * Shape::kWarps, Shape::kCtas) decode_mma_fp4_d128(const __grid_constant__ DecodeArgs a) {
     extern __shared__ uint8_t raw[];
     using Smem = DecodeSmem4<Shape>;
+    static_assert(Shape::kCtas * (decode_smem4_bytes<Shape>() + 1024) <= 228 << 10, "kCtas CTAs on an SM");
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(raw) + 127) & ~uintptr_t(127));
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t U = a.sdesc[a.n_seqs].x, N = (int64_t)gridDim.x * Shape::kWarps;
+    if constexpr (kPlan) {
+        if (threadIdx.x < 32) fp4_plan(a, sm.plan);
+        __syncthreads();
+    }
+    const int4 *const sdesc = kPlan ? sm.plan : a.sdesc;
+    const int64_t U = sdesc[a.n_seqs].x, N = (int64_t)gridDim.x * Shape::kWarps;
     const int32_t worker = blockIdx.x * Shape::kWarps + (threadIdx.x >> 5);
-    decode_fp4_worker<Shape>(sm, a, (int32_t)cta_start(worker, U, N), (int32_t)cta_start(worker + 1, U, N), worker);
+    decode_fp4_worker<Shape>(sm, a, sdesc, (int32_t)cta_start(worker, U, N), (int32_t)cta_start(worker + 1, U, N), worker);
 }

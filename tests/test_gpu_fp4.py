@@ -290,6 +290,19 @@ def test_decode_batch_long_and_many():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n_tok", [1, 2, 4])
+@pytest.mark.parametrize("B", [1, 31, 32, 33])
+def test_decode_where_the_plan_changes_hands(B, n_tok):
+    """Up to 32 sequences of one or two tokens have no launch for the plan; some are empty."""
+    rng = np.random.default_rng(B)
+    cached = [0 if i % 5 == 3 else int(x) for i, x in enumerate(rng.integers(0, 900, B))]
+    c = Case(cached, seed=120 + B, extra=16)
+    for i in range(2):
+        step(c, n_tok, 3100 + 100 * i)
+        c.sess.release(range(B))
+
+
+@pytest.mark.gpu
 def test_equal_inputs_equal_bits_captured_and_on_a_stream():
     """The same call again, from a graph, and on a side stream."""
     c = Case([700, 3000, 0, 65], seed=110, extra=16)
