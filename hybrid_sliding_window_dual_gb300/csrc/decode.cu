@@ -2848,6 +2848,52 @@ int decode_fp8(const hswa_pool *pool, const hswa_layer *layer, const void *q, vo
     return e == cudaSuccess ? HSWA_OK : HSWA_ERR_CUDA;
 }
 
+// Decode over FP4 pools of other shapes.
+int launch_decode_fp4_any(const hswa_pool *pool, const hswa_layer *layer, const void *q, void *o, const int32_t *d_bt,
+                          const int32_t *d_seq_len, int n_seqs, int n_tok, float scale, cudaStream_t st) {
+    const hswa_config &c = pool->cfg;
+    const int64_t rows = (int64_t)n_seqs * n_tok;
+    const int32_t group = c.n_q_heads / c.n_kv_heads;
+    const int64_t heads = (int64_t)c.n_kv_heads * ((group + kFp4AnyHeads - 1) / kFp4AnyHeads);
+    if (c.head_dim > kFp4AnyMaxD) return HSWA_ERR_UNSUPPORTED;
+    if ((((uintptr_t)layer->k_pool) & 7) || rows > INT32_MAX || heads > 65535)  // codes come 8 bytes at a time
+        return launch_attention_generic(pool, layer, q, o, d_bt, d_seq_len, nullptr, nullptr, (int32_t)rows, n_seqs, scale, 0,
+                                        st, n_tok);
+    Fp4AnyArgs a;
+    a.q = static_cast<const __nv_bfloat16 *>(q), a.o = static_cast<__nv_bfloat16 *>(o);
+    a.k = static_cast<const uint8_t *>(layer->k_pool), a.v = static_cast<const uint8_t *>(layer->v_pool);
+    a.ks = reinterpret_cast<const uint8_t *>(layer->k_scale), a.vs = reinterpret_cast<const uint8_t *>(layer->v_scale);
+    a.bt = d_bt, a.seq_len = d_seq_len;
+    a.n_tok = n_tok, a.bt_stride = c.max_pages_per_seq, a.hq = c.n_q_heads, a.hkv = c.n_kv_heads, a.d = c.head_dim;
+    a.page = c.page_size, a.window = layer->kind == HSWA_KIND_SWA ? layer->window : 0;
+    a.num_pages = layer->kind == HSWA_KIND_SWA ? c.swa_pages : c.full_pages;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.err = error_word();
+    // CTAs of a row: few rows are spread over the GPU
+    const int sms = sm_count();
+    if (sms <= 0) return HSWA_ERR_CUDA;
+    a.cluster = 1;
+    while (a.cluster < kFp4AnyCluster && rows * heads * a.cluster * 2 <= 2 * sms) a.cluster *= 2;
+    if (rows * a.cluster > INT32_MAX) return HSWA_ERR_UNSUPPORTED;
+    set_last_kernel("decode_fp4_any");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * a.cluster), (unsigned)heads);
+    cfg.blockDim = dim3(32 * kFp4AnyWarps);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = a.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = c.head_dim <= 64    ? cudaLaunchKernelEx(&cfg, decode_fp4_any<1>, a)
+                          : c.head_dim <= 128 ? cudaLaunchKernelEx(&cfg, decode_fp4_any<2>, a)
+                                              : cudaLaunchKernelEx(&cfg, decode_fp4_any<4>, a);
+    return e == cudaSuccess ? HSWA_OK : cuda_fail(e, "decode_fp4_any");
+}
+
 // Decode over an FP4 pool (a fused append quantizes first, as its own launch).
 int decode_fp4(const hswa_pool *pool, const hswa_layer *layer, const void *q, void *o, const int32_t *d_bt,
                const int32_t *d_seq_len, int n_seqs, int n_tok, float scale, void *ws, size_t ws_bytes,
@@ -2878,9 +2924,7 @@ int decode_fp4(const hswa_pool *pool, const hswa_layer *layer, const void *q, vo
         const int rc = hswa_append_kv(pool, layer, k_new, v_new, slots, n_seqs, stream);
         if (rc != HSWA_OK) return rc;
     }
-    if (!fast)
-        return launch_attention_generic(pool, layer, q, o, d_bt, d_seq_len, nullptr, nullptr, n_seqs * n_tok, n_seqs,
-                                        scale, 0, st, n_tok);
+    if (!fast) return launch_decode_fp4_any(pool, layer, q, o, d_bt, d_seq_len, n_seqs, n_tok, scale, st);
     DecodeArgs a;
     fill_args(a, pool, layer, q, o, d_bt, d_seq_len, n_seqs, scale, ws);
     a.n_tok = n_tok;

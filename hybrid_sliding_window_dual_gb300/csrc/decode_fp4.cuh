@@ -549,3 +549,198 @@ __global__ void __launch_bounds__(32 * Shape::kWarps, Shape::kCtas) decode_mma_f
     const int32_t worker = blockIdx.x * Shape::kWarps + (threadIdx.x >> 5);
     decode_fp4_worker<Shape>(sm, a, sdesc, (int32_t)cta_start(worker, U, N), (int32_t)cta_start(worker + 1, U, N), worker);
 }
+
+// Other shapes (any head size in blocks, head ratio and page): a cluster per
+// query row, kv head and up to four of its query heads, whose warps take tiles of
+// 32 keys in turn. Scores: a lane has a key, q comes from shared memory; a block's
+// sum of q times codes is multiplied by its scale. Output: a lane has bytes of
+// the row, pairs of elements. All in fp32. Bound by a few dependent steps where there
+// are few keys, by instructions otherwise (each element of K and V is converted for
+// four heads). d = 64, 4 heads on one: 16 sequences of 1000 to 2000 tokens 17 us (one
+// CTA a row 41, a warp a row and head 2440); d = 128, 32 heads on 8: 64 of 1K to 8K
+// 604 (with registers for one CTA an SM 866; a warp a row and head 16900), one of
+// 30000 135. 8 warps a CTA: 14, 1022 and 214.
+struct Fp4AnyArgs {
+    const __nv_bfloat16 *q;
+    __nv_bfloat16 *o;
+    const uint8_t *k, *v, *ks, *vs;
+    const int32_t *bt, *seq_len;
+    int32_t n_tok, bt_stride, hq, hkv, d, page, window, num_pages, cluster;
+    float scale_log2;
+    int *err;
+};
+
+constexpr int kFp4AnyHeads = 4, kFp4AnyWarps = 16, kFp4AnyMaxD = 256, kFp4AnyCluster = 8;
+
+// kE: bytes of a row that a lane has.
+template <int kE>
+__global__ void __launch_bounds__(32 * kFp4AnyWarps, kE <= 2 ? 2 : 1) decode_fp4_any(const Fp4AnyArgs a) {
+    constexpr int kH = kFp4AnyHeads, kW = kFp4AnyWarps;
+    __shared__ __align__(16) float q[kH][kFp4AnyMaxD];  // then the CTA's output
+    __shared__ __align__(16) float4 ps[kW][32];   // P of the four heads
+    __shared__ int64_t rows[kW][32];              // rows of V
+    __shared__ float2 ml[kW][kH];                 // a warp's reference and sum
+    __shared__ float2 cta_ml[kH];                 // those of the CTA
+    __shared__ __align__(16) float sum[kH][2 * 32 * kE][4];  // four warps' outputs
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int32_t group = a.hq / a.hkv, chunks = (group + kH - 1) / kH;
+    const int32_t rank = blockIdx.x % a.cluster;
+    const int64_t row = blockIdx.x / a.cluster;  // sequence n_tok + query token
+    const int32_t s = (int32_t)(row / a.n_tok), g = blockIdx.y / chunks, h0 = blockIdx.y % chunks * kH;
+    const int32_t heads = min(kH, group - h0);
+    const int64_t head0 = row * a.hq + g * group + h0;  // first of the CTA's in q and o
+    const int32_t t = a.seq_len[s] - a.n_tok + (int32_t)(row - (int64_t)s * a.n_tok);
+    const int32_t hi = t + 1, lo = a.window > 0 ? max(0, hi - a.window) : 0;
+    for (int i = threadIdx.x; i < kH * a.d; i += 32 * kW) {
+        const int h = i / a.d, c = i - h * a.d;
+        q[h][c] = h < heads ? __bfloat162float(a.q[(head0 + h) * a.d + c]) * a.scale_log2 : 0.f;
+    }
+    __syncthreads();
+    float m[kH], l[kH], acc[kH][kE][2];
+#pragma unroll
+    for (int h = 0; h < kH; ++h) {
+        m[h] = -INFINITY, l[h] = 0.f;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) acc[h][e][0] = acc[h][e][1] = 0.f;
+    }
+    const int32_t bytes = a.d / 2, blocks = a.d / kFp4Block;
+    for (int64_t at = lo + 32 * (rank * kW + w); at < hi; at += 32 * kW * a.cluster) {
+        const int32_t j0 = (int32_t)at, j = j0 + lane;
+        int64_t key = -1;
+        if (j < hi) {
+            const int32_t lp = j / a.page, pg = lp < a.bt_stride ? a.bt[(int64_t)s * a.bt_stride + lp] : -1;
+            if (pg >= 0 && pg < a.num_pages)
+                key = ((int64_t)pg * a.hkv + g) * a.page + (j - lp * a.page);
+            else
+                set_error(a.err, HSWA_ERR_BOUNDS);
+        }
+        float x[kH] = {};
+        if (key >= 0) {
+            const uint2 *codes = reinterpret_cast<const uint2 *>(a.k + key * bytes);
+            const uint8_t *scales = a.ks + key * blocks;
+#pragma unroll 4
+            for (int32_t b = 0; b < blocks; ++b) {
+                const uint2 c = codes[b];
+                const float scale = scale_value(scales[b]);
+                uint32_t p[8];
+                e2m1x8_f16(c.x, p[0], p[1], p[2], p[3]);
+                e2m1x8_f16(c.y, p[4], p[5], p[6], p[7]);
+                float part[kH] = {};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 u = __half22float2(*reinterpret_cast<const __half2 *>(&p[2 * i])), v = __half22float2(*reinterpret_cast<const __half2 *>(&p[2 * i + 1]));
+#pragma unroll
+                    for (int h = 0; h < kH; ++h) {
+                        const float4 y = *reinterpret_cast<const float4 *>(&q[h][16 * b + 4 * i]);
+                        part[h] = fmaf(y.w, v.y, fmaf(y.z, v.x, fmaf(y.y, u.y, fmaf(y.x, u.x, part[h]))));
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < kH; ++h) x[h] = fmaf(part[h], scale, x[h]);
+            }
+        }
+        float p[kH];
+#pragma unroll
+        for (int h = 0; h < kH; ++h) {
+            if (key < 0) x[h] = -INFINITY;
+            float top = x[h];
+            for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const float next = fmaxf(m[h], top);
+            const float alpha = next == -INFINITY ? 1.f : fast_exp2(m[h] - next);
+            p[h] = next == -INFINITY ? 0.f : fast_exp2(x[h] - next);
+            l[h] = l[h] * alpha + p[h];
+            m[h] = next;
+#pragma unroll
+            for (int e = 0; e < kE; ++e) acc[h][e][0] *= alpha, acc[h][e][1] *= alpha;
+        }
+        ps[w][lane] = make_float4(p[0], p[1], p[2], p[3]);
+        rows[w][lane] = key < 0 ? 0 : key;  // a row that P takes 0 times
+        __syncwarp();
+        const int32_t n = min(32, hi - j0);
+#pragma unroll 8
+        for (int32_t i = 0; i < n; ++i) {
+            const float4 pi = ps[w][i];
+            const int64_t r = rows[w][i];
+#pragma unroll
+            for (int e = 0; e < kE; ++e) {
+                const int32_t c = lane + 32 * e;
+                if (c >= bytes) continue;
+                const float scale = scale_value(a.vs[r * blocks + c / 8]);
+                uint32_t f;
+                asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t}" : "=r"(f) : "r"((uint32_t)a.v[r * bytes + c]));
+                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&f));
+                const float v0 = v.x * scale, v1 = v.y * scale;
+                acc[0][e][0] = fmaf(pi.x, v0, acc[0][e][0]), acc[0][e][1] = fmaf(pi.x, v1, acc[0][e][1]);
+                acc[1][e][0] = fmaf(pi.y, v0, acc[1][e][0]), acc[1][e][1] = fmaf(pi.y, v1, acc[1][e][1]);
+                acc[2][e][0] = fmaf(pi.z, v0, acc[2][e][0]), acc[2][e][1] = fmaf(pi.z, v1, acc[2][e][1]);
+                acc[3][e][0] = fmaf(pi.w, v0, acc[3][e][0]), acc[3][e][1] = fmaf(pi.w, v1, acc[3][e][1]);
+            }
+        }
+        __syncwarp();
+    }
+    // the warps' outputs relative to the CTA's largest reference, four warps at a time
+#pragma unroll
+    for (int h = 0; h < kH; ++h) {
+        for (int off = 16; off > 0; off >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
+        if (lane == 0) ml[w][h] = make_float2(m[h], l[h]);
+    }
+    __syncthreads();
+    float f[kH];
+#pragma unroll
+    for (int h = 0; h < kH; ++h) {
+        const float2 x = ml[lane % kW][h];
+        float top = x.x;
+        for (int off = kW / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        float L = x.x > -INFINITY ? x.y * fast_exp2(x.x - top) : 0.f;
+        for (int off = kW / 2; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+        f[h] = m[h] > -INFINITY ? fast_exp2(m[h] - top) : 0.f;
+        if (threadIdx.x == 0) cta_ml[h] = make_float2(top, L);
+    }
+    for (int from = 0; from < kW; from += 4) {
+        if (w >= from && w < from + 4) {
+#pragma unroll
+            for (int h = 0; h < kH; ++h)
+#pragma unroll
+                for (int e = 0; e < kE; ++e)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float &to = sum[h][2 * (lane + 32 * e) + i][w - from];
+                        to = (from ? to : 0.f) + acc[h][e][i] * f[h];
+                    }
+        }
+        __syncthreads();
+    }
+    for (int i = threadIdx.x; i < heads * a.d; i += 32 * kW) {
+        const int h = i / a.d, c = i - h * a.d;
+        const float4 x = *reinterpret_cast<const float4 *>(sum[h][c]);
+        q[h][c] = (x.x + x.y) + (x.z + x.w);
+    }
+    // and the CTAs', each of them joining a share of the elements
+    cluster_arrive();
+    cluster_wait();
+    for (int i = rank * 32 * kW + threadIdx.x; i < heads * a.d; i += a.cluster * 32 * kW) {
+        const int h = i / a.d, c = i - h * a.d;
+        float ref[kFp4AnyCluster], part_l[kFp4AnyCluster], part[kFp4AnyCluster];
+#pragma unroll
+        for (int r = 0; r < kFp4AnyCluster; ++r) {
+            const int from = min(r, a.cluster - 1);  // all loads at once, some for nothing
+            ref[r] = ld_cluster_f32(&cta_ml[h].x, from);
+            part_l[r] = ld_cluster_f32(&cta_ml[h].y, from);
+            part[r] = ld_cluster_f32(&q[h][c], from);
+        }
+        float top = -INFINITY, L = 0.f, x = 0.f;
+#pragma unroll
+        for (int r = 0; r < kFp4AnyCluster; ++r) top = fmaxf(top, ref[r]);
+#pragma unroll
+        for (int r = 0; r < kFp4AnyCluster; ++r) {
+            const float weight = r < a.cluster && ref[r] > -INFINITY ? fast_exp2(ref[r] - top) : 0.f;
+            L = fmaf(weight, part_l[r], L);
+            x = fmaf(weight, part[r], x);
+        }
+        a.o[(head0 + h) * a.d + c] = __float2bfloat16_rn(L > 0.f ? x / L : 0.f);
+    }
+    cluster_arrive();
+    cluster_wait();  // nobody leaves while its results are read
+}

@@ -230,8 +230,8 @@ def test_decode_head_counts_and_magnitudes(n_tok, hkv):
 def test_other_shapes(hq, hkv, d, P, W):
     """The shapes off the tensor cores: decode, several tokens, and a prefill chunk."""
     c = Case([0, 1, 15, 16, 63, 200], seed=104, extra=40, hq=hq, hkv=hkv, d=d, P=P, W=W)
-    assert step(c, 1, seed=2300) == {"decode_generic_fp4"}
-    assert step(c, 3, seed=2310) == {"decode_generic_fp4"}
+    assert step(c, 1, seed=2300) == {"decode_fp4_any"}
+    assert step(c, 3, seed=2310) == {"decode_fp4_any"}
     prefill(c, [1, 5, 17, 3, 9, 20], seed=2320)
 
 
