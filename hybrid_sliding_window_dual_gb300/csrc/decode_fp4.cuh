@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(32 * kFp4AnyWarps, kE <= 2 ? 2 : 1) decode_fp4
             for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
             const float next = fmaxf(m[h], top);
             const float alpha = next == -INFINITY ? 1.f : fast_exp2(m[h] - next);
-            p[h] = next == -INFINITY ? 0.f : fast_exp2(x[h] - next);
+            p[h] = x[h] == -INFINITY ? 0.f : fast_exp2(x[h] - (next == -INFINITY ? 0.f : next));  // a NaN stays one
             l[h] = l[h] * alpha + p[h];
             m[h] = next;
 #pragma unroll
@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(32 * kFp4AnyWarps, kE <= 2 ? 2 : 1) decode_fp4
         const float2 x = ml[lane % kW][h];
         float top = x.x;
         for (int off = kW / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        float L = x.x > -INFINITY ? x.y * fast_exp2(x.x - top) : 0.f;
+        float L = x.y * (x.x > -INFINITY ? fast_exp2(x.x - top) : 0.f);
         for (int off = kW / 2; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
         f[h] = m[h] > -INFINITY ? fast_exp2(m[h] - top) : 0.f;
         if (threadIdx.x == 0) cta_ml[h] = make_float2(top, L);
@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(32 * kFp4AnyWarps, kE <= 2 ? 2 : 1) decode_fp4
             L = fmaf(weight, part_l[r], L);
             x = fmaf(weight, part[r], x);
         }
-        a.o[(head0 + h) * a.d + c] = __float2bfloat16_rn(L > 0.f ? x / L : 0.f);
+        a.o[(head0 + h) * a.d + c] = __float2bfloat16_rn(L == 0.f ? 0.f : x / L);
     }
     cluster_arrive();
     cluster_wait();  // nobody leaves while its results are read

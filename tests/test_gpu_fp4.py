@@ -235,6 +235,30 @@ def test_other_shapes(hq, hkv, d, P, W):
     prefill(c, [1, 5, 17, 3, 9, 20], seed=2320)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,d,P", [(4, 1, 64, 16), (6, 2, 96, 16)])
+def test_other_shapes_nan_stays_in_its_head(hq, hkv, d, P):
+    """A NaN in a head's query makes that head's output NaN and no other's."""
+    c = Case([0, 5, 40, 700], seed=130, extra=10, hq=hq, hkv=hkv, d=d, P=P)
+    c.sess.reserve(range(c.B), [1] * c.B)
+    c.sess.sync()
+    q = wl.normal((c.B, hq, d), 3300, wl.DTYPE_BF16).cuda()
+    out = []
+    for bad in (False, True):
+        if bad:
+            q[1, 0, 3] = q[3, hq - 1, d - 1] = float("nan")
+        for layer in range(2):
+            o = torch.zeros_like(q)
+            c.sess.decode(layer, q, o, c.B, c.scale)
+            out.append(o)
+    assert c.sess.check() == 0
+    for clean, got in zip(out[:2], out[2:]):
+        nan = torch.zeros_like(got, dtype=torch.bool)
+        nan[1, 0] = nan[3, hq - 1] = True
+        assert torch.equal(got.isnan(), nan)
+        assert torch.equal(got[~nan], clean[~nan])
+
+
 def prefill(c, chunk, seed):
     _, _, cached = c.sess.tables()
     slots = c.sess.reserve(range(c.B), chunk)
