@@ -431,7 +431,8 @@ __global__ void __launch_bounds__(256, kMinCtas) rope_append_vec(const __grid_co
 // / 4) 1024 6.7 / 6.6, 2048 12.2 / 11.5; 640 (64 / 8) 2048 15.9 / 19.8, 4096 36.9 /
 // 32.2; fp32 32 / 4 heads 2048 13.3 / 16.8, 4096 32.4 / 32.0, 64 / 8 4096 52 / 58,
 // 16384 equal; FP8 32 / 4 1024 9.2 / 9.4, 2048 16.0 / 11.2, 64 / 8 1280 14.5 / 16.0, 1536
-// 17.1 / 16.4. (Up to 16 tokens a CTA for few heads gained nothing.)
+// 17.1 / 16.4; FP4 64 / 8 2560 25.7 / 26.0, 4096 40.5 / 33.7, 32 / 4 4096 27.0 /
+// 18.0. (Up to 16 tokens a CTA for few heads gained nothing.)
 template <typename T, int kQuant>
 int tile_from(int threads) {
     if (threads <= 160) return 640;
@@ -449,7 +450,9 @@ cudaError_t launch_rope_vec(const RopeArgs &a, cudaStream_t st) {
     const int64_t vt = tiled ? kVTile : 8;
     const int64_t nv = kQuant == 8 ? (a.n_tokens + vt - 1) / vt * a.hkv : 0;
     const dim3 grid((unsigned)(nq + nv)), block(units, 256 / units);
-    constexpr int kItems = kQuant || kAdjacent ? 3 : 2, kMinCtas = kQuant || kAdjacent ? 4 : 5;
+    // FP4, 32768 tokens of 64 / 8 heads: 216 us with 2 items, 224 with 3; 188 at a plain
+    // copy's rate, the quantizer's instructions between
+    constexpr int kItems = kQuant == 8 || kAdjacent ? 3 : 2, kMinCtas = kQuant || kAdjacent ? 4 : 5;
     return tiled ? launch_pdl(rope_append_vec<T, kQuant, kAdjacent, kMaxTile, kItems, kMinCtas>, grid, block, 0, st, a, (int32_t)nq)
                  : launch_pdl(rope_append_vec<T, kQuant, kAdjacent, 1, 3, 4>, grid, block, 0, st, a, (int32_t)nq);
 }
