@@ -26,6 +26,8 @@
 // Instinct MI355X", EAGLE3 section): up to 3 tokens the same kernel with one
 // consumer warp per token; 4 to 16 tokens a tcgen05 kernel whose
 // (token, head) rows form one M = 128 tile ("tensor-core multi-token" below).
+// FP4 pools: up to 4 tokens decode_mma_fp4_d128, other shapes decode_fp4_any
+// (decode_fp4.cuh); 5 to 16 tokens the tcgen05 kernel.
 // Generic path (any dtype / head_dim / ratio / page): one warp per
 // (sequence, query head) with CUDA-core dot products.
 #include <algorithm>
@@ -1170,7 +1172,7 @@ struct DecodeTcSmem {
     static constexpr bool kTcQ = true;
     static constexpr bool kWeights = false;
     static constexpr bool kQTmem = false;  // QK reads q from shared memory
-    [[maybe_unused]] static constexpr int kGroups = 0, kConvThreads = 1, kConvWarp = 7;  // no converters
+    static constexpr int kGroups = 0, kConvThreads = 1;  // no converters
     static constexpr int kThreads = 224;
     static constexpr uint32_t kQHalfBytes = 128 * 128;  // 128 rows x 64 columns of 16-bit values
     uint8_t k[kStages][kPageHeadBytes];                // [d half][64 keys][128 B], 128-byte swizzle
