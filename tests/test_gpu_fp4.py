@@ -236,6 +236,17 @@ def test_other_shapes(hq, hkv, d, P, W):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,d,P", [(4, 1, 64, 16), (10, 2, 80, 16), (3, 1, 256, 64)])
+@pytest.mark.parametrize("cached", [[9000, 4100, 3], [5 + 37 * i for i in range(45)]])
+def test_other_shapes_long_and_many(cached, hq, hkv, d, P):
+    """Several tiles of keys a warp; one CTA a row and eight."""
+    c = Case(cached, seed=140, extra=30, hq=hq, hkv=hkv, d=d, P=P, W=1000, wild=True)
+    step(c, 1, seed=3400)
+    c.sess.release(range(c.B))
+    step(c, 4, seed=3410)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("hq,hkv,d,P", [(4, 1, 64, 16), (6, 2, 96, 16)])
 def test_other_shapes_nan_stays_in_its_head(hq, hkv, d, P):
     """A NaN in a head's query makes that head's output NaN and no other's."""
