@@ -33,7 +33,7 @@ struct ProbsArgs {
     const float *bias;        // [n_seqs][n_bias]
     const uint32_t *mask;
     bool wide;                // fp32 rows start on 32 bytes
-    int32_t n_bias, n_tok, vocab, cluster, cluster_log2, slice;  // slice: elements per CTA, a multiple of 8
+    int32_t n_bias, n_tok, vocab, cluster, slice;  // slice: elements per CTA, a multiple of 8
     int32_t rows, ahead;  // ahead: rows that run at once, 0 if all do
     int *err;
 };
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_probs(const 
     cluster_arrive();
     pdl_wait();
     pdl_launch_dependents();
-    const uint32_t rank = blockIdx.x & (a.cluster - 1), row = blockIdx.x >> a.cluster_log2;
+    const uint32_t row = blockIdx.x / (uint32_t)a.cluster, rank = blockIdx.x - row * a.cluster;
     const uint32_t seq = row / (uint32_t)a.n_tok;
     const int32_t w = (int32_t)(row - seq * a.n_tok);
     float temperature = 1.f, rep = 1.f, freq = 0.f, pres = 0.f;
@@ -793,6 +793,10 @@ cudaError_t launch(const ProbsArgs &a, int64_t rows, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, logits_probs<TL, TP, kVec, kThreads, kGroups, kLoop>, a);
 }
 
+// The groups that a thread of a CTA of 512 has registers for, where a slice needs n.
+constexpr int kRowGroups = 5;
+int row_groups(int n) { return n <= 2 ? 2 : n <= 4 ? 4 : n; }
+
 // Registers for as few groups as hold a slice: an idle group costs its
 // instructions (8 x 4 rows of 8000 5.4 us with 2 groups, 6.8 with 5; 256 of 131000
 // 85 with 4, 91 with 5). Few rows take 1024 threads with half the groups (4 rows of
@@ -855,17 +859,26 @@ extern "C" int hswa_logits_probs(int logits_dtype, const void *logits, int64_t l
     a.rows = (int32_t)rows;
     a.err = error_word();
     // CTAs per row: few rows spread over the GPU, in slices of at least 1024
-    // values; many rows take as many as keep a thread's values in registers.
+    // values; many rows take as many as keep a thread's values in registers (256 rows of
+    // 100000 on 5 CTAs of 5 groups 54 us, on 8 of 4 64; of 50000 on 3 of 5 35, on 7 of 2 44).
     const int sms = sm_count();
     if (sms <= 0) return HSWA_ERR_CUDA;
     const auto slice_of = [&](int c) { return ((vocab + 8 * c - 1) / (8 * c)) * 8; };
     a.cluster = 1;
-    while (a.cluster < kMaxCluster &&
-           (slice_of(a.cluster) > 512 * 8 * 5 || (rows * a.cluster * 2 <= 2 * sms && slice_of(a.cluster) >= 2048)))
-        a.cluster *= 2;
+    if (rows * 4 <= 2 * sms) {
+        while (a.cluster < kMaxCluster &&
+               (slice_of(a.cluster) > kRowGroups * 4096 || (rows * a.cluster * 2 <= 2 * sms && slice_of(a.cluster) >= 2048)))
+            a.cluster *= 2;
+    } else {  // of those that hold the row, where a CTA costs its groups and about three more
+        int best = INT32_MAX;
+        for (int c = kMaxCluster; c >= 1; --c) {
+            const int groups = row_groups((slice_of(c) + 4095) / 4096);
+            if (groups > kRowGroups && c < kMaxCluster) break;
+            if (c * (groups + 3) < best) best = c * (groups + 3), a.cluster = c;
+        }
+    }
     a.slice = slice_of(a.cluster);
     a.ahead = rows * a.cluster > 2 * sms ? 2 * sms / a.cluster : 0;
-    a.cluster_log2 = a.cluster == 8 ? 3 : a.cluster / 2;
     const bool vec = (x0 & 15) == 0 && (y0 & 15) == 0 && logits_stride * el % 16 == 0 && p_stride * ep % 16 == 0 &&
                      (!counts || (((uintptr_t)counts & 15) == 0 && count_stride % 8 == 0));
     a.wide = (el == 2 || ((x0 & 31) == 0 && logits_stride % 8 == 0)) && (ep == 2 || ((y0 & 31) == 0 && p_stride % 8 == 0));
