@@ -122,7 +122,7 @@ struct ProbsRow {
     int32_t lo, hi;  // this CTA's tokens
     int32_t w;
     bool specials;
-    float rep, inv_rep, freq, pres;  // inv_rep 0: divide
+    float rep, freq, pres;
 
     // Element e of group k, counted from a thread's first (kVec: 8 neighbours, else
     // 8 as far apart as the CTA has threads).
@@ -136,16 +136,7 @@ struct ProbsRow {
 
     __device__ __forceinline__ float penalized(float z, uint32_t c, int extra) const {
         const int32_t n = (int32_t)(c & 0x7fff) + extra;
-        if (n > 0 || c >> 15) {
-            if (inv_rep > 0.f) {
-                // z / rep: the product with 1 / rep, corrected by its remainder
-                float q = __fmul_rn(z, inv_rep);
-                q = __fmaf_rn(__fmaf_rn(-rep, q, z), inv_rep, q);
-                z = z > 0.f ? (z <= FLT_MAX ? q : z) : __fmul_rn(z, rep);
-            } else {
-                z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
-            }
-        }
+        if (n > 0 || c >> 15) z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
         if (n > 0) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, (float)n)), pres);
         return z;
     }
@@ -457,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_probs(const 
                                penalties ? a.counts + seq * a.count_stride : nullptr,
                                a.mask ? a.mask + row * a.mask_stride : nullptr,
                                a.bias + (size_t)seq * a.n_bias, lo, hi, drafts ? w : 0, a.n_bias > 0 || drafts,
-                               rep, rep >= 0x1p-64f && rep <= 0x1p64f ? __frcp_rn(rep) : 0.f, freq, pres};
+                               rep, freq, pres};
     if (r.specials) {
         if (a.n_bias)
             for (int i = tid; i < kBiasSlots; i += kThreads) sm.key[i] = sm.at[i] = -1;

@@ -260,3 +260,59 @@ def test_count_tokens_many_of_one_and_outside():
     assert (counts == 1).all()
     H.hswa_count_tokens(counts, 300, None, 0, None, 2, 0, 300, True)
     assert H.hswa_check() == 0 and not counts.any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [2, 8])
+def test_probs_repetition_divides_as_fp32_does(V):
+    """A token that occurred against one that has the fp32 quotient (or product)
+    already: greedy rows with the one first and with the other first both
+    choose the first exactly where the two are equal, infinities, subnormal
+    values and zeros among them. (Rows of 2 are off the boundary, of 8 on it.)"""
+    rng = np.random.default_rng(V)
+    S = 60000
+    a = (rng.uniform(1, 2, S) * 2.0 ** rng.integers(-149, 128, S)).astype(np.float32)
+    a[::5] = rng.uniform(2e38, 3.4e38, len(a[::5]))
+    a[::7] = np.ldexp(rng.integers(1, 1 << 23, len(a[::7])), -149)
+    a[::11] *= -1
+    a[:4] = np.finfo(np.float32).max, np.finfo(np.float32).tiny, 0, np.inf
+    rep = rng.uniform(0.5, 2, S)
+    rep[::13] = 2.0 ** rng.uniform(-120, 120, len(rep[::13]))
+    rep = rep.astype(np.float32)
+    with np.errstate(over="ignore", under="ignore"):
+        b = np.where(a > 0, a / rep, a * rep).astype(np.float32)
+    keep = b > -np.inf  # a row of nothing but -inf chooses none
+    a, b, rep = a[keep], b[keep], rep[keep]
+    assert (b == np.inf).sum() > 1000 and (np.abs(b) < np.finfo(np.float32).tiny).sum() > 1000
+    S = len(a)
+    params = np.stack((np.zeros(S), rep, np.zeros(S), np.zeros(S)), 1).astype(np.float32)
+    for at in (0, 1):
+        logits = np.full((S, 1, V), -np.inf, np.float32)
+        logits[:, 0, at], logits[:, 0, 1 - at] = a, b
+        counts = np.zeros((S, V), np.int16)
+        counts[:, at] = 1
+        x = torch.as_tensor(logits, device="cuda")
+        p = run(x, torch.empty_like(x), torch.as_tensor(params, device="cuda"), torch.as_tensor(counts, device="cuda"))
+        wrong = (p[:, 0, 0] != 1).cpu().numpy()
+        assert not wrong.any(), (at, wrong.sum(), a[wrong][:5], rep[wrong][:5], b[wrong][:5])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [37, 30000, 400000])
+def test_probs_of_quotients_past_the_largest_value(V, dtype):
+    """Logits whose quotient by a repetition below 1 is +inf take the probability, in equal shares."""
+    most = torch.finfo(dtype).max
+    logits = torch.randn(6, 2, V, device="cuda").to(dtype)
+    counts = torch.zeros(6, V, dtype=torch.int16, device="cuda")
+    params = torch.tensor([[1.0, r, 0.3, -0.2] for r in (0.5, 0.6, 0.7, 0.8, 0.9, 0.99)], device="cuda")
+    logits[:, :, 3] = most
+    logits[:, 1, V - 1] = most
+    counts[:, 3] = 2
+    counts[:, V - 1] = -32768  # in the prompt
+    want = torch.zeros(6, 2, V, device="cuda")
+    want[:, 0, 3], want[:, 1, 3], want[:, 1, V - 1] = 1, 0.5, 0.5
+    assert torch.equal(run(logits, torch.empty_like(want), params, counts), want)
+    params[:, 0] = 0
+    want[:, 1, 3], want[:, 1, V - 1] = 1, 0
+    assert torch.equal(run(logits, torch.empty_like(want), params, counts), want)
