@@ -1579,7 +1579,7 @@ __device__ void decode_tc_softmax(Smem &sm, const DecodeArgs &a, int64_t n) {
 #pragma unroll
             for (int cc = 0; cc < kR; ++cc) {
                 const float mc = sm.ep_m[cc * kRows + j];
-                L += mc == -INFINITY ? 0.f : fast_exp2(mc - M) * sm.ep_l[cc * kRows + j];
+                L += (mc == -INFINITY ? 0.f : fast_exp2(mc - M)) * sm.ep_l[cc * kRows + j];  // a NaN stays one
             }
             wt = m_used == -INFINITY ? 0.f : fast_exp2(m_used - M);
             tc_fence_after();
@@ -1621,7 +1621,8 @@ __device__ void decode_tc_softmax(Smem &sm, const DecodeArgs &a, int64_t n) {
         if (!active || c != 0) continue;
         tc_fence_after();
         const bool row = w < a.n_tok;
-        const float inv = L > 0.f ? 1.f / L : 0.f;
+        // L = 0: no key seen, zeros (O may be unset). A score of NaN or +inf made L a NaN, and O
+        const float inv = L == 0.f ? 0.f : 1.f / L;
         if (d.flags & kDirect) {
             uint4 *dst = reinterpret_cast<uint4 *>(
                 a.o + (q_row(a, d.seq, row ? w : 0) * a.hq + (int64_t)d.kvh * kG + h) * kD);
@@ -1633,10 +1634,9 @@ __device__ void decode_tc_softmax(Smem &sm, const DecodeArgs &a, int64_t n) {
                 if (row) {
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        // L = 0: no key seen, write zeros (O may be unset)
                         float f[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] = L > 0.f ? __uint_as_float(ov[8 * x + e]) * inv : 0.f;
+                        for (int e = 0; e < 8; ++e) f[e] = L == 0.f ? 0.f : __uint_as_float(ov[8 * x + e]) * inv;
                         dst[q4 * 4 + x] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
                                                      pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
                     }
@@ -1655,7 +1655,7 @@ __device__ void decode_tc_softmax(Smem &sm, const DecodeArgs &a, int64_t n) {
                     for (int x = 0; x < 8; ++x) {
                         float f[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) f[e] = L > 0.f ? __uint_as_float(ov[4 * x + e]) : 0.f;
+                        for (int e = 0; e < 4; ++e) f[e] = L == 0.f ? 0.f : __uint_as_float(ov[4 * x + e]);
                         dst[q4 * 8 + x] = make_float4(f[0], f[1], f[2], f[3]);
                     }
                 }
