@@ -268,6 +268,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<uint32_t *>(&v);
 }
 
+// A value of a query that goes on as an f16: finite ones end at its largest;
+// infinities and NaN stay (their scores have no softmax, and the output says so).
+__device__ __forceinline__ float f16_range(float x) {
+    return fabsf(x) < INFINITY ? fminf(fmaxf(x, -65504.f), 65504.f) : x;
+}
+
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -1670,14 +1670,12 @@ __device__ void decode_tc_softmax(Smem &sm, const DecodeArgs &a, int64_t n) {
 }
 
 
-// Eight bf16 (one 16-byte chunk) to f16 in place, clamped to f16's finite range.
+// Eight bf16 (one 16-byte chunk) of a query to f16 (f16_range).
 __device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v) {
     uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float lo = fminf(fmaxf(__uint_as_float(w[e] << 16), -65504.f), 65504.f);
-        const float hi = fminf(fmaxf(__uint_as_float(w[e] & 0xFFFF0000u), -65504.f), 65504.f);
-        w[e] = pack_f16(lo, hi);
+        w[e] = pack_f16(f16_range(__uint_as_float(w[e] << 16)), f16_range(__uint_as_float(w[e] & 0xFFFF0000u)));
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }

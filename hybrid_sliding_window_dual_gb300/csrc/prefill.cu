@@ -1389,7 +1389,7 @@ __global__ void __launch_bounds__(256) prefill_stage_fp4(StageArgs a) {
 }
 
 // q (bf16) to fp16 for the fp16 MMAs: exact for magnitudes in
-// [2^-14, 65504], subnormal below, saturated above. 8 elements per step.
+// [2^-14, 65504], subnormal below, saturated above (f16_range). 8 elements per step.
 __global__ void __launch_bounds__(256) prefill_q_to_f16(const __nv_bfloat16 *__restrict__ q, __half *__restrict__ q16,
                                                         int64_t n8) {
     for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n8; i += (int64_t)gridDim.x * blockDim.x) {
@@ -1399,7 +1399,7 @@ __global__ void __launch_bounds__(256) prefill_q_to_f16(const __nv_bfloat16 *__r
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const float2 f = __bfloat1622float2(b[k]);
-            out[k] = __floats2half2_rn(fminf(fmaxf(f.x, -65504.f), 65504.f), fminf(fmaxf(f.y, -65504.f), 65504.f));
+            out[k] = __floats2half2_rn(f16_range(f.x), f16_range(f.y));
         }
         reinterpret_cast<uint4 *>(q16)[i] = *reinterpret_cast<const uint4 *>(out);
     }

@@ -1,8 +1,9 @@
-"""Queries with NaN and infinities.
+"""Queries with NaN, infinities and values beyond fp16 over every type of pool.
 
 A head whose query holds a NaN has no softmax: its output is NaN, and nothing
 else changes. So is that of a head with a score of NaN or +inf; keys whose
-score is -inf have no weight, and a head with no others gives 0."""
+score is -inf have no weight, and a head with no others gives 0. Where a kernel works
+on fp16 queries (FP8 and FP4 pools), finite values beyond +-65504 count as that."""
 import math
 
 import numpy as np
@@ -14,7 +15,7 @@ import hybrid_sliding_window_dual_gb300 as H
 from hybrid_sliding_window_dual_gb300.session import DualPoolSession
 
 FULL, SWA = wl.KIND_FULL, wl.KIND_SWA
-BF16 = H.HSWA_DTYPE_BF16
+BF16, FP8, FP4 = H.HSWA_DTYPE_BF16, H.HSWA_DTYPE_FP8_E4M3, H.HSWA_DTYPE_FP4
 LENGTHS = [40, 64, 700, 9000]  # the last is cut among many CTAs
 
 
@@ -58,7 +59,7 @@ def only_there(got, clean, rows, zero=()):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("n_tok", [1, 2, 3, 4, 5, 8, 9, 16])
-@pytest.mark.parametrize("dtype", [BF16])
+@pytest.mark.parametrize("dtype", [BF16, FP8, FP4])
 def test_decode_of_bad_queries(dtype, n_tok):
     s = session(dtype, LENGTHS, 4000, 0)
     q = wl.normal((len(LENGTHS) * n_tok, 64, 128), 4100, wl.DTYPE_BF16).cuda()
@@ -71,11 +72,18 @@ def test_decode_of_bad_queries(dtype, n_tok):
             for i, (row, head) in enumerate(bad):
                 x[row, head, (3 + 41 * i) % 128] = values[i]
             only_there(decode(s, layer, x, n_tok), clean, bad)
+        if dtype == FP4 or (dtype == FP8 and n_tok > 2):  # finite values beyond fp16's
+            outs = []
+            for big in (65536.0, 1e20, torch.finfo(torch.bfloat16).max):
+                x = q.clone()
+                x[n_tok - 1, 5, 7], x[-1, 40, 100] = big, -big
+                outs.append(decode(s, layer, x, n_tok))
+            assert torch.isfinite(outs[0]).all() and torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
     s.close()
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("dtype", [BF16])
+@pytest.mark.parametrize("dtype", [BF16, FP8, FP4])
 def test_prefill_of_bad_queries(dtype):
     chunk = [30, 64, 200, 1]
     s = session(dtype, LENGTHS, 4200, 0)  # the chunks' keys are there already
