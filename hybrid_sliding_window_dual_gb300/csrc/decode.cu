@@ -1303,6 +1303,12 @@ struct DecodeTc4Smem {
 static_assert(offsetof(DecodeTc4Smem, kc) % 1024 == 0 && offsetof(DecodeTc4Smem, vc) % 1024 == 0,
               "128-byte swizzled tiles need 1024-byte alignment");
 
+// FP4 pools: P is an f16, so its reference has to be near the largest score under
+// any scale. A negative scale turns q's signs instead, so that the largest
+// score is that of the largest product; 0 becomes so little that every score is 0.
+__device__ __forceinline__ float fp4_score_scale(const DecodeArgs &a) { return fmaxf(fabsf(a.scale_log2), 1e-30f); }
+__device__ __forceinline__ uint32_t fp4_query_flip(const DecodeArgs &a) { return a.scale_log2 < 0.f ? 0x80008000u : 0u; }
+
 template <class Smem>
 constexpr size_t decode_tc_smem_bytes() { return sizeof(Smem) + 1024; }
 
@@ -1459,6 +1465,7 @@ __device__ void decode_tc_softmax(Smem &sm, const DecodeArgs &a, int64_t n) {
         tmem_wait_st();
     }
     float m_used = -INFINITY, l = 0.f;  // reference max (log2 units) and sum of P
+    const float scale = Smem::kFP4 ? fp4_score_scale(a) : a.scale_log2;
     uint32_t ep_phase = 0;
     bool ok = true;
     for (int64_t i = 0; i < n && ok; ++i) {
@@ -1512,13 +1519,13 @@ __device__ void decode_tc_softmax(Smem &sm, const DecodeArgs &a, int64_t n) {
                 m0 = max3(m0, __uint_as_float(sr[x]), __uint_as_float(sr[x + 1]));
                 m1 = max3(m1, __uint_as_float(sr[x + 2]), __uint_as_float(sr[x + 3]));
             }
-            const float mx = Smem::kScaled ? fmaxf(m0, m1) : fmaxf(m0, m1) * a.scale_log2;
+            const float mx = Smem::kScaled ? fmaxf(m0, m1) : fmaxf(m0, m1) * scale;
             const bool need = mx > m_used + kTcRescaleLog2;
             const bool resc = need && m_used != -INFINITY;
             const float alpha = resc ? fast_exp2(m_used - mx) : 1.f;
             if (need) m_used = mx;
             const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-            const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(neg_m, neg_m);
+            const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(neg_m, neg_m);
             float2 sum2 = make_float2(0.f, 0.f);
             uint32_t pk[kK / 2];
 #pragma unroll
@@ -1670,12 +1677,12 @@ __device__ void decode_tc_softmax(Smem &sm, const DecodeArgs &a, int64_t n) {
 }
 
 
-// Eight bf16 (one 16-byte chunk) of a query to f16 (f16_range).
-__device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v) {
+// Eight bf16 (one 16-byte chunk) of a query to f16 (f16_range), with the signs of flip turned.
+__device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v, uint32_t flip) {
     uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        w[e] = pack_f16(f16_range(__uint_as_float(w[e] << 16)), f16_range(__uint_as_float(w[e] & 0xFFFF0000u)));
+        w[e] = pack_f16(f16_range(__uint_as_float(w[e] << 16)), f16_range(__uint_as_float(w[e] & 0xFFFF0000u))) ^ flip;
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -1726,6 +1733,7 @@ __device__ void decode_tc_convert(Smem &sm, const DecodeArgs &a, int64_t n) {
     const int t = (threadIdx.x - Smem::kConvWarp * 32) % kCT;
     const int quad = (threadIdx.x >> 5) & 3, row = 32 * quad + (threadIdx.x & 31);
     const uint32_t t_q = sm.tmem_base + ((uint32_t)(32 * quad) << 16) + kTmemQ;
+    const uint32_t flip = Smem::kFP4 ? fp4_query_flip(a) : 0u;
     int32_t pc = -1;
     bool ok = true;
     for (int64_t i = (threadIdx.x - Smem::kConvWarp * 32) / kCT; i < n && ok; i += Smem::kGroups) {
@@ -1744,7 +1752,7 @@ __device__ void decode_tc_convert(Smem &sm, const DecodeArgs &a, int64_t n) {
         if ((d.flags & kFirst) && !kQT) {  // f16 in place, for QK from shared memory
             uint4 *q = reinterpret_cast<uint4 *>(sm.q[pc % kQB]);
 #pragma unroll 4
-            for (int x = t; x < 2 * (int)Smem::kQHalfBytes / 16; x += kCT) q[x] = bf16x8_to_f16x8(q[x]);
+            for (int x = t; x < 2 * (int)Smem::kQHalfBytes / 16; x += kCT) q[x] = bf16x8_to_f16x8(q[x], flip);
             fence_proxy_async_shared();
             mbar_arrive(&sm.q_conv[pc % kQB]);
         } else if (d.flags & kFirst) {  // f16 pairs into TMEM
@@ -1754,7 +1762,7 @@ __device__ void decode_tc_convert(Smem &sm, const DecodeArgs &a, int64_t n) {
                 uint32_t w[32];
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    const uint4 f = bf16x8_to_f16x8(*reinterpret_cast<const uint4 *>(q + h * kQH + ((c ^ (row & 7)) << 4)));
+                    const uint4 f = bf16x8_to_f16x8(*reinterpret_cast<const uint4 *>(q + h * kQH + ((c ^ (row & 7)) << 4)), flip);
                     w[4 * c] = f.x, w[4 * c + 1] = f.y, w[4 * c + 2] = f.z, w[4 * c + 3] = f.w;
                 }
                 tmem_st32(t_q + 32 * h, w);

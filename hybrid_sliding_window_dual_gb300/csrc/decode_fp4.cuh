@@ -202,10 +202,8 @@ __device__ void decode_fp4_worker(DecodeSmem4<Shape> &sm, const DecodeArgs &a, c
     float2 m2 = make_float2(-INFINITY, -INFINITY);  // kTok 1: references of heads 2 t, 2 t + 1
 #pragma unroll
     for (int j = 0; j < kTok; ++j) m[j] = -INFINITY, l[j] = make_float2(0.f, 0.f);
-    // a negative scale turns q's sign instead, so that the largest score is
-    // that of the largest product; 0 becomes so little that every score is 0
-    const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);
-    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+    const float scale = fp4_score_scale(a);
+    const uint32_t flip = fp4_query_flip(a);
     // the key of a tile in column gr of S; this lane's two keys of a tile are
     // 2 t + b and 2 t + 1 - b
     const int b = t & 1, krow = (gr & ~1) + ((gr ^ (gr >> 1)) & 1);
@@ -235,16 +233,16 @@ __device__ void decode_fp4_worker(DecodeSmem4<Shape> &sm, const DecodeArgs &a, c
                     a.q + (q_row(a, d.seq & 0xffff, tok) * a.hq + (int64_t)(d.seq >> 16) * kG + gr) * kD + 32 * t);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const uint4 f = bf16x8_to_f16x8(q[x]);
+                    const uint4 f = bf16x8_to_f16x8(q[x], flip);
                     if constexpr (kTok > 1) {
                         // A operand: .x, .z the pair's first token, .y, .w its second
                         uint32_t *to = reinterpret_cast<uint32_t *>(&sm.q[w][j / 2][2 * x][lane]) + (j & 1);
-                        to[0] = f.x ^ flip, to[2] = f.y ^ flip;
+                        to[0] = f.x, to[2] = f.y;
                         to += 32 * 4;
-                        to[0] = f.z ^ flip, to[2] = f.w ^ flip;
+                        to[0] = f.z, to[2] = f.w;
                     } else {
-                        qf[2 * x][0] = f.x ^ flip, qf[2 * x][1] = f.y ^ flip;
-                        qf[2 * x + 1][0] = f.z ^ flip, qf[2 * x + 1][1] = f.w ^ flip;
+                        qf[2 * x][0] = f.x, qf[2 * x][1] = f.y;
+                        qf[2 * x + 1][0] = f.z, qf[2 * x + 1][1] = f.w;
                     }
                 }
                 m[j] = -INFINITY, l[j] = make_float2(0.f, 0.f);

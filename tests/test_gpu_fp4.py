@@ -423,3 +423,30 @@ def test_rope_append(hq, hkv, d, rot, P, T, adjacent):
     assert not s.k[0].cpu().numpy()[free // P, :, free % P].any()
     H.hswa_rope_destroy(rope)
     s.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [-0.4, -3.0, 0.0])
+@pytest.mark.parametrize("n_tok", [1, 2, 4, 5, 9, 16])
+@pytest.mark.parametrize("hq,hkv,d,P", [(64, 8, 128, 64), (6, 2, 96, 16)])
+def test_decode_under_scales_that_are_not_positive(hq, hkv, d, P, n_tok, scale):
+    """The softmax of scores times a negative scale, and the mean under 0: scores of
+    sequences that begin inside a page, of masked keys and of whole masked pages among them."""
+    c = Case([1, 63, 64, 200, 900, 4000], seed=150, extra=n_tok + 8, hq=hq, hkv=hkv, d=d, P=P)
+    c.sess.reserve(range(c.B), [n_tok] * c.B)
+    c.sess.sync()
+    _, _, lens = c.sess.tables()
+    pos = (lens[:, None] - n_tok + np.arange(n_tok)[None]).reshape(-1)
+    for layer in range(2):
+        q = wl.normal((c.B * n_tok, hq, d), 3500 + layer, wl.DTYPE_BF16).cuda()
+        o = torch.full_like(q, float("nan"))
+        if n_tok == 1:
+            c.sess.decode(layer, q, o, c.B, scale)
+        else:
+            c.sess.decode_multi(layer, q, o, c.B, n_tok, scale)
+        assert c.sess.check() == 0
+        k, v = c.values(layer)
+        qh = q.float().cpu().numpy()
+        exp = oracle.attention(qh, k, v, c.table(layer), np.repeat(np.arange(c.B), n_tok), pos, c.window(layer), scale)
+        off = np.abs(o.float().cpu().numpy() - exp) / tolerance(exp, qh, k, v, abs(scale), int(pos.max()) + 1)
+        assert off.max() <= 1, (layer, off.max())  # not for a NaN either
