@@ -2519,13 +2519,21 @@ __global__ void attention_generic(const T *__restrict__ q, T *__restrict__ o, co
     }
 }
 
+// Whether the generic kernel takes so many query rows of such a pool.
+constexpr int kGenericThreads = 256;
+int64_t generic_grid(const hswa_config &c, int64_t rows) { return (rows * c.n_q_heads * 32 + kGenericThreads - 1) / kGenericThreads; }
+bool generic_takes(const hswa_config &c, int64_t rows) {
+    return c.head_dim <= 256 && rows <= INT32_MAX && generic_grid(c, rows) <= INT32_MAX;
+}
+
 // Launch the generic kernel for decode (mode 0) or prefill (mode 1).
 int launch_attention_generic(const hswa_pool *pool, const hswa_layer *layer, const void *q, void *o,
                              const int32_t *bt, const int32_t *seq_len, const int32_t *prefix,
                              const int32_t *q_start, int32_t n_rows, int32_t n_seqs, float scale, int mode,
                              cudaStream_t st, int32_t n_tok) {
     const hswa_config &c = pool->cfg;
-    if (c.head_dim > 256 || c.dtype == HSWA_DTYPE_FP8_E4M3) return HSWA_ERR_UNSUPPORTED;
+    const int64_t rows = (int64_t)n_rows * (mode == 0 ? 1 : n_seqs);
+    if (c.dtype == HSWA_DTYPE_FP8_E4M3 || !generic_takes(c, rows)) return HSWA_ERR_UNSUPPORTED;
     if (c.dtype == HSWA_DTYPE_FP4) {
         if (c.head_dim % kFp4Block) return HSWA_ERR_UNSUPPORTED;
         if (!layer->k_scale || !layer->v_scale) return HSWA_ERR_INVALID_ARG;
@@ -2533,14 +2541,11 @@ int launch_attention_generic(const hswa_pool *pool, const hswa_layer *layer, con
     if (n_rows == 0) return HSWA_OK;
     const int32_t window = layer->kind == HSWA_KIND_SWA ? layer->window : 0;
     const int32_t num_pages = layer->kind == HSWA_KIND_SWA ? c.swa_pages : c.full_pages;
-    const int64_t threads = (int64_t)n_rows * (mode == 0 ? 1 : n_seqs) * c.n_q_heads * 32;
-    const int block = 256;
-    const int64_t grid = (threads + block - 1) / block;
-    if (grid > INT32_MAX) return HSWA_ERR_UNSUPPORTED;
+    const int64_t grid = generic_grid(c, rows);
     int *err = error_word();
     const auto run = [&](auto type, auto k, auto v) {
         using T = decltype(type);
-        attention_generic<T, 8><<<(int)grid, block, 0, st>>>(
+        attention_generic<T, 8><<<(int)grid, kGenericThreads, 0, st>>>(
             (const T *)q, (T *)o, k, v, bt, seq_len, prefix, q_start, n_rows, n_seqs, c.max_pages_per_seq,
             c.n_q_heads, c.n_kv_heads, c.head_dim, c.page_size, window, num_pages, scale, mode, n_tok, err);
     };
@@ -2856,15 +2861,15 @@ int decode_fp8(const hswa_pool *pool, const hswa_layer *layer, const void *q, vo
     return e == cudaSuccess ? HSWA_OK : HSWA_ERR_CUDA;
 }
 
-// Decode over FP4 pools of other shapes.
+// Decode over FP4 pools of other shapes (that generic_takes takes).
+static_assert(kFp4AnyMaxD == 256, "decode_fp4_any takes the generic kernel's head sizes");
 int launch_decode_fp4_any(const hswa_pool *pool, const hswa_layer *layer, const void *q, void *o, const int32_t *d_bt,
                           const int32_t *d_seq_len, int n_seqs, int n_tok, float scale, cudaStream_t st) {
     const hswa_config &c = pool->cfg;
     const int64_t rows = (int64_t)n_seqs * n_tok;
     const int32_t group = c.n_q_heads / c.n_kv_heads;
     const int64_t heads = (int64_t)c.n_kv_heads * ((group + kFp4AnyHeads - 1) / kFp4AnyHeads);
-    if (c.head_dim > kFp4AnyMaxD) return HSWA_ERR_UNSUPPORTED;
-    if ((((uintptr_t)layer->k_pool) & 7) || rows > INT32_MAX || heads > 65535)  // codes come 8 bytes at a time
+    if ((((uintptr_t)layer->k_pool) & 7) || heads > 65535)  // codes come 8 bytes at a time
         return launch_attention_generic(pool, layer, q, o, d_bt, d_seq_len, nullptr, nullptr, (int32_t)rows, n_seqs, scale, 0,
                                         st, n_tok);
     Fp4AnyArgs a;
@@ -2882,7 +2887,6 @@ int launch_decode_fp4_any(const hswa_pool *pool, const hswa_layer *layer, const 
     if (sms <= 0) return HSWA_ERR_CUDA;
     a.cluster = 1;
     while (a.cluster < kFp4AnyCluster && rows * heads * a.cluster * 2 <= 2 * sms) a.cluster *= 2;
-    if (rows * a.cluster > INT32_MAX) return HSWA_ERR_UNSUPPORTED;
     set_last_kernel("decode_fp4_any");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * a.cluster), (unsigned)heads);
@@ -2914,6 +2918,7 @@ int decode_fp4(const hswa_pool *pool, const hswa_layer *layer, const void *q, vo
     const uint64_t rows = (uint64_t)num_pages * c.n_kv_heads * c.page_size;
     // rows are counted in 32 bits
     const bool fast = decode_fp4_ok(pool, layer, q, o) && rows < (1ull << 31) && (int64_t)n_seqs * n_tok <= 65535 && c.n_kv_heads < 32768;
+    if (!fast && !generic_takes(c, (int64_t)n_seqs * n_tok)) return HSWA_ERR_UNSUPPORTED;  // before the append
     const bool tc = n_tok >= kTcMinTokensFp4;
     int workers = 0;
     if (fast) {
@@ -3022,6 +3027,7 @@ int decode_impl(const hswa_pool *pool, const hswa_layer *layer, const void *q, v
     }
     if (!decode_fast_ok(pool, layer, q, o) ||
         (fused && (((uintptr_t)k_new & 15) || ((uintptr_t)v_new & 15)))) {
+        if (!pw && !generic_takes(pool->cfg, (int64_t)n_seqs * n_tok)) return HSWA_ERR_UNSUPPORTED;  // before the append
         if (fused) {
             const int rc = hswa_append_kv(pool, layer, k_new, v_new, slots, n_seqs, stream);
             if (rc != HSWA_OK) return rc;

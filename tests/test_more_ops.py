@@ -267,3 +267,12 @@ def test_session_shapes():
         with pytest.raises(ValueError):
             s.read(0, f(3, **i32), k, v)
     s.close()
+
+
+@pytest.mark.parametrize("dtype", [H.HSWA_DTYPE_F32, H.HSWA_DTYPE_BF16, H.HSWA_DTYPE_FP4])
+def test_fused_decode_is_refused_before_its_append(dtype):
+    """Heads that no decode takes: the call comes back before the pool is written."""
+    p = pool(dtype, d=272)
+    for kind in (H.HSWA_KIND_FULL, H.HSWA_KIND_SWA):
+        refused(UNSUPPORTED, H.hswa_decode_append, p, layer(kind), X, X, X, X, X, X, X, 4, 1.0, X, 1 << 30)
+    H.hswa_pool_destroy(p)
