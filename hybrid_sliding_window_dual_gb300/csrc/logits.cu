@@ -727,6 +727,18 @@ __global__ void __launch_bounds__(256) count_clear(const CountArgs a) {
     }
 }
 
+// One count, 16 bits by themselves: the array's first or last, where its word is not all the array's.
+__device__ void count_alone(uint16_t *count, bool prompt) {
+    uint16_t was = *(volatile uint16_t *)count;
+    for (;;) {
+        const uint16_t next = prompt ? was | 0x8000 : (was & 0x7fff) == 0x7fff ? was : was + 1;
+        if (next == was) return;
+        const uint16_t seen = atomicCAS(reinterpret_cast<unsigned short *>(count), was, next);
+        if (seen == was) return;
+        was = seen;
+    }
+}
+
 // Tokens [from, to) of every sequence added to counts that are there: a thread
 // each. Additions and ors that need no answer, unless a count could pass 32767.
 __global__ void __launch_bounds__(256) count_each(const CountArgs a, int32_t from, int32_t to) {
@@ -740,8 +752,14 @@ __global__ void __launch_bounds__(256) count_each(const CountArgs a, int32_t fro
     if (v < 0 || v >= a.vocab) return;
     const int32_t prompt = a.n_prompt ? a.n_prompt[s] : 0;
     // the word that the count is half of (the other half stays as it is)
-    const uintptr_t n = reinterpret_cast<uintptr_t>(a.counts + s * a.count_stride + v);
+    uint16_t *const count = a.counts + s * a.count_stride + v;
+    const uintptr_t n = reinterpret_cast<uintptr_t>(count);
     uint32_t *word = reinterpret_cast<uint32_t *>(n & ~(uintptr_t)3);
+    if (reinterpret_cast<uint16_t *>(word) < a.counts ||
+        reinterpret_cast<uint16_t *>(word + 1) > a.counts + (a.n_seqs - 1) * a.count_stride + a.vocab) {
+        count_alone(count, i < prompt);
+        return;
+    }
     const int shift = n & 2 ? 16 : 0;
     if (i < prompt) {
         atomicOr(word, 0x8000u << shift);

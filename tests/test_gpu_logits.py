@@ -316,3 +316,29 @@ def test_probs_of_quotients_past_the_largest_value(V, dtype):
     params[:, 0] = 0
     want[:, 1, 3], want[:, 1, V - 1] = 1, 0
     assert torch.equal(run(logits, torch.empty_like(want), params, counts), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("first", [0, 1, 2, 3])
+@pytest.mark.parametrize("S,V,pad", [(1, 1, 0), (1, 2, 0), (1, 9, 0), (3, 17, 0), (3, 16, 0), (2, 33, 2), (5, 1000, 1), (5, 1001, 1)])
+def test_count_tokens_in_an_array_between_others(S, V, pad, first):
+    """Counts that begin and end within a 32-bit word: the array's own values
+    only change, its first and last counts are often met, up to 32767."""
+    rng = np.random.default_rng(S * V + first)
+    size = (S - 1) * (V + pad) + V
+    n = 700
+    tokens = rng.choice([0, 0, V - 1, V - 1, V // 2, -1], (S, n)).astype(np.int32)
+    prompt = rng.integers(0, 9, S).astype(np.int32)
+    for start in (0, 32400, 32767):
+        for clear in (True, False):
+            store = torch.as_tensor(rng.integers(-(1 << 15), 1 << 15, first + size + 3).astype(np.int16), device="cuda")
+            counts = store[first:first + size].as_strided((S, V), (V + pad, 1))
+            counts.copy_(torch.as_tensor(np.where(rng.random((S, V)) < 0.5, start, 5).astype(np.int16)))
+            mine = torch.zeros(first + size + 3, dtype=torch.bool, device="cuda")
+            mine[first:first + size].as_strided((S, V), (V + pad, 1)).fill_(True)
+            before = store.clone()
+            want = serving.count_tokens(tokens, prompt, V, None if clear else counts.cpu().numpy().view(np.uint16))
+            H.hswa_count_tokens(counts, V + pad, torch.as_tensor(tokens, device="cuda"), n, torch.as_tensor(prompt, device="cuda"), S, n, V, clear)
+            assert H.hswa_check() == 0
+            assert np.array_equal(counts.cpu().numpy().view(np.uint16), want)
+            assert torch.equal(store[~mine], before[~mine])
