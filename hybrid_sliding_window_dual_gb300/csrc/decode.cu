@@ -2728,7 +2728,6 @@ int fp4_workers() {
         static int planning[kMaxDevices] = {};
         per_sm = std::min(per_sm, kernel_setup(decode_mma_fp4_d128<Shape, true>, decode_smem4_bytes<Shape>(), 32 * Shape::kWarps, planning));
     }
-    static_assert(Shape::kCtas * Shape::kWarps <= kFp4WorkersPerSm, "the workspace has records for that many");
     return per_sm <= 0 ? -1 : sm_count() * std::min(per_sm, Shape::kCtas) * Shape::kWarps;
 }
 
@@ -2747,6 +2746,14 @@ cudaError_t launch_decode_fp4(int workers, cudaStream_t st, const DecodeArgs &a)
 // and there two launches (560 + 209).
 constexpr int kTcMinTokensFp4 = 5;
 
+// The most partial records that a decode of n_tok tokens, or of fewer, leaves on an SM.
+constexpr int kFp4TcCtas = 1;  // of the tensor-core kernel
+constexpr int fp4_records(int n_tok) {
+    constexpr int one = 2 * Fp4One::kCtas * Fp4One::kWarps, two = 2 * Fp4Two::kCtas * Fp4Two::kWarps * 2,
+                  token = 2 * Fp4Four::kCtas * Fp4Four::kWarps, four = token * (kTcMinTokensFp4 - 1);
+    return n_tok == 1 ? one : n_tok == 2 ? std::max(one, two) : n_tok < kTcMinTokensFp4 ? std::max(two, token * n_tok) : std::max(four, 2 * kFp4TcCtas * n_tok);
+}
+
 size_t desc_bytes(int n_seqs) { return ((size_t)(n_seqs + 1) * sizeof(int4) + 255) & ~(size_t)255; }
 
 }  // namespace
@@ -2760,9 +2767,10 @@ extern "C" size_t hswa_decode_multi_workspace_size(const hswa_pool *pool, int n_
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         sms = 192;  // no device visible: size for the largest part
-    // FP4 pools: every warp leaves records of its own
-    const int per_sm = pool->cfg.dtype == HSWA_DTYPE_FP4 && n_tok < kTcMinTokensFp4 ? kFp4WorkersPerSm : kMaxCtasPerSm;
-    return desc_bytes(n_seqs) + (size_t)sms * per_sm * 2 * n_tok * sizeof(Partial);
+    // records on an SM: two of each CTA and token, or, of FP4 pools, of each worker
+    // (few tokens' workers leave more than the CTAs of up to 16 do: more tokens never need less)
+    const int records = pool->cfg.dtype == HSWA_DTYPE_FP4 ? fp4_records(n_tok) : kMaxCtasPerSm * 2 * n_tok;
+    return desc_bytes(n_seqs) + (size_t)sms * records * sizeof(Partial);
 }
 
 extern "C" size_t hswa_decode_workspace_size(const hswa_pool *pool, int n_seqs) {
@@ -2924,7 +2932,7 @@ int decode_fp4(const hswa_pool *pool, const hswa_layer *layer, const void *q, vo
     if (fast) {
         const int sms = sm_count();
         if (sms <= 0) return HSWA_ERR_CUDA;
-        workers = tc           ? sms * std::min(decode_tc_ctas_per_sm<DecodeTc4Smem>(n_tok), 1)
+        workers = tc           ? sms * std::min(decode_tc_ctas_per_sm<DecodeTc4Smem>(n_tok), kFp4TcCtas)
                   : n_tok == 1 ? fp4_workers<Fp4One>()
                   : n_tok == 2 ? fp4_workers<Fp4Two>()
                                : fp4_workers<Fp4Four>();

@@ -48,7 +48,6 @@ struct Fp4Shape {
 using Fp4One = Fp4Shape<1, 64, 4, 4, 3>;
 using Fp4Two = Fp4Shape<2, 64, 4, 4, 2>;
 using Fp4Four = Fp4Shape<4, 32, 4, 6, 2>;
-constexpr int kFp4WorkersPerSm = 16;  // the most of these
 constexpr int kFp4Ahead = 8;          // units whose descriptors are made at once
 constexpr int kFp4PlanSeqs = 32;      // sequences whose descriptors every CTA makes for itself
 

@@ -509,7 +509,8 @@ int hswa_evict_select(const hswa_pool *pool, const int32_t *d_seq_len, const flo
 #define HSWA_DECODE_MAX_TOKENS 16
 
 /* Bytes of workspace hswa_decode_multi needs for n_seqs sequences of n_tok
- * query tokens each (0 for an n_tok outside [1, HSWA_DECODE_MAX_TOKENS]). */
+ * query tokens each (0 for an n_tok outside [1, HSWA_DECODE_MAX_TOKENS]);
+ * it is enough for fewer of either. */
 size_t hswa_decode_multi_workspace_size(const hswa_pool *pool, int n_seqs, int n_tok);
 
 /* Decode of n_tok query tokens per sequence in one pass over the KV pages:

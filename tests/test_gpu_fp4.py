@@ -450,3 +450,17 @@ def test_decode_under_scales_that_are_not_positive(hq, hkv, d, P, n_tok, scale):
         exp = oracle.attention(qh, k, v, c.table(layer), np.repeat(np.arange(c.B), n_tok), pos, c.window(layer), scale)
         off = np.abs(o.float().cpu().numpy() - exp) / tolerance(exp, qh, k, v, abs(scale), int(pos.max()) + 1)
         assert off.max() <= 1, (layer, off.max())  # not for a NaN either
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("most", [5, 7, 4, 3])
+def test_a_workspace_serves_fewer_tokens(most):
+    """The workspace that the most tokens ask for serves fewer: a captured call keeps it."""
+    c = Case([300, 5000, 64, 3], seed=160, extra=80)
+    step(c, most, seed=3600)
+    ws = c.sess.ws
+    assert ws.numel() == H.hswa_decode_multi_workspace_size(c.sess.pool, c.B, most)
+    for n_tok in range(most - 1, 0, -1):
+        c.sess.release(range(c.B))
+        step(c, n_tok, seed=3610 + n_tok)
+        assert c.sess.ws is ws

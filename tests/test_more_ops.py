@@ -276,3 +276,13 @@ def test_fused_decode_is_refused_before_its_append(dtype):
     for kind in (H.HSWA_KIND_FULL, H.HSWA_KIND_SWA):
         refused(UNSUPPORTED, H.hswa_decode_append, p, layer(kind), X, X, X, X, X, X, X, 4, 1.0, X, 1 << 30)
     H.hswa_pool_destroy(p)
+
+
+@pytest.mark.parametrize("dtype", [H.HSWA_DTYPE_F32, H.HSWA_DTYPE_BF16, H.HSWA_DTYPE_FP8_E4M3, H.HSWA_DTYPE_FP4])
+def test_a_decode_workspace_serves_fewer_tokens_and_sequences(dtype):
+    p = pool(dtype, S=64)
+    for n in (1, 64):
+        sizes = [H.hswa_decode_multi_workspace_size(p, n, t) for t in range(1, H.HSWA_DECODE_MAX_TOKENS + 1)]
+        assert sizes == sorted(sizes) and sizes[0] == H.hswa_decode_workspace_size(p, n)
+        assert all(a <= b for a, b in zip(sizes, (H.hswa_decode_multi_workspace_size(p, 64, t) for t in range(1, 17))))
+    H.hswa_pool_destroy(p)
