@@ -69,6 +69,7 @@ class DualPoolSession:
                                        k_scale=ks.data_ptr() if ks is not None else None,
                                        v_scale=vs.data_ptr() if vs is not None else None))
         self.ws = None
+        self.ws_made = []  # every self.ws there has been
         self.prefill_ws = None
         self.weights_ws = None
         self.tree = None
@@ -138,9 +139,14 @@ class DualPoolSession:
 
     # ------------------------------------------------------------ device
     def workspace(self, n_seqs, n_tok=1):
-        need = B.hswa_decode_multi_workspace_size(self.pool, n_seqs, n_tok)
+        """The workspace of decodes of up to n_tok tokens, for every sequence.
+        The session's calls, captured ones among them, share it: two of them
+        must not run at the same time. One that more tokens replace stays
+        allocated, since captured calls may hold it."""
+        need = B.hswa_decode_multi_workspace_size(self.pool, max(n_seqs, self.cfg.max_seqs), n_tok)
         if self.ws is None or self.ws.numel() < need:
             self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+            self.ws_made.append(self.ws)
         return self.ws
 
     def append(self, layer, k, v, d_slots):
@@ -271,14 +277,15 @@ class DualPoolSession:
     def prefill(self, layer, q, o, d_prefix_len, d_q_start, n_seqs, max_q_len, scale, prefix_host=None,
                 q_start_host=None):
         """prefix_host / q_start_host: host copies of the device arrays; with
-        them an FP8 pool's staging workspace is sized for this chunk exactly,
-        without them for any chunk of n_seqs sequences of max_q_len rows."""
+        them an FP8 or FP4 pool's staging workspace is sized for this chunk exactly,
+        without them for any chunk of n_seqs sequences of max_q_len rows. A chunk
+        that needs more replaces it: capture calls on such pools after the largest."""
         if prefix_host is not None and q_start_host is not None:
             need = B.hswa_prefill_workspace_size_exact(self.pool, self.layers[layer], prefix_host, q_start_host)
         else:
             need = B.hswa_prefill_workspace_size(self.pool, self.layers[layer], n_seqs, max_q_len)
         ws = None
-        if need:  # FP8 pools stage f16 copies of the pages the chunk reads (and of q)
+        if need:  # FP8 and FP4 pools stage f16 copies of the pages the chunk reads (and of q)
             if self.prefill_ws is None or self.prefill_ws.numel() < need:
                 self.prefill_ws = torch.empty(need, dtype=torch.uint8, device=self.device)
             ws = self.prefill_ws

@@ -1,7 +1,9 @@
 """FP4 pools and the step from logits to probabilities on the CPU: pins of the
 oracle (quantizer, penalties, counts) and the library's refusals, each of which
 comes before a launch."""
+import gc
 import math
+import weakref
 
 import numpy as np
 import pytest
@@ -286,3 +288,20 @@ def test_a_decode_workspace_serves_fewer_tokens_and_sequences(dtype):
         assert sizes == sorted(sizes) and sizes[0] == H.hswa_decode_workspace_size(p, n)
         assert all(a <= b for a, b in zip(sizes, (H.hswa_decode_multi_workspace_size(p, 64, t) for t in range(1, 17))))
     H.hswa_pool_destroy(p)
+
+
+def test_session_keeps_the_workspaces_that_captured_calls_may_hold():
+    cfg = H.Config(window=128, page_size=64, n_q_heads=16, n_kv_heads=2, head_dim=128, dtype=H.HSWA_DTYPE_FP4, full_pages=4, swa_pages=5, max_seqs=40, max_pages_per_seq=4)
+    s = DualPoolSession(cfg, [H.HSWA_KIND_FULL], device="cpu")
+    one = s.workspace(1, 1)
+    assert s.workspace(40, 1) is one  # more sequences need no other
+    held = [weakref.ref(one)]
+    del one
+    for n_tok in (4, 16):
+        held.append(weakref.ref(s.workspace(3, n_tok)))
+    at = s.ws.data_ptr()
+    for n_tok in (16, 5, 4, 2, 1):
+        assert s.workspace(40, n_tok).data_ptr() == at
+    gc.collect()
+    assert all(x() is not None for x in held)
+    s.close()
