@@ -2028,7 +2028,8 @@ struct Pieces {
 constexpr int kMergeHeads = 2;  // heads of a block
 constexpr int kMergeAhead = 32;
 
-// per head: (weight, sum) and place of each piece
+// per head: (weight, sum) and place of each piece. At most 43,776 bytes, those of an
+// FP4 decode's 1824 workers: within the 48 KB that a kernel has without being set up for more.
 __host__ __device__ inline int merge_pieces(int n_ctas) { return (n_ctas + kMergeAhead - 1) / kMergeAhead * kMergeAhead; }
 size_t merge_heads_smem(int n_ctas) { return kMergeHeads * merge_pieces(n_ctas) * (sizeof(float2) + sizeof(int32_t)); }
 
@@ -2700,11 +2701,6 @@ cudaError_t launch_finish_weights(const PageWeights &pw, const hswa_config &c, c
 }
 
 cudaError_t launch_combine(const hswa_config &c, const DecodeArgs &a, int n_ctas, cudaStream_t st) {
-    const size_t smem = merge_heads_smem(n_ctas);
-    if (smem > (47u << 10)) {  // the workers of an FP4 decode: more than a kernel has by itself
-        static int cache[kMaxDevices] = {};
-        if (kernel_setup(decode_combine_heads, 100u << 10, 256, cache) < 0 || smem > (100u << 10)) return cudaErrorInvalidConfiguration;
-    }
     if (merge_by_heads((int64_t)a.n_seqs * c.n_kv_heads * a.n_tok, n_ctas))
         return launch_pdl(decode_combine_heads, dim3(c.n_kv_heads * (kG / kMergeHeads), a.n_seqs * a.n_tok), dim3(256),
                           merge_heads_smem(n_ctas), st, a, n_ctas);
