@@ -160,6 +160,7 @@ struct DecodeArgs {
     int32_t n_seqs, bt_stride, hkv, hq, window, num_pages;
     int32_t n_tok;  // query tokens per sequence (multi-token decode), 1 otherwise
     float scale_log2;
+    uint32_t q_flip;  // FP4: signs of q to turn, two 16-bit values at a time
     int *err;
     // decode with page weights (null otherwise): log2 of the sum of 2^score
     // over a page, [n_seqs][Hkv][bt_stride][8 heads]; over a whole segment
@@ -1303,12 +1304,6 @@ struct DecodeTc4Smem {
 static_assert(offsetof(DecodeTc4Smem, kc) % 1024 == 0 && offsetof(DecodeTc4Smem, vc) % 1024 == 0,
               "128-byte swizzled tiles need 1024-byte alignment");
 
-// FP4 pools: P is an f16, so its reference has to be near the largest score under
-// any scale. A negative scale turns q's signs instead, so that the largest
-// score is that of the largest product; 0 becomes so little that every score is 0.
-__device__ __forceinline__ float fp4_score_scale(const DecodeArgs &a) { return fmaxf(fabsf(a.scale_log2), 1e-30f); }
-__device__ __forceinline__ uint32_t fp4_query_flip(const DecodeArgs &a) { return a.scale_log2 < 0.f ? 0x80008000u : 0u; }
-
 template <class Smem>
 constexpr size_t decode_tc_smem_bytes() { return sizeof(Smem) + 1024; }
 
@@ -1465,7 +1460,6 @@ __device__ void decode_tc_softmax(Smem &sm, const DecodeArgs &a, int64_t n) {
         tmem_wait_st();
     }
     float m_used = -INFINITY, l = 0.f;  // reference max (log2 units) and sum of P
-    const float scale = Smem::kFP4 ? fp4_score_scale(a) : a.scale_log2;
     uint32_t ep_phase = 0;
     bool ok = true;
     for (int64_t i = 0; i < n && ok; ++i) {
@@ -1519,13 +1513,13 @@ __device__ void decode_tc_softmax(Smem &sm, const DecodeArgs &a, int64_t n) {
                 m0 = max3(m0, __uint_as_float(sr[x]), __uint_as_float(sr[x + 1]));
                 m1 = max3(m1, __uint_as_float(sr[x + 2]), __uint_as_float(sr[x + 3]));
             }
-            const float mx = Smem::kScaled ? fmaxf(m0, m1) : fmaxf(m0, m1) * scale;
+            const float mx = Smem::kScaled ? fmaxf(m0, m1) : fmaxf(m0, m1) * a.scale_log2;
             const bool need = mx > m_used + kTcRescaleLog2;
             const bool resc = need && m_used != -INFINITY;
             const float alpha = resc ? fast_exp2(m_used - mx) : 1.f;
             if (need) m_used = mx;
             const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-            const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(neg_m, neg_m);
+            const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(neg_m, neg_m);
             float2 sum2 = make_float2(0.f, 0.f);
             uint32_t pk[kK / 2];
 #pragma unroll
@@ -1677,14 +1671,9 @@ __device__ void decode_tc_softmax(Smem &sm, const DecodeArgs &a, int64_t n) {
 }
 
 
-// Eight bf16 (one 16-byte chunk) of a query to f16 (f16_range), with the signs of flip turned.
+// Eight bf16 (one 16-byte chunk) of a query to f16, with the signs of flip turned.
 __device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v, uint32_t flip) {
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        w[e] = pack_f16(f16_range(__uint_as_float(w[e] << 16)), f16_range(__uint_as_float(w[e] & 0xFFFF0000u))) ^ flip;
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint4(query_f16x2(v.x) ^ flip, query_f16x2(v.y) ^ flip, query_f16x2(v.z) ^ flip, query_f16x2(v.w) ^ flip);
 }
 
 // Sixteen E4M3 codes (one 16-byte chunk) as sixteen exact f16 values.
@@ -1733,7 +1722,7 @@ __device__ void decode_tc_convert(Smem &sm, const DecodeArgs &a, int64_t n) {
     const int t = (threadIdx.x - Smem::kConvWarp * 32) % kCT;
     const int quad = (threadIdx.x >> 5) & 3, row = 32 * quad + (threadIdx.x & 31);
     const uint32_t t_q = sm.tmem_base + ((uint32_t)(32 * quad) << 16) + kTmemQ;
-    const uint32_t flip = Smem::kFP4 ? fp4_query_flip(a) : 0u;
+    const uint32_t flip = Smem::kFP4 ? a.q_flip : 0u;
     int32_t pc = -1;
     bool ok = true;
     for (int64_t i = (threadIdx.x - Smem::kConvWarp * 32) / kCT; i < n && ok; i += Smem::kGroups) {
@@ -2801,6 +2790,7 @@ int fill_args(DecodeArgs &a, const hswa_pool *pool, const hswa_layer *layer, con
     a.num_pages = num_pages;
     a.n_tok = 1;
     a.scale_log2 = scale * 1.4426950408889634f;
+    a.q_flip = 0;
     a.err = error_word();
     a.page_lse = a.seq_lse = a.piece_lse = nullptr;
     return num_pages;
@@ -2945,6 +2935,11 @@ int decode_fp4(const hswa_pool *pool, const hswa_layer *layer, const void *q, vo
     DecodeArgs a;
     fill_args(a, pool, layer, q, o, d_bt, d_seq_len, n_seqs, scale, ws);
     a.n_tok = n_tok;
+    // P is an f16, so its reference has to be near the largest score under any
+    // scale. A negative scale turns q's signs instead, so that the largest score is that
+    // of the largest product; 0 becomes so little that every score is 0.
+    a.q_flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+    a.scale_log2 = std::max(std::abs(a.scale_log2), 1e-30f);
     CUtensorMap tq;
     if (tc && !make_q_tmap(&tq, q, c, n_seqs, n_tok)) return HSWA_ERR_CUDA;
     set_last_kernel(tc ? "decode_tc_fp4_d128" : slots ? "append_kv_fp4+decode_mma_fp4_d128" : "decode_mma_fp4_d128");

@@ -201,8 +201,8 @@ __device__ void decode_fp4_worker(DecodeSmem4<Shape> &sm, const DecodeArgs &a, c
     float2 m2 = make_float2(-INFINITY, -INFINITY);  // kTok 1: references of heads 2 t, 2 t + 1
 #pragma unroll
     for (int j = 0; j < kTok; ++j) m[j] = -INFINITY, l[j] = make_float2(0.f, 0.f);
-    const float scale = fp4_score_scale(a);
-    const uint32_t flip = fp4_query_flip(a);
+    const float scale = a.scale_log2;  // above 0
+    const uint32_t flip = a.q_flip;
     // the key of a tile in column gr of S; this lane's two keys of a tile are
     // 2 t + b and 2 t + 1 - b
     const int b = t & 1, krow = (gr & ~1) + ((gr ^ (gr >> 1)) & 1);

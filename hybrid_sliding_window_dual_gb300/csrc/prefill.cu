@@ -1389,19 +1389,12 @@ __global__ void __launch_bounds__(256) prefill_stage_fp4(StageArgs a) {
 }
 
 // q (bf16) to fp16 for the fp16 MMAs: exact for magnitudes in
-// [2^-14, 65504], subnormal below, saturated above (f16_range). 8 elements per step.
+// [2^-14, 65504], subnormal below, saturated above (query_f16x2). 8 elements per step.
 __global__ void __launch_bounds__(256) prefill_q_to_f16(const __nv_bfloat16 *__restrict__ q, __half *__restrict__ q16,
                                                         int64_t n8) {
     for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n8; i += (int64_t)gridDim.x * blockDim.x) {
-        const uint4 raw = reinterpret_cast<const uint4 *>(q)[i];
-        const __nv_bfloat162 *b = reinterpret_cast<const __nv_bfloat162 *>(&raw);
-        __align__(16) __half2 out[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 f = __bfloat1622float2(b[k]);
-            out[k] = __floats2half2_rn(f16_range(f.x), f16_range(f.y));
-        }
-        reinterpret_cast<uint4 *>(q16)[i] = *reinterpret_cast<const uint4 *>(out);
+        const uint4 x = reinterpret_cast<const uint4 *>(q)[i];
+        reinterpret_cast<uint4 *>(q16)[i] = make_uint4(query_f16x2(x.x), query_f16x2(x.y), query_f16x2(x.z), query_f16x2(x.w));
     }
 }
 

@@ -116,7 +116,8 @@ extern "C" {
  * (infinities too; what a NaN becomes is not defined, but finite), and every
  * stored value is exact in fp16 and in bf16. d must be a multiple of 16.
  * Attention with d = 128 (and 8 query heads per kv head, P = 64 for a decode)
- * works on q as fp16: finite values beyond +-65504 count as that there.
+ * works on q as fp16: finite values beyond +-65504 count as that there, and
+ * infinities as NaN.
  * Supported by hswa_append_kv, hswa_rope_append, hswa_read_kv, hswa_decode,
  * hswa_decode_append, hswa_decode_multi and hswa_prefill_chunk_ws
  * (hswa_prefill_chunk where the workspace size of that is 0), any head ratio and
@@ -670,7 +671,8 @@ size_t hswa_prefill_workspace_size_exact(const hswa_pool *pool, const hswa_layer
  * Same arguments and result as hswa_prefill_chunk. Over an FP8 pool the
  * pages the chunk reads are first dequantized (E4M3 code x scale, rounded
  * once to fp16, saturating at 65504) and q is converted to fp16 (exact for
- * magnitudes in [2^-14, 65504], finite ones above as 65504) into ws; the tensor-core kernel then
+ * magnitudes in [2^-14, 65504]; finite ones above count as 65504, infinities
+ * as NaN) into ws; the tensor-core kernel then
  * attends with fp16 operands. q and o are bf16. ws: device, 256-byte
  * aligned, caller-owned, not read before it is written; it must not be
  * reused until the call's work on stream has finished. The page copies are
