@@ -603,11 +603,13 @@ __global__ void __launch_bounds__(32 * kFp4AnyWarps, kE <= 2 ? 2 : 1) decode_fp4
         for (int e = 0; e < kE; ++e) acc[h][e][0] = acc[h][e][1] = 0.f;
     }
     const int32_t bytes = a.d / 2, blocks = a.d / kFp4Block;
-    for (int64_t at = lo + 32 * (rank * kW + w); at < hi; at += 32 * kW * a.cluster) {
-        const int32_t j0 = (int32_t)at, j = j0 + lane;
+    // positions past the table's last page are reported and left out (a length may be any int32)
+    const int32_t end = (int32_t)min((int64_t)hi, (int64_t)a.bt_stride * a.page);
+    if (hi > end && threadIdx.x == 0) set_error(a.err, HSWA_ERR_BOUNDS);
+    for (int64_t at = lo + 32 * (int64_t)(rank * kW + w); at < end; at += 32 * kW * a.cluster) {
         int64_t key = -1;
-        if (j < hi) {
-            const int32_t lp = j / a.page, pg = lp < a.bt_stride ? a.bt[(int64_t)s * a.bt_stride + lp] : -1;
+        if (at + lane < end) {
+            const int32_t j = (int32_t)at + lane, lp = j / a.page, pg = a.bt[(int64_t)s * a.bt_stride + lp];
             if (pg >= 0 && pg < a.num_pages)
                 key = ((int64_t)pg * a.hkv + g) * a.page + (j - lp * a.page);
             else
@@ -655,7 +657,7 @@ __global__ void __launch_bounds__(32 * kFp4AnyWarps, kE <= 2 ? 2 : 1) decode_fp4
         ps[w][lane] = make_float4(p[0], p[1], p[2], p[3]);
         rows[w][lane] = key < 0 ? 0 : key;  // a row that P takes 0 times
         __syncwarp();
-        const int32_t n = min(32, hi - j0);
+        const int32_t n = (int32_t)min((int64_t)32, end - at);
 #pragma unroll 8
         for (int32_t i = 0; i < n; ++i) {
             const float4 pi = ps[w][i];

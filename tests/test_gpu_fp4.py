@@ -464,3 +464,40 @@ def test_a_workspace_serves_fewer_tokens(most):
         c.sess.release(range(c.B))
         step(c, n_tok, seed=3610 + n_tok)
         assert c.sess.ws is ws
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n_tok", [1, 3])
+def test_other_shapes_of_lengths_past_the_table(n_tok):
+    """Positions behind a table's last page are left out and reported, whatever
+    the length says; those that the window still holds are attended."""
+    hq, hkv, d, P, W = 6, 2, 96, 16, 100
+    c = Case([200, 60, 200, 200, 200, 200], seed=170, extra=0, hq=hq, hkv=hkv, d=d, P=P, W=W)
+    cap = c.cfg.max_pages_per_seq * P
+    c.sess.release(range(c.B))
+    c.sess.reserve([0], [cap - 200])  # a row without a free entry
+    c.sess.sync()
+    for layer in range(2):
+        table = c.table(layer)
+        k, v = (x.astype(np.float64) for x in c.values(layer))
+        q = wl.normal((c.B * n_tok, hq, d), 3700 + layer, wl.DTYPE_BF16).cuda()
+        qh = q.double().cpu().numpy()
+        for lens in ([cap + 1, 60, cap + 50, 200, 200, 200], [cap + W + 20, 60, (1 << 31) - 1, 200, cap + (1 << 20), (1 << 31) - 200]):
+            c.sess.d_seq_len.copy_(torch.tensor(lens, dtype=torch.int32))
+            o = torch.full_like(q, float("nan"))
+            c.sess.decode_multi(layer, q, o, c.B, n_tok, c.scale)
+            assert c.sess.check() == H.HSWA_ERR_BOUNDS
+            got = o.double().cpu().numpy()
+            for row in range(c.B * n_tok):
+                s, t = row // n_tok, lens[row // n_tok] - n_tok + row % n_tok
+                first = max(0, t - W + 1) if c.kinds[layer] == SWA else 0
+                at = [j for j in range(first, min(t + 1, cap)) if table[s, j // P] >= 0]
+                for h in range(hq):
+                    if not at:
+                        assert not got[row, h].any()
+                        continue
+                    pages, rows, g = [table[s, j // P] for j in at], [j % P for j in at], h // (hq // hkv)
+                    x = k[pages, g, rows] @ qh[row, h] * c.scale
+                    w = np.exp(x - x.max())
+                    exp = w @ v[pages, g, rows] / w.sum()
+                    assert (np.abs(got[row, h] - exp) <= tolerance(exp, qh, k, v, c.scale, cap)).all(), (layer, lens[s], row, h)
