@@ -501,3 +501,31 @@ def test_other_shapes_of_lengths_past_the_table(n_tok):
                     w = np.exp(x - x.max())
                     exp = w @ v[pages, g, rows] / w.sum()
                     assert (np.abs(got[row, h] - exp) <= tolerance(exp, qh, k, v, c.scale, cap)).all(), (layer, lens[s], row, h)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("P", [16, 48])
+@pytest.mark.parametrize("dtype", [H.HSWA_DTYPE_F32, H.HSWA_DTYPE_BF16, H.HSWA_DTYPE_FP8_E4M3])
+def test_read_of_other_pages(dtype, P):
+    """Rows read back from pools of other pages, from the last slot too."""
+    hkv, d, pages = 3, 128, 9
+    cfg = H.Config(window=128, page_size=P, n_q_heads=hkv, n_kv_heads=hkv, head_dim=d, dtype=dtype, full_pages=pages, swa_pages=pages, max_seqs=1, max_pages_per_seq=pages)
+    s = DualPoolSession(cfg, [FULL])
+    t = torch.float32 if dtype == H.HSWA_DTYPE_F32 else torch.bfloat16
+    x = wl.normal((2, pages * P, hkv, d), 7, wl.DTYPE_BF16).to(t).cuda()
+    slots = torch.randperm(pages * P).int().cuda()
+    s.append(0, x[0], x[1], slots)
+    k, v = (torch.full((pages * P, hkv, d), float("nan"), dtype=t, device="cuda") for _ in range(2))
+    s.read(0, slots, k, v)
+    assert s.check() == 0
+    for which, got in enumerate((k, v)):
+        exp = x[which]
+        if dtype == H.HSWA_DTYPE_FP8_E4M3:  # K rows of 128 codes, V columns of a page
+            pool, scales = (s.k[0], s.ks[0]) if which == 0 else (s.v[0].view(pages, hkv, d, P).transpose(2, 3), s.vs[0])
+            page, row = slots.long() // P, slots.long() % P
+            exp = (pool[page, :, row].contiguous().view(torch.float8_e4m3fn).float() * scales[page, :, row]).bfloat16()
+            # these rows: off by half a code's step (2^-4 of the value, 2^-10 of the scale below the normal codes) and the bf16's
+            y, most = x[which].float(), scales.max() * 2.0 ** -10
+            assert ((exp.float() - y).abs() <= (2.0 ** -4 + 2.0 ** -8 + 2.0 ** -12) * y.abs() + 1.01 * most).all()
+        assert torch.equal(got, exp)
+    s.close()

@@ -342,3 +342,25 @@ def test_count_tokens_in_an_array_between_others(S, V, pad, first):
             assert H.hswa_check() == 0
             assert np.array_equal(counts.cpu().numpy().view(np.uint16), want)
             assert torch.equal(store[~mine], before[~mine])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("S,n,V", [(80, 1, 50021), (40, 2, 131071), (170, 1, 9999)])
+def test_probs_of_odd_vocabularies_in_batches(S, n, V, dtype):
+    """Rows off every boundary, more of them than an SM each."""
+    logits, params, counts, draft, bt, bias, allowed = inputs(S, n, V, dtype, seed=S + n)
+    p = torch.full(logits.shape, float("nan"), device="cuda")
+    check(run(logits, p, params, counts, draft, bt, bias, bits(allowed)), logits, params, counts, draft, bt, bias, allowed)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [1003, 30001, 400001, 400000])
+def test_probs_in_place_of_long_rows(V):
+    """p is the logits: rows in registers and rows read three times, on and off a boundary."""
+    for dtype in CODE:
+        logits, params, counts, draft, bt, bias, allowed = inputs(3, 2, V, dtype, seed=V)
+        apart = run(logits, torch.empty_like(logits), params, counts, draft, bt, bias, bits(allowed))
+        same = logits.clone()
+        run(same, same, params, counts, draft, bt, bias, bits(allowed))
+        assert torch.equal(same, apart)
