@@ -1255,7 +1255,7 @@ static_assert(offsetof(DecodeTc8Smem, q) % 1024 == 0 && offsetof(DecodeTc8Smem, 
 // FP4 pools: as for FP8, but the converter multiplies each code by its block's
 // scale (exact in f16), so that the MMAs and the softmax are those of 16-bit
 // pages: V is written as [keys][d]. 64 sequences of 1K to 32K tokens, 8 query
-// tokens each: 695 us (with one group of converters 775), 16 763; 1.25 GB, 189 us
+// tokens each: 696 us (with one group of converters 775), 16 771; 1.25 GB, 189 us
 // at a plain copy's rate: an SM needs about 1500 cycles for a page, in which
 // conversion, scores, softmax and PV of neighbouring pages overlap in part.
 struct DecodeTc4Smem {
@@ -2727,8 +2727,8 @@ cudaError_t launch_decode_fp4(int workers, cudaStream_t st, const DecodeArgs &a)
 
 // Query tokens per sequence from which an FP4 decode runs on the tensor-core
 // kernel; below it decode_mma_fp4_d128 takes them in one launch. 64 sequences of
-// 1K to 32K tokens: 4 tokens each 560 to 585 us there, 694 here; 5 tokens 717 here,
-// and there two launches (560 + 209).
+// 1K to 32K tokens: 4 tokens each 555 to 564 us there, 694 here; 5 tokens 717 to 732
+// here, and there two launches (560 + 209).
 constexpr int kTcMinTokensFp4 = 5;
 
 // The most partial records that a decode of n_tok tokens, or of fewer, leaves on an SM.

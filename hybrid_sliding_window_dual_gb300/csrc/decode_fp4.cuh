@@ -6,8 +6,8 @@
 // element, not the loads, decide how near the kernel comes to the memory's rate:
 // conversions, their products with scales, and the MMAs, which an SM's quarter
 // issues one after the other (64 sequences of 1K to 32K tokens, one token each:
-// 209 us, 0.9 of a plain copy's rate; four each 570, where the MMAs alone are
-// 240). Every choice below saves some; times are that first case's.
+// 210 us, 0.9 of a plain copy's rate; two each 306; four each 555 to 564, where the
+// MMAs alone are 240). Every choice below saves some; times are that first case's.
 //   * A warp is a worker of its own. It takes an equal share of the units (a
 //     page of a kv head), streams them through its own ring of kParts parts
 //     and leaves its own partial records: no barriers between warps, no
@@ -526,7 +526,7 @@ static_assert(kFp4PlanSeqs <= 32, "a lane each");
 
 // kPlan: without decode_plan before it, one launch less (3 sequences of 700 to
 // 2500 tokens 12.5 us against 13.3). With 64 sequences it was 1 us slower, and with
-// Fp4Four's registers 10 (570 us).
+// Fp4Four's registers 10.
 template <class Shape>
 bool fp4_plans(int n_seqs) { return Shape::kTok <= 2 && n_seqs <= kFp4PlanSeqs; }
 template <class Shape, bool kPlan>

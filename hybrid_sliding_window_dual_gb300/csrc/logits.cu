@@ -495,7 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_probs(const 
         }
         const uint32_t own = r.load_all(bits, z);  // bit g: group g goes on the list
         if constexpr (kVec) {
-            // what a CTA in this one's place will read: on its way to L2 while this one computes
+            // what a CTA in this one's place will read, under a mask whole slices all the
+            // same: on its way to L2 while this one computes
             if (tid == 0 && a.ahead > 0 && (int64_t)row + a.ahead < a.rows) {
                 const int64_t next = (int64_t)row + a.ahead;
                 prefetch_l2(r.logits + a.ahead * a.logits_stride + lo, (hi - lo) * (int32_t)sizeof(TL));
@@ -807,10 +808,10 @@ constexpr int kRowGroups = 5;
 int row_groups(int n) { return n <= 2 ? 2 : n <= 4 ? 4 : n; }
 
 // Registers for as few groups as hold a slice: an idle group costs its
-// instructions (8 x 4 rows of 8000 5.4 us with 2 groups, 6.8 with 5; 256 of 131000
-// 85 with 4, 91 with 5). Few rows take 1024 threads with half the groups (4 rows of
-// 100003 11.6 us against 14.5); many are faster with CTAs of 512, two an SM (256
-// rows of 150000 93 us against 100).
+// instructions (256 rows of 131000 fp32 under grammars 82 us with 4, 89 with 5). Few
+// rows take 1024 threads with half the groups (4 rows of 100003 9.2 us against 9.6);
+// many are faster with CTAs of 512, two an SM (256 rows of 150000 79 us, with 1024
+// threads of 3 groups 128).
 template <typename TL, typename TP, bool kVec>
 cudaError_t launch_row(const ProbsArgs &a, int64_t rows, cudaStream_t st) {
     const int32_t groups = (a.slice / 8 + 511) / 512;  // of 512 threads
@@ -869,7 +870,9 @@ extern "C" int hswa_logits_probs(int logits_dtype, const void *logits, int64_t l
     a.err = error_word();
     // CTAs per row: few rows spread over the GPU, in slices of at least 1024
     // values; many rows take as many as keep a thread's values in registers (256 rows of
-    // 100000 on 5 CTAs of 5 groups 54 us, on 8 of 4 64; of 50000 on 3 of 5 35, on 7 of 2 44).
+    // 100000, bf16 to fp32, on 5 CTAs of 5 groups 53.5 us, on 8 of 4 63.4; of 50000 on 3 of
+    // 5 35.4, on 7 of 2 44). Not the best everywhere: 8 of 2 groups take 34.5 for those
+    // 50000, and 37.5 in place of 39.8 where the logits are fp32.
     const int sms = sm_count();
     if (sms <= 0) return HSWA_ERR_CUDA;
     const auto slice_of = [&](int c) { return ((vocab + 8 * c - 1) / (8 * c)) * 8; };

@@ -528,11 +528,13 @@ size_t hswa_decode_multi_workspace_size(const hswa_pool *pool, int n_seqs, int n
  * i * n_tok + w). A token with t < 0 gets o = 0. n_tok = 1 is hswa_decode.
  * ws: device workspace of at least hswa_decode_multi_workspace_size bytes.
  * The SWA pages must still hold positions from L - n_tok + 1 - W on: release
- * out-of-window pages before the draft tokens are reserved. Bf16 and FP8
- * pools; every page is streamed once for all n_tok tokens. n_tok outside
+ * out-of-window pages before the draft tokens are reserved. On the kernels
+ * for d = 128, 8 query heads per kv head and P = 64 (bf16, FP8 and FP4 pools)
+ * every page is streamed once for all n_tok tokens; other shapes read it for
+ * each token. n_tok outside
  * [1, HSWA_DECODE_MAX_TOKENS] gives HSWA_ERR_INVALID_ARG; n_seqs * n_tok
  * above 65535 (query rows the merge of split pages takes in one launch)
- * gives HSWA_ERR_UNSUPPORTED. */
+ * gives HSWA_ERR_UNSUPPORTED on bf16 and FP8 pools of that shape. */
 int hswa_decode_multi(const hswa_pool *pool, const hswa_layer *layer, const void *q, void *o,
                       const int32_t *d_bt, const int32_t *d_seq_len, int n_seqs, int n_tok, float scale,
                       void *ws, size_t ws_bytes, hswa_stream_t stream);
@@ -603,7 +605,8 @@ int hswa_count_tokens(uint16_t *counts, int64_t count_stride, const int32_t *tok
  * the largest z and 0 elsewhere. Values of +inf share the probability evenly;
  * a row with nothing but -inf becomes zeros. Sums have a fixed order: equal
  * inputs give equal bits. p is within about 1e-6 of that in relative terms
- * (times 1 + |z| / temperature for z's own roundings), rounded once to its type.
+ * (times 1 + |z| / temperature for z's own roundings), rounded once to its type;
+ * one below 2^-126 may come out as 0.
  * logits, p: device rows of vocab values, HSWA_DTYPE_F32 or HSWA_DTYPE_BF16
  * each by itself, logits_stride / p_stride (>= vocab) elements apart; p may be the
  * logits if type and stride are the same (an overlap otherwise is
