@@ -3024,7 +3024,9 @@ int decode_impl(const hswa_pool *pool, const hswa_layer *layer, const void *q, v
         return decode_fp4(pool, layer, q, o, d_bt, d_seq_len, n_seqs, n_tok, scale, ws, ws_bytes, slots, k_new, v_new,
                           stream);
     }
-    if (!decode_fast_ok(pool, layer, q, o) ||
+    const bool tc = n_tok >= kTcMinTokens;
+    // (the tensor-core kernel takes the score of the largest product for the largest)
+    if (!decode_fast_ok(pool, layer, q, o) || (tc && !(scale > 0.f)) ||
         (fused && (((uintptr_t)k_new & 15) || ((uintptr_t)v_new & 15)))) {
         if (!pw && !generic_takes(pool->cfg, (int64_t)n_seqs * n_tok)) return HSWA_ERR_UNSUPPORTED;  // before the append
         if (fused) {
@@ -3040,7 +3042,6 @@ int decode_impl(const hswa_pool *pool, const hswa_layer *layer, const void *q, v
     if ((int64_t)n_seqs * n_tok > 65535) return HSWA_ERR_UNSUPPORTED;  // rows of the combine grid
     const int sms = sm_count();
     if (sms <= 0) return HSWA_ERR_CUDA;
-    const bool tc = n_tok >= kTcMinTokens;
     const bool large = decode_large(c, *layer, n_seqs, layer->kind == HSWA_KIND_SWA ? c.swa_pages : c.full_pages);
     const int per_sm = tc   ? decode_tc_ctas_per_sm<DecodeTcSmem>(n_tok)
                        : pw ? decode_ctas_per_sm_t<1, true>()

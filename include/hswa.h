@@ -530,8 +530,9 @@ size_t hswa_decode_multi_workspace_size(const hswa_pool *pool, int n_seqs, int n
  * The SWA pages must still hold positions from L - n_tok + 1 - W on: release
  * out-of-window pages before the draft tokens are reserved. On the kernels
  * for d = 128, 8 query heads per kv head and P = 64 (bf16, FP8 and FP4 pools)
- * every page is streamed once for all n_tok tokens; other shapes read it for
- * each token. n_tok outside
+ * every page is streamed once for all n_tok tokens; other shapes (and bf16
+ * pools from 4 tokens on under a scale that is not above 0) read it for each
+ * token. n_tok outside
  * [1, HSWA_DECODE_MAX_TOKENS] gives HSWA_ERR_INVALID_ARG; n_seqs * n_tok
  * above 65535 (query rows the merge of split pages takes in one launch)
  * gives HSWA_ERR_UNSUPPORTED on bf16 and FP8 pools of that shape. */

@@ -117,3 +117,53 @@ def test_prefill_of_bad_queries(dtype):
             alone = (x[30, 7, 44] * first[layer][0, 44]).item()
             only_there(prefill(layer, x), clean, bad, [bad[1]] if dtype == BF16 and alone == -math.inf else [])
     s.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [-0.4, -3.0, 0.0])
+@pytest.mark.parametrize("n_tok", [1, 3, 4, 8, 16])
+def test_decode_under_scales_that_are_not_positive(n_tok, scale):
+    """bf16 pools: against 64-bit attention over the rows read back. Weights are
+    rounded to bf16 (2^-8 of each, so at most that of the largest value), scores
+    summed and scaled in fp32 (d + 8 roundings of at most 2^-23 of |q| |k| scale, twice
+    that of the largest value), the output rounded to bf16."""
+    lengths, W = [16, 63, 64, 200, 900, 4000], 128
+    s = session(BF16, lengths, 4400, 0)
+    for layer in range(2):
+        q = wl.normal((len(lengths) * n_tok, 64, 128), 4500 + layer, wl.DTYPE_BF16).cuda()
+        o = torch.full_like(q, float("nan"))
+        s.decode_multi(layer, q, o, len(lengths), n_tok, scale)
+        assert s.check() == 0
+        for i, L in enumerate(lengths):
+            pos = torch.arange(L, device="cuda")
+            slots = (s.bt(layer)[i, pos // 64] * 64 + pos % 64).int()
+            k, v = (torch.empty(L, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+            s.read(layer, slots, k, v)
+            k, v = (x.double().repeat_interleave(8, 1) for x in (k, v))
+            for w in range(n_tok):
+                t = L - n_tok + w
+                first = max(0, t - W + 1) if layer else 0
+                x = q[i * n_tok + w].double()
+                z = torch.einsum("hd,lhd->hl", x, k[first:t + 1]) * scale
+                exp = torch.einsum("hl,lhd->hd", z.softmax(1), v[first:t + 1])
+                score = (128 + 8) * 2.0 ** -23 * x.norm(dim=1).max() * k.norm(dim=2).max() * abs(scale) + 2.0 ** -20
+                tol = 2.0 ** -8 * exp.abs() + v.abs().max() * (2.0 ** -8 + 2 * score)
+                assert ((o[i * n_tok + w].double() - exp).abs() <= tol).all(), (layer, L, w)
+    s.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n_tok", [1, 2, 3, 4, 5, 9, 16])
+@pytest.mark.parametrize("dtype", [FP8, FP4])
+def test_a_negative_scale_is_that_of_the_negative_query(dtype, n_tok):
+    """Equal bits: products and sums of the one are those of the other."""
+    s = session(dtype, LENGTHS, 4600, 0)
+    for layer in range(2):
+        q = wl.normal((len(LENGTHS) * n_tok, 64, 128), 4700 + layer, wl.DTYPE_BF16).cuda()
+        outs = []
+        for x, scale in ((q, -0.3), (-q, 0.3)):
+            o = torch.full_like(q, float("nan"))
+            s.decode_multi(layer, x, o, len(LENGTHS), n_tok, scale)
+            outs.append(o)
+        assert s.check() == 0 and torch.isfinite(outs[0]).all() and torch.equal(outs[0], outs[1])
+    s.close()
